@@ -354,6 +354,132 @@ sgl_status sgl_cascade_decode_attention_fp8(
     int32_t max_group_members, int32_t max_depth, void* out, void* workspace,
     size_t workspace_bytes, const sgl_attn_dims* dims, sgl_stream_t stream);
 
+/*
+ * Sliding-window attention with a few first tokens that stay visible.
+ *
+ * The query at position P of a request sees the key at position j when
+ *     j <= P  and  (j < sinks  or  j > P - window):
+ * the `window` most recent tokens, itself among them, and the request's first
+ * `sinks` tokens.  window >= 1 (else SGL_ERR_INVALID_ARG; from the longest
+ * length on it is full causal attention), sinks >= 0.
+ * Only positions that some query of the call sees are read, in req_to_token
+ * as in the pools: a request's other entries may be stale (their slots freed
+ * and serving other requests) or hold anything.  Rows that are read hold
+ * finite values, as in every attention call here.
+ *
+ * sgl_decode_attention_window -- sgl_decode_attention over those keys (the
+ *   query is at position seq_lens[r] - 1).  Arguments, types and errors as
+ *   there, but:
+ *     seq_lens  : a length below 1 is a padding row: nothing of it is read and
+ *                 its row of out stays as it was.  Keys past max_seq_len are
+ *                 never read.
+ *     workspace : >= sgl_decode_window_workspace_bytes(batch, max_seq_len,
+ *                 window, sinks, dims); scratch, nothing in it outlasts a call.
+ * sgl_extend_attention_window -- the suffix queries of sgl_extend_attention
+ *   over those keys (suffix query i is at position prefix_lens[r] + i).  Every
+ *   key and value, the suffix's too, is read from the pool through
+ *   req_to_token: row positions prefix_lens[r] .. + extend_lens[r] - 1 hold the
+ *   suffix's slots, already stored (sgl_qk_norm_rope_store_kv or
+ *   sgl_store_kv).  Arguments, types and errors as for sgl_extend_attention
+ *   without k_new / v_new, but:
+ *     max_prefix: >= max(prefix_lens) (host value)
+ *     workspace : >= sgl_extend_window_workspace_bytes(batch, total_extend,
+ *                 max_extend, max_prefix, window, sinks, dims); its first 256
+ *                 bytes zero-filled once before first use (word 0: the
+ *                 bounded-wait status, as for sgl_extend_attention).
+ * The _fp8 calls are the same over e4m3 pools (values are code * scale; see
+ * "FP8 KV pool" above; the extend's query range is sgl_extend_attention_fp8's).
+ */
+size_t sgl_decode_window_workspace_bytes(int32_t batch, int32_t max_seq_len, int32_t window,
+                                         int32_t sinks, const sgl_attn_dims* dims);
+size_t sgl_extend_window_workspace_bytes(int32_t batch, int32_t total_extend, int32_t max_extend,
+                                         int32_t max_prefix, int32_t window, int32_t sinks,
+                                         const sgl_attn_dims* dims);
+sgl_status sgl_decode_attention_window(const void* q, const void* pool_k, const void* pool_v,
+                                       const int32_t* req_to_token, int32_t rtt_rows,
+                                       int32_t rtt_stride, const int32_t* req_pool_idx,
+                                       const int32_t* seq_lens, int32_t batch, int32_t max_seq_len,
+                                       int32_t window, int32_t sinks, void* out, void* workspace,
+                                       size_t workspace_bytes, const sgl_attn_dims* dims,
+                                       sgl_stream_t stream);
+sgl_status sgl_decode_attention_window_fp8(const void* q, const void* pool_k, const void* pool_v,
+                                           float k_scale, float v_scale,
+                                           const int32_t* req_to_token, int32_t rtt_rows,
+                                           int32_t rtt_stride, const int32_t* req_pool_idx,
+                                           const int32_t* seq_lens, int32_t batch,
+                                           int32_t max_seq_len, int32_t window, int32_t sinks,
+                                           void* out, void* workspace, size_t workspace_bytes,
+                                           const sgl_attn_dims* dims, sgl_stream_t stream);
+sgl_status sgl_extend_attention_window(const void* q, const void* pool_k, const void* pool_v,
+                                       const int32_t* req_to_token, int32_t rtt_rows,
+                                       int32_t rtt_stride, const int32_t* req_pool_idx,
+                                       const int32_t* prefix_lens, const int32_t* extend_lens,
+                                       int32_t batch, int32_t total_extend, int32_t max_extend,
+                                       int32_t max_prefix, int32_t window, int32_t sinks, void* out,
+                                       void* workspace, size_t workspace_bytes,
+                                       const sgl_attn_dims* dims, sgl_stream_t stream);
+sgl_status sgl_extend_attention_window_fp8(const void* q, const void* pool_k, const void* pool_v,
+                                           float k_scale, float v_scale,
+                                           const int32_t* req_to_token, int32_t rtt_rows,
+                                           int32_t rtt_stride, const int32_t* req_pool_idx,
+                                           const int32_t* prefix_lens, const int32_t* extend_lens,
+                                           int32_t batch, int32_t total_extend, int32_t max_extend,
+                                           int32_t max_prefix, int32_t window, int32_t sinks,
+                                           void* out, void* workspace, size_t workspace_bytes,
+                                           const sgl_attn_dims* dims, sgl_stream_t stream);
+
+/*
+ * sgl_qk_norm_rope_store_kv -- what a layer does between its projections and
+ * its attention, in one pass: head norms of Q and K, rotary positions, and the
+ * store of K and V into their slots.
+ *
+ * For token t and each head row x (D values): y = x * r * w with
+ * r = 1 / sqrt(mean(x^2) + eps) and the head weight w (y = x without a
+ * weight); then the pairs (a, b) of the first rot_dim values of y turn by
+ * their angle: (a cos - b sin, b cos + a sin).  Pair i (0 <= i < rot_dim / 2)
+ * is values (i, i + rot_dim / 2), or (2 i, 2 i + 1) when interleaved, and its
+ * angle is positions[axis, t] * inv_freq[i], axis = freq_axis[i] (0 with one
+ * axis).  Q rows go to q_out, K rows to pool_k[slots[t]], the V rows
+ * unchanged to pool_v[slots[t]].  Arithmetic is fp32 with one rounding at the
+ * end; angles keep 2^-24 turns at any int32 position.
+ *   q            : bf16, token t's Hq rows of D side by side at t * q_stride
+ *                  elements; k, v: Hkv rows at t * k_stride, t * v_stride.  The
+ *                  strides (multiples of 8, >= the rows) let the three be
+ *                  parts of one packed projection.
+ *   q_weight, k_weight : bf16 [D], each may be NULL (no norm of those rows);
+ *                  eps > 0 and finite when one is given
+ *   positions    : int32 [n_axes, n], any values (several axes: time, height
+ *                  and width of an image or video token)
+ *   inv_freq     : fp32 [rot_dim / 2];  freq_axis: int32 [rot_dim / 2], the axis
+ *                  of each frequency (clamped to [0, n_axes)), unread with one
+ *   rot_dim      : 0 (no rotation: positions and inv_freq unread) up to D, a
+ *                  multiple of 16 (else SGL_ERR_UNSUPPORTED)
+ *   slots        : int32 [n], distinct; a token whose slot is outside
+ *                  [0, pool_size) is padding: nothing of it is written, its
+ *                  q_out rows included
+ *   q_out        : bf16 [n, Hq, D]; q itself when q_stride is Hq * D, else apart
+ *                  from q, k and v (an overlap is SGL_ERR_INVALID_ARG)
+ * sgl_qk_norm_rope_store_kv_fp8 -- the same into e4m3 pools: codes of the fp32
+ *   rows over the scales, rounded and saturated as by sgl_store_kv_fp8 (K
+ *   rows are not rounded to bf16 first).
+ */
+sgl_status sgl_qk_norm_rope_store_kv(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                     const void* v, int64_t v_stride, const void* q_weight,
+                                     const void* k_weight, float eps, const int32_t* positions,
+                                     int32_t n_axes, const float* inv_freq, const int32_t* freq_axis,
+                                     int32_t rot_dim, int32_t interleaved, const int32_t* slots,
+                                     int32_t n, void* q_out, void* pool_k, void* pool_v,
+                                     const sgl_attn_dims* dims, sgl_stream_t stream);
+sgl_status sgl_qk_norm_rope_store_kv_fp8(const void* q, int64_t q_stride, const void* k,
+                                         int64_t k_stride, const void* v, int64_t v_stride,
+                                         const void* q_weight, const void* k_weight, float eps,
+                                         const int32_t* positions, int32_t n_axes,
+                                         const float* inv_freq, const int32_t* freq_axis,
+                                         int32_t rot_dim, int32_t interleaved, const int32_t* slots,
+                                         int32_t n, void* q_out, void* pool_k, void* pool_v,
+                                         float k_scale, float v_scale, const sgl_attn_dims* dims,
+                                         sgl_stream_t stream);
+
 /* Workspace sizes (host only; no device call). */
 size_t sgl_extend_workspace_bytes(int32_t batch, int32_t total_extend, const sgl_attn_dims* dims);
 size_t sgl_decode_workspace_bytes(int32_t batch, int32_t max_seq_len, const sgl_attn_dims* dims);
@@ -386,6 +512,10 @@ size_t sgl_cascade_decode_workspace_bytes(int32_t batch, int32_t max_seq_len, in
  * (the ones sgl_extend_attention reads); sgl_check_extend_fp8_indices those
  * of positions 0..p+e-1 (sgl_extend_attention_fp8 reads the suffix from the
  * pool too).
+ * sgl_check_decode_window_indices and sgl_check_extend_window_indices check the
+ * positions that the sliding-window calls read (a decode length of 0 is a
+ * padding row there, a negative one kind 3).  The slots of
+ * sgl_qk_norm_rope_store_kv are checked like a store's, padding left out.
  * sgl_check_store_kv_indices needs a scratch bitmap of (pool_size+7)/8 bytes
  * (rounded up to 16) in `bitmap`; it is cleared by the call.
  * sgl_check_cascade_groups needs sgl_check_cascade_scratch_bytes(batch,
@@ -411,6 +541,17 @@ sgl_status sgl_check_decode_indices(const int32_t* req_to_token, int32_t rtt_row
                                     const int32_t* req_pool_idx, const int32_t* seq_lens,
                                     int32_t batch, int32_t max_seq_len, int64_t pool_size,
                                     int32_t* d_error, sgl_stream_t stream);
+sgl_status sgl_check_decode_window_indices(const int32_t* req_to_token, int32_t rtt_rows,
+                                           int32_t rtt_stride, const int32_t* req_pool_idx,
+                                           const int32_t* seq_lens, int32_t batch,
+                                           int32_t max_seq_len, int32_t window, int32_t sinks,
+                                           int64_t pool_size, int32_t* d_error, sgl_stream_t stream);
+sgl_status sgl_check_extend_window_indices(const int32_t* req_to_token, int32_t rtt_rows,
+                                           int32_t rtt_stride, const int32_t* req_pool_idx,
+                                           const int32_t* prefix_lens, const int32_t* extend_lens,
+                                           int32_t batch, int32_t total_extend, int32_t max_extend,
+                                           int32_t max_prefix, int32_t window, int32_t sinks,
+                                           int64_t pool_size, int32_t* d_error, sgl_stream_t stream);
 size_t sgl_check_cascade_scratch_bytes(int32_t batch, int32_t max_depth);
 sgl_status sgl_check_cascade_groups(const int32_t* req_to_token, int32_t rtt_rows,
                                     int32_t rtt_stride, const int32_t* req_pool_idx,

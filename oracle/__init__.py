@@ -28,6 +28,9 @@ What it computes, and where the pages fix it:
     rows read back from the pool like the prefix) and cascade decode over
     the dequantised rows -- "Inside SGLang", Step 6 (Decide how much memory
     becomes KV cache: --kv-cache-dtype fp8_e4m3, scales from the checkpoint).
+  * sliding-window decode and extend with first tokens that stay visible
+    (``oracle.window``), and head norms with rotary positions
+    (``oracle.rope``): the definitions the header states.
   * radix tree (``oracle.radix``): token runs with their KV slots, match
     with node splitting, insert, lock counts on the path to the root,
     leaf-first LRU eviction -- "Inside SGLang", Step 4 and the "SGLang"
@@ -50,3 +53,5 @@ from .attention import (  # noqa: F401
 )
 from . import fp8  # noqa: F401
 from . import radix  # noqa: F401
+from . import rope  # noqa: F401
+from . import window  # noqa: F401

@@ -10,6 +10,7 @@ there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 from . import build as _build
@@ -84,6 +85,27 @@ _SIGS = {
                                                         _P(sgl_attn_dims), c_vp]),
     "sgl_check_extend_fp8_indices": (ctypes.c_int, [c_vp, c_i32, c_i32, c_vp, c_vp, c_vp, c_i32, c_i32,
                                                     c_i32, c_i32, c_i64, c_vp, c_vp]),
+    "sgl_decode_window_workspace_bytes": (c_size, [c_i32, c_i32, c_i32, c_i32, _P(sgl_attn_dims)]),
+    "sgl_extend_window_workspace_bytes": (c_size, [c_i32] * 6 + [_P(sgl_attn_dims)]),
+    "sgl_decode_attention_window": (ctypes.c_int, [c_vp] * 4 + [c_i32, c_i32, c_vp, c_vp] + [c_i32] * 4
+                                    + [c_vp, c_vp, c_size, _P(sgl_attn_dims), c_vp]),
+    "sgl_decode_attention_window_fp8": (ctypes.c_int, [c_vp] * 3 + [c_f32, c_f32, c_vp, c_i32, c_i32, c_vp, c_vp]
+                                        + [c_i32] * 4 + [c_vp, c_vp, c_size, _P(sgl_attn_dims), c_vp]),
+    "sgl_extend_attention_window": (ctypes.c_int, [c_vp] * 4 + [c_i32, c_i32, c_vp, c_vp, c_vp] + [c_i32] * 6
+                                    + [c_vp, c_vp, c_size, _P(sgl_attn_dims), c_vp]),
+    "sgl_extend_attention_window_fp8": (ctypes.c_int, [c_vp] * 3 + [c_f32, c_f32, c_vp, c_i32, c_i32, c_vp, c_vp,
+                                                                    c_vp] + [c_i32] * 6
+                                        + [c_vp, c_vp, c_size, _P(sgl_attn_dims), c_vp]),
+    "sgl_check_decode_window_indices": (ctypes.c_int, [c_vp, c_i32, c_i32, c_vp, c_vp] + [c_i32] * 4
+                                        + [c_i64, c_vp, c_vp]),
+    "sgl_check_extend_window_indices": (ctypes.c_int, [c_vp, c_i32, c_i32, c_vp, c_vp, c_vp] + [c_i32] * 6
+                                        + [c_i64, c_vp, c_vp]),
+    "sgl_qk_norm_rope_store_kv": (ctypes.c_int, [c_vp, c_i64] * 3 + [c_vp, c_vp, c_f32, c_vp, c_i32, c_vp, c_vp,
+                                                                     c_i32, c_i32, c_vp, c_i32, c_vp, c_vp, c_vp,
+                                                                     _P(sgl_attn_dims), c_vp]),
+    "sgl_qk_norm_rope_store_kv_fp8": (ctypes.c_int, [c_vp, c_i64] * 3
+                                      + [c_vp, c_vp, c_f32, c_vp, c_i32, c_vp, c_vp, c_i32, c_i32, c_vp, c_i32,
+                                         c_vp, c_vp, c_vp, c_f32, c_f32, _P(sgl_attn_dims), c_vp]),
     "sgl_check_cascade_scratch_bytes": (c_size, [c_i32, c_i32]),
     "sgl_check_cascade_groups": (ctypes.c_int, [c_vp, c_i32, c_i32, c_vp, c_vp, c_i32, c_vp, c_vp, c_vp,
                                                 c_vp, c_vp, c_i32, c_i32, c_i32, c_vp, c_size, c_vp,
@@ -360,6 +382,247 @@ def sgl_extend_attention_fp8(q, pool_k, pool_v, k_scale, v_scale, req_to_token, 
         _ptr(extend_lens), B, T, int(max_extend), int(max_prefix), _ptr(out), _ptr(workspace),
         int(workspace.numel() * workspace.element_size()), ctypes.byref(d), _stream(stream)))
     return out
+
+
+# ----------------------------------------------------------------- sliding window
+
+@functools.lru_cache(maxsize=256)
+def _dims_ref(num_q_heads, num_kv_heads, head_dim, pool_size, sm_scale):
+    return ctypes.byref(make_dims(num_q_heads, num_kv_heads, head_dim, pool_size, sm_scale))
+
+
+def _need(name, ok, what):
+    if not ok:
+        raise ValueError(f"{name}: {what}")
+
+
+def _need_dense(name, dtype, **tensors):
+    """Dense tensors of one type on the current device (None passes)."""
+    import torch
+    dev = torch.cuda.current_device()
+    for arg, t in tensors.items():
+        if t is not None and not (t.dtype is dtype and t.is_contiguous() and t.get_device() == dev):
+            raise ValueError(f"{name}: {arg} must be a dense {dtype} tensor on the current CUDA device")
+
+
+def _raw_stream(stream):
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _on(stream):
+    """Context whose allocations belong to the stream that a call runs on, so
+    that a scratch buffer dropped on return is not handed out again before
+    the call's kernels are done with it."""
+    import contextlib
+
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)))
+    return torch.cuda.stream(stream)
+
+
+def decode_window_workspace_bytes(batch, max_seq_len, window, sinks, dims: sgl_attn_dims) -> int:
+    return int(lib().sgl_decode_window_workspace_bytes(int(batch), int(max_seq_len), int(window), int(sinks),
+                                                       ctypes.byref(dims)))
+
+
+def extend_window_workspace_bytes(batch, total_extend, max_extend, max_prefix, window, sinks,
+                                  dims: sgl_attn_dims) -> int:
+    return int(lib().sgl_extend_window_workspace_bytes(int(batch), int(total_extend), int(max_extend),
+                                                       int(max_prefix), int(window), int(sinks),
+                                                       ctypes.byref(dims)))
+
+
+def _window_tensors(name, q, pool_k, pool_v, req_to_token, lens, out, workspace, kv_dtype):
+    import torch
+    _need_dense(name, torch.bfloat16, q=q, out=out)
+    _need_dense(name, kv_dtype, pool_k=pool_k, pool_v=pool_v)
+    _need_dense(name, torch.int32, req_to_token=req_to_token, **lens)
+    _need(name, q.dim() == 3 and pool_k.dim() == 3 and pool_v.shape == pool_k.shape
+          and q.shape[2] == pool_k.shape[2], "q [T, Hq, D] and pools [S, Hkv, D]")
+    _need(name, req_to_token.dim() == 2, "req_to_token [rows, stride]")
+    batch = next(iter(lens.values())).shape[0]
+    _need(name, all(t.dim() == 1 and t.shape[0] == batch for t in lens.values()), "one entry a request in "
+          + ", ".join(lens))
+    _need(name, out is None or out.shape == q.shape, "out of q's shape")
+    if workspace is not None:
+        _need(name, workspace.is_contiguous() and workspace.get_device() == q.get_device(),
+              "workspace: a dense buffer on q's device")
+
+
+def _decode_window(name, q, pool_k, pool_v, scales, req_to_token, req_pool_idx, seq_lens, out, max_seq_len,
+                   window, sinks, workspace, sm_scale, stream):
+    import torch
+    _window_tensors(name, q, pool_k, pool_v, req_to_token, dict(req_pool_idx=req_pool_idx, seq_lens=seq_lens),
+                    out, workspace, torch.uint8 if scales else torch.bfloat16)
+    batch, hq, d = q.shape
+    _need(name, req_pool_idx.shape[0] == batch, "one query a request")
+    dims = _dims_ref(hq, pool_k.shape[1], d, pool_k.shape[0], float(sm_scale))
+    if out is None or workspace is None:
+        with _on(stream):
+            if out is None:
+                out = torch.empty_like(q)
+            if workspace is None:
+                workspace = torch.empty(max(16, lib().sgl_decode_window_workspace_bytes(
+                    batch, int(max_seq_len), int(window), int(sinks), dims)), dtype=torch.uint8, device=q.device)
+    code = getattr(lib(), name)(
+        q.data_ptr(), pool_k.data_ptr(), pool_v.data_ptr(), *scales, req_to_token.data_ptr(),
+        req_to_token.shape[0], req_to_token.shape[1], req_pool_idx.data_ptr(), seq_lens.data_ptr(), batch,
+        int(max_seq_len), int(window), int(sinks), out.data_ptr(), workspace.data_ptr(), workspace.nbytes, dims,
+        _raw_stream(stream))
+    if code != 0:
+        raise SglError(name, code)
+    return out
+
+
+def sgl_decode_attention_window(q, pool_k, pool_v, req_to_token, req_pool_idx, seq_lens, out=None, *,
+                                max_seq_len, window, sinks=0, workspace=None, sm_scale=0.0, stream=None):
+    """One query per request over its last ``window`` keys (the new token's
+    among them) and its first ``sinks``; rows of length 0 are left as they were."""
+    return _decode_window("sgl_decode_attention_window", q, pool_k, pool_v, (), req_to_token, req_pool_idx,
+                          seq_lens, out, max_seq_len, window, sinks, workspace, sm_scale, stream)
+
+
+def sgl_decode_attention_window_fp8(q, pool_k, pool_v, k_scale, v_scale, req_to_token, req_pool_idx, seq_lens,
+                                    out=None, *, max_seq_len, window, sinks=0, workspace=None, sm_scale=0.0,
+                                    stream=None):
+    """``sgl_decode_attention_window`` over an e4m3 pool (values are code * scale)."""
+    return _decode_window("sgl_decode_attention_window_fp8", q, pool_k, pool_v, (float(k_scale), float(v_scale)),
+                          req_to_token, req_pool_idx, seq_lens, out, max_seq_len, window, sinks, workspace,
+                          sm_scale, stream)
+
+
+def _extend_window(name, q, pool_k, pool_v, scales, req_to_token, req_pool_idx, prefix_lens, extend_lens, out,
+                   max_extend, max_prefix, window, sinks, total_extend, workspace, sm_scale, stream):
+    import torch
+    _window_tensors(name, q, pool_k, pool_v, req_to_token,
+                    dict(req_pool_idx=req_pool_idx, prefix_lens=prefix_lens, extend_lens=extend_lens), out,
+                    workspace, torch.uint8 if scales else torch.bfloat16)
+    tokens, hq, d = q.shape
+    total = tokens if total_extend is None else int(total_extend)
+    _need(name, total <= tokens, "total_extend within q's rows")
+    batch = req_pool_idx.shape[0]
+    dims = _dims_ref(hq, pool_k.shape[1], d, pool_k.shape[0], float(sm_scale))
+    if out is None or workspace is None:
+        with _on(stream):
+            if out is None:
+                out = torch.empty_like(q)
+            if workspace is None:
+                workspace = new_workspace(lib().sgl_extend_window_workspace_bytes(
+                    batch, total, int(max_extend), int(max_prefix), int(window), int(sinks), dims), q.device)
+    code = getattr(lib(), name)(
+        q.data_ptr(), pool_k.data_ptr(), pool_v.data_ptr(), *scales, req_to_token.data_ptr(),
+        req_to_token.shape[0], req_to_token.shape[1], req_pool_idx.data_ptr(), prefix_lens.data_ptr(),
+        extend_lens.data_ptr(), batch, total, int(max_extend), int(max_prefix), int(window), int(sinks),
+        out.data_ptr(), workspace.data_ptr(), workspace.nbytes, dims, _raw_stream(stream))
+    if code != 0:
+        raise SglError(name, code)
+    return out
+
+
+def sgl_extend_attention_window(q, pool_k, pool_v, req_to_token, req_pool_idx, prefix_lens, extend_lens, out=None,
+                                *, max_extend, max_prefix, window, sinks=0, total_extend=None, workspace=None,
+                                sm_scale=0.0, stream=None):
+    """Attention of the suffix tokens over their last ``window`` keys and the
+    request's first ``sinks``; prefix AND suffix keys are read from the pool
+    through ``req_to_token`` (the suffix stored first)."""
+    return _extend_window("sgl_extend_attention_window", q, pool_k, pool_v, (), req_to_token, req_pool_idx,
+                          prefix_lens, extend_lens, out, max_extend, max_prefix, window, sinks, total_extend,
+                          workspace, sm_scale, stream)
+
+
+def sgl_extend_attention_window_fp8(q, pool_k, pool_v, k_scale, v_scale, req_to_token, req_pool_idx, prefix_lens,
+                                    extend_lens, out=None, *, max_extend, max_prefix, window, sinks=0,
+                                    total_extend=None, workspace=None, sm_scale=0.0, stream=None):
+    """``sgl_extend_attention_window`` over an e4m3 pool (values are code * scale)."""
+    return _extend_window("sgl_extend_attention_window_fp8", q, pool_k, pool_v, (float(k_scale), float(v_scale)),
+                          req_to_token, req_pool_idx, prefix_lens, extend_lens, out, max_extend, max_prefix,
+                          window, sinks, total_extend, workspace, sm_scale, stream)
+
+
+def sgl_check_decode_window_indices(req_to_token, req_pool_idx, seq_lens, *, max_seq_len, window, sinks=0,
+                                    pool_size, d_error, stream=None):
+    _check("sgl_check_decode_window_indices", lib().sgl_check_decode_window_indices(
+        _ptr(req_to_token), int(req_to_token.shape[0]), int(req_to_token.shape[1]), _ptr(req_pool_idx),
+        _ptr(seq_lens), int(req_pool_idx.shape[0]), int(max_seq_len), int(window), int(sinks), int(pool_size),
+        _ptr(d_error), _stream(stream)))
+
+
+def sgl_check_extend_window_indices(req_to_token, req_pool_idx, prefix_lens, extend_lens, *, total_extend,
+                                    max_extend, max_prefix, window, sinks=0, pool_size, d_error, stream=None):
+    _check("sgl_check_extend_window_indices", lib().sgl_check_extend_window_indices(
+        _ptr(req_to_token), int(req_to_token.shape[0]), int(req_to_token.shape[1]), _ptr(req_pool_idx),
+        _ptr(prefix_lens), _ptr(extend_lens), int(req_pool_idx.shape[0]), int(total_extend), int(max_extend),
+        int(max_prefix), int(window), int(sinks), int(pool_size), _ptr(d_error), _stream(stream)))
+
+
+# ----------------------------------------------------------------- norms, rotary positions, store
+
+def _qk_norm_rope_store(name, q, k, v, positions, inv_freq, slots, pool_k, pool_v, scales, q_weight, k_weight,
+                        eps, freq_axis, interleaved, q_out, stream):
+    import torch
+    bf16, dev = torch.bfloat16, torch.cuda.current_device()
+    n, hq, d = q.shape
+    hkv = pool_k.shape[1]
+    for arg, t, h in (("q", q, hq), ("k", k, hkv), ("v", v, hkv)):
+        # dense rows; tokens may lie apart (parts of a packed projection)
+        _need(name, t.dtype is bf16 and t.shape == (n, h, d) and t.get_device() == dev and t.stride(2) == 1
+              and (h == 1 or t.stride(1) == d), f"{arg}: bf16 [n, heads, D] with dense rows on the current device")
+    _need_dense(name, bf16, q_weight=q_weight, k_weight=k_weight, q_out=q_out)
+    _need_dense(name, torch.uint8 if scales else bf16, pool_k=pool_k, pool_v=pool_v)
+    _need_dense(name, torch.int32, positions=positions, slots=slots, freq_axis=freq_axis)
+    _need_dense(name, torch.float32, inv_freq=inv_freq)
+    rot = 0 if inv_freq is None else 2 * inv_freq.shape[0]
+    axes = positions.shape[0] if positions is not None and positions.dim() == 2 else 1
+    _need(name, pool_k.dim() == 3 and pool_v.shape == pool_k.shape and pool_k.shape[2] == d, "pools [S, Hkv, D]")
+    _need(name, slots.shape == (n,), "one slot a token")
+    _need(name, rot == 0 or (positions is not None and inv_freq.dim() == 1
+                             and positions.numel() == axes * n), "positions [n] or [axes, n] and inv_freq [rot / 2]")
+    _need(name, axes == 1 or rot == 0 or (freq_axis is not None and freq_axis.shape == inv_freq.shape),
+          "an axis for each frequency")
+    for arg, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        _need(name, w is None or w.shape == (d,), f"{arg} [D]")
+    _need(name, q_out is None or q_out.shape == q.shape, "q_out of q's shape")
+    if q_out is None:
+        with _on(stream):
+            q_out = torch.empty((n, hq, d), dtype=bf16, device=q.device)
+    ptr = [None if t is None else t.data_ptr() for t in (q_weight, k_weight, positions, inv_freq, freq_axis)]
+    code = getattr(lib(), name)(
+        q.data_ptr(), q.stride(0) if n > 1 else hq * d, k.data_ptr(), k.stride(0) if n > 1 else hkv * d,
+        v.data_ptr(), v.stride(0) if n > 1 else hkv * d, ptr[0], ptr[1], float(eps), ptr[2], axes, ptr[3], ptr[4],
+        rot, 1 if interleaved else 0, slots.data_ptr(), n, q_out.data_ptr(), pool_k.data_ptr(), pool_v.data_ptr(),
+        *scales, _dims_ref(hq, hkv, d, pool_k.shape[0], 0.0), _raw_stream(stream))
+    if code != 0:
+        raise SglError(name, code)
+    return q_out
+
+
+def sgl_qk_norm_rope_store_kv(q, k, v, positions, inv_freq, slots, pool_k, pool_v, *, q_weight=None, k_weight=None,
+                              eps=1e-6, freq_axis=None, interleaved=False, q_out=None, stream=None):
+    """Head norms of Q and K, rotary positions, and the store of K and V into
+    their slots, in one pass; returns the finished queries.
+
+    ``q`` [n, Hq, D], ``k`` and ``v`` [n, Hkv, D] may be parts of one packed
+    projection.  ``inv_freq`` [rot / 2] (None: no rotation) turns the first
+    ``rot`` values of each row by ``positions`` [n], or [axes, n] with
+    ``freq_axis`` naming each frequency's axis.  Tokens whose slot lies
+    outside the pool are padding and leave everything as it was."""
+    return _qk_norm_rope_store("sgl_qk_norm_rope_store_kv", q, k, v, positions, inv_freq, slots, pool_k, pool_v,
+                               (), q_weight, k_weight, eps, freq_axis, interleaved, q_out, stream)
+
+
+def sgl_qk_norm_rope_store_kv_fp8(q, k, v, positions, inv_freq, slots, pool_k, pool_v, k_scale, v_scale, *,
+                                  q_weight=None, k_weight=None, eps=1e-6, freq_axis=None, interleaved=False,
+                                  q_out=None, stream=None):
+    """``sgl_qk_norm_rope_store_kv`` into an e4m3 pool (code = e4m3(row / scale))."""
+    return _qk_norm_rope_store("sgl_qk_norm_rope_store_kv_fp8", q, k, v, positions, inv_freq, slots, pool_k, pool_v,
+                               (float(k_scale), float(v_scale)), q_weight, k_weight, eps, freq_axis, interleaved,
+                               q_out, stream)
 
 
 # ----------------------------------------------------------------- radix tree

@@ -19,7 +19,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_NAME = "libsgl_attn.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
-SOURCES = ["api.cu", "store_kv.cu", "decode.cu", "extend.cu", "mixed.cu", "decode_noalloc.cu", "radix.cpp"]
+SOURCES = ["api.cu", "store_kv.cu", "decode.cu", "extend.cu", "mixed.cu", "decode_noalloc.cu",
+           "decode_window.cu", "extend_window.cu", "qk_rope.cu", "radix.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]

@@ -68,18 +68,22 @@ __global__ void check_store_kernel(const int32_t* __restrict__ slots, int32_t n,
 
 // mode 0: extend (lens_a = prefix, lens_b = extend; the prefix slots are read);
 // mode 2: the same over an e4m3 pool (prefix and suffix slots are read);
-// mode 1: decode (lens_a = seq)
+// mode 1: decode (lens_a = seq).
+// With a window (window > 0, modes 1 and 2) only the positions some query sees
+// are checked: [0, sinks) and those past the first query's position less the
+// window; decode lengths may then be 0 (a padding row).
 __global__ void check_rows_kernel(const int32_t* __restrict__ rtt, int32_t rtt_rows, int32_t stride,
                                   const int32_t* __restrict__ rpi, const int32_t* __restrict__ lens_a,
                                   const int32_t* __restrict__ lens_b, int32_t mode, int64_t S,
-                                  int32_t max_a, int32_t max_b, int32_t* err) {
+                                  int32_t max_a, int32_t max_b, int32_t window, int32_t sinks,
+                                  int32_t* err) {
   const int r = blockIdx.x;
   const int32_t row = rpi[r];
   if (row < 0 || row >= rtt_rows) {
     if (threadIdx.x == 0) report(err, 2, r, 0, row);
     return;
   }
-  int32_t n;
+  int32_t n, lo = 0;  // positions [sinks, lo) are hidden
   if (mode != 1) {
     const int32_t pl = lens_a[r], el = lens_b[r];
     if (pl < 0 || el < 0) {
@@ -95,9 +99,13 @@ __global__ void check_rows_kernel(const int32_t* __restrict__ rtt, int32_t rtt_r
       return;
     }
     n = mode == 2 ? pl + el : pl;
+    if (window > 0) {
+      lo = max(0, pl - window + 1);
+      if (el == 0) n = 0;
+    }
   } else {
     const int32_t sl = lens_a[r];
-    if (sl < 1) {
+    if (sl < (window > 0 ? 0 : 1)) {
       if (threadIdx.x == 0) report(err, 3, r, 0, sl);
       return;
     }
@@ -110,9 +118,11 @@ __global__ void check_rows_kernel(const int32_t* __restrict__ rtt, int32_t rtt_r
       return;
     }
     n = sl;
+    if (window > 0) lo = max(0, sl - window);
   }
   const int32_t* row_p = rtt + (int64_t)row * stride;
   for (int32_t j = threadIdx.x; j < n; j += blockDim.x) {
+    if (j >= sinks && j < lo) continue;
     const int32_t s = row_p[j];
     if (s < 0 || s >= S) report(err, 1, r, j, s);
   }
@@ -316,10 +326,11 @@ size_t sgl_cascade_decode_workspace_bytes(int32_t batch, int32_t max_seq_len, in
 }
 
 namespace {
-// k_new / v_new are null on an e4m3 pool (the suffix is read from the pool)
-// Host checks of an extend call; fills *a.  *empty: nothing to launch.
+// k_new / v_new are null on an e4m3 pool and with a window (the suffix is read
+// from the pool).  Host checks of an extend call; fills *a.  *empty: nothing
+// to launch.
 sgl_status extend_args(const void* q, const void* k_new, const void* v_new, const void* pool_k,
-                       const void* pool_v, bool kv_fp8, float k_scale, float v_scale,
+                       const void* pool_v, bool kv_fp8, bool suffix_in_pool, float k_scale, float v_scale,
                        const int32_t* req_to_token, int32_t rtt_rows, int32_t rtt_stride,
                        const int32_t* req_pool_idx, const int32_t* prefix_lens,
                        const int32_t* extend_lens, int32_t batch, int32_t total_extend,
@@ -331,7 +342,7 @@ sgl_status extend_args(const void* q, const void* k_new, const void* v_new, cons
   if (batch < 0 || total_extend < 0 || max_extend < 0 || max_prefix < 0) return SGL_ERR_INVALID_ARG;
   *empty = batch == 0 || total_extend == 0;
   if (*empty) return SGL_OK;
-  if (!kv_fp8 && (!k_new || !v_new || !aligned16(k_new) || !aligned16(v_new)))
+  if (!suffix_in_pool && (!k_new || !v_new || !aligned16(k_new) || !aligned16(v_new)))
     return SGL_ERR_INVALID_ARG;
   if (!q || !pool_k || !pool_v || !req_to_token || !req_pool_idx || !prefix_lens || !extend_lens ||
       !out)
@@ -377,8 +388,8 @@ sgl_status extend_entry(const void* q, const void* k_new, const void* v_new, con
                         size_t workspace_bytes, const sgl_attn_dims* dims, sgl_stream_t stream) {
   ExtendArgs a;
   bool empty = false;
-  const sgl_status st = extend_args(q, k_new, v_new, pool_k, pool_v, kv_fp8, k_scale, v_scale, req_to_token,
-                                    rtt_rows, rtt_stride, req_pool_idx, prefix_lens, extend_lens, batch,
+  const sgl_status st = extend_args(q, k_new, v_new, pool_k, pool_v, kv_fp8, kv_fp8, k_scale, v_scale,
+                                    req_to_token, rtt_rows, rtt_stride, req_pool_idx, prefix_lens, extend_lens, batch,
                                     total_extend, max_extend, max_prefix, out, workspace, workspace_bytes,
                                     dims, &a, &empty);
   if (st != SGL_OK || empty) return st;
@@ -652,7 +663,7 @@ sgl_status check_extend(const int32_t* req_to_token, int32_t rtt_rows, int32_t r
                         const int32_t* req_pool_idx, const int32_t* prefix_lens,
                         const int32_t* extend_lens, int32_t batch, int32_t total_extend,
                         int32_t max_extend, int32_t max_prefix, int64_t pool_size, int32_t* d_error,
-                        sgl_stream_t stream, int mode) {
+                        sgl_stream_t stream, int mode, int32_t window = 0, int32_t sinks = 0) {
   if (batch < 0 || rtt_rows <= 0 || rtt_stride <= 0 || pool_size <= 0 || d_error == nullptr)
     return SGL_ERR_INVALID_ARG;
   if (batch == 0) return SGL_OK;
@@ -660,7 +671,7 @@ sgl_status check_extend(const int32_t* req_to_token, int32_t rtt_rows, int32_t r
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   check_rows_kernel<<<(unsigned)batch, 256, 0, s>>>(req_to_token, rtt_rows, rtt_stride, req_pool_idx,
                                                     prefix_lens, extend_lens, mode, pool_size,
-                                                    max_prefix, max_extend, d_error);
+                                                    max_prefix, max_extend, window, sinks, d_error);
   check_sum_kernel<<<1, 1024, 0, s>>>(extend_lens, batch, total_extend, d_error);
   return last_launch();
 }
@@ -695,9 +706,263 @@ sgl_status sgl_check_decode_indices(const int32_t* req_to_token, int32_t rtt_row
   if (!req_to_token || !req_pool_idx || !seq_lens) return SGL_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   check_rows_kernel<<<(unsigned)batch, 256, 0, s>>>(req_to_token, rtt_rows, rtt_stride, req_pool_idx,
-                                                    seq_lens, nullptr, 1, pool_size, max_seq_len, 0,
+                                                    seq_lens, nullptr, 1, pool_size, max_seq_len, 0, 0, 0,
                                                     d_error);
   return last_launch();
+}
+
+// ---------------------------------------------------------------- sliding window
+
+size_t sgl_decode_window_workspace_bytes(int32_t batch, int32_t max_seq_len, int32_t window, int32_t sinks,
+                                         const sgl_attn_dims* dims) {
+  if (dims == nullptr || dims->num_kv_heads <= 0 || dims->num_q_heads <= 0) return 0;
+  return decode_window_workspace_bytes(batch, max_seq_len, window, sinks, dims->num_q_heads, dims->num_kv_heads,
+                                       dims->head_dim);
+}
+
+size_t sgl_extend_window_workspace_bytes(int32_t batch, int32_t total_extend, int32_t max_extend,
+                                         int32_t max_prefix, int32_t window, int32_t sinks,
+                                         const sgl_attn_dims* dims) {
+  (void)batch;
+  (void)total_extend;
+  (void)max_extend;
+  (void)max_prefix;
+  (void)window;
+  (void)sinks;
+  (void)dims;
+  return extend_workspace_bytes();
+}
+
+namespace {
+bool valid_window(int32_t window, int32_t sinks) { return window >= 1 && sinks >= 0; }
+
+sgl_status decode_window_entry(const void* q, const void* pool_k, const void* pool_v, bool kv_fp8, float k_scale,
+                               float v_scale, const int32_t* req_to_token, int32_t rtt_rows, int32_t rtt_stride,
+                               const int32_t* req_pool_idx, const int32_t* seq_lens, int32_t batch,
+                               int32_t max_seq_len, int32_t window, int32_t sinks, void* out, void* workspace,
+                               size_t workspace_bytes, const sgl_attn_dims* dims, sgl_stream_t stream) {
+  float scale;
+  const sgl_status st = validate_decode_call(q, pool_k, pool_v, req_to_token, rtt_rows, rtt_stride, req_pool_idx,
+                                             seq_lens, batch, max_seq_len, out, dims, &scale);
+  if (st != SGL_OK) return st;
+  if (!valid_window(window, sinks)) return SGL_ERR_INVALID_ARG;
+  if (batch == 0) return SGL_OK;
+  if (workspace == nullptr || !aligned16(workspace) ||
+      workspace_bytes < sgl_decode_window_workspace_bytes(batch, max_seq_len, window, sinks, dims))
+    return SGL_ERR_WORKSPACE;
+  DecodeArgs a;
+  a.q = q;
+  a.pool_k = pool_k;
+  a.pool_v = pool_v;
+  a.req_to_token = req_to_token;
+  a.rtt_stride = rtt_stride;
+  a.req_pool_idx = req_pool_idx;
+  a.seq_lens = seq_lens;
+  a.batch = batch;
+  a.max_seq_len = max_seq_len;
+  a.out = out;
+  a.workspace = workspace;
+  a.workspace_bytes = workspace_bytes;
+  a.num_q_heads = dims->num_q_heads;
+  a.num_kv_heads = dims->num_kv_heads;
+  a.head_dim = dims->head_dim;
+  a.sm_scale = scale;
+  a.kv_fp8 = kv_fp8;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.window = window;
+  a.sinks = sinks;
+  return launch_decode_window(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+sgl_status extend_window_entry(const void* q, const void* pool_k, const void* pool_v, bool kv_fp8, float k_scale,
+                               float v_scale, const int32_t* req_to_token, int32_t rtt_rows, int32_t rtt_stride,
+                               const int32_t* req_pool_idx, const int32_t* prefix_lens, const int32_t* extend_lens,
+                               int32_t batch, int32_t total_extend, int32_t max_extend, int32_t max_prefix,
+                               int32_t window, int32_t sinks, void* out, void* workspace, size_t workspace_bytes,
+                               const sgl_attn_dims* dims, sgl_stream_t stream) {
+  if (!valid_window(window, sinks)) return SGL_ERR_INVALID_ARG;
+  ExtendArgs a;
+  bool empty = false;
+  const sgl_status st = extend_args(q, nullptr, nullptr, pool_k, pool_v, kv_fp8, true, k_scale, v_scale,
+                                    req_to_token, rtt_rows, rtt_stride, req_pool_idx, prefix_lens, extend_lens,
+                                    batch, total_extend, max_extend, max_prefix, out, workspace, workspace_bytes,
+                                    dims, &a, &empty);
+  if (st != SGL_OK || empty) return st;
+  a.window = window;
+  a.sinks = sinks;
+  return launch_extend_window(a, reinterpret_cast<cudaStream_t>(stream));
+}
+}  // namespace
+
+sgl_status sgl_decode_attention_window(const void* q, const void* pool_k, const void* pool_v,
+                                       const int32_t* req_to_token, int32_t rtt_rows, int32_t rtt_stride,
+                                       const int32_t* req_pool_idx, const int32_t* seq_lens, int32_t batch,
+                                       int32_t max_seq_len, int32_t window, int32_t sinks, void* out,
+                                       void* workspace, size_t workspace_bytes, const sgl_attn_dims* dims,
+                                       sgl_stream_t stream) {
+  return decode_window_entry(q, pool_k, pool_v, false, 1.f, 1.f, req_to_token, rtt_rows, rtt_stride, req_pool_idx,
+                             seq_lens, batch, max_seq_len, window, sinks, out, workspace, workspace_bytes, dims,
+                             stream);
+}
+
+sgl_status sgl_decode_attention_window_fp8(const void* q, const void* pool_k, const void* pool_v, float k_scale,
+                                           float v_scale, const int32_t* req_to_token, int32_t rtt_rows,
+                                           int32_t rtt_stride, const int32_t* req_pool_idx,
+                                           const int32_t* seq_lens, int32_t batch, int32_t max_seq_len,
+                                           int32_t window, int32_t sinks, void* out, void* workspace,
+                                           size_t workspace_bytes, const sgl_attn_dims* dims,
+                                           sgl_stream_t stream) {
+  if (!valid_kv_scale(k_scale) || !valid_kv_scale(v_scale)) return SGL_ERR_INVALID_ARG;
+  return decode_window_entry(q, pool_k, pool_v, true, k_scale, v_scale, req_to_token, rtt_rows, rtt_stride,
+                             req_pool_idx, seq_lens, batch, max_seq_len, window, sinks, out, workspace,
+                             workspace_bytes, dims, stream);
+}
+
+sgl_status sgl_extend_attention_window(const void* q, const void* pool_k, const void* pool_v,
+                                       const int32_t* req_to_token, int32_t rtt_rows, int32_t rtt_stride,
+                                       const int32_t* req_pool_idx, const int32_t* prefix_lens,
+                                       const int32_t* extend_lens, int32_t batch, int32_t total_extend,
+                                       int32_t max_extend, int32_t max_prefix, int32_t window, int32_t sinks,
+                                       void* out, void* workspace, size_t workspace_bytes,
+                                       const sgl_attn_dims* dims, sgl_stream_t stream) {
+  return extend_window_entry(q, pool_k, pool_v, false, 1.f, 1.f, req_to_token, rtt_rows, rtt_stride, req_pool_idx,
+                             prefix_lens, extend_lens, batch, total_extend, max_extend, max_prefix, window, sinks,
+                             out, workspace, workspace_bytes, dims, stream);
+}
+
+sgl_status sgl_extend_attention_window_fp8(const void* q, const void* pool_k, const void* pool_v, float k_scale,
+                                           float v_scale, const int32_t* req_to_token, int32_t rtt_rows,
+                                           int32_t rtt_stride, const int32_t* req_pool_idx,
+                                           const int32_t* prefix_lens, const int32_t* extend_lens, int32_t batch,
+                                           int32_t total_extend, int32_t max_extend, int32_t max_prefix,
+                                           int32_t window, int32_t sinks, void* out, void* workspace,
+                                           size_t workspace_bytes, const sgl_attn_dims* dims,
+                                           sgl_stream_t stream) {
+  if (!valid_kv_scale(k_scale) || !valid_kv_scale(v_scale)) return SGL_ERR_INVALID_ARG;
+  return extend_window_entry(q, pool_k, pool_v, true, k_scale, v_scale, req_to_token, rtt_rows, rtt_stride,
+                             req_pool_idx, prefix_lens, extend_lens, batch, total_extend, max_extend, max_prefix,
+                             window, sinks, out, workspace, workspace_bytes, dims, stream);
+}
+
+sgl_status sgl_check_decode_window_indices(const int32_t* req_to_token, int32_t rtt_rows, int32_t rtt_stride,
+                                           const int32_t* req_pool_idx, const int32_t* seq_lens, int32_t batch,
+                                           int32_t max_seq_len, int32_t window, int32_t sinks, int64_t pool_size,
+                                           int32_t* d_error, sgl_stream_t stream) {
+  if (batch < 0 || rtt_rows <= 0 || rtt_stride <= 0 || pool_size <= 0 || d_error == nullptr ||
+      !valid_window(window, sinks))
+    return SGL_ERR_INVALID_ARG;
+  if (batch == 0) return SGL_OK;
+  if (!req_to_token || !req_pool_idx || !seq_lens) return SGL_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  check_rows_kernel<<<(unsigned)batch, 256, 0, s>>>(req_to_token, rtt_rows, rtt_stride, req_pool_idx, seq_lens,
+                                                    nullptr, 1, pool_size, max_seq_len, 0, window, sinks, d_error);
+  return last_launch();
+}
+
+sgl_status sgl_check_extend_window_indices(const int32_t* req_to_token, int32_t rtt_rows, int32_t rtt_stride,
+                                           const int32_t* req_pool_idx, const int32_t* prefix_lens,
+                                           const int32_t* extend_lens, int32_t batch, int32_t total_extend,
+                                           int32_t max_extend, int32_t max_prefix, int32_t window, int32_t sinks,
+                                           int64_t pool_size, int32_t* d_error, sgl_stream_t stream) {
+  if (!valid_window(window, sinks)) return SGL_ERR_INVALID_ARG;
+  return check_extend(req_to_token, rtt_rows, rtt_stride, req_pool_idx, prefix_lens, extend_lens, batch,
+                      total_extend, max_extend, max_prefix, pool_size, d_error, stream, 2, window, sinks);
+}
+
+// ---------------------------------------------------------------- norms, rotary positions, store
+
+namespace {
+bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+sgl_status qk_rope_entry(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                         int64_t v_stride, const void* q_weight, const void* k_weight, float eps,
+                         const int32_t* positions, int32_t n_axes, const float* inv_freq,
+                         const int32_t* freq_axis, int32_t rot_dim, int32_t interleaved, const int32_t* slots,
+                         int32_t n, void* q_out, void* pool_k, void* pool_v, bool kv_fp8, float k_scale,
+                         float v_scale, const sgl_attn_dims* dims, sgl_stream_t stream) {
+  float scale;
+  const sgl_status st = check_dims(dims, &scale);
+  if (st != SGL_OK) return st;
+  const int64_t q_row = (int64_t)dims->num_q_heads * dims->head_dim;
+  const int64_t kv_row = (int64_t)dims->num_kv_heads * dims->head_dim;
+  if (n < 0 || n_axes < 1 || rot_dim < 0 || rot_dim > dims->head_dim || (interleaved != 0 && interleaved != 1))
+    return SGL_ERR_INVALID_ARG;
+  if (rot_dim % 16 != 0) return SGL_ERR_UNSUPPORTED;
+  if ((q_weight || k_weight) && (!(eps > 0.f) || isinf(eps))) return SGL_ERR_INVALID_ARG;
+  if (q_stride < q_row || k_stride < kv_row || v_stride < kv_row || q_stride % 8 || k_stride % 8 || v_stride % 8)
+    return SGL_ERR_INVALID_ARG;
+  if (n == 0) return SGL_OK;
+  if (!q || !k || !v || !slots || !q_out || !pool_k || !pool_v) return SGL_ERR_INVALID_ARG;
+  if (rot_dim > 0 && (!positions || !inv_freq || (n_axes > 1 && !freq_axis))) return SGL_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(pool_k) ||
+      !aligned16(pool_v) || !aligned16(q_weight) || !aligned16(k_weight))
+    return SGL_ERR_INVALID_ARG;
+  // rows are read and written at the same time: q_out is q itself or apart
+  // from everything that is read
+  const size_t out_bytes = (size_t)n * (size_t)q_row * 2;
+  const auto span = [&](int64_t stride, int64_t row) { return ((size_t)(n - 1) * (size_t)stride + (size_t)row) * 2; };
+  const bool in_place = q_out == q && q_stride == q_row;
+  if ((!in_place && overlaps(q_out, out_bytes, q, span(q_stride, q_row))) ||
+      overlaps(q_out, out_bytes, k, span(k_stride, kv_row)) || overlaps(q_out, out_bytes, v, span(v_stride, kv_row)))
+    return SGL_ERR_INVALID_ARG;
+  RopeArgs a;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.eps = eps;
+  a.positions = positions;
+  a.n_axes = n_axes;
+  a.inv_freq = inv_freq;
+  a.freq_axis = n_axes > 1 ? freq_axis : nullptr;
+  a.rot_dim = rot_dim;
+  a.interleaved = interleaved != 0;
+  a.slots = slots;
+  a.n = n;
+  a.q_out = q_out;
+  a.pool_k = pool_k;
+  a.pool_v = pool_v;
+  a.pool_size = dims->pool_size;
+  a.num_q_heads = dims->num_q_heads;
+  a.num_kv_heads = dims->num_kv_heads;
+  a.head_dim = dims->head_dim;
+  a.kv_fp8 = kv_fp8;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  return launch_qk_norm_rope_store(a, reinterpret_cast<cudaStream_t>(stream));
+}
+}  // namespace
+
+sgl_status sgl_qk_norm_rope_store_kv(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                     const void* v, int64_t v_stride, const void* q_weight, const void* k_weight,
+                                     float eps, const int32_t* positions, int32_t n_axes, const float* inv_freq,
+                                     const int32_t* freq_axis, int32_t rot_dim, int32_t interleaved,
+                                     const int32_t* slots, int32_t n, void* q_out, void* pool_k, void* pool_v,
+                                     const sgl_attn_dims* dims, sgl_stream_t stream) {
+  return qk_rope_entry(q, q_stride, k, k_stride, v, v_stride, q_weight, k_weight, eps, positions, n_axes, inv_freq,
+                       freq_axis, rot_dim, interleaved, slots, n, q_out, pool_k, pool_v, false, 1.f, 1.f, dims,
+                       stream);
+}
+
+sgl_status sgl_qk_norm_rope_store_kv_fp8(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                         const void* v, int64_t v_stride, const void* q_weight,
+                                         const void* k_weight, float eps, const int32_t* positions, int32_t n_axes,
+                                         const float* inv_freq, const int32_t* freq_axis, int32_t rot_dim,
+                                         int32_t interleaved, const int32_t* slots, int32_t n, void* q_out,
+                                         void* pool_k, void* pool_v, float k_scale, float v_scale,
+                                         const sgl_attn_dims* dims, sgl_stream_t stream) {
+  if (!valid_kv_scale(k_scale) || !valid_kv_scale(v_scale)) return SGL_ERR_INVALID_ARG;
+  return qk_rope_entry(q, q_stride, k, k_stride, v, v_stride, q_weight, k_weight, eps, positions, n_axes, inv_freq,
+                       freq_axis, rot_dim, interleaved, slots, n, q_out, pool_k, pool_v, true, k_scale, v_scale,
+                       dims, stream);
 }
 
 sgl_status sgl_mixed_attention(
@@ -711,7 +976,7 @@ sgl_status sgl_mixed_attention(
   ExtendArgs ea;
   DecodeArgs da;
   bool e_empty = true, d_empty = true;
-  sgl_status st = extend_args(q_ext, k_new, v_new, pool_k, pool_v, false, 1.f, 1.f, req_to_token, rtt_rows,
+  sgl_status st = extend_args(q_ext, k_new, v_new, pool_k, pool_v, false, false, 1.f, 1.f, req_to_token, rtt_rows,
                               rtt_stride, ext_req_pool_idx, prefix_lens, extend_lens, ext_batch, total_extend,
                               max_extend, max_prefix, out_ext, ext_workspace, ext_workspace_bytes, dims, &ea,
                               &e_empty);

@@ -143,6 +143,28 @@ inline size_t ws_layout(int32_t batch, int64_t max_items, int32_t Hkv, int32_t G
   return off;
 }
 
+// A sliding-window decode.  The query of a request of len keys sees positions
+// [0, sinks) and [len - window, len); in order they are its visible keys
+// 0 .. n - 1, n = min(len, sinks + window), and visible key i sits at
+// position i below `sinks` and at i + (len - n) from there on.  A request's
+// visible keys are cut into at most n_splits near-equal runs; run s of
+// request r is item r * n_splits + s.
+struct Window {
+  int32_t sinks;
+  int32_t max_keys;  // min(max_seq_len, sinks + window)
+  int32_t max_seq;   // longer requests are cut to it
+  int32_t n_splits;  // runs of at most Params::chunk visible keys
+};
+struct WindowRun {
+  int32_t len, n;     // keys of the request, and how many its query sees
+  int32_t ns;         // runs
+  SGL_DEV WindowRun(const Window& w, int32_t chunk, int32_t seq_len) {
+    len = max(0, min(seq_len, w.max_seq));
+    n = min(len, w.max_keys);
+    ns = (n + chunk - 1) / chunk;
+  }
+};
+
 struct Params {
   const __nv_bfloat16* q;
   const uint8_t* pool_k;  // [S, Hkv, D] rows of bf16 or e4m3 values
@@ -165,6 +187,7 @@ struct Params {
   Ws ws;
   int64_t group_base;  // first partial entry of the group states (= max_items)
   int32_t max_depth;   // group states per request (cascade), else 0
+  Window win;          // sliding-window decode (split_units<.., kWindow>)
 };
 
 // ---------------------------------------------------------------- plan
@@ -942,8 +965,10 @@ struct SplitRing {
 // in shared memory head by head, so warp w finds its head's keys where a
 // per-head stage keeps warp w's slice of the keys, and every warp's state is
 // the whole item's for its head (no merge across warps).
-template <int D, int G, int LPT, typename KV, int kDepth = 0, bool kSpans = false, class Sync, class Next,
-          class HeadOf, class ItemOf>
+// kWindow: item_of(u) is the run of a sliding-window decode (Window), and a
+// unit past its request's last run ends the call.
+template <int D, int G, int LPT, typename KV, int kDepth = 0, bool kSpans = false, bool kWindow = false, class Sync,
+          class Next, class HeadOf, class ItemOf>
 SGL_DEV void split_units(const Params& p, uint8_t* smem, int32_t* s_item, int gtid, int32_t n_units, Sync sync,
                          Next next, HeadOf head_of, ItemOf item_of) {
   using L = Lane<D, LPT, KV>;
@@ -976,18 +1001,36 @@ SGL_DEV void split_units(const Params& p, uint8_t* smem, int32_t* s_item, int gt
     const int kvh0 = head_of(unit);                // the unit's (first) KV head
     const int kvh = kSpans ? kvh0 + warp : kvh0;    // this warp's
     const int32_t item = item_of(unit);
-    const int2 it = p.ws.items[item];
-    const int r = it.x;
-    // the request's keys past its shared groups (all of them in plain decode)
-    // are cut into ceil(n / chunk) near-equal items
-    const int2 info = p.ws.req_info != nullptr ? p.ws.req_info[r] : make_int2(0, 0);
-    const int32_t tail = max(p.seq_lens[r] - info.x, 0);
-    const int32_t ns = (tail + p.chunk - 1) / p.chunk;
-    const int32_t base = tail / ns, rem = tail % ns;
-    const int32_t t0 = info.x + it.y * base + min(it.y, rem);
-    const int32_t n = base + (it.y < rem ? 1 : 0);
-    const int32_t* rtt = p.req_to_token + (int64_t)p.req_pool_idx[r] * p.rtt_stride + t0;
-    for (int i = tid; i < n; i += kThreads) s_slots[i] = rtt[i];
+    int r;
+    int32_t ns, n;
+    bool grouped = false;  // the request has shared groups as well
+    if constexpr (kWindow) {
+      r = item / p.win.n_splits;
+      const int32_t run = item % p.win.n_splits;
+      const WindowRun w(p.win, p.chunk, p.seq_lens[r]);
+      ns = w.ns;
+      if (run >= ns) return;
+      const int32_t base = w.n / ns, rem = w.n % ns;
+      const int32_t t0 = run * base + min(run, rem);
+      n = base + (run < rem ? 1 : 0);
+      const int32_t* rtt = p.req_to_token + (int64_t)p.req_pool_idx[r] * p.rtt_stride;
+      for (int i = tid; i < n; i += kThreads)
+        s_slots[i] = rtt[t0 + i + (t0 + i >= p.win.sinks ? w.len - w.n : 0)];
+    } else {
+      const int2 it = p.ws.items[item];
+      r = it.x;
+      // the request's keys past its shared groups (all of them in plain decode)
+      // are cut into ceil(n / chunk) near-equal items
+      const int2 info = p.ws.req_info != nullptr ? p.ws.req_info[r] : make_int2(0, 0);
+      grouped = info.y != 0;
+      const int32_t tail = max(p.seq_lens[r] - info.x, 0);
+      ns = (tail + p.chunk - 1) / p.chunk;
+      const int32_t base = tail / ns, rem = tail % ns;
+      const int32_t t0 = info.x + it.y * base + min(it.y, rem);
+      n = base + (it.y < rem ? 1 : 0);
+      const int32_t* rtt = p.req_to_token + (int64_t)p.req_pool_idx[r] * p.rtt_stride + t0;
+      for (int i = tid; i < n; i += kThreads) s_slots[i] = rtt[i];
+    }
     st.load_q(p.q + ((int64_t)r * p.Hq + (int64_t)kvh * G) * D, p.scale_log2);
     sync();  // slots visible; previous item's reduction scratch free
 
@@ -1053,7 +1096,7 @@ SGL_DEV void split_units(const Params& p, uint8_t* smem, int32_t* s_item, int gt
     float* red_l = red_m + kWarps * G;
     st.publish(red_acc, red_m, red_l);
     sync();
-    const bool single = ns == 1 && info.y == 0;
+    const bool single = ns == 1 && !grouped;
     // (head, query head, dim) outputs of the unit: kWarps heads with spans
     constexpr int kHeads = kSpans ? kWarps : 1;
     for (int idx = tid; idx < kHeads * G * D; idx += kThreads) {
@@ -1117,18 +1160,26 @@ decode_split_kernel(Params p) {
 
 // ---------------------------------------------------------------- combine
 
-template <int D>
+// kWindow: the runs of a sliding-window decode
+template <int D, bool kWindow = false>
 __global__ void __launch_bounds__(128) decode_combine_kernel(Params p) {
   grid_dep_wait();  // launched dependent on the split kernel (or the group pass)
   const int lane = threadIdx.x & 31;
   const int64_t gw = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
   if (gw >= (int64_t)p.batch * p.Hq) return;
   const int r = (int)(gw / p.Hq), h = (int)(gw % p.Hq);
-  const int32_t s0 = p.ws.item_start[r];
-  const int32_t n_split = p.ws.item_start[r + 1] - s0;
-  const int32_t n_grp = p.ws.req_info != nullptr ? p.ws.req_info[r].y : 0;
-  if (n_grp == 0 && n_split <= 1) return;     // a single split wrote the output
-  if (s0 + n_split > *p.ws.n_items) return;   // lengths above max_seq_len
+  int32_t s0, n_split, n_grp = 0;
+  if constexpr (kWindow) {
+    s0 = r * p.win.n_splits;
+    n_split = WindowRun(p.win, p.chunk, p.seq_lens[r]).ns;
+    if (n_split <= 1) return;  // a single run wrote the output (none: no keys)
+  } else {
+    s0 = p.ws.item_start[r];
+    n_split = p.ws.item_start[r + 1] - s0;
+    n_grp = p.ws.req_info != nullptr ? p.ws.req_info[r].y : 0;
+    if (n_grp == 0 && n_split <= 1) return;    // a single split wrote the output
+    if (s0 + n_split > *p.ws.n_items) return;  // lengths above max_seq_len
+  }
   const int32_t ns = n_grp + n_split;
   const int G = p.Hq / p.Hkv;
   const int kvh = h / G, hh = h % G;

@@ -274,6 +274,32 @@ struct Params {
   int64_t part_base;
   int32_t max_depth;
   int32_t batch;  // member indices outside [0, batch) are skipped
+  int32_t window, sinks;  // sliding-window extend (WindowKeys)
+};
+
+// The keys a CTA's queries see in a sliding-window extend.  Query position P
+// sees position j when j <= P and (j < sinks or j > P - window).  The CTA's
+// first query is at position P0, its last at end - 1, so its keys are the
+// positions [0, sinks) and [lo, end), lo = max(0, P0 - window + 1): key i of
+// that list is position i below n_first = min(sinks, lo) and lo + i - n_first
+// from there on.  Sinks and window share the list's 128-key blocks, so a few
+// sinks cost no block of their own.
+struct WindowKeys {
+  int32_t lo, n_first, n;  // n: keys of the list
+  int32_t sinks, window;
+  SGL_DEV WindowKeys(const Params& p, int32_t first_pos, int32_t end) {
+    sinks = p.sinks;
+    window = p.window;
+    lo = max(0, first_pos - window + 1);
+    n_first = min(sinks, lo);
+    n = n_first + end - lo;
+  }
+  SGL_DEV int32_t pos(int32_t i) const { return i < n_first ? i : lo + (i - n_first); }
+  // Query position P sees the list's keys i < hi(P) with i < sinks or i >=
+  // first(P).  (Where lo < sinks the list is the positions from 0 on, so i <
+  // sinks is position i < sinks in either case.)
+  SGL_DEV int32_t hi(int32_t P) const { return P - lo + n_first + 1; }
+  SGL_DEV int32_t first(int32_t P) const { return max(0, P - window + 1) - lo + n_first; }
 };
 
 // byte offset of 16-byte chunk `ci` (0..7) of row `row` inside one
@@ -415,10 +441,10 @@ SGL_DEV void load_q_tiles(const Params& p, uint32_t sQ_a, uint64_t* q_full, int 
 // ordered for the tensor core with a proxy fence before the arrival.  Prefix
 // keys are positions 0..pfx-1 of the request's row, suffix keys positions
 // pfx..pfx+q_end-1 (stored into the pool before the call).
-template <int D, bool kGroup>
+template <int D, bool kGroup, bool kWindow>
 SGL_DEV void produce_fp8(const Params& p, uint32_t sQ_a, uint8_t* sKV, uint8_t* sRaw, Bars* bars,
                          int ptid, int r, int kvh, int e, int mbeg, int q0, int pfx, int q_end, int nb_pre, int nb,
-                         int off) {
+                         int off, const WindowKeys& wk) {
   const uint32_t sRaw_a = smem_u32(sRaw);
   using C = Cfg<D, true>;
   using R = Roles<true>;
@@ -455,6 +481,10 @@ SGL_DEV void produce_fp8(const Params& p, uint32_t sQ_a, uint8_t* sKV, uint8_t* 
   // position of row `row` of block b in the row of req_to_token, or -1 when
   // the row holds no key (past the prefix, or past this CTA's last query)
   auto key_pos = [&](int b, int row) {
+    if constexpr (kWindow) {
+      const int i = b * BN + row;
+      return i < wk.n ? wk.pos(i) : -1;
+    }
     if (b < nb_pre) {
       const int pos = b * BN + row;
       return pos < pfx ? pos : -1;
@@ -595,7 +625,11 @@ SGL_DEV void produce_fp8(const Params& p, uint32_t sQ_a, uint8_t* sKV, uint8_t* 
 // barriers before its first tile; each tile then invalidates and initialises
 // them again (the previous tile ended with every thread past its final
 // barrier, every copy landed and every MMA drained).
-template <int D, bool kGroup, bool kFp8, int kTiles = 2, bool kPersistent = false>
+//
+// kWindow: a sliding-window extend.  Every key, the suffix's included, is
+// read from the pool through req_to_token (both pool types); the CTA walks
+// only the keys one of its queries sees (WindowKeys).
+template <int D, bool kGroup, bool kFp8, int kTiles = 2, bool kPersistent = false, bool kWindow = false>
 SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz) {
   using C = Cfg<D, kFp8, kTiles>;
   using R = Roles<kFp8, kTiles>;
@@ -617,8 +651,9 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz) {
   const int q0 = bx * kTiles * p.tpt;                         // first token of this tile
   const int pfx = kGroup ? p.group_len[r] : p.prefix_lens[r];  // keys read from the pool
   const int q_end = min(e, q0 + kTiles * p.tpt);
-  const int nb_pre = (pfx + BN - 1) / BN;
-  const int nb = nb_pre + (kGroup ? 0 : (q_end + BN - 1) / BN);
+  const WindowKeys wk(p, pfx + q0, pfx + q_end);  // kWindow only
+  const int nb_pre = ((kWindow ? wk.n : pfx) + BN - 1) / BN;
+  const int nb = nb_pre + (kGroup || kWindow ? 0 : (q_end + BN - 1) / BN);
   // Group mode: Q tile 1 holds no member (a cascade group of at most tpt
   // members, most groups of a tree): its MMAs and softmax are skipped and tile
   // 0 runs alone (tree cascade +4-5%).  Extend mode keeps both tiles: the
@@ -696,6 +731,9 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz) {
     const int tok = q0 + t * p.tpt + row / p.g;
     const bool row_valid = row < p.rows_used && tok < e;
     const int tok_i = row_valid ? tok : (1 << 30);  // padding rows see every key
+    // kWindow: the row's bounds in the CTA's key list (padding rows: every key)
+    const int row_hi = row_valid ? wk.hi(pfx + tok) : (1 << 30);
+    const int row_first = row_valid ? wk.first(pfx + tok) : 0;
     const float2 sc = make_float2(p.scale_log2, p.scale_log2);
     float m_ref = -INFINITY, l = 0.f;
     bool ok = t == 0 || two_tiles;  // an empty tile's warps only meet the final barrier
@@ -706,9 +744,17 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz) {
       }
       tc_fence_after();
       // visible keys of this block: c < limit (key index within the block)
-      int limit;
-      if (b < nb_pre) limit = pfx - b * BN;
-      else limit = tok_i - (b - nb_pre) * BN + 1;
+      // (kWindow: and c < w_sinks or c >= w_first)
+      int limit, w_sinks = BN, w_first = 0;
+      if constexpr (kWindow) {
+        limit = row_hi - b * BN;
+        w_sinks = wk.sinks - b * BN;
+        w_first = row_first - b * BN;
+      } else if (b < nb_pre) {
+        limit = pfx - b * BN;
+      } else {
+        limit = tok_i - (b - nb_pre) * BN + 1;
+      }
       limit = max(0, min(BN, limit));
       uint32_t sr[BN];
       auto load_s = [&]() {
@@ -720,6 +766,11 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz) {
 #pragma unroll
           for (int c = 0; c < BN; ++c)
             if (c >= limit) sr[c] = __float_as_uint(-INFINITY);
+        }
+        if (kWindow && w_first > 0 && w_first > w_sinks) {
+#pragma unroll
+          for (int c = 0; c < BN; ++c)
+            if (c >= w_sinks && c < w_first) sr[c] = __float_as_uint(-INFINITY);
         }
       };
       // P of the row's 128 keys against reference m_use, packed in place
@@ -850,6 +901,9 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz) {
     const int tok = q0 + t * p.tpt + row / p.g;
     const bool row_valid = row < p.rows_used && tok < e;
     const int tok_i = row_valid ? tok : (1 << 30);  // padding rows see every key
+    // kWindow: the row's bounds in the CTA's key list (padding rows: every key)
+    const int row_hi = row_valid ? wk.hi(pfx + tok) : (1 << 30);
+    const int row_first = row_valid ? wk.first(pfx + tok) : 0;
     const float2 sc = make_float2(p.scale_log2, p.scale_log2);
     float m_ref = -INFINITY, l = 0.f;  // l: this half's share of the row sum
     bool ok = t == 0 || two_tiles;  // an empty tile's warps only meet the barriers
@@ -857,9 +911,17 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz) {
       const bool ok_w = warp_wait(&bars->s_full[t], b & 1, bars, p);
       tc_fence_after();
       // visible keys of this block: c < limit (key index within the block)
-      int limit;
-      if (b < nb_pre) limit = pfx - b * BN;
-      else limit = tok_i - (b - nb_pre) * BN + 1;
+      // (kWindow: and c < w_sinks or c >= w_first)
+      int limit, w_sinks = 64, w_first = 0;
+      if constexpr (kWindow) {
+        limit = row_hi - b * BN;
+        w_sinks = wk.sinks - b * BN - 64 * h;
+        w_first = row_first - b * BN - 64 * h;
+      } else if (b < nb_pre) {
+        limit = pfx - b * BN;
+      } else {
+        limit = tok_i - (b - nb_pre) * BN + 1;
+      }
       limit = max(0, min(BN, limit)) - 64 * h;  // relative to this half's first key
       uint32_t sr[64];
       auto load_s = [&]() {
@@ -870,6 +932,11 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz) {
 #pragma unroll
           for (int c = 0; c < 64; ++c)
             if (c >= limit) sr[c] = __float_as_uint(-INFINITY);
+        }
+        if (kWindow && w_first > 0 && w_first > w_sinks) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (c >= w_sinks && c < w_first) sr[c] = __float_as_uint(-INFINITY);
         }
       };
       // P of this half's 64 keys against reference m_use, packed as bf16
@@ -1010,8 +1077,8 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz) {
   } else if (warp < R::kMmaWarp) {
     // ------------------------------------------------------------ producers
     if constexpr (kFp8) {
-      produce_fp8<D, kGroup>(p, sQ_a, sKV, sRaw, bars, tid - R::kSoftmaxWarps * 32, r, kvh, e, mbeg, q0, pfx,
-                             q_end, nb_pre, nb, off);
+      produce_fp8<D, kGroup, kWindow>(p, sQ_a, sKV, sRaw, bars, tid - R::kSoftmaxWarps * 32, r, kvh, e, mbeg, q0,
+                                      pfx, q_end, nb_pre, nb, off, wk);
     } else {
     constexpr int kRowStep = R::kRowStep, kRowsPerThread = R::kRowsPerThread;
     const int ptid = tid - R::kSoftmaxWarps * 32;
@@ -1028,7 +1095,10 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz) {
 #pragma unroll
       for (int i = 0; i < kRowsPerThread; ++i) {
         const int j = b * BN + rbase + kRowStep * i;
-        dst[i] = (b < nb_pre && j < pfx && rbase + kRowStep * i < BN) ? rtt[j] : -1;
+        if constexpr (kWindow)
+          dst[i] = (j < wk.n && rbase + kRowStep * i < BN) ? rtt[wk.pos(j)] : -1;
+        else
+          dst[i] = (b < nb_pre && j < pfx && rbase + kRowStep * i < BN) ? rtt[j] : -1;
       }
     };
     if (nb_pre > 0) load_slots(0, slot_next);
@@ -1046,7 +1116,7 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz) {
         if (b + 1 < nb_pre) load_slots(b + 1, slot_next);
       }
       const uint32_t dst0 = sKV_a + stage * C::kTileBytes;
-      if (b < nb_pre) {
+      if (kWindow || b < nb_pre) {
         const __nv_bfloat16* pool = is_v ? p.pool_v : p.pool_k;
 #pragma unroll
         for (int i = 0; i < kRowsPerThread; ++i) {
@@ -1184,9 +1254,9 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz) {
   }
 }
 
-template <int D, bool kFp8>
+template <int D, bool kFp8, bool kWindow = false>
 __global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1) extend_kernel(Params p) {
-  attend_tiles<D, false, kFp8>(p, blockIdx.x, blockIdx.y, blockIdx.z);
+  attend_tiles<D, false, kFp8, 2, false, kWindow>(p, blockIdx.x, blockIdx.y, blockIdx.z);
 }
 
 // one Q tile: two CTAs an SM (11 warps a CTA are allocated registers as 12,
@@ -1231,6 +1301,8 @@ inline sgl_status make_extend_params(const ExtendArgs& a, Params* out) {
   prm.o_scale = a.kv_fp8 ? a.v_scale * kFp8Operand : 1.f;
   prm.status = static_cast<int*>(a.workspace);
   prm.wait_ns = device_wait_limit_ns();
+  prm.window = a.window;
+  prm.sinks = a.sinks;
   *out = prm;
   return SGL_OK;
 }

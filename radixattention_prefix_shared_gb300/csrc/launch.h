@@ -50,6 +50,34 @@ sgl_status launch_store_kv_fp8(const void* k_new, const void* v_new, const int32
                                int32_t n, void* pool_k, void* pool_v, int32_t row_elems,
                                float k_scale, float v_scale, cudaStream_t stream);
 
+// Head norms, rotary positions and the store of K and V in one pass
+// (qk_rope.cu); the fields follow sgl_qk_norm_rope_store_kv.
+struct RopeArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_stride, k_stride, v_stride;  // elements between tokens
+  const void* q_weight;
+  const void* k_weight;
+  float eps;
+  const int32_t* positions;
+  int32_t n_axes;
+  const float* inv_freq;
+  const int32_t* freq_axis;
+  int32_t rot_dim;
+  bool interleaved;
+  const int32_t* slots;
+  int32_t n;
+  void* q_out;
+  void* pool_k;
+  void* pool_v;
+  int64_t pool_size;
+  int32_t num_q_heads, num_kv_heads, head_dim;
+  bool kv_fp8;
+  float k_scale, v_scale;
+};
+sgl_status launch_qk_norm_rope_store(const RopeArgs& a, cudaStream_t stream);
+
 struct DecodeArgs {
   const void* q;
   const void* pool_k;
@@ -76,9 +104,15 @@ struct DecodeArgs {
   // e4m3 pool (kv_fp8): pool rows hold codes; K/V values are code * scale
   bool kv_fp8 = false;
   float k_scale = 1.f, v_scale = 1.f;
+  // sliding window (launch_decode_window): keys [0, sinks) and the last `window`
+  int32_t window = 0, sinks = 0;
 };
 // bytes in front of a cascade workspace: word 0 is the bounded-wait status
 constexpr size_t kCascadeStatusBytes = 256;
+// sliding-window decode (decode_window.cu): the window fields of DecodeArgs
+size_t decode_window_workspace_bytes(int32_t batch, int32_t max_seq_len, int32_t window, int32_t sinks,
+                                     int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim);
+sgl_status launch_decode_window(const DecodeArgs& a, cudaStream_t stream);
 size_t decode_workspace_bytes(int32_t batch, int32_t max_seq_len, int32_t num_q_heads,
                               int32_t num_kv_heads, int32_t head_dim, bool cascade = false,
                               int32_t max_depth = 0);
@@ -184,9 +218,13 @@ struct ExtendArgs {
   // from the pool through req_to_token; k_new / v_new are unused
   bool kv_fp8 = false;
   float k_scale = 1.f, v_scale = 1.f;
+  // sliding window (window > 0, launch_extend_window): the suffix is read
+  // from the pool on both pool types
+  int32_t window = 0, sinks = 0;
 };
 size_t extend_workspace_bytes();
 sgl_status launch_extend(const ExtendArgs& a, cudaStream_t stream);
+sgl_status launch_extend_window(const ExtendArgs& a, cudaStream_t stream);
 
 // One launch for an extend batch and a plain decode batch over the same bf16
 // pools (mixed.cu): persistent CTAs, one an SM, the first extend_ctas taking
