@@ -405,10 +405,11 @@ def _need_dense(name, dtype, **tensors):
             raise ValueError(f"{name}: {arg} must be a dense {dtype} tensor on the current CUDA device")
 
 
-def _raw_stream(stream):
-    import torch
+def _raw_stream(stream, device):
     if stream is None:
-        stream = torch.cuda.current_stream()
+        import torch
+        # the handle alone: torch.cuda.current_stream() builds an object around it
+        return torch._C._cuda_getCurrentRawStream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -438,7 +439,8 @@ def extend_window_workspace_bytes(batch, total_extend, max_extend, max_prefix, w
                                                        ctypes.byref(dims)))
 
 
-def _window_tensors(name, q, pool_k, pool_v, req_to_token, lens, out, workspace, kv_dtype):
+def _refuse_window(name, q, pool_k, pool_v, kv_dtype, req_to_token, lens, out, workspace):
+    """Names what a sliding-window call cannot take (its checks failed)."""
     import torch
     _need_dense(name, torch.bfloat16, q=q, out=out)
     _need_dense(name, kv_dtype, pool_k=pool_k, pool_v=pool_v)
@@ -446,35 +448,48 @@ def _window_tensors(name, q, pool_k, pool_v, req_to_token, lens, out, workspace,
     _need(name, q.dim() == 3 and pool_k.dim() == 3 and pool_v.shape == pool_k.shape
           and q.shape[2] == pool_k.shape[2], "q [T, Hq, D] and pools [S, Hkv, D]")
     _need(name, req_to_token.dim() == 2, "req_to_token [rows, stride]")
-    batch = next(iter(lens.values())).shape[0]
-    _need(name, all(t.dim() == 1 and t.shape[0] == batch for t in lens.values()), "one entry a request in "
-          + ", ".join(lens))
     _need(name, out is None or out.shape == q.shape, "out of q's shape")
-    if workspace is not None:
-        _need(name, workspace.is_contiguous() and workspace.get_device() == q.get_device(),
-              "workspace: a dense buffer on q's device")
+    _need(name, workspace is None or (workspace.is_contiguous() and workspace.get_device() == q.get_device()),
+          "workspace: a dense buffer on q's device")
+    raise ValueError(f"{name}: one entry a request in {', '.join(lens)}"
+                     + ("" if "prefix_lens" in lens else ", one query a request"))
 
+
+# The calls check their tensors in one expression and look for what was wrong
+# only when it fails: a decode step's kernels last a few microseconds.
 
 def _decode_window(name, q, pool_k, pool_v, scales, req_to_token, req_pool_idx, seq_lens, out, max_seq_len,
                    window, sinks, workspace, sm_scale, stream):
     import torch
-    _window_tensors(name, q, pool_k, pool_v, req_to_token, dict(req_pool_idx=req_pool_idx, seq_lens=seq_lens),
-                    out, workspace, torch.uint8 if scales else torch.bfloat16)
-    batch, hq, d = q.shape
-    _need(name, req_pool_idx.shape[0] == batch, "one query a request")
-    dims = _dims_ref(hq, pool_k.shape[1], d, pool_k.shape[0], float(sm_scale))
+    bf16, i32, dev = torch.bfloat16, torch.int32, torch.cuda.current_device()
+    kv = torch.uint8 if scales else bf16
+    qs, ks, ts = q.shape, pool_k.shape, req_to_token.shape
+    if not (q.dtype is bf16 and q.is_contiguous() and q.get_device() == dev and len(qs) == 3
+            and pool_k.dtype is kv and pool_k.is_contiguous() and pool_k.get_device() == dev and len(ks) == 3
+            and pool_v.dtype is kv and pool_v.is_contiguous() and pool_v.get_device() == dev
+            and pool_v.shape == ks and qs[2] == ks[2]
+            and req_to_token.dtype is i32 and req_to_token.is_contiguous() and req_to_token.get_device() == dev
+            and len(ts) == 2
+            and req_pool_idx.dtype is i32 and req_pool_idx.is_contiguous() and req_pool_idx.get_device() == dev
+            and seq_lens.dtype is i32 and seq_lens.is_contiguous() and seq_lens.get_device() == dev
+            and req_pool_idx.shape == qs[:1] and seq_lens.shape == qs[:1]
+            and (out is None or (out.dtype is bf16 and out.is_contiguous() and out.get_device() == dev
+                                 and out.shape == qs))
+            and (workspace is None or (workspace.is_contiguous() and workspace.get_device() == dev))):
+        _refuse_window(name, q, pool_k, pool_v, kv, req_to_token, dict(req_pool_idx=req_pool_idx, seq_lens=seq_lens),
+                       out, workspace)
+    dims = _dims_ref(qs[1], ks[1], ks[2], ks[0], float(sm_scale))
     if out is None or workspace is None:
         with _on(stream):
             if out is None:
                 out = torch.empty_like(q)
             if workspace is None:
                 workspace = torch.empty(max(16, lib().sgl_decode_window_workspace_bytes(
-                    batch, int(max_seq_len), int(window), int(sinks), dims)), dtype=torch.uint8, device=q.device)
+                    qs[0], int(max_seq_len), int(window), int(sinks), dims)), dtype=torch.uint8, device=q.device)
     code = getattr(lib(), name)(
-        q.data_ptr(), pool_k.data_ptr(), pool_v.data_ptr(), *scales, req_to_token.data_ptr(),
-        req_to_token.shape[0], req_to_token.shape[1], req_pool_idx.data_ptr(), seq_lens.data_ptr(), batch,
-        int(max_seq_len), int(window), int(sinks), out.data_ptr(), workspace.data_ptr(), workspace.nbytes, dims,
-        _raw_stream(stream))
+        q.data_ptr(), pool_k.data_ptr(), pool_v.data_ptr(), *scales, req_to_token.data_ptr(), ts[0], ts[1],
+        req_pool_idx.data_ptr(), seq_lens.data_ptr(), qs[0], int(max_seq_len), int(window), int(sinks), out.data_ptr(),
+        workspace.data_ptr(), workspace.nbytes, dims, _raw_stream(stream, dev))
     if code != 0:
         raise SglError(name, code)
     return out
@@ -500,26 +515,39 @@ def sgl_decode_attention_window_fp8(q, pool_k, pool_v, k_scale, v_scale, req_to_
 def _extend_window(name, q, pool_k, pool_v, scales, req_to_token, req_pool_idx, prefix_lens, extend_lens, out,
                    max_extend, max_prefix, window, sinks, total_extend, workspace, sm_scale, stream):
     import torch
-    _window_tensors(name, q, pool_k, pool_v, req_to_token,
-                    dict(req_pool_idx=req_pool_idx, prefix_lens=prefix_lens, extend_lens=extend_lens), out,
-                    workspace, torch.uint8 if scales else torch.bfloat16)
-    tokens, hq, d = q.shape
-    total = tokens if total_extend is None else int(total_extend)
-    _need(name, total <= tokens, "total_extend within q's rows")
-    batch = req_pool_idx.shape[0]
-    dims = _dims_ref(hq, pool_k.shape[1], d, pool_k.shape[0], float(sm_scale))
+    bf16, i32, dev = torch.bfloat16, torch.int32, torch.cuda.current_device()
+    kv = torch.uint8 if scales else bf16
+    qs, ks, ts, bs = q.shape, pool_k.shape, req_to_token.shape, req_pool_idx.shape
+    if not (q.dtype is bf16 and q.is_contiguous() and q.get_device() == dev and len(qs) == 3
+            and pool_k.dtype is kv and pool_k.is_contiguous() and pool_k.get_device() == dev and len(ks) == 3
+            and pool_v.dtype is kv and pool_v.is_contiguous() and pool_v.get_device() == dev
+            and pool_v.shape == ks and qs[2] == ks[2]
+            and req_to_token.dtype is i32 and req_to_token.is_contiguous() and req_to_token.get_device() == dev
+            and len(ts) == 2
+            and req_pool_idx.dtype is i32 and req_pool_idx.is_contiguous() and req_pool_idx.get_device() == dev
+            and prefix_lens.dtype is i32 and prefix_lens.is_contiguous() and prefix_lens.get_device() == dev
+            and extend_lens.dtype is i32 and extend_lens.is_contiguous() and extend_lens.get_device() == dev
+            and len(bs) == 1 and prefix_lens.shape == bs and extend_lens.shape == bs
+            and (out is None or (out.dtype is bf16 and out.is_contiguous() and out.get_device() == dev
+                                 and out.shape == qs))
+            and (workspace is None or (workspace.is_contiguous() and workspace.get_device() == dev))):
+        _refuse_window(name, q, pool_k, pool_v, kv, req_to_token,
+                       dict(req_pool_idx=req_pool_idx, prefix_lens=prefix_lens, extend_lens=extend_lens), out,
+                       workspace)
+    total = qs[0] if total_extend is None else int(total_extend)
+    _need(name, total <= qs[0], "total_extend within q's rows")
+    dims = _dims_ref(qs[1], ks[1], ks[2], ks[0], float(sm_scale))
     if out is None or workspace is None:
         with _on(stream):
             if out is None:
                 out = torch.empty_like(q)
             if workspace is None:
                 workspace = new_workspace(lib().sgl_extend_window_workspace_bytes(
-                    batch, total, int(max_extend), int(max_prefix), int(window), int(sinks), dims), q.device)
+                    bs[0], total, int(max_extend), int(max_prefix), int(window), int(sinks), dims), q.device)
     code = getattr(lib(), name)(
-        q.data_ptr(), pool_k.data_ptr(), pool_v.data_ptr(), *scales, req_to_token.data_ptr(),
-        req_to_token.shape[0], req_to_token.shape[1], req_pool_idx.data_ptr(), prefix_lens.data_ptr(),
-        extend_lens.data_ptr(), batch, total, int(max_extend), int(max_prefix), int(window), int(sinks),
-        out.data_ptr(), workspace.data_ptr(), workspace.nbytes, dims, _raw_stream(stream))
+        q.data_ptr(), pool_k.data_ptr(), pool_v.data_ptr(), *scales, req_to_token.data_ptr(), ts[0], ts[1],
+        req_pool_idx.data_ptr(), prefix_lens.data_ptr(), extend_lens.data_ptr(), bs[0], total, int(max_extend),
+        int(max_prefix), int(window), int(sinks), out.data_ptr(), workspace.data_ptr(), workspace.nbytes, dims, _raw_stream(stream, dev))
     if code != 0:
         raise SglError(name, code)
     return out
@@ -563,40 +591,76 @@ def sgl_check_extend_window_indices(req_to_token, req_pool_idx, prefix_lens, ext
 
 # ----------------------------------------------------------------- norms, rotary positions, store
 
+def _refuse_rope(name, q, k, v, positions, inv_freq, slots, pool_k, pool_v, kv_dtype, q_weight, k_weight, freq_axis,
+                 q_out):
+    """Names what the call cannot take (its checks failed)."""
+    import torch
+    bf16, dev = torch.bfloat16, torch.cuda.current_device()
+    _need_dense(name, kv_dtype, pool_k=pool_k, pool_v=pool_v)
+    _need(name, pool_k.dim() == 3 and pool_v.shape == pool_k.shape, "pools [S, Hkv, D]")
+    for arg, t in (("q", q), ("k", k), ("v", v)):
+        _need(name, t.dim() == 3 and t.dtype is bf16 and t.get_device() == dev and t.shape[0] == q.shape[0]
+              and t.shape[2] == pool_k.shape[2] and (arg == "q" or t.shape[1] == pool_k.shape[1])
+              and t.stride(2) == 1 and (t.shape[1] == 1 or t.stride(1) == t.shape[2]),
+              f"{arg}: bf16 [n, heads, D] with dense rows on the current CUDA device")
+    _need_dense(name, bf16, q_weight=q_weight, k_weight=k_weight, q_out=q_out)
+    _need_dense(name, torch.int32, positions=positions, slots=slots, freq_axis=freq_axis)
+    _need_dense(name, torch.float32, inv_freq=inv_freq)
+    for arg, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        _need(name, w is None or w.shape == pool_k.shape[2:], f"{arg} [D]")
+    _need(name, q_out is None or q_out.shape == q.shape, "q_out of q's shape")
+    raise ValueError(f"{name}: one slot a token, positions [n] or [axes, n], inv_freq [rot / 2] and, with several "
+                     "axes, freq_axis [rot / 2]")
+
+
+def _dense_rows(t, shape, bf16, dev):
+    return (t.dtype is bf16 and t.shape == shape and t.get_device() == dev
+            and (t.is_contiguous() or (t.stride(2) == 1 and (shape[1] == 1 or t.stride(1) == shape[2]))))
+
+
 def _qk_norm_rope_store(name, q, k, v, positions, inv_freq, slots, pool_k, pool_v, scales, q_weight, k_weight,
                         eps, freq_axis, interleaved, q_out, stream):
     import torch
-    bf16, dev = torch.bfloat16, torch.cuda.current_device()
-    n, hq, d = q.shape
-    hkv = pool_k.shape[1]
-    for arg, t, h in (("q", q, hq), ("k", k, hkv), ("v", v, hkv)):
-        # dense rows; tokens may lie apart (parts of a packed projection)
-        _need(name, t.dtype is bf16 and t.shape == (n, h, d) and t.get_device() == dev and t.stride(2) == 1
-              and (h == 1 or t.stride(1) == d), f"{arg}: bf16 [n, heads, D] with dense rows on the current device")
-    _need_dense(name, bf16, q_weight=q_weight, k_weight=k_weight, q_out=q_out)
-    _need_dense(name, torch.uint8 if scales else bf16, pool_k=pool_k, pool_v=pool_v)
-    _need_dense(name, torch.int32, positions=positions, slots=slots, freq_axis=freq_axis)
-    _need_dense(name, torch.float32, inv_freq=inv_freq)
-    rot = 0 if inv_freq is None else 2 * inv_freq.shape[0]
-    axes = positions.shape[0] if positions is not None and positions.dim() == 2 else 1
-    _need(name, pool_k.dim() == 3 and pool_v.shape == pool_k.shape and pool_k.shape[2] == d, "pools [S, Hkv, D]")
-    _need(name, slots.shape == (n,), "one slot a token")
-    _need(name, rot == 0 or (positions is not None and inv_freq.dim() == 1
-                             and positions.numel() == axes * n), "positions [n] or [axes, n] and inv_freq [rot / 2]")
-    _need(name, axes == 1 or rot == 0 or (freq_axis is not None and freq_axis.shape == inv_freq.shape),
-          "an axis for each frequency")
-    for arg, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        _need(name, w is None or w.shape == (d,), f"{arg} [D]")
-    _need(name, q_out is None or q_out.shape == q.shape, "q_out of q's shape")
+    bf16, i32, dev = torch.bfloat16, torch.int32, torch.cuda.current_device()
+    kv = torch.uint8 if scales else bf16
+    qs, ps = q.shape, pool_k.shape
+    n, d, rot, axes = qs[0], ps[-1], 0, 1
+    new = (n, ps[-2], d) if len(ps) == 3 else None
+    ok = (len(qs) == 3 and new is not None and _dense_rows(q, (n, qs[1], d), bf16, dev)
+          and _dense_rows(k, new, bf16, dev) and _dense_rows(v, new, bf16, dev)
+          and pool_k.dtype is kv and pool_k.is_contiguous() and pool_k.get_device() == dev
+          and pool_v.dtype is kv and pool_v.is_contiguous() and pool_v.get_device() == dev and pool_v.shape == ps
+          and slots.dtype is i32 and slots.is_contiguous() and slots.get_device() == dev and slots.shape == qs[:1])
+    if ok and inv_freq is not None:
+        fs, xs = inv_freq.shape, positions.shape if positions is not None else ()
+        rot, axes = 2 * fs[0], xs[0] if len(xs) == 2 else 1
+        ok = (inv_freq.dtype is torch.float32 and inv_freq.is_contiguous() and inv_freq.get_device() == dev
+              and len(fs) == 1 and 0 < len(xs) <= 2 and xs[-1] == n and axes > 0
+              and positions.dtype is i32 and positions.is_contiguous() and positions.get_device() == dev
+              and (axes == 1 or (freq_axis is not None and freq_axis.dtype is i32 and freq_axis.shape == fs
+                                 and freq_axis.is_contiguous() and freq_axis.get_device() == dev)))
+    for w in (q_weight, k_weight):
+        ok = ok and (w is None or (w.dtype is bf16 and w.shape == ps[2:] and w.is_contiguous()
+                                   and w.get_device() == dev))
+    ok = ok and (q_out is None or (q_out.dtype is bf16 and q_out.is_contiguous() and q_out.get_device() == dev
+                                   and q_out.shape == qs))
+    if not ok:
+        _refuse_rope(name, q, k, v, positions, inv_freq, slots, pool_k, pool_v, kv, q_weight, k_weight, freq_axis,
+                     q_out)
     if q_out is None:
         with _on(stream):
-            q_out = torch.empty((n, hq, d), dtype=bf16, device=q.device)
-    ptr = [None if t is None else t.data_ptr() for t in (q_weight, k_weight, positions, inv_freq, freq_axis)]
+            q_out = torch.empty(qs, dtype=bf16, device=q.device)
+    if n > 1:
+        strides = q.stride(0), k.stride(0), v.stride(0)
+    else:   # the stride of a single token means nothing
+        strides = qs[1] * d, ps[1] * d, ps[1] * d
     code = getattr(lib(), name)(
-        q.data_ptr(), q.stride(0) if n > 1 else hq * d, k.data_ptr(), k.stride(0) if n > 1 else hkv * d,
-        v.data_ptr(), v.stride(0) if n > 1 else hkv * d, ptr[0], ptr[1], float(eps), ptr[2], axes, ptr[3], ptr[4],
-        rot, 1 if interleaved else 0, slots.data_ptr(), n, q_out.data_ptr(), pool_k.data_ptr(), pool_v.data_ptr(),
-        *scales, _dims_ref(hq, hkv, d, pool_k.shape[0], 0.0), _raw_stream(stream))
+        q.data_ptr(), strides[0], k.data_ptr(), strides[1], v.data_ptr(), strides[2],
+        None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(), float(eps),
+        positions.data_ptr() if rot else None, axes, inv_freq.data_ptr() if rot else None,
+        freq_axis.data_ptr() if axes > 1 else None, rot, 1 if interleaved else 0, slots.data_ptr(), n,
+        q_out.data_ptr(), pool_k.data_ptr(), pool_v.data_ptr(), *scales, _dims_ref(qs[1], ps[1], d, ps[0], 0.0),
+        _raw_stream(stream, dev))
     if code != 0:
         raise SglError(name, code)
     return q_out

@@ -723,14 +723,9 @@ size_t sgl_decode_window_workspace_bytes(int32_t batch, int32_t max_seq_len, int
 size_t sgl_extend_window_workspace_bytes(int32_t batch, int32_t total_extend, int32_t max_extend,
                                          int32_t max_prefix, int32_t window, int32_t sinks,
                                          const sgl_attn_dims* dims) {
-  (void)batch;
-  (void)total_extend;
-  (void)max_extend;
-  (void)max_prefix;
-  (void)window;
-  (void)sinks;
-  (void)dims;
-  return extend_workspace_bytes();
+  if (dims == nullptr || dims->num_kv_heads <= 0 || dims->num_q_heads <= 0) return 0;
+  return extend_window_workspace_bytes(batch, total_extend, max_extend, max_prefix, window, sinks,
+                                       dims->num_q_heads, dims->num_kv_heads, dims->head_dim);
 }
 
 namespace {
@@ -789,8 +784,12 @@ sgl_status extend_window_entry(const void* q, const void* pool_k, const void* po
                                     batch, total_extend, max_extend, max_prefix, out, workspace, workspace_bytes,
                                     dims, &a, &empty);
   if (st != SGL_OK || empty) return st;
+  if (workspace_bytes < sgl_extend_window_workspace_bytes(batch, total_extend, max_extend, max_prefix, window, sinks,
+                                                          dims))
+    return SGL_ERR_WORKSPACE;
   a.window = window;
   a.sinks = sinks;
+  a.max_prefix = max_prefix;
   return launch_extend_window(a, reinterpret_cast<cudaStream_t>(stream));
 }
 }  // namespace

@@ -14,11 +14,10 @@ using namespace dec;
 
 namespace {
 
-// Runs are made as short as it takes to give the part kFillUnits units of
-// work, but no shorter than kMinRun keys and no longer than kItemMax (the
-// slot run buffer).
-constexpr int kFillUnits = 1824;
-constexpr int kMinRun = 128;
+// Runs are made as short as it takes to give the part kFillUnits CTAs, but no
+// shorter than kMinRun keys and no longer than kItemMax (the slot run buffer).
+constexpr int kFillUnits = 456;
+constexpr int kMinRun = 256;
 
 int32_t splits_for(int64_t units, int32_t keys) {
   const int32_t fill = (int32_t)((kFillUnits + units - 1) / units);
@@ -28,23 +27,27 @@ int32_t splits_for(int64_t units, int32_t keys) {
   return s > least ? s : least;
 }
 
-// Virtual KV heads, their grid groups, and the runs a request is cut into.
+// Virtual KV heads, and the runs and clusters a request is cut into.
 struct Shape {
   int32_t split, Hkv, G;
-  int32_t keys, n_splits, chunk;
+  int32_t keys, chunk, n_splits, cluster, n_states;
   Shape(int32_t batch, int32_t max_seq_len, int32_t window, int32_t sinks, int32_t Hq, int32_t Hkv_pool) {
     split = kv_split_for(Hq / Hkv_pool);
     Hkv = Hkv_pool * split;
     G = Hq / Hkv;
     const int64_t seen = (int64_t)window + sinks;
     keys = (int32_t)(seen < max_seq_len ? seen : max_seq_len);
-    n_splits = splits_for((int64_t)batch * Hkv, keys);
+    const int64_t units = (int64_t)batch * Hkv;
+    const int32_t runs = splits_for(units, keys);
+    cluster = units * runs > 2 * kFillUnits ? 1 : (runs < kMaxCluster ? runs : kMaxCluster);
+    n_states = (runs + cluster - 1) / cluster;
+    n_splits = cluster * n_states;
     chunk = (keys + n_splits - 1) / n_splits;
   }
 };
 
 size_t ws_bytes(int32_t batch, const Shape& s, int32_t D, void* base, Ws* ws) {
-  const size_t n = s.n_splits > 1 ? (size_t)batch * s.n_splits * s.Hkv * s.G : 0;
+  const size_t n = s.n_states > 1 ? (size_t)batch * s.n_states * s.Hkv * s.G : 0;
   const size_t o_acc = align256(sizeof(float2) * n);
   if (ws != nullptr) {
     char* b = static_cast<char*>(base);
@@ -59,9 +62,13 @@ __global__ void __launch_bounds__(kThreads, (split_min_blocks<D, G, LPT, KV>()))
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int32_t s_item[2];
   grid_dep_launch();
-  // KV heads fastest: the CTAs of a run gather the heads of the same slots
-  const int32_t heads = kSpans ? p.Hkv / kWarps : p.Hkv;
-  const int32_t unit = (int32_t)(blockIdx.x / (unsigned)heads), y = (int32_t)(blockIdx.x % (unsigned)heads);
+  // a cluster's CTAs are the runs of one request and KV head; without
+  // clusters the KV heads come fastest, so that the CTAs next to each other
+  // gather the heads of the same slots
+  const uint32_t heads = kSpans ? p.Hkv / kWarps : p.Hkv, cs = p.win.cluster;
+  const uint32_t group = blockIdx.x / cs;
+  const int32_t y = (int32_t)(group % heads);
+  const int32_t item = (int32_t)(group / heads * cs + blockIdx.x % cs);
   bool taken = false;
   split_units<D, G, LPT, KV, 0, kSpans, true>(
       p, smem, s_item, threadIdx.x, 1, [] { __syncthreads(); },
@@ -70,23 +77,98 @@ __global__ void __launch_bounds__(kThreads, (split_min_blocks<D, G, LPT, KV>()))
         taken = true;
         return u;
       },
-      [&](int32_t) { return kSpans ? kWarps * y : y; }, [&](int32_t) { return unit; });
+      [&](int32_t) { return kSpans ? kWarps * y : y; }, [&](int32_t) { return item; });
+}
+
+// Merges the clusters' states of requests with more than one: a block a
+// (request, query head), its warps taking the states in turn, four loads of
+// each in flight (one warp reading 33 states one after the other took 14 us,
+// longer than the split kernel).
+template <int D>
+__global__ void __launch_bounds__(128) window_combine_kernel(Params p) {
+  constexpr int E = D / 32, kBatch = 4;
+  __shared__ float s_m[4], s_l[4];
+  __shared__ float s_acc[4][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq;
+  const int32_t runs = WindowRun(p.win, p.chunk, p.seq_lens[r]).ns;
+  const int32_t ns = (runs + p.win.cluster - 1) / p.win.cluster;
+  if (ns <= 1) return;  // a single cluster wrote the output (none: no keys)
+  grid_dep_wait();      // launched dependent on the split kernel
+  const int64_t first = (int64_t)r * p.win.n_states * p.Hq + h, step = p.Hq;
+  float M = -INFINITY, L = 0.f, acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  for (int32_t s0 = warp; s0 < ns; s0 += 4 * kBatch) {
+    float2 ml[kBatch];
+    float a[kBatch][E];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int64_t slot = first + (int64_t)min(s0 + 4 * u, ns - 1) * step;
+      ml[u] = p.ws.part_ml[slot];
+#pragma unroll
+      for (int e = 0; e < E; ++e) a[u][e] = p.ws.part_acc[slot * D + lane + 32 * e];
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (s0 + 4 * u >= ns) break;
+      const float m = fmaxf(M, ml[u].x);
+      const float f = ex2(M - m), w = ex2(ml[u].x - m);
+      M = m;
+      L = L * f + ml[u].y * w;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = acc[e] * f + a[u][e] * w;
+    }
+  }
+  if (lane == 0) s_m[warp] = M, s_l[warp] = L;
+#pragma unroll
+  for (int e = 0; e < E; ++e) s_acc[warp][lane + 32 * e] = acc[e];
+  __syncthreads();
+  M = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+  float f[4];
+  L = 0.f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    f[w] = ex2(s_m[w] - M);  // 0 for a warp without a run (-inf)
+    L += s_l[w] * f[w];
+  }
+  const int d = threadIdx.x;
+  if (d < D) {
+    float o = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) o += s_acc[w][d] * f[w];
+    p.out[((int64_t)r * p.Hq + h) * D + d] = __float2bfloat16_rn(o * (p.v_scale / L));
+  }
 }
 
 template <int D, int G, int LPT, typename KV, bool kSpans>
 sgl_status launch(const Params& prm, cudaStream_t stream) {
   constexpr size_t smem = SplitRing<KV, G>::template bytes<D>() + kItemMax * sizeof(int32_t);
-  static_assert(kWarps * G * (D + 2) * sizeof(float) <= SplitRing<KV, G>::template bytes<D>(),
-                "reduction scratch must fit in the ring");
+  static_assert((kWarps + 1) * G * (D + 2) * sizeof(float) <= SplitRing<KV, G>::template bytes<D>(),
+                "the warps' states and the CTA's must fit in the ring");
   if (kernel_blocks_per_sm<decode_window_kernel<D, G, LPT, KV, kSpans>>((int)smem, kThreads) < 0) return SGL_ERR_CUDA;
   const int64_t heads = kSpans ? prm.Hkv / kWarps : prm.Hkv;
-  const int64_t units = (int64_t)prm.batch * prm.win.n_splits * heads;
-  if (units > 0x7fffffff) return SGL_ERR_UNSUPPORTED;
-  decode_window_kernel<D, G, LPT, KV, kSpans><<<(unsigned)units, kThreads, smem, stream>>>(prm);
-  if (prm.win.n_splits > 1) {
-    const int64_t warps = (int64_t)prm.batch * prm.Hq;
-    if (launch_dependent(decode_combine_kernel<D, true>, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0, stream,
-                         prm) != cudaSuccess)
+  const int64_t ctas = (int64_t)prm.batch * prm.win.n_splits * heads;
+  if (ctas > 0x7fffffff) return SGL_ERR_UNSUPPORTED;
+  if (prm.win.cluster == 1) {
+    decode_window_kernel<D, G, LPT, KV, kSpans><<<(unsigned)ctas, kThreads, smem, stream>>>(prm);
+  } else {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {(unsigned)prm.win.cluster, 1, 1};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, decode_window_kernel<D, G, LPT, KV, kSpans>, prm) != cudaSuccess)
+      return SGL_ERR_CUDA;
+  }
+  if (prm.win.n_states > 1) {
+    const int64_t rows = (int64_t)prm.batch * prm.Hq;
+    if (launch_dependent(window_combine_kernel<D>, dim3((unsigned)rows), dim3(128), 0, stream, prm) != cudaSuccess)
       return SGL_ERR_CUDA;
   }
   return cudaGetLastError() == cudaSuccess ? SGL_OK : SGL_ERR_CUDA;
@@ -155,7 +237,7 @@ sgl_status launch_decode_window(const DecodeArgs& a, cudaStream_t stream) {
   prm.chunk = s.chunk;
   prm.scale_log2 = a.sm_scale * 1.4426950408889634f * (a.kv_fp8 ? a.k_scale : 1.f);
   prm.v_scale = a.kv_fp8 ? a.v_scale : 1.f;
-  prm.win = Window{a.sinks, s.keys, a.max_seq_len, s.n_splits};
+  prm.win = Window{a.sinks, s.keys, a.max_seq_len, s.n_splits, s.cluster, s.n_states};
   if (a.head_dim == 128)
     return a.kv_fp8 ? run_g<128, uint8_t>(s.G, prm, stream) : run_g<128, __nv_bfloat16>(s.G, prm, stream);
   if (a.head_dim == 64)

@@ -275,6 +275,10 @@ struct Params {
   int32_t max_depth;
   int32_t batch;  // member indices outside [0, batch) are skipped
   int32_t window, sinks;  // sliding-window extend (WindowKeys)
+  // A sliding-window extend of few tiles deals each tile's key blocks to
+  // n_runs CTAs, whose fp32 states go to entry (row * Hq + head) * n_runs + run
+  // of part_ml / part_acc for a combine (1: the CTA writes the output).
+  int32_t n_runs;
 };
 
 // The keys a CTA's queries see in a sliding-window extend.  Query position P
@@ -284,22 +288,36 @@ struct Params {
 // that list is position i below n_first = min(sinks, lo) and lo + i - n_first
 // from there on.  Sinks and window share the list's 128-key blocks, so a few
 // sinks cost no block of their own.
+//
+// kRuns: the CTA takes run `run` of the list's blocks; its keys are i0 .. of
+// the list, and the indices below count from there.
+template <bool kRuns>
 struct WindowKeys {
-  int32_t lo, n_first, n;  // n: keys of the list
+  int32_t lo, n_first, n;  // n: keys of the list, or of the run
+  int32_t i0 = 0;
   int32_t sinks, window;
-  SGL_DEV WindowKeys(const Params& p, int32_t first_pos, int32_t end) {
-    sinks = p.sinks;
+  SGL_DEV WindowKeys(const Params& p, int32_t first_pos, int32_t end, int32_t run) {
     window = p.window;
     lo = max(0, first_pos - window + 1);
-    n_first = min(sinks, lo);
+    n_first = min(p.sinks, lo);
     n = n_first + end - lo;
+    sinks = p.sinks;
+    if constexpr (kRuns) {
+      const int32_t blocks = (n + BN - 1) / BN, base = blocks / p.n_runs, rem = blocks % p.n_runs;
+      i0 = BN * (run * base + min(run, rem));
+      n = max(0, min(n - i0, BN * (base + (run < rem ? 1 : 0))));
+      sinks -= i0;
+    }
   }
-  SGL_DEV int32_t pos(int32_t i) const { return i < n_first ? i : lo + (i - n_first); }
-  // Query position P sees the list's keys i < hi(P) with i < sinks or i >=
-  // first(P).  (Where lo < sinks the list is the positions from 0 on, so i <
-  // sinks is position i < sinks in either case.)
-  SGL_DEV int32_t hi(int32_t P) const { return P - lo + n_first + 1; }
-  SGL_DEV int32_t first(int32_t P) const { return max(0, P - window + 1) - lo + n_first; }
+  SGL_DEV int32_t pos(int32_t i) const {
+    const int32_t j = i + i0;
+    return j < n_first ? j : lo + (j - n_first);
+  }
+  // Query position P sees the keys i < hi(P) with i < sinks or i >= first(P).
+  // (Where lo < sinks the list is the positions from 0 on, so the first
+  // `sinks` of it are the sinks in either case.)
+  SGL_DEV int32_t hi(int32_t P) const { return P - lo + n_first + 1 - i0; }
+  SGL_DEV int32_t first(int32_t P) const { return max(0, P - window + 1) - lo + n_first - i0; }
 };
 
 // byte offset of 16-byte chunk `ci` (0..7) of row `row` inside one
@@ -441,10 +459,10 @@ SGL_DEV void load_q_tiles(const Params& p, uint32_t sQ_a, uint64_t* q_full, int 
 // ordered for the tensor core with a proxy fence before the arrival.  Prefix
 // keys are positions 0..pfx-1 of the request's row, suffix keys positions
 // pfx..pfx+q_end-1 (stored into the pool before the call).
-template <int D, bool kGroup, bool kWindow>
+template <int D, bool kGroup, bool kWindow, class Keys>
 SGL_DEV void produce_fp8(const Params& p, uint32_t sQ_a, uint8_t* sKV, uint8_t* sRaw, Bars* bars,
                          int ptid, int r, int kvh, int e, int mbeg, int q0, int pfx, int q_end, int nb_pre, int nb,
-                         int off, const WindowKeys& wk) {
+                         int off, const Keys& wk) {
   const uint32_t sRaw_a = smem_u32(sRaw);
   using C = Cfg<D, true>;
   using R = Roles<true>;
@@ -626,14 +644,19 @@ SGL_DEV void produce_fp8(const Params& p, uint32_t sQ_a, uint8_t* sKV, uint8_t* 
 // them again (the previous tile ended with every thread past its final
 // barrier, every copy landed and every MMA drained).
 //
-// kWindow: a sliding-window extend.  Every key, the suffix's included, is
-// read from the pool through req_to_token (both pool types); the CTA walks
-// only the keys one of its queries sees (WindowKeys).
-template <int D, bool kGroup, bool kFp8, int kTiles = 2, bool kPersistent = false, bool kWindow = false>
-SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz) {
+// kMode kWindowed: a sliding-window extend.  Every key, the suffix's included,
+// is read from the pool through req_to_token (both pool types); the CTA walks
+// only the keys one of its queries sees (WindowKeys).  kWindowedRuns: run
+// `run` of them, leaving fp32 states; an empty second Q tile is skipped (as
+// in group mode; that branch and the states cost long CTAs 5%, 482 -> 506 us on
+// 8 chunks of 2,048 tokens, so whole tiles run without).
+enum Mode { kCausal, kWindowed, kWindowedRuns };
+template <int D, bool kGroup, bool kFp8, int kTiles = 2, bool kPersistent = false, Mode kMode = kCausal>
+SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz, int run = 0) {
   using C = Cfg<D, kFp8, kTiles>;
   using R = Roles<kFp8, kTiles>;
   constexpr uint32_t kTmemCols = tmem_cols<kTiles>();
+  constexpr bool kWindow = kMode != kCausal, kRuns = kMode == kWindowedRuns;
   uint8_t* smem = smem_base();
   uint8_t* sQ = smem;
   uint8_t* sKV = smem + kTiles * C::kTileBytes;
@@ -651,15 +674,28 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz) {
   const int q0 = bx * kTiles * p.tpt;                         // first token of this tile
   const int pfx = kGroup ? p.group_len[r] : p.prefix_lens[r];  // keys read from the pool
   const int q_end = min(e, q0 + kTiles * p.tpt);
-  const WindowKeys wk(p, pfx + q0, pfx + q_end);  // kWindow only
+  const WindowKeys<kRuns> wk(p, pfx + q0, pfx + q_end, run);  // kWindow only
   const int nb_pre = ((kWindow ? wk.n : pfx) + BN - 1) / BN;
   const int nb = nb_pre + (kGroup || kWindow ? 0 : (q_end + BN - 1) / BN);
   // Group mode: Q tile 1 holds no member (a cascade group of at most tpt
   // members, most groups of a tree): its MMAs and softmax are skipped and tile
   // 0 runs alone (tree cascade +4-5%).  Extend mode keeps both tiles: the
   // branches cost the long extend CTAs ~1%.
-  const bool two_tiles = kTiles == 2 && (kGroup ? q0 + p.tpt < e : true);
-  if (q0 >= e || nb <= 0) return;  // nothing to do (uniform across the CTA)
+  const bool two_tiles = kTiles == 2 && (kGroup || kRuns ? q0 + p.tpt < e : true);
+  if (q0 >= e || (!kRuns && nb <= 0)) return;  // nothing to do (uniform across the CTA)
+  if constexpr (kRuns) {
+    if (nb <= 0) {  // more runs than blocks: states without keys
+      int32_t at = 0;
+      for (int i = lane; i < r; i += 32) at += p.extend_lens[i];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) at += __shfl_xor_sync(0xffffffffu, at, o);
+      for (int i = tid; i < (q_end - q0) * p.g; i += (int)blockDim.x) {
+        const int64_t row = (int64_t)(at + q0 + i / p.g) * p.Hq + (int64_t)kvh * p.g + i % p.g;
+        p.part_ml[row * p.n_runs + run] = make_float2(-INFINITY, 0.f);
+      }
+      return;
+    }
+  }
 
   // exclusive prefix sum of extend_lens: where request r's rows start
   if constexpr (!kGroup) {
@@ -857,6 +893,24 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz) {
           }
         }
         if (wr) p.part_ml[ent] = make_float2(m_ref, l);
+      } else if (kRuns) {
+        // the run's state, P.V rows in units of o_scale
+        const int64_t ent =
+            ((int64_t)(off + tok) * p.Hq + (int64_t)kvh * p.g + row % p.g) * p.n_runs + run;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+          uint32_t o[32];
+          tmem_ld32(tO + 32 * j, o);
+          tmem_wait_ld();
+          if (row_valid && l > 0.f) {
+            float4* d4 = reinterpret_cast<float4*>(p.part_acc + ent * D + 32 * j);
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+              d4[v] = make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
+                                  __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
+          }
+        }
+        if (row_valid) p.part_ml[ent] = make_float2(m_ref, l);
       } else {
         const float inv = l > 0.f ? (kFp8 ? p.o_scale : 1.f) / l : 0.f;
         constexpr int kStride = out_stride<D>();
@@ -1045,6 +1099,27 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz) {
           }
         }
         if (wr && h == 0) p.part_ml[ent] = make_float2(m_ref, lrow);
+      }
+    } else if (kRuns) {
+      if (ok) {
+        tc_fence_after();
+        // the run's state: this half holds columns [h*D/2, (h+1)*D/2)
+        const int64_t ent =
+            ((int64_t)(off + tok) * p.Hq + (int64_t)kvh * p.g + row % p.g) * p.n_runs + run;
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) {
+          uint32_t o[32];
+          tmem_ld32(tO + (D / 2) * h + 32 * j, o);
+          tmem_wait_ld();
+          if (row_valid && lrow > 0.f) {
+            float4* d4 = reinterpret_cast<float4*>(p.part_acc + ent * D + (D / 2) * h + 32 * j);
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+              d4[v] = make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
+                                  __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
+          }
+        }
+        if (row_valid && h == 0) p.part_ml[ent] = make_float2(m_ref, lrow);
       }
     } else if (ok) {
       tc_fence_after();
@@ -1254,9 +1329,21 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz) {
   }
 }
 
-template <int D, bool kFp8, bool kWindow = false>
+template <int D, bool kFp8>
 __global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1) extend_kernel(Params p) {
-  attend_tiles<D, false, kFp8, 2, false, kWindow>(p, blockIdx.x, blockIdx.y, blockIdx.z);
+  attend_tiles<D, false, kFp8>(p, blockIdx.x, blockIdx.y, blockIdx.z);
+}
+
+// grid x: pairs of Q tiles, times the runs of their keys
+template <int D, bool kFp8, bool kRuns>
+__global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1) extend_window_kernel(Params p) {
+  if constexpr (kRuns) {
+    grid_dep_launch();  // the combine may start; it waits for the states
+    attend_tiles<D, false, kFp8, 2, false, kWindowedRuns>(p, blockIdx.x / p.n_runs, blockIdx.y, blockIdx.z,
+                                                          blockIdx.x % p.n_runs);
+  } else {
+    attend_tiles<D, false, kFp8, 2, false, kWindowed>(p, blockIdx.x, blockIdx.y, blockIdx.z);
+  }
 }
 
 // one Q tile: two CTAs an SM (11 warps a CTA are allocated registers as 12,
@@ -1303,6 +1390,7 @@ inline sgl_status make_extend_params(const ExtendArgs& a, Params* out) {
   prm.wait_ns = device_wait_limit_ns();
   prm.window = a.window;
   prm.sinks = a.sinks;
+  prm.n_runs = 1;
   *out = prm;
   return SGL_OK;
 }

@@ -1,5 +1,6 @@
-// Launcher of the sliding-window extend: the extend pipeline (extend_dev.cuh)
-// over the keys each CTA's queries see.
+// Launchers of the sliding-window extend: the extend pipeline (extend_dev.cuh)
+// over the keys each CTA's queries see, and the combine of tiles whose keys
+// were dealt to several CTAs.
 #include "extend_dev.cuh"
 #include "launch.h"
 
@@ -9,32 +10,136 @@ using namespace ext;
 
 namespace {
 
-template <int D, bool kFp8>
-sgl_status run(const Params& prm, int32_t batch, int32_t max_extend, cudaStream_t stream) {
+// A call with fewer tiles than this part has SMs deals each tile's key blocks
+// to as many CTAs as fill them (one CTA of this pipeline an SM).
+constexpr int kFillCtas = 152;
+constexpr int kMaxRuns = 32;  // a lane each in the combine
+
+struct Shape {
+  int32_t per_cta;  // tokens of a CTA's two Q tiles
+  int32_t tiles;    // CTAs along x for the longest request
+  int32_t n_runs;
+  Shape(int32_t batch, int32_t total_extend, int32_t max_extend, int32_t max_prefix, int32_t window, int32_t sinks,
+        int32_t Hq, int32_t Hkv) {
+    per_cta = 2 * (BM / (Hq / Hkv));
+    tiles = (max_extend + per_cta - 1) / per_cta;
+    // tiles with queries: every request's last one may be short
+    int64_t live = (int64_t)total_extend / per_cta + batch;
+    if (live > (int64_t)tiles * batch) live = (int64_t)tiles * batch;
+    // keys of a tile: its queries' positions, the window before them, the sinks
+    const int64_t own = max_extend < per_cta ? max_extend : per_cta;
+    int64_t keys = (int64_t)window - 1 + own + sinks;
+    if (keys > (int64_t)max_prefix + max_extend) keys = (int64_t)max_prefix + max_extend;
+    int64_t runs = live * Hkv > 0 ? kFillCtas / (live * Hkv) : 1;
+    const int64_t blocks = (keys + BN - 1) / BN;
+    if (runs > blocks) runs = blocks;
+    if (runs > kMaxRuns) runs = kMaxRuns;
+    n_runs = runs < 1 ? 1 : (int32_t)runs;
+  }
+};
+
+// status word (256 bytes), then (max, sum) and P.V rows of every (token, query
+// head, run)
+size_t layout(const Shape& s, int32_t total_extend, int32_t Hq, int32_t D, void* base, Params* prm) {
+  const size_t entries = s.n_runs > 1 ? (size_t)total_extend * Hq * s.n_runs : 0;
+  const size_t o_ml = extend_workspace_bytes();
+  const size_t o_acc = o_ml + (entries * sizeof(float2) + 255) / 256 * 256;
+  if (prm != nullptr) {
+    prm->part_ml = reinterpret_cast<float2*>(static_cast<char*>(base) + o_ml);
+    prm->part_acc = reinterpret_cast<float*>(static_cast<char*>(base) + o_acc);
+  }
+  return o_acc + entries * D * sizeof(float);
+}
+
+// A warp a (token, query head): lane i holds run i's (max, sum); rows past
+// the last request's are left alone.
+template <int D>
+__global__ void __launch_bounds__(128) extend_window_combine_kernel(Params p) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  int64_t tokens = 0;
+  for (int i = lane; i < p.batch; i += 32) tokens += p.extend_lens[i];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) tokens += __shfl_xor_sync(0xffffffffu, tokens, o);
+  if (row >= tokens * p.Hq) return;
+  grid_dep_wait();  // launched dependent on the extend kernel
+  float2 ml = make_float2(-INFINITY, 0.f);
+  if (lane < p.n_runs) ml = p.part_ml[row * p.n_runs + lane];
+  float M = ml.x;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float w = ml.y > 0.f ? ex2(ml.x - M) : 0.f;
+  float L = ml.y * w;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  float acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  const float* a = p.part_acc + row * p.n_runs * D;
+#pragma unroll 8
+  for (int s = 0; s < p.n_runs; ++s) {
+    const float f = __shfl_sync(0xffffffffu, w, s);
+    if (f != 0.f) {  // (a run without keys left its rows unwritten)
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(f, a[s * D + lane + 32 * e], acc[e]);
+    }
+  }
+  const float inv = p.o_scale / L;
+  __nv_bfloat16* o = p.out + row * D;
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[lane + 32 * e] = __float2bfloat16_rn(acc[e] * inv);
+}
+
+template <int D, bool kFp8, bool kRuns>
+sgl_status launch(const Params& prm, const ExtendArgs& a, const Shape& s, cudaStream_t stream) {
   constexpr int kThreads = Roles<kFp8>::kThreads;
   constexpr int kSmem = smem_bytes<D, kFp8>();
-  if (kernel_blocks_per_sm<extend_kernel<D, kFp8, true>>(kSmem, kThreads) < 0) return SGL_ERR_CUDA;
-  if (Roles<kFp8>::kSplitRegs && !kernel_regs_at_least<extend_kernel<D, kFp8, true>>(Roles<kFp8>::kLaunchRegs))
+  auto kern = extend_window_kernel<D, kFp8, kRuns>;
+  if (kernel_blocks_per_sm<extend_window_kernel<D, kFp8, kRuns>>(kSmem, kThreads) < 0) return SGL_ERR_CUDA;
+  if (Roles<kFp8>::kSplitRegs && !kernel_regs_at_least<extend_window_kernel<D, kFp8, kRuns>>(Roles<kFp8>::kLaunchRegs))
     return SGL_ERR_UNSUPPORTED;
-  const int per_cta = 2 * prm.tpt;
-  const dim3 grid((unsigned)((max_extend + per_cta - 1) / per_cta), (unsigned)prm.Hkv, (unsigned)batch);
-  extend_kernel<D, kFp8, true><<<grid, kThreads, kSmem, stream>>>(prm);
+  const dim3 grid((unsigned)(s.tiles * s.n_runs), (unsigned)prm.Hkv, (unsigned)a.batch);
+  kern<<<grid, kThreads, kSmem, stream>>>(prm);
+  if (kRuns) {
+    const int64_t rows = (int64_t)a.total_extend * prm.Hq;
+    if (launch_dependent(extend_window_combine_kernel<D>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, stream,
+                         prm) != cudaSuccess)
+      return SGL_ERR_CUDA;
+  }
   return cudaGetLastError() == cudaSuccess ? SGL_OK : SGL_ERR_CUDA;
 }
 
+template <int D, bool kFp8>
+sgl_status run(const Params& prm, const ExtendArgs& a, const Shape& s, cudaStream_t stream) {
+  return s.n_runs > 1 ? launch<D, kFp8, true>(prm, a, s, stream) : launch<D, kFp8, false>(prm, a, s, stream);
+}
+
 }  // namespace
+
+size_t extend_window_workspace_bytes(int32_t batch, int32_t total_extend, int32_t max_extend, int32_t max_prefix,
+                                     int32_t window, int32_t sinks, int32_t Hq, int32_t Hkv, int32_t D) {
+  if (batch <= 0 || total_extend <= 0 || max_extend <= 0 || max_prefix < 0 || window <= 0 || sinks < 0 || Hkv <= 0 ||
+      Hq < Hkv || Hq / Hkv > BM)
+    return extend_workspace_bytes();
+  return layout(Shape(batch, total_extend, max_extend, max_prefix, window, sinks, Hq, Hkv), total_extend, Hq, D,
+                nullptr, nullptr);
+}
 
 sgl_status launch_extend_window(const ExtendArgs& a, cudaStream_t stream) {
   if (a.batch == 0 || a.total_extend == 0 || a.max_extend == 0) return SGL_OK;
   Params prm;
   const sgl_status st = make_extend_params(a, &prm);
   if (st != SGL_OK) return st;
+  const Shape s(a.batch, a.total_extend, a.max_extend, a.max_prefix, a.window, a.sinks, a.num_q_heads,
+                a.num_kv_heads);
+  prm.batch = a.batch;
+  prm.n_runs = s.n_runs;
+  layout(s, a.total_extend, a.num_q_heads, a.head_dim, a.workspace, &prm);
   if (a.head_dim == 128)
-    return a.kv_fp8 ? run<128, true>(prm, a.batch, a.max_extend, stream)
-                    : run<128, false>(prm, a.batch, a.max_extend, stream);
+    return a.kv_fp8 ? run<128, true>(prm, a, s, stream) : run<128, false>(prm, a, s, stream);
   if (a.head_dim == 64)
-    return a.kv_fp8 ? run<64, true>(prm, a.batch, a.max_extend, stream)
-                    : run<64, false>(prm, a.batch, a.max_extend, stream);
+    return a.kv_fp8 ? run<64, true>(prm, a, s, stream) : run<64, false>(prm, a, s, stream);
   return SGL_ERR_UNSUPPORTED;
 }
 

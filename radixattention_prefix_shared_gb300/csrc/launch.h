@@ -220,10 +220,13 @@ struct ExtendArgs {
   float k_scale = 1.f, v_scale = 1.f;
   // sliding window (window > 0, launch_extend_window): the suffix is read
   // from the pool on both pool types
-  int32_t window = 0, sinks = 0;
+  int32_t window = 0, sinks = 0, max_prefix = 0;
 };
 size_t extend_workspace_bytes();
 sgl_status launch_extend(const ExtendArgs& a, cudaStream_t stream);
+size_t extend_window_workspace_bytes(int32_t batch, int32_t total_extend, int32_t max_extend, int32_t max_prefix,
+                                     int32_t window, int32_t sinks, int32_t num_q_heads, int32_t num_kv_heads,
+                                     int32_t head_dim);
 sgl_status launch_extend_window(const ExtendArgs& a, cudaStream_t stream);
 
 // One launch for an extend batch and a plain decode batch over the same bf16

@@ -15,10 +15,11 @@
 // besides its norm.
 //
 // The angle is kept exact modulo a turn: inv_freq / 2 pi as a 64-bit fixed
-// point fraction of a turn, multiplied by the position in wrapping 64-bit
-// integers.  The frequency's rounding (2^-53 of it, once a warp) grows with
-// the position to 2^-33 turns at position 2^20; a float32 product would be off
-// by a twentieth of a radian there.
+// point fraction of a turn (turn_fraction), multiplied by the position in
+// wrapping 64-bit integers.  For frequencies up to 1 the fraction is good to
+// 2^-64 turns, the angle at position 2^31 to 2^-33; a float32 product would be
+// off by a twentieth of a radian at 2^20 already.  (In float64 the fraction
+// took each warp some 20 instructions of a pipe that needs 16 cycles each.)
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -29,7 +30,8 @@ namespace sgl {
 namespace {
 
 constexpr int kRopeWarps = 8;
-constexpr int kRopeBatch = 4;  // row groups a warp loads before it works on them
+constexpr int kRopeBatch = 4;   // row groups a warp loads at a time
+constexpr int kRopeBlocks = 3;  // resident blocks an SM
 
 struct RopeParams {
   const __nv_bfloat16* src[3];  // q, k, v
@@ -64,55 +66,110 @@ SGL_DEV uint32_t e4m3x2(float a, float b, float scale) {
                                             __NV_E4M3);
 }
 
-// D / 8 lanes hold a row, 8 consecutive values each: a warp works on a group
-// of 32 / (D / 8) rows (heads of one token) at a time.
-template <int D, bool kFp8>
-__global__ void __launch_bounds__(kRopeWarps * 32) qk_norm_rope_store_kernel(RopeParams p) {
-  constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+// f / 2 pi modulo 1, in units of 2^-64: f = m 2^e with m an integer of 24
+// bits, and m times the first 64 bits of 1 / 2 pi, 2^66 / 2 pi, shifted to the
+// place of 2^-64.
+SGL_DEV uint64_t turn_fraction(float f) {
+  constexpr uint64_t kInv2Pi = 0xa2f9836e4e441529ull;  // 2^66 / 2 pi
+  const uint32_t bits = __float_as_uint(f);
+  const int ex = (bits >> 23) & 0xff;
+  const uint64_t m = (bits & 0x7fffffu) | (ex > 0 ? 0x800000u : 0u);
+  const int sh = max(ex, 1) - 150 - 2;
+  const uint64_t lo = m * kInv2Pi, hi = __umul64hi(m, kInv2Pi);
+  uint64_t t;
+  if (sh >= 0)
+    t = sh < 64 ? lo << sh : 0;
+  else if (sh > -64)
+    t = (lo >> -sh) | (hi << (64 + sh));
+  else
+    t = sh > -128 ? hi >> (-sh - 64) : 0;
+  return (bits >> 31) ? 0 - t : t;
+}
+
+// A warp works on batches of kRopeBatch row groups, a group being the 32 / (D /
+// 8) rows (heads of one token) that its lanes hold, 8 consecutive values each.
+// A token's batches are those of its Q rows, its K rows and its V rows in
+// turn; block y takes an even share of them.  The next batch's rows, and the
+// next token's slot and positions, are loaded before the current batch is
+// worked on.
+template <int D, bool kFp8, bool kInterleaved>
+__global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) qk_norm_rope_store_kernel(RopeParams p) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kF = D / 64;
   __shared__ float2 s_turn[kRopeWarps][D / 2];  // (cos, sin) of the warp's token
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int li = lane % kLanes, sub = lane / kLanes;
   float2* turn = s_turn[warp];
 
-  // this lane's share of the frequencies, in turns a position
+  constexpr int kBatchRows = kRows * kRopeBatch;
+  const int nq = (p.heads[0] + kBatchRows - 1) / kBatchRows, nk = (p.heads[1] + kBatchRows - 1) / kBatchRows;
+  const int b0 = (nq + 2 * nk) * blockIdx.y / gridDim.y, b1 = (nq + 2 * nk) * (blockIdx.y + 1) / gridDim.y;
   const int nf = p.rot_dim / 2;
-  uint64_t freq[D / 64];
-  const int32_t* fpos[D / 64];
-#pragma unroll
-  for (int i = 0; i < D / 64; ++i) {
-    const int f = lane + 32 * i;
-    freq[i] = 0;
-    fpos[i] = p.positions;
-    if (f < nf) {
-      const double t = (double)p.inv_freq[f] * 0.15915494309189533577;  // 1 / 2 pi
-      freq[i] = (uint64_t)((t - floor(t)) * 18446744073709551616.0);
-      if (p.freq_axis != nullptr) fpos[i] += (int64_t)min(max(p.freq_axis[f], 0), p.n_axes - 1) * p.n;
-    }
-  }
-  // this lane's values 8 li .. 8 li + 7: the lane holding their partners, the
-  // first frequency and the sign of the sine
+  const bool turns = b0 < nq + nk && nf > 0;  // this block has rows to turn
+
+  // this lane's values 8 li .. 8 li + 7: the lane that holds their partners
   const bool rotated = 8 * li < p.rot_dim;
   const int half = p.rot_dim / 16;
   const bool low = li < half;
-  const int plane = p.interleaved || !rotated ? li : (low ? li + half : li - half);
+  const int plane = kInterleaved || !rotated ? li : (low ? li + half : li - half);
 
-  // this part's row groups of the list q, k, v
-  const int gq = (p.heads[0] + kRows - 1) / kRows, gk = (p.heads[1] + kRows - 1) / kRows;
-  const int total = gq + 2 * gk, part = blockIdx.y, parts = gridDim.y;
-  const int g0 = (int)((int64_t)total * part / parts), g1 = (int)((int64_t)total * (part + 1) / parts);
+  int32_t t = blockIdx.x * kRopeWarps + warp;
+  const int32_t stride = gridDim.x * kRopeWarps;
+  if (t >= p.n) return;
+  int b = b0;
+  uint4 raw[kRopeBatch];
+  int32_t slot, pos[kF];
+  auto section = [&](int bb) { return bb < nq ? 0 : (bb < nq + nk ? 1 : 2); };
+  auto load_rows = [&](int32_t tt, int bb) {
+    const int sec = section(bb);
+    const int h0 = (bb - (sec == 0 ? 0 : (sec == 1 ? nq : nq + nk))) * kBatchRows + sub;
+    const __nv_bfloat16* src = p.src[sec] + tt * p.stride[sec] + (int64_t)h0 * D + 8 * li;
+    const int n_heads = p.heads[sec > 0];
+#pragma unroll
+    for (int u = 0; u < kRopeBatch; ++u)
+      if (h0 + u * kRows < n_heads) raw[u] = ld_row(src + u * kRows * D);
+  };
+  const int32_t* fpos[kF];
+  auto load_token = [&](int32_t tt) {
+    slot = p.slots[tt];
+    if (turns) {
+#pragma unroll
+      for (int i = 0; i < kF; ++i)
+        if (lane + 32 * i < nf) pos[i] = fpos[i][tt];
+    }
+  };
+  load_rows(t, b);
+  uint64_t freq[kF];
+#pragma unroll
+  for (int i = 0; i < kF; ++i) {
+    const int f = lane + 32 * i;
+    freq[i] = 0;
+    fpos[i] = p.positions;
+    pos[i] = 0;
+    if (turns && f < nf) {
+      freq[i] = turn_fraction(p.inv_freq[f]);
+      if (p.freq_axis != nullptr) fpos[i] += (int64_t)min(max(p.freq_axis[f], 0), p.n_axes - 1) * p.n;
+    }
+  }
+  load_token(t);
+  bool fresh = true;  // the token's first batch here
 
-  for (int64_t t = (int64_t)blockIdx.x * kRopeWarps + warp; t < p.n; t += (int64_t)gridDim.x * kRopeWarps) {
-    const int64_t slot = p.slots[t];
-    if (slot < 0 || slot >= p.pool_size) continue;  // a padding token
-
-    float c[8], s[8];
-    if (g0 < gq + gk && nf > 0) {
+  while (true) {
+    const int sec = section(b);
+    const int h0 = (b - (sec == 0 ? 0 : (sec == 1 ? nq : nq + nk))) * kBatchRows + sub;
+    const int n_heads = p.heads[sec > 0];
+    const int64_t at = slot;
+    const bool live = at >= 0 && at < p.pool_size;  // else a padding token
+    const int32_t tok = t;
+    uint4 cur[kRopeBatch];
+#pragma unroll
+    for (int u = 0; u < kRopeBatch; ++u) cur[u] = raw[u];
+    if (fresh && turns) {
       __syncwarp();
 #pragma unroll
-      for (int i = 0; i < D / 64; ++i) {
+      for (int i = 0; i < kF; ++i) {
         const int f = lane + 32 * i;
         if (f < nf) {
-          const uint64_t a = (uint64_t)(int64_t)fpos[i][t] * freq[i];
+          const uint64_t a = (uint64_t)(int64_t)pos[i] * freq[i];
           float sn, cs;
           sincospif((float)(int32_t)(a >> 32) * 0x1p-31f, &sn, &cs);
           turn[f] = make_float2(cs, sn);
@@ -120,119 +177,127 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qk_norm_rope_store_kernel(Rop
       }
       __syncwarp();
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float2 v = make_float2(1.f, 0.f);
-      if (rotated) v = turn[p.interleaved ? 4 * li + e / 2 : (low ? 8 * li + e : 8 * (li - half) + e)];
-      c[e] = v.x;
-      s[e] = (p.interleaved ? (e & 1) == 0 : low) ? -v.y : v.y;
+    // on to the next batch
+    fresh = ++b == b1;
+    if (fresh) {
+      b = b0;
+      t += stride;
     }
-    int first = 0;  // first group of the section
-#pragma unroll
-    for (int sec = 0; sec < 3; ++sec) {
-      const int n_groups = sec == 0 ? gq : gk, n_heads = p.heads[sec > 0];
-      const int a0 = max(g0 - first, 0), a1 = min(g1 - first, n_groups);
-      first += n_groups;
-      if (a0 >= a1) continue;
-      float A[8], B[8];
-      bool norm = false;
+    const bool more = t < p.n;
+    if (more) {
+      load_rows(t, b);
+      if (fresh) load_token(t);
+    }
+    if (live) {
       if (sec < 2) {
-        float w[8], wp[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = wp[e] = 1.f;
-        norm = p.weight[sec & 1] != nullptr;
-        if (norm) {
-          bf16x8_to_f32(*reinterpret_cast<const uint4*>(p.weight[sec & 1] + 8 * li), w);
-          bf16x8_to_f32(*reinterpret_cast<const uint4*>(p.weight[sec & 1] + 8 * plane), wp);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          A[e] = w[e] * c[e];
-          B[e] = (p.interleaved ? w[e ^ 1] : wp[e]) * s[e];
-        }
-      }
-      const __nv_bfloat16* src = p.src[sec] + t * p.stride[sec] + 8 * li;
-      for (int g = a0; g < a1; g += kRopeBatch) {
-        uint4 raw[kRopeBatch];
-#pragma unroll
-        for (int u = 0; u < kRopeBatch; ++u) {
-          const int h = (g + u) * kRows + sub;
-          raw[u] = make_uint4(0u, 0u, 0u, 0u);
-          if (g + u < a1 && h < n_heads) raw[u] = ld_row(src + (int64_t)h * D);
-        }
-#pragma unroll
-        for (int u = 0; u < kRopeBatch; ++u) {
-          if (g + u >= a1) break;
-          const int h = (g + u) * kRows + sub;
-          uint4 out = raw[u];
-          float y[8];
-          if (sec < 2 || kFp8) bf16x8_to_f32(raw[u], y);
-          if (sec < 2) {
-            float r = 1.f;
-            if (norm) {
-              float q2 = 0.f;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) q2 = fmaf(y[e], y[e], q2);
-#pragma unroll
-              for (int o = 1; o < kLanes; o <<= 1) q2 += __shfl_xor_sync(0xffffffffu, q2, o);
-              r = rsqrtf(q2 * (1.f / D) + p.eps);
-            }
-            float x[8];
-            if (p.interleaved) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) x[e] = y[e ^ 1];
-            } else {
-              uint4 other;
-              other.x = __shfl_sync(0xffffffffu, raw[u].x, sub * kLanes + plane);
-              other.y = __shfl_sync(0xffffffffu, raw[u].y, sub * kLanes + plane);
-              other.z = __shfl_sync(0xffffffffu, raw[u].z, sub * kLanes + plane);
-              other.w = __shfl_sync(0xffffffffu, raw[u].w, sub * kLanes + plane);
-              bf16x8_to_f32(other, x);
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = r * fmaf(y[e], A[e], rotated ? x[e] * B[e] : 0.f);
-          }
-          if (h >= n_heads) continue;
-          if (kFp8 && sec > 0) {
-            const float sc = p.scale[sec - 1];
-            const uint2 code = make_uint2(e4m3x2(y[0], y[1], sc) | (e4m3x2(y[2], y[3], sc) << 16),
-                                          e4m3x2(y[4], y[5], sc) | (e4m3x2(y[6], y[7], sc) << 16));
-            *reinterpret_cast<uint2*>(p.pool[sec - 1] + (slot * p.heads[1] + h) * D + 8 * li) = code;
+        const __nv_bfloat16* w = p.weight[sec];
+        float A[8], B[8];
+        {
+          float wo[8], wp[8];
+          if (w != nullptr) {
+            bf16x8_to_f32(*reinterpret_cast<const uint4*>(w + 8 * li), wo);
+            bf16x8_to_f32(*reinterpret_cast<const uint4*>(w + 8 * plane), wp);
           } else {
-            if (sec < 2)
-              out = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                               pack_bf16x2(y[6], y[7]));
-            __nv_bfloat16* dst = sec == 0 ? p.q_out + (t * p.heads[0] + h) * D
-                                          : reinterpret_cast<__nv_bfloat16*>(p.pool[sec - 1]) +
-                                                (slot * p.heads[1] + h) * D;
-            *reinterpret_cast<uint4*>(dst + 8 * li) = out;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) wo[e] = wp[e] = 1.f;
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float2 v = make_float2(1.f, 0.f);
+            if (rotated) v = turn[kInterleaved ? 4 * li + e / 2 : 8 * (low ? li : li - half) + e];
+            A[e] = wo[e] * v.x;
+            B[e] = (kInterleaved ? wo[e ^ 1] : wp[e]) * ((kInterleaved ? (e & 1) == 0 : low) ? -v.y : v.y);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kRopeBatch; ++u) {
+          const int h = h0 + u * kRows;
+          if (h - sub >= n_heads) break;
+          float y[8], x[8];
+          bf16x8_to_f32(cur[u], y);
+          float r = 1.f;
+          if (w != nullptr) {
+            float q2 = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) q2 = fmaf(y[e], y[e], q2);
+#pragma unroll
+            for (int o = 1; o < kLanes; o <<= 1) q2 += __shfl_xor_sync(0xffffffffu, q2, o);
+            r = rsqrtf(q2 * (1.f / D) + p.eps);
+          }
+          if constexpr (kInterleaved) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = y[e ^ 1];
+          } else {
+            uint4 o;
+            o.x = __shfl_sync(0xffffffffu, cur[u].x, sub * kLanes + plane);
+            o.y = __shfl_sync(0xffffffffu, cur[u].y, sub * kLanes + plane);
+            o.z = __shfl_sync(0xffffffffu, cur[u].z, sub * kLanes + plane);
+            o.w = __shfl_sync(0xffffffffu, cur[u].w, sub * kLanes + plane);
+            bf16x8_to_f32(o, x);
+          }
+          // (a select, not 0 * x: rows that do not turn keep their infinities)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = r * fmaf(y[e], A[e], rotated ? x[e] * B[e] : 0.f);
+          if (h >= n_heads) continue;
+          if (kFp8 && sec == 1) {
+            const float sc = p.scale[0];
+            *reinterpret_cast<uint2*>(p.pool[0] + (at * p.heads[1] + h) * D + 8 * li) =
+                make_uint2(e4m3x2(y[0], y[1], sc) | (e4m3x2(y[2], y[3], sc) << 16),
+                           e4m3x2(y[4], y[5], sc) | (e4m3x2(y[6], y[7], sc) << 16));
+          } else {
+            __nv_bfloat16* dst = sec == 0 ? p.q_out + ((int64_t)tok * p.heads[0] + h) * D
+                                          : reinterpret_cast<__nv_bfloat16*>(p.pool[0]) + (at * p.heads[1] + h) * D;
+            *reinterpret_cast<uint4*>(dst + 8 * li) =
+                make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                           pack_bf16x2(y[6], y[7]));
+          }
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < kRopeBatch; ++u) {
+          const int h = h0 + u * kRows;
+          if (h >= n_heads) break;
+          if constexpr (kFp8) {
+            float y[8];
+            bf16x8_to_f32(cur[u], y);
+            const float sc = p.scale[1];
+            *reinterpret_cast<uint2*>(p.pool[1] + (at * p.heads[1] + h) * D + 8 * li) =
+                make_uint2(e4m3x2(y[0], y[1], sc) | (e4m3x2(y[2], y[3], sc) << 16),
+                           e4m3x2(y[4], y[5], sc) | (e4m3x2(y[6], y[7], sc) << 16));
+          } else {
+            *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.pool[1]) + (at * p.heads[1] + h) * D +
+                                      8 * li) = cur[u];
           }
         }
       }
     }
+    if (!more) return;
   }
 }
 
-template <int D, bool kFp8>
-sgl_status run(RopeParams p, cudaStream_t stream) {
-  constexpr int kThreads = kRopeWarps * 32;
-  const int per_sm = kernel_blocks_per_sm<qk_norm_rope_store_kernel<D, kFp8>>(0, kThreads);
+template <int D, bool kFp8, bool kInterleaved>
+sgl_status run(const RopeParams& p, cudaStream_t stream) {
+  constexpr int kThreads = kRopeWarps * 32, kBatchRows = 32 / (D / 8) * kRopeBatch;
+  const int per_sm = kernel_blocks_per_sm<qk_norm_rope_store_kernel<D, kFp8, kInterleaved>>(0, kThreads);
   if (per_sm < 0) return SGL_ERR_CUDA;
-  constexpr int kRows = 32 / (D / 8);
-  const int groups = (p.heads[0] + kRows - 1) / kRows + 2 * ((p.heads[1] + kRows - 1) / kRows);
-  // A token's row groups are dealt to several warps while there are fewer
-  // tokens than the part has warps for; a warp keeps at least a batch of them
-  // unless that still leaves warps idle.
-  const int64_t warps = (int64_t)num_sms() * per_sm * kRopeWarps;
-  const int batches = (groups + kRopeBatch - 1) / kRopeBatch;
-  const int64_t most = (int64_t)p.n * batches < warps ? groups : batches;
-  int64_t parts = (warps + p.n - 1) / p.n;
-  if (parts > most) parts = most;
-  const int64_t cap = ((int64_t)num_sms() * per_sm + parts - 1) / parts;
+  // a token's batches are dealt to several blocks while there are fewer
+  // tokens than the part has warps for
+  const int batches = (p.heads[0] + kBatchRows - 1) / kBatchRows + 2 * ((p.heads[1] + kBatchRows - 1) / kBatchRows);
+  const int64_t resident = (int64_t)num_sms() * per_sm;
+  int64_t parts = (resident * kRopeWarps + p.n - 1) / p.n;
+  if (parts > batches) parts = batches;
   int64_t blocks = ((int64_t)p.n + kRopeWarps - 1) / kRopeWarps;
+  const int64_t cap = (resident + parts - 1) / parts;
   if (blocks > cap) blocks = cap;
-  qk_norm_rope_store_kernel<D, kFp8><<<dim3((unsigned)blocks, (unsigned)parts), kThreads, 0, stream>>>(p);
+  qk_norm_rope_store_kernel<D, kFp8, kInterleaved>
+      <<<dim3((unsigned)blocks, (unsigned)parts), kThreads, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? SGL_OK : SGL_ERR_CUDA;
+}
+
+template <int D>
+sgl_status run_d(const RopeParams& p, bool kv_fp8, cudaStream_t stream) {
+  if (kv_fp8) return p.interleaved ? run<D, true, true>(p, stream) : run<D, true, false>(p, stream);
+  return p.interleaved ? run<D, false, true>(p, stream) : run<D, false, false>(p, stream);
 }
 
 }  // namespace
@@ -265,8 +330,8 @@ sgl_status launch_qk_norm_rope_store(const RopeArgs& a, cudaStream_t stream) {
   p.heads[1] = a.num_kv_heads;
   p.scale[0] = a.k_scale;
   p.scale[1] = a.v_scale;
-  if (a.head_dim == 128) return a.kv_fp8 ? run<128, true>(p, stream) : run<128, false>(p, stream);
-  if (a.head_dim == 64) return a.kv_fp8 ? run<64, true>(p, stream) : run<64, false>(p, stream);
+  if (a.head_dim == 128) return run_d<128>(p, a.kv_fp8, stream);
+  if (a.head_dim == 64) return run_d<64>(p, a.kv_fp8, stream);
   return SGL_ERR_UNSUPPORTED;
 }
 

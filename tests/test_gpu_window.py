@@ -165,6 +165,21 @@ def test_extend_windows_across_blocks(window, sinks, fp8):
     assert_within(W.bf16_bits(case.extend()), want, terms, fp8, rows=tokens)
 
 
+# (Hq, Hkv, D, requests, window, sinks): enough tiles for every SM, so that no
+# tile's keys are dealt to several CTAs (the shapes above are dealt)
+MANY = [(16, 16, 64, 12, 200, 3), (40, 20, 128, 9, 70, 0), (96, 32, 64, 5, 300, 130)]
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("shape", MANY, ids=lambda s: f"{s[0]}q{s[1]}kv{s[2]}d_b{s[3]}")
+def test_extend_of_many_tiles(shape, fp8):
+    Hq, Hkv, D, n, window, sinks = shape
+    g = np.random.default_rng(n)
+    case = Case(attention_case(n, Hq=Hq, Hkv=Hkv, D=D, prefix=g.integers(0, 400, n).tolist(),
+                               ext=g.integers(0, 25, n).tolist(), window=window, sinks=sinks, fp8=fp8))
+    assert_within(W.bf16_bits(case.extend()), *case.want_extend(), fp8, what=str(shape))
+
+
 def test_extend_full_window_equals_extend():
     """With a window over everything the call is sgl_extend_attention over the stored suffix."""
     case = Case(attention_case(21, Hq=8, Hkv=4, D=128, prefix=[130, 0], ext=[70, 200], window=1000, sinks=0))
