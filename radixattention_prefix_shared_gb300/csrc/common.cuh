@@ -201,23 +201,6 @@ SGL_DEV bool mbar_wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abo
 SGL_DEV void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 SGL_DEV void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// ----------------------------------------------------------------- clusters
-
-// Barrier over the cluster's threads; shared memory written before it is
-// visible to the whole cluster after it.
-SGL_DEV void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// The float at this CTA's shared-memory address `addr` in the cluster's CTA `rank`.
-SGL_DEV float ld_cluster_f32(uint32_t addr, int32_t rank) {
-  uint32_t there;
-  float v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(there) : "memory");
-  return v;
-}
-
 // ----------------------------------------------------------------- named barriers
 
 SGL_DEV void named_bar_sync(uint32_t id, uint32_t nthreads) {

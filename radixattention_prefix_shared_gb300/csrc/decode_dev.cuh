@@ -147,16 +147,13 @@ inline size_t ws_layout(int32_t batch, int64_t max_items, int32_t Hkv, int32_t G
 // [0, sinks) and [len - window, len); in order they are its visible keys
 // 0 .. n - 1, n = min(len, sinks + window), and visible key i sits at
 // position i below `sinks` and at i + (len - n) from there on.  A request's
-// visible keys are cut into ns <= n_splits near-equal runs of at most
-// Params::chunk keys, taken by n_splits CTAs: clusters of `cluster` of them
-// merge their runs' states through distributed shared memory, and where a
-// request's runs fill more than one cluster the clusters' states (item r *
-// n_states + c) go to the workspace for the combine.
+// visible keys are cut into at most n_splits near-equal runs; run s of request
+// r is item r * n_splits + s.
 struct Window {
   int32_t sinks;
   int32_t max_keys;  // min(max_seq_len, sinks + window)
   int32_t max_seq;   // longer requests are cut to it
-  int32_t n_splits, cluster, n_states;  // n_splits = cluster * n_states
+  int32_t n_splits;  // runs of at most Params::chunk visible keys
 };
 struct WindowRun {
   int32_t len, n;     // keys of the request, and how many its query sees
@@ -952,93 +949,6 @@ struct SplitRing {
   static constexpr size_t bytes() { return (size_t)kDepth * 2 * kTileB * D * 2; }
 };
 
-// Most CTAs of a cluster that merge their states through distributed shared
-// memory (the portable limit).
-constexpr int kMaxCluster = 8;
-
-// The end of a sliding-window run.  red holds the warps' states: acc
-// [warp][G][D], then m and l [warp][G].  Without spans a head's keys are spread
-// over the warps, whose states are merged behind them first, so that a CTA
-// has one state a query head (with spans warp w's is head kvh0 + w's).  The
-// cluster's CTAs then read one another's states, each doing its share of the
-// (head, query head, dim) outputs.  A state without keys has m = -inf and
-// weighs nothing; the first CTA of a cluster always has keys.
-template <int D, int G, bool kSpans>
-SGL_DEV void window_publish(const Params& p, float* red, int r, int kvh0, int32_t ns, int32_t run) {
-  const int tid = threadIdx.x;
-  const int32_t cs = p.win.cluster, rank = run % cs, state = run / cs;
-  constexpr int kRows = (kSpans ? kWarps : 1) * G;  // query heads of the unit
-  const bool single = ns <= cs;                     // the cluster holds the whole request
-  auto put = [&](int idx, float M, float L, float A) {
-    const int64_t row = (int64_t)kvh0 * G + idx / D;  // query head
-    if (single) {
-      p.out[((int64_t)r * p.Hq + row) * D + idx % D] = __float2bfloat16_rn(A * (p.v_scale / L));
-    } else {
-      const int64_t slot = ((int64_t)r * p.win.n_states + state) * p.Hq + row;
-      p.ws.part_acc[slot * D + idx % D] = A;
-      if (idx % D == 0) p.ws.part_ml[slot] = make_float2(M, L);
-    }
-  };
-  float* acc = red;
-  float* m = red + kWarps * G * D;
-  float* l = m + kWarps * G;
-  if constexpr (!kSpans) {
-    float* const out = l + kWarps * G;
-    for (int idx = tid; idx < G * D; idx += kThreads) {
-      const int h = idx / D;
-      float M = -INFINITY, L = 0.f, A = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, m[w * G + h]);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = M == -INFINITY ? 0.f : ex2(m[w * G + h] - M);
-        L += l[w * G + h] * f;
-        A += acc[w * G * D + idx] * f;
-      }
-      if (cs == 1) {
-        put(idx, M, L, A);
-      } else {
-        out[idx] = A;
-        if (idx % D == 0) out[G * D + h] = M, out[G * D + G + h] = L;
-      }
-    }
-    acc = out;
-    m = out + G * D;
-    l = m + G;
-  } else {
-    if (cs == 1)
-      for (int idx = tid; idx < kRows * D; idx += kThreads) put(idx, m[idx / D], l[idx / D], acc[idx]);
-  }
-  if (cs == 1) return;
-  cluster_sync();
-  const int32_t live = min(cs, ns - state * cs);  // CTAs of the cluster that have a run
-  const uint32_t acc_a = smem_u32(acc), m_a = smem_u32(m), l_a = smem_u32(l);
-  for (int idx = rank * kThreads + tid; idx < kRows * D; idx += cs * kThreads) {
-    float mv[kMaxCluster], lv[kMaxCluster], av[kMaxCluster];
-#pragma unroll
-    for (int c = 0; c < kMaxCluster; ++c) {
-      mv[c] = -INFINITY;
-      lv[c] = av[c] = 0.f;
-      if (c < live) {
-        mv[c] = ld_cluster_f32(m_a + 4 * (idx / D), c);
-        lv[c] = ld_cluster_f32(l_a + 4 * (idx / D), c);
-        av[c] = ld_cluster_f32(acc_a + 4 * idx, c);
-      }
-    }
-    float M = mv[0], L = 0.f, A = 0.f;
-#pragma unroll
-    for (int c = 1; c < kMaxCluster; ++c) M = fmaxf(M, mv[c]);
-#pragma unroll
-    for (int c = 0; c < kMaxCluster; ++c) {
-      const float f = ex2(mv[c] - M);
-      L += lv[c] * f;
-      A += av[c] * f;
-    }
-    put(idx, M, L, A);
-  }
-  cluster_sync();  // no CTA leaves while another reads its states
-}
-
 // Split-KV work units run by one group of kWarps warps (kThreads threads):
 // gtid is the thread's index in the group, sync() the group's barrier,
 // next() (called by gtid 0) the group's next unit, n_units the end of the
@@ -1100,10 +1010,10 @@ SGL_DEV void split_units(const Params& p, uint8_t* smem, int32_t* s_item, int gt
       const int32_t row = p.req_pool_idx[r];
       const WindowRun w(p.win, p.chunk, p.seq_lens[r]);
       ns = w.ns;
-      if (run - run % p.win.cluster >= ns) return;  // the whole cluster has no run
+      if (run >= ns) return;
       const int32_t base = w.n / ns, rem = w.n % ns;
       const int32_t t0 = run * base + min(run, rem);
-      n = run < ns ? base + (run < rem ? 1 : 0) : 0;
+      n = base + (run < rem ? 1 : 0);
       const int32_t* rtt = p.req_to_token + (int64_t)row * p.rtt_stride;
       for (int i = tid; i < n; i += kThreads)
         s_slots[i] = rtt[t0 + i + (t0 + i >= p.win.sinks ? w.len - w.n : 0)];
@@ -1187,10 +1097,6 @@ SGL_DEV void split_units(const Params& p, uint8_t* smem, int32_t* s_item, int gt
     float* red_l = red_m + kWarps * G;
     st.publish(red_acc, red_m, red_l);
     sync();
-    if constexpr (kWindow) {
-      window_publish<D, G, kSpans>(p, s_red, r, kvh0, ns, item % p.win.n_splits);
-      return;
-    }
     const bool single = ns == 1 && !grouped;
     // (head, query head, dim) outputs of the unit: kWarps heads with spans
     constexpr int kHeads = kSpans ? kWarps : 1;

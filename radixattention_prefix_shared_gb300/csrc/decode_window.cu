@@ -14,9 +14,15 @@ using namespace dec;
 
 namespace {
 
-// Runs are made as short as it takes to give the part kFillUnits CTAs, but no
+// Runs are made as short as it takes to give the part kFillUnits CTAs (four
+// waves: the runs' lengths vary and a CTA lasts as long as its run), but no
 // shorter than kMinRun keys and no longer than kItemMax (the slot run buffer).
-constexpr int kFillUnits = 456;
+// Measured: 64 requests of 32 KV heads over an e4m3 pool, window 1,024: 102 us
+// at 456 CTAs, 96.9 at 912, 93.2 at 1,824; 93.2 us with runs of 256 keys, 95.1
+// with 512; one request of 8 KV heads, window 4,096: 12.6 us with runs of 256
+// keys or 128, 16.3 with 512.  Runs merged by clusters of up to 8 CTAs
+// through distributed shared memory took as long as the combine (12.6 us).
+constexpr int kFillUnits = 1824;
 constexpr int kMinRun = 256;
 
 int32_t splits_for(int64_t units, int32_t keys) {
@@ -27,27 +33,25 @@ int32_t splits_for(int64_t units, int32_t keys) {
   return s > least ? s : least;
 }
 
-// Virtual KV heads, and the runs and clusters a request is cut into.
+// Virtual KV heads, and the runs a request is cut into.
 struct Shape {
   int32_t split, Hkv, G;
-  int32_t keys, chunk, n_splits, cluster, n_states;
-  Shape(int32_t batch, int32_t max_seq_len, int32_t window, int32_t sinks, int32_t Hq, int32_t Hkv_pool) {
+  int32_t keys, n_splits, chunk;
+  Shape(int32_t batch, int32_t max_seq_len, int32_t window, int32_t sinks, int32_t Hq, int32_t Hkv_pool,
+        bool kv_fp8) {
     split = kv_split_for(Hq / Hkv_pool);
     Hkv = Hkv_pool * split;
     G = Hq / Hkv;
     const int64_t seen = (int64_t)window + sinks;
     keys = (int32_t)(seen < max_seq_len ? seen : max_seq_len);
-    const int64_t units = (int64_t)batch * Hkv;
-    const int32_t runs = splits_for(units, keys);
-    cluster = units * runs > 2 * kFillUnits ? 1 : (runs < kMaxCluster ? runs : kMaxCluster);
-    n_states = (runs + cluster - 1) / cluster;
-    n_splits = cluster * n_states;
+    const int64_t units = (int64_t)batch * (spans_for(Hkv, split, kv_fp8) ? Hkv / kWarps : Hkv);
+    n_splits = splits_for(units, keys);
     chunk = (keys + n_splits - 1) / n_splits;
   }
 };
 
 size_t ws_bytes(int32_t batch, const Shape& s, int32_t D, void* base, Ws* ws) {
-  const size_t n = s.n_states > 1 ? (size_t)batch * s.n_states * s.Hkv * s.G : 0;
+  const size_t n = s.n_splits > 1 ? (size_t)batch * s.n_splits * s.Hkv * s.G : 0;
   const size_t o_acc = align256(sizeof(float2) * n);
   if (ws != nullptr) {
     char* b = static_cast<char*>(base);
@@ -62,13 +66,10 @@ __global__ void __launch_bounds__(kThreads, (split_min_blocks<D, G, LPT, KV>()))
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int32_t s_item[2];
   grid_dep_launch();
-  // a cluster's CTAs are the runs of one request and KV head; without
-  // clusters the KV heads come fastest, so that the CTAs next to each other
-  // gather the heads of the same slots
-  const uint32_t heads = kSpans ? p.Hkv / kWarps : p.Hkv, cs = p.win.cluster;
-  const uint32_t group = blockIdx.x / cs;
-  const int32_t y = (int32_t)(group % heads);
-  const int32_t item = (int32_t)(group / heads * cs + blockIdx.x % cs);
+  // KV heads fastest: the CTAs next to each other gather the heads of the same
+  // slots
+  const uint32_t heads = kSpans ? p.Hkv / kWarps : p.Hkv;
+  const int32_t item = (int32_t)(blockIdx.x / heads), y = (int32_t)(blockIdx.x % heads);
   bool taken = false;
   split_units<D, G, LPT, KV, 0, kSpans, true>(
       p, smem, s_item, threadIdx.x, 1, [] { __syncthreads(); },
@@ -80,10 +81,10 @@ __global__ void __launch_bounds__(kThreads, (split_min_blocks<D, G, LPT, KV>()))
       [&](int32_t) { return kSpans ? kWarps * y : y; }, [&](int32_t) { return item; });
 }
 
-// Merges the clusters' states of requests with more than one: a block a
-// (request, query head), its warps taking the states in turn, four loads of
-// each in flight (one warp reading 33 states one after the other took 14 us,
-// longer than the split kernel).
+// Merges the states of requests with more than one run: a block a (request,
+// query head), its warps taking the runs in turn, four loads of each in flight
+// (one warp reading 33 runs one after the other took 14 us, longer than the
+// split kernel).
 template <int D>
 __global__ void __launch_bounds__(128) window_combine_kernel(Params p) {
   constexpr int E = D / 32, kBatch = 4;
@@ -91,11 +92,10 @@ __global__ void __launch_bounds__(128) window_combine_kernel(Params p) {
   __shared__ float s_acc[4][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq;
-  const int32_t runs = WindowRun(p.win, p.chunk, p.seq_lens[r]).ns;
-  const int32_t ns = (runs + p.win.cluster - 1) / p.win.cluster;
-  if (ns <= 1) return;  // a single cluster wrote the output (none: no keys)
+  const int32_t ns = WindowRun(p.win, p.chunk, p.seq_lens[r]).ns;
+  if (ns <= 1) return;  // a single run wrote the output (none: no keys)
   grid_dep_wait();      // launched dependent on the split kernel
-  const int64_t first = (int64_t)r * p.win.n_states * p.Hq + h, step = p.Hq;
+  const int64_t first = (int64_t)r * p.win.n_splits * p.Hq + h, step = p.Hq;
   float M = -INFINITY, L = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
@@ -144,29 +144,14 @@ __global__ void __launch_bounds__(128) window_combine_kernel(Params p) {
 template <int D, int G, int LPT, typename KV, bool kSpans>
 sgl_status launch(const Params& prm, cudaStream_t stream) {
   constexpr size_t smem = SplitRing<KV, G>::template bytes<D>() + kItemMax * sizeof(int32_t);
-  static_assert((kWarps + 1) * G * (D + 2) * sizeof(float) <= SplitRing<KV, G>::template bytes<D>(),
-                "the warps' states and the CTA's must fit in the ring");
+  static_assert(kWarps * G * (D + 2) * sizeof(float) <= SplitRing<KV, G>::template bytes<D>(),
+                "reduction scratch must fit in the ring");
   if (kernel_blocks_per_sm<decode_window_kernel<D, G, LPT, KV, kSpans>>((int)smem, kThreads) < 0) return SGL_ERR_CUDA;
   const int64_t heads = kSpans ? prm.Hkv / kWarps : prm.Hkv;
   const int64_t ctas = (int64_t)prm.batch * prm.win.n_splits * heads;
   if (ctas > 0x7fffffff) return SGL_ERR_UNSUPPORTED;
-  if (prm.win.cluster == 1) {
-    decode_window_kernel<D, G, LPT, KV, kSpans><<<(unsigned)ctas, kThreads, smem, stream>>>(prm);
-  } else {
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim = {(unsigned)prm.win.cluster, 1, 1};
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, decode_window_kernel<D, G, LPT, KV, kSpans>, prm) != cudaSuccess)
-      return SGL_ERR_CUDA;
-  }
-  if (prm.win.n_states > 1) {
+  decode_window_kernel<D, G, LPT, KV, kSpans><<<(unsigned)ctas, kThreads, smem, stream>>>(prm);
+  if (prm.win.n_splits > 1) {
     const int64_t rows = (int64_t)prm.batch * prm.Hq;
     if (launch_dependent(window_combine_kernel<D>, dim3((unsigned)rows), dim3(128), 0, stream, prm) != cudaSuccess)
       return SGL_ERR_CUDA;
@@ -211,14 +196,16 @@ sgl_status run_g(int G, const Params& prm, cudaStream_t stream) {
 size_t decode_window_workspace_bytes(int32_t batch, int32_t max_seq_len, int32_t window, int32_t sinks, int32_t Hq,
                                      int32_t Hkv, int32_t D) {
   if (batch <= 0 || max_seq_len <= 0 || window <= 0 || sinks < 0 || Hkv <= 0 || Hq < Hkv) return 256;
-  const Shape s(batch, max_seq_len, window, sinks, Hq, Hkv);
-  return 256 + ws_bytes(batch, s, D, nullptr, nullptr);
+  // (either pool type)
+  const size_t a = ws_bytes(batch, Shape(batch, max_seq_len, window, sinks, Hq, Hkv, false), D, nullptr, nullptr);
+  const size_t b = ws_bytes(batch, Shape(batch, max_seq_len, window, sinks, Hq, Hkv, true), D, nullptr, nullptr);
+  return 256 + (a > b ? a : b);
 }
 
 sgl_status launch_decode_window(const DecodeArgs& a, cudaStream_t stream) {
   if (a.batch == 0) return SGL_OK;
   if (decode_shape_supported(a.num_q_heads, a.num_kv_heads) != SGL_OK) return SGL_ERR_UNSUPPORTED;
-  const Shape s(a.batch, a.max_seq_len, a.window, a.sinks, a.num_q_heads, a.num_kv_heads);
+  const Shape s(a.batch, a.max_seq_len, a.window, a.sinks, a.num_q_heads, a.num_kv_heads, a.kv_fp8);
   Params prm = {};
   if (ws_bytes(a.batch, s, a.head_dim, a.workspace, &prm.ws) > a.workspace_bytes) return SGL_ERR_WORKSPACE;
   prm.q = static_cast<const __nv_bfloat16*>(a.q);
@@ -237,7 +224,7 @@ sgl_status launch_decode_window(const DecodeArgs& a, cudaStream_t stream) {
   prm.chunk = s.chunk;
   prm.scale_log2 = a.sm_scale * 1.4426950408889634f * (a.kv_fp8 ? a.k_scale : 1.f);
   prm.v_scale = a.kv_fp8 ? a.v_scale : 1.f;
-  prm.win = Window{a.sinks, s.keys, a.max_seq_len, s.n_splits, s.cluster, s.n_states};
+  prm.win = Window{a.sinks, s.keys, a.max_seq_len, s.n_splits};
   if (a.head_dim == 128)
     return a.kv_fp8 ? run_g<128, uint8_t>(s.G, prm, stream) : run_g<128, __nv_bfloat16>(s.G, prm, stream);
   if (a.head_dim == 64)

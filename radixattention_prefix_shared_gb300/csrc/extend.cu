@@ -81,6 +81,7 @@ sgl_status launch_cascade_groups(const GroupArgs& a, cudaStream_t stream, bool d
   prm.g = g;
   prm.tpt = BM / g;
   prm.rows_used = prm.tpt * g;
+  prm.g_inv = row_token_inv(g);
   // e4m3: scores in units of the widened codes (code * 2^-8) times the K
   // scale; the states' P.V rows are left in code units (the decode combine
   // applies the V scale)

@@ -57,6 +57,8 @@
 // in-flight copies and MMAs, frees TMEM and returns.
 #pragma once
 
+#include <cuda_fp8.h>
+
 #include "common.cuh"
 #include "launch.h"
 
@@ -68,6 +70,22 @@ constexpr int BM = 128;  // rows per Q tile
 constexpr int BN = 128;  // keys per KV block
 // e4m3 codes widened by bit placement hold code * 2^-8
 constexpr float kFp8Operand = 256.0f;
+// The sliding-window extend widens them with the hardware's conversion instead
+// (code as f16, exact): two instructions where placing the bits of four codes
+// takes seven.  Its producers are issue-limited: 64 x 256 tokens, window 2,048,
+// 628 -> 604 us.  (A NaN code stays NaN; placed, it reads as +-480.)
+constexpr float kFp8OperandWindow = 1.0f;
+template <bool kWindow>
+SGL_DEV void widen_codes(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (kWindow) {
+    const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
+    const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
+    lo = *reinterpret_cast<const uint32_t*>(&a);
+    hi = *reinterpret_cast<const uint32_t*>(&b);
+  } else {
+    e4m3x4_to_f16x2_scaled(w, lo, hi);
+  }
+}
 // Q tiles a cascade-group CTA holds over a bf16 pool
 constexpr int kGroupTilesBf16 = 1;
 // e4m3 pools: f16 ring stages at D = 128 (twice as many at D = 64), raw code
@@ -253,6 +271,7 @@ struct Params {
   const int32_t* extend_lens;
   __nv_bfloat16* out;
   int32_t Hq, Hkv, g, tpt, rows_used;
+  uint32_t g_inv;  // row_token
   float scale_log2;
   // multiplies the normalised output (extend) or the unnormalised P.V rows
   // (group mode); 1 on a bf16 pool
@@ -320,6 +339,20 @@ struct WindowKeys {
   SGL_DEV int32_t first(int32_t P) const { return max(0, P - window + 1) - lo + n_first - i0; }
 };
 
+// Token of row `row` < 128 of a Q tile, row / g, by the 16-bit reciprocal g_inv
+// = ceil(2^16 / g): exact, since its error of less than g / 2^16 a row stays
+// below 1 / g over 128 rows.  (The compiler's division by a runtime g made the
+// Q copies and the output's stores issue-bound.)
+__host__ __device__ inline uint32_t row_token_inv(int32_t g) { return (65536u + (uint32_t)g - 1u) / (uint32_t)g; }
+SGL_DEV int row_token(const Params& p, int row) { return (int)(((uint32_t)row * p.g_inv) >> 16); }
+
+// The lowest n bits (none for n <= 0, all from 32 on).
+SGL_DEV uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u); }
+// Bit c: column c < hi with c < sinks or c >= first.
+SGL_DEV uint32_t window_mask(int hi, int sinks, int first) {
+  return low_bits(hi) & (low_bits(sinks) | ~low_bits(first));
+}
+
 // byte offset of 16-byte chunk `ci` (0..7) of row `row` inside one
 // 128-row x 128-byte swizzled chunk
 SGL_DEV uint32_t sw128(int row, int ci) { return row * 128 + ((ci ^ (row & 7)) << 4); }
@@ -360,16 +393,26 @@ SGL_DEV void warp_store_rows(uint32_t stage, int row0, DstFn dst) {
   }
 }
 
-// both tiles' staged rows fit in the Q tiles and the ring, below the
-// barriers
+// both tiles' staged rows (bf16 output, or fp32 states of a run) fit in the Q
+// tiles and the ring, below the barriers
 template <int D, bool kFp8>
 constexpr bool staging_fits() {
   using C = Cfg<D, kFp8>;
-  return 256 * out_stride<D>() <= (2 + C::kStages) * C::kTileBytes;
+  return 256 * out_stride<D>() <= (2 + C::kStages) * C::kTileBytes &&
+         256 * (4 * D + 16) <= (2 + C::kStages) * C::kTileBytes;
 }
 static_assert(staging_fits<128, false>() && staging_fits<64, false>() && staging_fits<128, true>() &&
                   staging_fits<64, true>(),
               "epilogue staging");
+
+// Where a run's fp32 P.V row of row rr of tile t goes (nullptr: no query).
+template <int D>
+SGL_DEV uint8_t* state_row(const Params& p, int q0, int t, int rr, int e, int off, int kvh, int run) {
+  const int rt = row_token(p, rr), tok = q0 + t * p.tpt + rt;
+  if (rr >= p.rows_used || tok >= e) return nullptr;
+  const int64_t row = (int64_t)(off + tok) * p.Hq + (int64_t)kvh * p.g + (rr - rt * p.g);
+  return reinterpret_cast<uint8_t*>(p.part_acc + (row * p.n_runs + run) * D);
+}
 
 // Whether the softmax warps, idle until the first S, load the Q tiles (so
 // the producers start on K/V at once).  Always on bf16 pools; on e4m3 pools
@@ -387,18 +430,20 @@ constexpr bool q_by_softmax() { return !kFp8 || kGroup; }
 // queries.
 template <int D, bool kGroup, int kTiles>
 SGL_DEV void issue_q_copies(const Params& p, uint32_t sQ_a, int ltid, int nthreads, int kvh, int e, int mbeg,
-                            int q0, int off) {
+                            int q0, int off, int tiles) {
   using C = Cfg<D, false>;
   const int ci = ltid & 7, step = nthreads >> 3;
 #pragma unroll
   for (int t = 0; t < kTiles; ++t) {
+    if (t >= tiles) break;
     for (int row = ltid >> 3; row < 128; row += step) {
-      const int tok = q0 + t * p.tpt + row / p.g;
+      const int rt = row_token(p, row), rh = row - rt * p.g;
+      const int tok = q0 + t * p.tpt + rt;
       bool valid = row < p.rows_used && tok < e;
       // the query row: suffix token off+tok, or member tok's decode query
       int64_t qrow = valid ? (kGroup ? (int64_t)p.members[mbeg + tok] : (int64_t)(off + tok)) : 0;
       if (kGroup && (qrow < 0 || qrow >= p.batch)) valid = false, qrow = 0;
-      const __nv_bfloat16* src = p.q + (qrow * p.Hq + (int64_t)kvh * p.g + row % p.g) * D + ci * 8;
+      const __nv_bfloat16* src = p.q + (qrow * p.Hq + (int64_t)kvh * p.g + rh) * D + ci * 8;
 #pragma unroll
       for (int c = 0; c < C::kChunks; ++c)
         cp_async_16(sQ_a + t * C::kTileBytes + c * C::kChunkBytes + sw128(row, ci),
@@ -432,13 +477,13 @@ SGL_DEV void widen_q_in_place(uint32_t sQ_a, int ltid, int nthreads) {
 }
 
 // The Q tiles loaded by the softmax warps (ltid = thread index among the
-// nthreads of them), signalled on q_full: on a bf16 pool each thread's
+// nthreads of them; the first `tiles` tiles only), signalled on q_full: on a bf16 pool each thread's
 // arrival fires when its copies land; on an e4m3 pool each thread waits for
 // its own copies, widens them and orders them for the tensor core first.
 template <int D, bool kGroup, bool kFp8, int kTiles>
 SGL_DEV void load_q_tiles(const Params& p, uint32_t sQ_a, uint64_t* q_full, int ltid, int nthreads, int kvh,
-                          int e, int mbeg, int q0, int off) {
-  issue_q_copies<D, kGroup, kTiles>(p, sQ_a, ltid, nthreads, kvh, e, mbeg, q0, off);
+                          int e, int mbeg, int q0, int off, int tiles) {
+  issue_q_copies<D, kGroup, kTiles>(p, sQ_a, ltid, nthreads, kvh, e, mbeg, q0, off, tiles);
   if constexpr (kFp8) {
     cp_async_wait_all();
     widen_q_in_place<D>(sQ_a, ltid, nthreads);
@@ -462,7 +507,8 @@ SGL_DEV void load_q_tiles(const Params& p, uint32_t sQ_a, uint64_t* q_full, int 
 template <int D, bool kGroup, bool kWindow, class Keys>
 SGL_DEV void produce_fp8(const Params& p, uint32_t sQ_a, uint8_t* sKV, uint8_t* sRaw, Bars* bars,
                          int ptid, int r, int kvh, int e, int mbeg, int q0, int pfx, int q_end, int nb_pre, int nb,
-                         int off, const Keys& wk) {
+                         int off, const Keys& wk,
+                         int32_t table_row) {
   const uint32_t sRaw_a = smem_u32(sRaw);
   using C = Cfg<D, true>;
   using R = Roles<true>;
@@ -495,7 +541,7 @@ SGL_DEV void produce_fp8(const Params& p, uint32_t sQ_a, uint8_t* sKV, uint8_t* 
   const int32_t* rtt =
       kGroup ? p.req_to_token + (int64_t)p.req_pool_idx[p.members[mbeg]] * p.rtt_stride +
                    p.group_start[r]
-             : p.req_to_token + (int64_t)p.req_pool_idx[r] * p.rtt_stride;
+             : p.req_to_token + (int64_t)(kWindow ? table_row : p.req_pool_idx[r]) * p.rtt_stride;
   // position of row `row` of block b in the row of req_to_token, or -1 when
   // the row holds no key (past the prefix, or past this CTA's last query)
   auto key_pos = [&](int b, int row) {
@@ -613,10 +659,10 @@ SGL_DEV void produce_fp8(const Params& p, uint32_t sQ_a, uint8_t* sKV, uint8_t* 
           if (i0 + j >= C::kRawRows || rr >= C::kUnitRows) break;
           const int row = C::kUnitRows * part + rr;
           uint4 lo, hi;
-          e4m3x4_to_f16x2_scaled(w[j].x, lo.x, lo.y);
-          e4m3x4_to_f16x2_scaled(w[j].y, lo.z, lo.w);
-          e4m3x4_to_f16x2_scaled(w[j].z, hi.x, hi.y);
-          e4m3x4_to_f16x2_scaled(w[j].w, hi.z, hi.w);
+          widen_codes<kWindow>(w[j].x, lo.x, lo.y);
+          widen_codes<kWindow>(w[j].y, lo.z, lo.w);
+          widen_codes<kWindow>(w[j].z, hi.x, hi.y);
+          widen_codes<kWindow>(w[j].w, hi.z, hi.w);
           *reinterpret_cast<uint4*>(dst0 + sw128(row, piece)) = lo;
           *reinterpret_cast<uint4*>(dst0 + sw128(row, piece + 1)) = hi;
         }
@@ -674,6 +720,8 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz, int run = 0) 
   const int q0 = bx * kTiles * p.tpt;                         // first token of this tile
   const int pfx = kGroup ? p.group_len[r] : p.prefix_lens[r];  // keys read from the pool
   const int q_end = min(e, q0 + kTiles * p.tpt);
+  // (with the lengths: the producers' first slots wait for it)
+  const int32_t table_row = kWindow ? p.req_pool_idx[r] : 0;
   const WindowKeys<kRuns> wk(p, pfx + q0, pfx + q_end, run);  // kWindow only
   const int nb_pre = ((kWindow ? wk.n : pfx) + BN - 1) / BN;
   const int nb = nb_pre + (kGroup || kWindow ? 0 : (q_end + BN - 1) / BN);
@@ -752,7 +800,8 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz, int run = 0) 
     if constexpr (R::kFullRows) {
     // ------------------------------------------------------------ softmax (whole rows)
     if constexpr (kQSoft)
-      load_q_tiles<D, kGroup, kFp8, kTiles>(p, sQ_a, &bars->q_full, tid, kQThreads, kvh, e, mbeg, q0, off);
+      load_q_tiles<D, kGroup, kFp8, kTiles>(p, sQ_a, &bars->q_full, tid, kQThreads, kvh, e, mbeg, q0, off,
+                                                kRuns && !two_tiles ? 1 : kTiles);
     // warp w: Q tile t = w / 4, TMEM lane quarter q = w % 4 (rows 32q..);
     // every thread owns one row: all 128 keys of a block, all D columns of O.
     // A row whose block sum breaks the bound moves its own reference (the
@@ -764,7 +813,7 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz, int run = 0) 
     const uint32_t lane_off = (uint32_t)(q * 32) << 16;
     const uint32_t tS = tmem + lane_off + col_s(t);
     const uint32_t tO = tmem + lane_off + col_o<kTiles>(t);
-    const int tok = q0 + t * p.tpt + row / p.g;
+    const int tok = q0 + t * p.tpt + row_token(p, row);
     const bool row_valid = row < p.rows_used && tok < e;
     const int tok_i = row_valid ? tok : (1 << 30);  // padding rows see every key
     // kWindow: the row's bounds in the CTA's key list (padding rows: every key)
@@ -798,15 +847,20 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz, int run = 0) 
         for (int j = 0; j < BN / 32; ++j)
           tmem_ld32(tS + 32 * j, *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * j]));
         tmem_wait_ld();
-        if (limit < BN) {
+        if constexpr (kWindow) {
+          if (limit < BN || (w_first > 0 && w_first > w_sinks)) {
+#pragma unroll
+            for (int w = 0; w < BN / 32; ++w) {
+              const uint32_t seen = window_mask(limit - 32 * w, w_sinks - 32 * w, w_first - 32 * w);
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (!(seen & (1u << c))) sr[32 * w + c] = __float_as_uint(-INFINITY);
+            }
+          }
+        } else if (limit < BN) {
 #pragma unroll
           for (int c = 0; c < BN; ++c)
             if (c >= limit) sr[c] = __float_as_uint(-INFINITY);
-        }
-        if (kWindow && w_first > 0 && w_first > w_sinks) {
-#pragma unroll
-          for (int c = 0; c < BN; ++c)
-            if (c >= w_sinks && c < w_first) sr[c] = __float_as_uint(-INFINITY);
         }
       };
       // P of the row's 128 keys against reference m_use, packed in place
@@ -894,22 +948,21 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz, int run = 0) 
         }
         if (wr) p.part_ml[ent] = make_float2(m_ref, l);
       } else if (kRuns) {
-        // the run's state, P.V rows in units of o_scale
-        const int64_t ent =
-            ((int64_t)(off + tok) * p.Hq + (int64_t)kvh * p.g + row % p.g) * p.n_runs + run;
+        // the run's state: P.V rows through shared memory, in units of o_scale
+        constexpr int kStride = 4 * D + 16;
+        const uint32_t stage = smem_a + t * 128 * kStride;
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) {
           uint32_t o[32];
           tmem_ld32(tO + 32 * j, o);
           tmem_wait_ld();
-          if (row_valid && l > 0.f) {
-            float4* d4 = reinterpret_cast<float4*>(p.part_acc + ent * D + 32 * j);
 #pragma unroll
-            for (int v = 0; v < 8; ++v)
-              d4[v] = make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
-                                  __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
-          }
+          for (int v = 0; v < 8; ++v)
+            st_shared_v4(stage + row * kStride + 128 * j + 16 * v, o[4 * v], o[4 * v + 1], o[4 * v + 2],
+                         o[4 * v + 3]);
         }
+        warp_store_rows<4 * D, kStride>(stage, q * 32, [&](int rr) { return state_row<D>(p, q0, t, rr, e, off, kvh, run); });
+        const int64_t ent = ((int64_t)(off + tok) * p.Hq + (int64_t)kvh * p.g + (row - row_token(p, row) * p.g)) * p.n_runs + run;
         if (row_valid) p.part_ml[ent] = make_float2(m_ref, l);
       } else {
         const float inv = l > 0.f ? (kFp8 ? p.o_scale : 1.f) / l : 0.f;
@@ -930,10 +983,10 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz, int run = 0) 
                          w[4 * v + 3]);
         }
         warp_store_rows<2 * D, kStride>(stage, q * 32, [&](int rr) -> uint8_t* {
-          const int tk = q0 + t * p.tpt + rr / p.g;
+          const int rt = row_token(p, rr), tk = q0 + t * p.tpt + rt;
           if (rr >= p.rows_used || tk >= e) return nullptr;
           return reinterpret_cast<uint8_t*>(p.out +
-                                            ((int64_t)(off + tk) * p.Hq + (int64_t)kvh * p.g + rr % p.g) * D);
+                                            ((int64_t)(off + tk) * p.Hq + (int64_t)kvh * p.g + (rr - rt * p.g)) * D);
         });
       }
     }
@@ -942,7 +995,8 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz, int run = 0) 
     if constexpr (!R::kFullRows) {
     // ------------------------------------------------------------ softmax
     if constexpr (kQSoft)
-      load_q_tiles<D, kGroup, kFp8, kTiles>(p, sQ_a, &bars->q_full, tid, kQThreads, kvh, e, mbeg, q0, off);
+      load_q_tiles<D, kGroup, kFp8, kTiles>(p, sQ_a, &bars->q_full, tid, kQThreads, kvh, e, mbeg, q0, off,
+                                                kRuns && !two_tiles ? 1 : kTiles);
     // warp w: Q tile t, key-column half h, TMEM lane quarter q (rows 32q..)
     const int t = (warp >> 2) % kTiles, h = warp / (4 * kTiles), q = warp & 3;
     const int row = q * 32 + lane;
@@ -952,7 +1006,7 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz, int run = 0) 
     const uint32_t pair_bar = 1 + t * 4 + q;  // named barrier of the two halves of these rows
     float* xchg_mine = &bars->xchg[t][h][row];
     const float* xchg_other = &bars->xchg[t][h ^ 1][row];
-    const int tok = q0 + t * p.tpt + row / p.g;
+    const int tok = q0 + t * p.tpt + row_token(p, row);
     const bool row_valid = row < p.rows_used && tok < e;
     const int tok_i = row_valid ? tok : (1 << 30);  // padding rows see every key
     // kWindow: the row's bounds in the CTA's key list (padding rows: every key)
@@ -982,15 +1036,20 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz, int run = 0) 
         tmem_ld32(tS + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
         tmem_ld32(tS + 64 * h + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
         tmem_wait_ld();
-        if (limit < 64) {
+        if constexpr (kWindow) {
+          if (limit < 64 || (w_first > 0 && w_first > w_sinks)) {
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              const uint32_t seen = window_mask(limit - 32 * w, w_sinks - 32 * w, w_first - 32 * w);
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (!(seen & (1u << c))) sr[32 * w + c] = __float_as_uint(-INFINITY);
+            }
+          }
+        } else if (limit < 64) {
 #pragma unroll
           for (int c = 0; c < 64; ++c)
             if (c >= limit) sr[c] = __float_as_uint(-INFINITY);
-        }
-        if (kWindow && w_first > 0 && w_first > w_sinks) {
-#pragma unroll
-          for (int c = 0; c < 64; ++c)
-            if (c >= w_sinks && c < w_first) sr[c] = __float_as_uint(-INFINITY);
         }
       };
       // P of this half's 64 keys against reference m_use, packed as bf16
@@ -1103,22 +1162,25 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz, int run = 0) 
     } else if (kRuns) {
       if (ok) {
         tc_fence_after();
-        // the run's state: this half holds columns [h*D/2, (h+1)*D/2)
-        const int64_t ent =
-            ((int64_t)(off + tok) * p.Hq + (int64_t)kvh * p.g + row % p.g) * p.n_runs + run;
+        // the run's state through shared memory: this half holds columns
+        // [h*D/2, (h+1)*D/2)
+        constexpr int kStride = 4 * D + 16;
+        const uint32_t stage = smem_a + t * 128 * kStride + 2 * D * h;
 #pragma unroll
         for (int j = 0; j < D / 64; ++j) {
           uint32_t o[32];
           tmem_ld32(tO + (D / 2) * h + 32 * j, o);
           tmem_wait_ld();
-          if (row_valid && lrow > 0.f) {
-            float4* d4 = reinterpret_cast<float4*>(p.part_acc + ent * D + (D / 2) * h + 32 * j);
 #pragma unroll
-            for (int v = 0; v < 8; ++v)
-              d4[v] = make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
-                                  __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
-          }
+          for (int v = 0; v < 8; ++v)
+            st_shared_v4(stage + row * kStride + 128 * j + 16 * v, o[4 * v], o[4 * v + 1], o[4 * v + 2],
+                         o[4 * v + 3]);
         }
+        warp_store_rows<2 * D, kStride>(stage, q * 32, [&](int rr) -> uint8_t* {
+          uint8_t* dst = state_row<D>(p, q0, t, rr, e, off, kvh, run);
+          return dst == nullptr ? dst : dst + 2 * D * h;
+        });
+        const int64_t ent = ((int64_t)(off + tok) * p.Hq + (int64_t)kvh * p.g + (row - row_token(p, row) * p.g)) * p.n_runs + run;
         if (row_valid && h == 0) p.part_ml[ent] = make_float2(m_ref, lrow);
       }
     } else if (ok) {
@@ -1142,10 +1204,10 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz, int run = 0) 
                        w[4 * v + 3]);
       }
       warp_store_rows<D, kStride>(stage, q * 32, [&](int rr) -> uint8_t* {
-        const int tk = q0 + t * p.tpt + rr / p.g;
+        const int rt = row_token(p, rr), tk = q0 + t * p.tpt + rt;
         if (rr >= p.rows_used || tk >= e) return nullptr;
         return reinterpret_cast<uint8_t*>(
-            p.out + ((int64_t)(off + tk) * p.Hq + (int64_t)kvh * p.g + rr % p.g) * D + (D / 2) * h);
+            p.out + ((int64_t)(off + tk) * p.Hq + (int64_t)kvh * p.g + (rr - rt * p.g)) * D + (D / 2) * h);
       });
     }
     }
@@ -1153,7 +1215,7 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz, int run = 0) 
     // ------------------------------------------------------------ producers
     if constexpr (kFp8) {
       produce_fp8<D, kGroup, kWindow>(p, sQ_a, sKV, sRaw, bars, tid - R::kSoftmaxWarps * 32, r, kvh, e, mbeg, q0,
-                                      pfx, q_end, nb_pre, nb, off, wk);
+                                      pfx, q_end, nb_pre, nb, off, wk, table_row);
     } else {
     constexpr int kRowStep = R::kRowStep, kRowsPerThread = R::kRowsPerThread;
     const int ptid = tid - R::kSoftmaxWarps * 32;
@@ -1164,7 +1226,7 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz, int run = 0) 
     const int32_t* rtt =
         kGroup ? p.req_to_token + (int64_t)p.req_pool_idx[p.members[mbeg]] * p.rtt_stride +
                      p.group_start[r]
-               : p.req_to_token + (int64_t)p.req_pool_idx[r] * p.rtt_stride;
+               : p.req_to_token + (int64_t)(kWindow ? table_row : p.req_pool_idx[r]) * p.rtt_stride;
     int32_t slot_cur[kRowsPerThread], slot_next[kRowsPerThread];
     auto load_slots = [&](int b, int32_t (&dst)[kRowsPerThread]) {
 #pragma unroll
@@ -1382,10 +1444,12 @@ inline sgl_status make_extend_params(const ExtendArgs& a, Params* out) {
   prm.g = g;
   prm.tpt = BM / g;
   prm.rows_used = prm.tpt * g;
+  prm.g_inv = row_token_inv(g);
   // e4m3: scores in units of the widened codes (code * 2^-8) times the K
   // scale; the output takes the V scale and the 2^8 back
-  prm.scale_log2 = a.sm_scale * 1.4426950408889634f * (a.kv_fp8 ? a.k_scale * kFp8Operand : 1.f);
-  prm.o_scale = a.kv_fp8 ? a.v_scale * kFp8Operand : 1.f;
+  const float operand = a.window > 0 ? kFp8OperandWindow : kFp8Operand;
+  prm.scale_log2 = a.sm_scale * 1.4426950408889634f * (a.kv_fp8 ? a.k_scale * operand : 1.f);
+  prm.o_scale = a.kv_fp8 ? a.v_scale * operand : 1.f;
   prm.status = static_cast<int*>(a.workspace);
   prm.wait_ns = device_wait_limit_ns();
   prm.window = a.window;

@@ -9,10 +9,10 @@
 // pool_v[slots[t]] (e4m3 pools: value / scale as a code).  All of it is fp32
 // from the bf16 inputs to the one rounding of what is stored.
 //
-// Written out per value, y' = r (x A + x' B) with x' the pair's other value,
-// A = w cos and B = -+ w' sin: A and B depend on the token and the lane only,
-// so the rows of a token share them and a row costs two multiply-adds a value
-// besides its norm.
+// A lane holds both values of its pairs, so a row needs no exchange but its
+// norm's sum: with the products of weights and cosines or sines in registers
+// (they depend on the token and the lane, not on the head) it costs four
+// multiply-adds a pair and the scaling by r, on packed pairs of floats.
 //
 // The angle is kept exact modulo a turn: inv_freq / 2 pi as a 64-bit fixed
 // point fraction of a turn (turn_fraction), multiplied by the position in
@@ -29,9 +29,9 @@ namespace sgl {
 
 namespace {
 
-constexpr int kRopeWarps = 8;
+constexpr int kRopeWarps = 4;
 constexpr int kRopeBatch = 4;   // row groups a warp loads at a time
-constexpr int kRopeBlocks = 3;  // resident blocks an SM
+constexpr int kRopeBlocks = 4;  // resident blocks an SM
 
 struct RopeParams {
   const __nv_bfloat16* src[3];  // q, k, v
@@ -50,20 +50,49 @@ struct RopeParams {
   int64_t pool_size;
   int32_t heads[2];  // query, KV
   float scale[2];    // k, v
+  float rcp[2];      // 1 / scale, or 0 (quotient)
 };
 
 // (not .nc: q_out may be q)
-SGL_DEV uint4 ld_row(const __nv_bfloat16* p) {
+SGL_DEV uint4 ld_row16(const __nv_bfloat16* p) {
   uint4 v;
   asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
 }
+SGL_DEV uint2 ld_row8(const __nv_bfloat16* p) {
+  uint2 v;
+  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+// 4 bf16 -> two packed pairs of floats
+SGL_DEV void unpack4(uint32_t a, uint32_t b, float2 (&f)[2]) {
+  f[0] = make_float2(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u));
+  f[1] = make_float2(__uint_as_float(b << 16), __uint_as_float(b & 0xFFFF0000u));
+}
+SGL_DEV float2 fmul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+SGL_DEV float2 dup(float x) { return make_float2(x, x); }
 
-SGL_DEV uint32_t e4m3x2(float a, float b, float scale) {
-  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(a, scale), __fdiv_rn(b, scale)), __NV_SATFINITE,
-                                            __NV_E4M3);
+// y / s in IEEE float32.  With rcp the rounded 1 / s, q = y rcp is off by a few
+// units in the last place, y - q s is exact in a fused multiply-add, and q plus
+// that times rcp is the rounded quotient (Markstein, "Computation of elementary
+// functions on the IBM RISC System/6000 processor", 1990).  It takes s and rcp
+// far from the ends of the range (rcp = 0: they are not, and the quotient is
+// divided out) and a q that does not overflow; from 1024 on the code saturates
+// whatever q's last bits.  The divisions took 4 of 37 us on 8,191 tokens of 32
+// query and 8 KV heads.
+SGL_DEV float quotient(float y, float s, float rcp) {
+  if (rcp == 0.f) return __fdiv_rn(y, s);
+  const float q = y * rcp;
+  const float d = fmaf(fmaf(-q, s, y), rcp, q);
+  return copysignf(fabsf(q) < 1024.f ? d : q, y);  // (d loses the sign of a zero)
+}
+SGL_DEV uint32_t e4m3x4(const float2 (&y)[2], float s, float rcp) {
+  const float2 a = make_float2(quotient(y[0].x, s, rcp), quotient(y[0].y, s, rcp));
+  const float2 b = make_float2(quotient(y[1].x, s, rcp), quotient(y[1].y, s, rcp));
+  return (uint32_t)__nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3) |
+         ((uint32_t)__nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3) << 16);
 }
 
 // f / 2 pi modulo 1, in units of 2^-64: f = m 2^e with m an integer of 24
@@ -87,7 +116,10 @@ SGL_DEV uint64_t turn_fraction(float f) {
 }
 
 // A warp works on batches of kRopeBatch row groups, a group being the 32 / (D /
-// 8) rows (heads of one token) that its lanes hold, 8 consecutive values each.
+// 8) rows (heads of one token) that its lanes hold, 8 values each: lane i < rot
+// / 8 of a row holds pairs 4 i .. 4 i + 3 (8 consecutive values when
+// interleaved, else two runs of 4), the others 8 consecutive values that do
+// not turn.
 // A token's batches are those of its Q rows, its K rows and its V rows in
 // turn; block y takes an even share of them.  The next batch's rows, and the
 // next token's slot and positions, are loaded before the current batch is
@@ -106,11 +138,10 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) qk_norm_rope_sto
   const int nf = p.rot_dim / 2;
   const bool turns = b0 < nq + nk && nf > 0;  // this block has rows to turn
 
-  // this lane's values 8 li .. 8 li + 7: the lane that holds their partners
+  // this lane's values: o0 .. o0 + 3 and o1 .. o1 + 3
   const bool rotated = 8 * li < p.rot_dim;
-  const int half = p.rot_dim / 16;
-  const bool low = li < half;
-  const int plane = kInterleaved || !rotated ? li : (low ? li + half : li - half);
+  const int o0 = rotated && !kInterleaved ? 4 * li : 8 * li;
+  const int o1 = rotated && !kInterleaved ? 4 * li + nf : 8 * li + 4;
 
   int32_t t = blockIdx.x * kRopeWarps + warp;
   const int32_t stride = gridDim.x * kRopeWarps;
@@ -122,11 +153,21 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) qk_norm_rope_sto
   auto load_rows = [&](int32_t tt, int bb) {
     const int sec = section(bb);
     const int h0 = (bb - (sec == 0 ? 0 : (sec == 1 ? nq : nq + nk))) * kBatchRows + sub;
-    const __nv_bfloat16* src = p.src[sec] + tt * p.stride[sec] + (int64_t)h0 * D + 8 * li;
+    const __nv_bfloat16* src = p.src[sec] + tt * p.stride[sec] + h0 * D;
     const int n_heads = p.heads[sec > 0];
+    if (kInterleaved || sec == 2) {
+      src += 8 * li;
 #pragma unroll
-    for (int u = 0; u < kRopeBatch; ++u)
-      if (h0 + u * kRows < n_heads) raw[u] = ld_row(src + u * kRows * D);
+      for (int u = 0; u < kRopeBatch; ++u)
+        if (h0 + u * kRows < n_heads) raw[u] = ld_row16(src + u * kRows * D);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kRopeBatch; ++u)
+        if (h0 + u * kRows < n_heads) {
+          const uint2 lo = ld_row8(src + u * kRows * D + o0), hi = ld_row8(src + u * kRows * D + o1);
+          raw[u] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        }
+    }
   };
   const int32_t* fpos[kF];
   auto load_token = [&](int32_t tt) {
@@ -191,65 +232,84 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) qk_norm_rope_sto
     if (live) {
       if (sec < 2) {
         const __nv_bfloat16* w = p.weight[sec];
-        float A[8], B[8];
+        // y' = y C + other S, other being the pair's other value
+        float2 C0[2], C1[2], S0[2], S1[2];
         {
-          float wo[8], wp[8];
+          float2 w0[2] = {dup(1.f), dup(1.f)}, w1[2] = {dup(1.f), dup(1.f)};
           if (w != nullptr) {
-            bf16x8_to_f32(*reinterpret_cast<const uint4*>(w + 8 * li), wo);
-            bf16x8_to_f32(*reinterpret_cast<const uint4*>(w + 8 * plane), wp);
-          } else {
+            const uint2 a = *reinterpret_cast<const uint2*>(w + o0), c = *reinterpret_cast<const uint2*>(w + o1);
+            unpack4(a.x, a.y, w0);
+            unpack4(c.x, c.y, w1);
+          }
+          float2 v[4] = {make_float2(1.f, 0.f), make_float2(1.f, 0.f), make_float2(1.f, 0.f), make_float2(1.f, 0.f)};
+          if (rotated) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) wo[e] = wp[e] = 1.f;
+            for (int e = 0; e < 4; ++e) v[e] = turn[4 * li + e];
           }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            float2 v = make_float2(1.f, 0.f);
-            if (rotated) v = turn[kInterleaved ? 4 * li + e / 2 : 8 * (low ? li : li - half) + e];
-            A[e] = wo[e] * v.x;
-            B[e] = (kInterleaved ? wo[e ^ 1] : wp[e]) * ((kInterleaved ? (e & 1) == 0 : low) ? -v.y : v.y);
+          for (int j = 0; j < 2; ++j) {
+            if constexpr (kInterleaved) {  // pair = the two floats of a packed pair
+              C0[j] = fmul2(w0[j], dup(v[j].x));
+              S0[j] = make_float2(-w0[j].y * v[j].y, w0[j].x * v[j].y);
+              C1[j] = fmul2(w1[j], dup(v[2 + j].x));
+              S1[j] = make_float2(-w1[j].y * v[2 + j].y, w1[j].x * v[2 + j].y);
+            } else {  // pair = the same place of the two runs
+              const float2 c = make_float2(v[2 * j].x, v[2 * j + 1].x), sn = make_float2(v[2 * j].y, v[2 * j + 1].y);
+              C0[j] = fmul2(w0[j], c);
+              C1[j] = fmul2(w1[j], c);
+              S1[j] = fmul2(w0[j], sn);
+              S0[j] = fmul2(w1[j], make_float2(-sn.x, -sn.y));
+            }
           }
         }
 #pragma unroll
         for (int u = 0; u < kRopeBatch; ++u) {
           const int h = h0 + u * kRows;
           if (h - sub >= n_heads) break;
-          float y[8], x[8];
-          bf16x8_to_f32(cur[u], y);
+          float2 y0[2], y1[2];
+          unpack4(cur[u].x, cur[u].y, y0);
+          unpack4(cur[u].z, cur[u].w, y1);
           float r = 1.f;
           if (w != nullptr) {
-            float q2 = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) q2 = fmaf(y[e], y[e], q2);
+            const float2 q = ffma2(y1[1], y1[1], ffma2(y1[0], y1[0], ffma2(y0[1], y0[1], fmul2(y0[0], y0[0]))));
+            float q2 = q.x + q.y;
 #pragma unroll
             for (int o = 1; o < kLanes; o <<= 1) q2 += __shfl_xor_sync(0xffffffffu, q2, o);
             r = rsqrtf(q2 * (1.f / D) + p.eps);
           }
-          if constexpr (kInterleaved) {
+          float2 z0[2], z1[2];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = y[e ^ 1];
-          } else {
-            uint4 o;
-            o.x = __shfl_sync(0xffffffffu, cur[u].x, sub * kLanes + plane);
-            o.y = __shfl_sync(0xffffffffu, cur[u].y, sub * kLanes + plane);
-            o.z = __shfl_sync(0xffffffffu, cur[u].z, sub * kLanes + plane);
-            o.w = __shfl_sync(0xffffffffu, cur[u].w, sub * kLanes + plane);
-            bf16x8_to_f32(o, x);
+          for (int j = 0; j < 2; ++j) {
+            z0[j] = fmul2(y0[j], C0[j]);
+            z1[j] = fmul2(y1[j], C1[j]);
+            if (rotated) {  // (not + 0 * other: rows that do not turn keep their infinities)
+              z0[j] = ffma2(kInterleaved ? make_float2(y0[j].y, y0[j].x) : y1[j], S0[j], z0[j]);
+              z1[j] = ffma2(kInterleaved ? make_float2(y1[j].y, y1[j].x) : y0[j], S1[j], z1[j]);
+            }
+            z0[j] = fmul2(z0[j], dup(r));
+            z1[j] = fmul2(z1[j], dup(r));
           }
-          // (a select, not 0 * x: rows that do not turn keep their infinities)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = r * fmaf(y[e], A[e], rotated ? x[e] * B[e] : 0.f);
           if (h >= n_heads) continue;
           if (kFp8 && sec == 1) {
-            const float sc = p.scale[0];
-            *reinterpret_cast<uint2*>(p.pool[0] + (at * p.heads[1] + h) * D + 8 * li) =
-                make_uint2(e4m3x2(y[0], y[1], sc) | (e4m3x2(y[2], y[3], sc) << 16),
-                           e4m3x2(y[4], y[5], sc) | (e4m3x2(y[6], y[7], sc) << 16));
+            uint8_t* dst = p.pool[0] + (at * p.heads[1] + h) * D;
+            const uint32_t lo = e4m3x4(z0, p.scale[0], p.rcp[0]), hi = e4m3x4(z1, p.scale[0], p.rcp[0]);
+            if constexpr (kInterleaved) {
+              *reinterpret_cast<uint2*>(dst + o0) = make_uint2(lo, hi);
+            } else {
+              *reinterpret_cast<uint32_t*>(dst + o0) = lo;
+              *reinterpret_cast<uint32_t*>(dst + o1) = hi;
+            }
           } else {
             __nv_bfloat16* dst = sec == 0 ? p.q_out + ((int64_t)tok * p.heads[0] + h) * D
                                           : reinterpret_cast<__nv_bfloat16*>(p.pool[0]) + (at * p.heads[1] + h) * D;
-            *reinterpret_cast<uint4*>(dst + 8 * li) =
-                make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                           pack_bf16x2(y[6], y[7]));
+            const uint2 lo = make_uint2(pack_bf16x2(z0[0].x, z0[0].y), pack_bf16x2(z0[1].x, z0[1].y));
+            const uint2 hi = make_uint2(pack_bf16x2(z1[0].x, z1[0].y), pack_bf16x2(z1[1].x, z1[1].y));
+            if constexpr (kInterleaved) {
+              *reinterpret_cast<uint4*>(dst + o0) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            } else {
+              *reinterpret_cast<uint2*>(dst + o0) = lo;
+              *reinterpret_cast<uint2*>(dst + o1) = hi;
+            }
           }
         }
       } else {
@@ -258,12 +318,11 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) qk_norm_rope_sto
           const int h = h0 + u * kRows;
           if (h >= n_heads) break;
           if constexpr (kFp8) {
-            float y[8];
-            bf16x8_to_f32(cur[u], y);
-            const float sc = p.scale[1];
+            float2 y0[2], y1[2];
+            unpack4(cur[u].x, cur[u].y, y0);
+            unpack4(cur[u].z, cur[u].w, y1);
             *reinterpret_cast<uint2*>(p.pool[1] + (at * p.heads[1] + h) * D + 8 * li) =
-                make_uint2(e4m3x2(y[0], y[1], sc) | (e4m3x2(y[2], y[3], sc) << 16),
-                           e4m3x2(y[4], y[5], sc) | (e4m3x2(y[6], y[7], sc) << 16));
+                make_uint2(e4m3x4(y0, p.scale[1], p.rcp[1]), e4m3x4(y1, p.scale[1], p.rcp[1]));
           } else {
             *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.pool[1]) + (at * p.heads[1] + h) * D +
                                       8 * li) = cur[u];
@@ -330,6 +389,7 @@ sgl_status launch_qk_norm_rope_store(const RopeArgs& a, cudaStream_t stream) {
   p.heads[1] = a.num_kv_heads;
   p.scale[0] = a.k_scale;
   p.scale[1] = a.v_scale;
+  for (int i = 0; i < 2; ++i) p.rcp[i] = p.scale[i] >= 0x1p-60f && p.scale[i] <= 0x1p60f ? 1.f / p.scale[i] : 0.f;
   if (a.head_dim == 128) return run_d<128>(p, a.kv_fp8, stream);
   if (a.head_dim == 64) return run_d<64>(p, a.kv_fp8, stream);
   return SGL_ERR_UNSUPPORTED;

@@ -173,6 +173,23 @@ def test_stored_rows_are_what_the_store_writes():
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
 
 
+@pytest.mark.parametrize("scale", [1.0, 0.0173, 1 / 3, 0.031, 7.77, 2.0**-60, 3e-20, 2.0**61, 1e-40, 3e38])
+def test_codes_of_every_bf16_value(scale):
+    """Every finite bf16 value over the scale: the codes of sgl_store_kv_fp8, bit for bit."""
+    bits = np.arange(1 << 16, dtype=np.uint32).astype(np.uint16)
+    bits = bits[(bits & 0x7F80) != 0x7F80]
+    rows = np.zeros((512, 1, 128), np.uint16)
+    rows.reshape(-1)[: bits.size] = bits
+    x = W.bf16_tensor(rows, DEV)
+    slots = torch.arange(512, dtype=torch.int32, device=DEV)
+    got = [torch.zeros(512, 1, 128, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    want = [torch.zeros_like(p) for p in got]
+    B.sgl_qk_norm_rope_store_kv_fp8(x, x, x, None, None, slots, *got, scale, scale)
+    B.sgl_store_kv_fp8(x, x, slots, *want, scale, scale)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_binding_refuses_what_it_would_misread():
     c = Case(13, n=9, Hq=4, Hkv=2, D=64)
     for i, bad in ((0, c.t[0].transpose(1, 2)), (1, c.t[1][:, :1]), (2, c.t[2].float()), (0, c.t[0].cpu())):
