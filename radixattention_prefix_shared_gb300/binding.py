@@ -405,11 +405,25 @@ def _need_dense(name, dtype, **tensors):
             raise ValueError(f"{name}: {arg} must be a dense {dtype} tensor on the current CUDA device")
 
 
-def _raw_stream(stream, device):
-    if stream is None:
+class _Torch:
+    """What the calls below look up in torch at every call (bound at the first)."""
+
+    def __init__(self):
         import torch
+        self.bf16, self.i32, self.u8, self.f32 = torch.bfloat16, torch.int32, torch.uint8, torch.float32
+        self.current_device = torch.cuda.current_device
         # the handle alone: torch.cuda.current_stream() builds an object around it
-        return torch._C._cuda_getCurrentRawStream(device)
+        self.current_stream = torch._C._cuda_getCurrentRawStream
+        self.empty = torch.empty
+        self.empty_like = torch.empty_like
+
+
+@functools.lru_cache(maxsize=1)
+def _torch():
+    return _Torch()
+
+
+def _raw_stream(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -460,9 +474,9 @@ def _refuse_window(name, q, pool_k, pool_v, kv_dtype, req_to_token, lens, out, w
 
 def _decode_window(name, q, pool_k, pool_v, scales, req_to_token, req_pool_idx, seq_lens, out, max_seq_len,
                    window, sinks, workspace, sm_scale, stream):
-    import torch
-    bf16, i32, dev = torch.bfloat16, torch.int32, torch.cuda.current_device()
-    kv = torch.uint8 if scales else bf16
+    T = _torch()
+    bf16, i32, dev = T.bf16, T.i32, T.current_device()
+    kv = T.u8 if scales else bf16
     qs, ks, ts = q.shape, pool_k.shape, req_to_token.shape
     if not (q.dtype is bf16 and q.is_contiguous() and q.get_device() == dev and len(qs) == 3
             and pool_k.dtype is kv and pool_k.is_contiguous() and pool_k.get_device() == dev and len(ks) == 3
@@ -482,14 +496,15 @@ def _decode_window(name, q, pool_k, pool_v, scales, req_to_token, req_pool_idx, 
     if out is None or workspace is None:
         with _on(stream):
             if out is None:
-                out = torch.empty_like(q)
+                out = T.empty_like(q)
             if workspace is None:
-                workspace = torch.empty(max(16, lib().sgl_decode_window_workspace_bytes(
-                    qs[0], int(max_seq_len), int(window), int(sinks), dims)), dtype=torch.uint8, device=q.device)
+                workspace = T.empty(max(16, lib().sgl_decode_window_workspace_bytes(
+                    qs[0], int(max_seq_len), int(window), int(sinks), dims)), dtype=T.u8, device=q.device)
     code = getattr(lib(), name)(
         q.data_ptr(), pool_k.data_ptr(), pool_v.data_ptr(), *scales, req_to_token.data_ptr(), ts[0], ts[1],
         req_pool_idx.data_ptr(), seq_lens.data_ptr(), qs[0], int(max_seq_len), int(window), int(sinks), out.data_ptr(),
-        workspace.data_ptr(), workspace.nbytes, dims, _raw_stream(stream, dev))
+        workspace.data_ptr(), workspace.nbytes, dims,
+        T.current_stream(dev) if stream is None else _raw_stream(stream))
     if code != 0:
         raise SglError(name, code)
     return out
@@ -514,9 +529,9 @@ def sgl_decode_attention_window_fp8(q, pool_k, pool_v, k_scale, v_scale, req_to_
 
 def _extend_window(name, q, pool_k, pool_v, scales, req_to_token, req_pool_idx, prefix_lens, extend_lens, out,
                    max_extend, max_prefix, window, sinks, total_extend, workspace, sm_scale, stream):
-    import torch
-    bf16, i32, dev = torch.bfloat16, torch.int32, torch.cuda.current_device()
-    kv = torch.uint8 if scales else bf16
+    T = _torch()
+    bf16, i32, dev = T.bf16, T.i32, T.current_device()
+    kv = T.u8 if scales else bf16
     qs, ks, ts, bs = q.shape, pool_k.shape, req_to_token.shape, req_pool_idx.shape
     if not (q.dtype is bf16 and q.is_contiguous() and q.get_device() == dev and len(qs) == 3
             and pool_k.dtype is kv and pool_k.is_contiguous() and pool_k.get_device() == dev and len(ks) == 3
@@ -540,14 +555,15 @@ def _extend_window(name, q, pool_k, pool_v, scales, req_to_token, req_pool_idx, 
     if out is None or workspace is None:
         with _on(stream):
             if out is None:
-                out = torch.empty_like(q)
+                out = T.empty_like(q)
             if workspace is None:
                 workspace = new_workspace(lib().sgl_extend_window_workspace_bytes(
                     bs[0], total, int(max_extend), int(max_prefix), int(window), int(sinks), dims), q.device)
     code = getattr(lib(), name)(
         q.data_ptr(), pool_k.data_ptr(), pool_v.data_ptr(), *scales, req_to_token.data_ptr(), ts[0], ts[1],
         req_pool_idx.data_ptr(), prefix_lens.data_ptr(), extend_lens.data_ptr(), bs[0], total, int(max_extend),
-        int(max_prefix), int(window), int(sinks), out.data_ptr(), workspace.data_ptr(), workspace.nbytes, dims, _raw_stream(stream, dev))
+        int(max_prefix), int(window), int(sinks), out.data_ptr(), workspace.data_ptr(), workspace.nbytes, dims,
+        T.current_stream(dev) if stream is None else _raw_stream(stream))
     if code != 0:
         raise SglError(name, code)
     return out
@@ -613,54 +629,59 @@ def _refuse_rope(name, q, k, v, positions, inv_freq, slots, pool_k, pool_v, kv_d
                      "axes, freq_axis [rot / 2]")
 
 
-def _dense_rows(t, shape, bf16, dev):
-    return (t.dtype is bf16 and t.shape == shape and t.get_device() == dev
-            and (t.is_contiguous() or (t.stride(2) == 1 and (shape[1] == 1 or t.stride(1) == shape[2]))))
-
-
 def _qk_norm_rope_store(name, q, k, v, positions, inv_freq, slots, pool_k, pool_v, scales, q_weight, k_weight,
                         eps, freq_axis, interleaved, q_out, stream):
-    import torch
-    bf16, i32, dev = torch.bfloat16, torch.int32, torch.cuda.current_device()
-    kv = torch.uint8 if scales else bf16
-    qs, ps = q.shape, pool_k.shape
-    n, d, rot, axes = qs[0], ps[-1], 0, 1
-    new = (n, ps[-2], d) if len(ps) == 3 else None
-    ok = (len(qs) == 3 and new is not None and _dense_rows(q, (n, qs[1], d), bf16, dev)
-          and _dense_rows(k, new, bf16, dev) and _dense_rows(v, new, bf16, dev)
+    T = _torch()
+    bf16, i32, dev = T.bf16, T.i32, T.current_device()
+    kv = T.u8 if scales else bf16
+    qs, ps, qt, kt, vt = q.shape, pool_k.shape, q.stride(), k.stride(), v.stride()
+    rot, axes, new, width = 0, 1, None, None
+    if len(qs) == 3 == len(ps):
+        new, width = (qs[0], ps[1], ps[2]), ps[2:]
+    # dense rows; tokens may lie apart (parts of a packed projection)
+    ok = (new is not None and q.dtype is bf16 and k.dtype is bf16 and v.dtype is bf16 and qs[2] == ps[2]
+          and k.shape == new and v.shape == new and qt[2] == kt[2] == vt[2] == 1
+          and (qt[1] == ps[2] or qs[1] == 1) and (kt[1] == vt[1] == ps[2] or ps[1] == 1)
+          and q.get_device() == dev and k.get_device() == dev and v.get_device() == dev
           and pool_k.dtype is kv and pool_k.is_contiguous() and pool_k.get_device() == dev
           and pool_v.dtype is kv and pool_v.is_contiguous() and pool_v.get_device() == dev and pool_v.shape == ps
           and slots.dtype is i32 and slots.is_contiguous() and slots.get_device() == dev and slots.shape == qs[:1])
     if ok and inv_freq is not None:
         fs, xs = inv_freq.shape, positions.shape if positions is not None else ()
-        rot, axes = 2 * fs[0], xs[0] if len(xs) == 2 else 1
-        ok = (inv_freq.dtype is torch.float32 and inv_freq.is_contiguous() and inv_freq.get_device() == dev
-              and len(fs) == 1 and 0 < len(xs) <= 2 and xs[-1] == n and axes > 0
+        if len(xs) == 2:
+            axes = xs[0]
+        ok = (len(fs) == 1 and inv_freq.dtype is T.f32 and inv_freq.is_contiguous() and inv_freq.get_device() == dev
+              and 0 < len(xs) <= 2 and xs[-1] == qs[0] and axes > 0
               and positions.dtype is i32 and positions.is_contiguous() and positions.get_device() == dev
               and (axes == 1 or (freq_axis is not None and freq_axis.dtype is i32 and freq_axis.shape == fs
                                  and freq_axis.is_contiguous() and freq_axis.get_device() == dev)))
-    for w in (q_weight, k_weight):
-        ok = ok and (w is None or (w.dtype is bf16 and w.shape == ps[2:] and w.is_contiguous()
-                                   and w.get_device() == dev))
-    ok = ok and (q_out is None or (q_out.dtype is bf16 and q_out.is_contiguous() and q_out.get_device() == dev
-                                   and q_out.shape == qs))
+        rot = 2 * fs[0] if ok else 0
+    if ok and q_weight is not None:
+        ok = (q_weight.dtype is bf16 and q_weight.shape == width and q_weight.is_contiguous()
+              and q_weight.get_device() == dev)
+    if ok and k_weight is not None:
+        ok = (k_weight.dtype is bf16 and k_weight.shape == width and k_weight.is_contiguous()
+              and k_weight.get_device() == dev)
+    if ok and q_out is not None:
+        ok = q_out.dtype is bf16 and q_out.is_contiguous() and q_out.get_device() == dev and q_out.shape == qs
     if not ok:
         _refuse_rope(name, q, k, v, positions, inv_freq, slots, pool_k, pool_v, kv, q_weight, k_weight, freq_axis,
                      q_out)
+    n, hq, d = qs
     if q_out is None:
         with _on(stream):
-            q_out = torch.empty(qs, dtype=bf16, device=q.device)
+            q_out = T.empty(qs, dtype=bf16, device=q.device)
     if n > 1:
-        strides = q.stride(0), k.stride(0), v.stride(0)
+        qt, kt, vt = qt[0], kt[0], vt[0]
     else:   # the stride of a single token means nothing
-        strides = qs[1] * d, ps[1] * d, ps[1] * d
+        qt, kt, vt = hq * d, ps[1] * d, ps[1] * d
     code = getattr(lib(), name)(
-        q.data_ptr(), strides[0], k.data_ptr(), strides[1], v.data_ptr(), strides[2],
-        None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(), float(eps),
-        positions.data_ptr() if rot else None, axes, inv_freq.data_ptr() if rot else None,
+        q.data_ptr(), qt, k.data_ptr(), kt, v.data_ptr(), vt,
+        None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
+        float(eps), positions.data_ptr() if rot else None, axes, inv_freq.data_ptr() if rot else None,
         freq_axis.data_ptr() if axes > 1 else None, rot, 1 if interleaved else 0, slots.data_ptr(), n,
-        q_out.data_ptr(), pool_k.data_ptr(), pool_v.data_ptr(), *scales, _dims_ref(qs[1], ps[1], d, ps[0], 0.0),
-        _raw_stream(stream, dev))
+        q_out.data_ptr(), pool_k.data_ptr(), pool_v.data_ptr(), *scales, _dims_ref(hq, ps[1], d, ps[0], 0.0),
+        T.current_stream(dev) if stream is None else _raw_stream(stream))
     if code != 0:
         raise SglError(name, code)
     return q_out

@@ -14,6 +14,9 @@ namespace {
 // to as many CTAs as fill them (one CTA of this pipeline an SM).
 constexpr int kFillCtas = 152;
 constexpr int kMaxRuns = 32;  // a lane each in the combine
+// Key blocks from which dealing them out pays for the combine: a block takes a
+// CTA 1.6 us, the combine 2 us and its launch as much of the host's time.
+constexpr int kMinBlocks = 4;
 
 struct Shape {
   int32_t per_cta;  // tokens of a CTA's two Q tiles
@@ -33,6 +36,7 @@ struct Shape {
     int64_t runs = live * Hkv > 0 ? kFillCtas / (live * Hkv) : 1;
     const int64_t blocks = (keys + BN - 1) / BN;
     if (runs > blocks) runs = blocks;
+    if (blocks < kMinBlocks) runs = 1;
     if (runs > kMaxRuns) runs = kMaxRuns;
     n_runs = runs < 1 ? 1 : (int32_t)runs;
   }
