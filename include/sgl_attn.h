@@ -387,8 +387,8 @@ sgl_status sgl_cascade_decode_attention_fp8(
  *                 max_extend, max_prefix, window, sinks, dims); its first 256
  *                 bytes zero-filled once before first use (word 0: the
  *                 bounded-wait status, as for sgl_extend_attention).
- * The _fp8 calls are the same over e4m3 pools (values are code * scale; see
- * "FP8 KV pool" above; the extend's query range is sgl_extend_attention_fp8's).
+ * In both, out may be q itself.  The _fp8 calls are the same over e4m3 pools
+ * (values are code * scale; see "FP8 KV pool" below; the extend's query range is sgl_extend_attention_fp8's).
  */
 size_t sgl_decode_window_workspace_bytes(int32_t batch, int32_t max_seq_len, int32_t window,
                                          int32_t sinks, const sgl_attn_dims* dims);
@@ -457,8 +457,9 @@ sgl_status sgl_extend_attention_window_fp8(const void* q, const void* pool_k, co
  *   slots        : int32 [n], distinct; a token whose slot is outside
  *                  [0, pool_size) is padding: nothing of it is written, its
  *                  q_out rows included
- *   q_out        : bf16 [n, Hq, D]; q itself when q_stride is Hq * D, else apart
- *                  from q, k and v (an overlap is SGL_ERR_INVALID_ARG)
+ *   q_out        : bf16 [n, Hq, D]; may be q itself when q_stride is Hq * D
+ * q_out, pool_k and pool_v otherwise lie apart from q, k and v and from one
+ * another (an overlap is SGL_ERR_INVALID_ARG).
  * sgl_qk_norm_rope_store_kv_fp8 -- the same into e4m3 pools: codes of the fp32
  *   rows over the scales, rounded and saturated as by sgl_store_kv_fp8 (K
  *   rows are not rounded to bf16 first).

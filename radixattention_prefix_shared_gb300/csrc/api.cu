@@ -900,13 +900,22 @@ sgl_status qk_rope_entry(const void* q, int64_t q_stride, const void* k, int64_t
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(pool_k) ||
       !aligned16(pool_v) || !aligned16(q_weight) || !aligned16(k_weight))
     return SGL_ERR_INVALID_ARG;
-  // rows are read and written at the same time: q_out is q itself or apart
-  // from everything that is read
-  const size_t out_bytes = (size_t)n * (size_t)q_row * 2;
+  // rows are read and written at the same time: what is written lies apart from
+  // what is read and from one another, but q_out may be q
   const auto span = [&](int64_t stride, int64_t row) { return ((size_t)(n - 1) * (size_t)stride + (size_t)row) * 2; };
+  const size_t out_bytes = (size_t)n * (size_t)q_row * 2;
+  const size_t pool_bytes = (size_t)dims->pool_size * (size_t)kv_row * (kv_fp8 ? 1 : 2);
+  const struct {
+    const void* p;
+    size_t n;
+  } in[3] = {{q, span(q_stride, q_row)}, {k, span(k_stride, kv_row)}, {v, span(v_stride, kv_row)}};
   const bool in_place = q_out == q && q_stride == q_row;
-  if ((!in_place && overlaps(q_out, out_bytes, q, span(q_stride, q_row))) ||
-      overlaps(q_out, out_bytes, k, span(k_stride, kv_row)) || overlaps(q_out, out_bytes, v, span(v_stride, kv_row)))
+  for (int i = 0; i < 3; ++i)
+    if ((!(i == 0 && in_place) && overlaps(q_out, out_bytes, in[i].p, in[i].n)) ||
+        overlaps(pool_k, pool_bytes, in[i].p, in[i].n) || overlaps(pool_v, pool_bytes, in[i].p, in[i].n))
+      return SGL_ERR_INVALID_ARG;
+  if (overlaps(pool_k, pool_bytes, pool_v, pool_bytes) || overlaps(q_out, out_bytes, pool_k, pool_bytes) ||
+      overlaps(q_out, out_bytes, pool_v, pool_bytes))
     return SGL_ERR_INVALID_ARG;
   RopeArgs a;
   a.q = q;

@@ -161,7 +161,7 @@ struct WindowRun {
   SGL_DEV WindowRun(const Window& w, int32_t chunk, int32_t seq_len) {
     len = max(0, min(seq_len, w.max_seq));
     n = min(len, w.max_keys);
-    ns = (n + chunk - 1) / chunk;
+    ns = n > 0 ? 1 + (n - 1) / chunk : 0;
   }
 };
 

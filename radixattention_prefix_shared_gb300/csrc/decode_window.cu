@@ -27,8 +27,8 @@ constexpr int kMinRun = 256;
 
 int32_t splits_for(int64_t units, int32_t keys) {
   const int32_t fill = (int32_t)((kFillUnits + units - 1) / units);
-  const int32_t most = (keys + kMinRun - 1) / kMinRun;
-  const int32_t least = (keys + kItemMax - 1) / kItemMax;
+  const int32_t most = (int32_t)(((int64_t)keys + kMinRun - 1) / kMinRun);
+  const int32_t least = (int32_t)(((int64_t)keys + kItemMax - 1) / kItemMax);
   const int32_t s = fill < most ? fill : most;
   return s > least ? s : least;
 }
@@ -46,7 +46,7 @@ struct Shape {
     keys = (int32_t)(seen < max_seq_len ? seen : max_seq_len);
     const int64_t units = (int64_t)batch * (spans_for(Hkv, split, kv_fp8) ? Hkv / kWarps : Hkv);
     n_splits = splits_for(units, keys);
-    chunk = (keys + n_splits - 1) / n_splits;
+    chunk = (int32_t)(((int64_t)keys + n_splits - 1) / n_splits);
   }
 };
 
@@ -93,8 +93,10 @@ __global__ void __launch_bounds__(128) window_combine_kernel(Params p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq;
   const int32_t ns = WindowRun(p.win, p.chunk, p.seq_lens[r]).ns;
+  // launched dependent on the split kernel; every block waits, so that this
+  // grid never ends (and what follows it never starts) before that one
+  grid_dep_wait();
   if (ns <= 1) return;  // a single run wrote the output (none: no keys)
-  grid_dep_wait();      // launched dependent on the split kernel
   const int64_t first = (int64_t)r * p.win.n_splits * p.Hq + h, step = p.Hq;
   float M = -INFINITY, L = 0.f, acc[E];
 #pragma unroll

@@ -66,8 +66,10 @@ __global__ void __launch_bounds__(128) extend_window_combine_kernel(Params p) {
   for (int i = lane; i < p.batch; i += 32) tokens += p.extend_lens[i];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) tokens += __shfl_xor_sync(0xffffffffu, tokens, o);
+  // launched dependent on the extend kernel; every warp waits, so that this
+  // grid never ends (and what follows it never starts) before that one
+  grid_dep_wait();
   if (row >= tokens * p.Hq) return;
-  grid_dep_wait();  // launched dependent on the extend kernel
   float2 ml = make_float2(-INFINITY, 0.f);
   if (lane < p.n_runs) ml = p.part_ml[row * p.n_runs + lane];
   float M = ml.x;

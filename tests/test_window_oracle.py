@@ -216,11 +216,11 @@ def test_extend_window_validation(cuda_lib):
 
 def test_qk_rope_validation(cuda_lib):
     d = _dims()
-    Q, K, V, OUT = 0x10000000, 0x20000000, 0x30000000, 0x40000000
+    Q, K, V, OUT, PK, PV = (i * 0x10000000 for i in range(1, 7))
 
     def call(fp8=False, d=d, **kw):
         a = dict(q=Q, qs=512, k=K, ks_=256, v=V, vs_=256, qw=FAKE, kw=FAKE, eps=1e-6, pos=FAKE, axes=1, f=FAKE,
-                 ax=None, rot=128, inter=0, slots=FAKE, n=8, out=OUT, pk=FAKE, pv=FAKE, s=0.1)
+                 ax=None, rot=128, inter=0, slots=FAKE, n=8, out=OUT, pk=PK, pv=PV, s=0.1)
         a.update(kw)
         f = cuda_lib.sgl_qk_norm_rope_store_kv_fp8 if fp8 else cuda_lib.sgl_qk_norm_rope_store_kv
         tail = (a["s"], a["s"]) if fp8 else ()
@@ -243,6 +243,9 @@ def test_qk_rope_validation(cuda_lib):
         assert call(fp8, out=Q + 4096) == 1
         assert call(fp8, out=K + 512) == 1
         assert call(fp8, out=V - 16) == 1
+        # pools over what is read, over q_out, over one another
+        for kw in (dict(pk=Q), dict(pv=K), dict(pk=V), dict(pv=OUT), dict(pk=PV + 1024)):
+            assert call(fp8, **kw) == 1, kw
         assert call(fp8, d=_dims(head_dim=96)) == 2
     assert call(True, s=0.0) == 1
 
