@@ -388,7 +388,8 @@ sgl_status sgl_cascade_decode_attention_fp8(
  *                 bytes zero-filled once before first use (word 0: the
  *                 bounded-wait status, as for sgl_extend_attention).
  * In both, out may be q itself.  The _fp8 calls are the same over e4m3 pools
- * (values are code * scale; see "FP8 KV pool" below; the extend's query range is sgl_extend_attention_fp8's).
+ * (values are code * scale; see "FP8 KV pool" above; the extend's query range
+ * is sgl_extend_attention_fp8's).
  */
 size_t sgl_decode_window_workspace_bytes(int32_t batch, int32_t max_seq_len, int32_t window,
                                          int32_t sinks, const sgl_attn_dims* dims);

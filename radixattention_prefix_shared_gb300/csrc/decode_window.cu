@@ -61,6 +61,19 @@ size_t ws_bytes(int32_t batch, const Shape& s, int32_t D, void* base, Ws* ws) {
   return o_acc + sizeof(float) * n * D;
 }
 
+// Ring stages: the split kernel's, but four on the CUDA-core path over an e4m3
+// pool, whose conversions want the fifth CTA on an SM more than the deeper
+// ring (64 requests of 32 KV heads, window 1,024: 95.0 us with 6 stages, 94.2
+// with 5, 90.4 with 4, 93.5 with 3).
+template <int G, typename KV>
+constexpr int ring_depth() {
+  return !use_mma<KV, G>() && sizeof(KV) == 1 ? 4 : SplitRing<KV, G>::kDepth;
+}
+template <int D, int G, typename KV>
+constexpr size_t ring_bytes() {
+  return SplitRing<KV, G>::template bytes<D>() / SplitRing<KV, G>::kDepth * ring_depth<G, KV>();
+}
+
 template <int D, int G, int LPT, typename KV, bool kSpans>
 __global__ void __launch_bounds__(kThreads, (split_min_blocks<D, G, LPT, KV>())) decode_window_kernel(Params p) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -71,7 +84,7 @@ __global__ void __launch_bounds__(kThreads, (split_min_blocks<D, G, LPT, KV>()))
   const uint32_t heads = kSpans ? p.Hkv / kWarps : p.Hkv;
   const int32_t item = (int32_t)(blockIdx.x / heads), y = (int32_t)(blockIdx.x % heads);
   bool taken = false;
-  split_units<D, G, LPT, KV, 0, kSpans, true>(
+  split_units<D, G, LPT, KV, ring_depth<G, KV>(), kSpans, true>(
       p, smem, s_item, threadIdx.x, 1, [] { __syncthreads(); },
       [&] {
         const int32_t u = taken ? 1 : 0;
@@ -145,8 +158,8 @@ __global__ void __launch_bounds__(128) window_combine_kernel(Params p) {
 
 template <int D, int G, int LPT, typename KV, bool kSpans>
 sgl_status launch(const Params& prm, cudaStream_t stream) {
-  constexpr size_t smem = SplitRing<KV, G>::template bytes<D>() + kItemMax * sizeof(int32_t);
-  static_assert(kWarps * G * (D + 2) * sizeof(float) <= SplitRing<KV, G>::template bytes<D>(),
+  constexpr size_t smem = ring_bytes<D, G, KV>() + kItemMax * sizeof(int32_t);
+  static_assert(kWarps * G * (D + 2) * sizeof(float) <= ring_bytes<D, G, KV>(),
                 "reduction scratch must fit in the ring");
   if (kernel_blocks_per_sm<decode_window_kernel<D, G, LPT, KV, kSpans>>((int)smem, kThreads) < 0) return SGL_ERR_CUDA;
   const int64_t heads = kSpans ? prm.Hkv / kWarps : prm.Hkv;

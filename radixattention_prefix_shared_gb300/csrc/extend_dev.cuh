@@ -1396,15 +1396,16 @@ __global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1) extend_kernel(Params
   attend_tiles<D, false, kFp8>(p, blockIdx.x, blockIdx.y, blockIdx.z);
 }
 
-// grid x: pairs of Q tiles, times the runs of their keys
-template <int D, bool kFp8, bool kRuns>
-__global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1) extend_window_kernel(Params p) {
+// grid x: the Q tiles of a CTA (kTiles: two, or one with two CTAs an SM), times
+// the runs of their keys
+template <int D, bool kFp8, bool kRuns, int kTiles>
+__global__ void __launch_bounds__(Roles<kFp8, kTiles>::kThreads, 3 - kTiles) extend_window_kernel(Params p) {
   if constexpr (kRuns) {
     grid_dep_launch();  // the combine may start; it waits for the states
     attend_tiles<D, false, kFp8, 2, false, kWindowedRuns>(p, blockIdx.x / p.n_runs, blockIdx.y, blockIdx.z,
                                                           blockIdx.x % p.n_runs);
   } else {
-    attend_tiles<D, false, kFp8, 2, false, kWindowed>(p, blockIdx.x, blockIdx.y, blockIdx.z);
+    attend_tiles<D, false, kFp8, kTiles, false, kWindowed>(p, blockIdx.x, blockIdx.y, blockIdx.z);
   }
 }
 

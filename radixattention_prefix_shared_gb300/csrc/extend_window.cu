@@ -10,35 +10,46 @@ using namespace ext;
 
 namespace {
 
-// A call with fewer tiles than this part has SMs deals each tile's key blocks
-// to as many CTAs as fill them (one CTA of this pipeline an SM).
+// A call with fewer tile pairs than this part has SMs deals each pair's key
+// blocks to as many CTAs as fill them (one CTA of two Q tiles an SM).
 constexpr int kFillCtas = 152;
 constexpr int kMaxRuns = 32;  // a lane each in the combine
 // Key blocks from which dealing them out pays for the combine: a block takes a
 // CTA 1.6 us, the combine 2 us and its launch as much of the host's time.
 constexpr int kMinBlocks = 4;
+// bf16 pools: up to this many key blocks, more CTAs than SMs hold one Q tile
+// each, two on an SM, so that one's start and end overlap the other's work;
+// longer lists are bound by the K/V copies, which one-tile CTAs make twice.
+// 17 requests of up to 700 tokens, 4 query heads of 64 a KV head: 16.3 -> 15.5
+// us with 2 blocks, 23.3 -> 19.6 with 3, 34.1 -> 35.5 with 8; 16 of 300 tokens,
+// 2 heads of 128: 33.6 -> 26.9, 39.4 -> 40.0 with 3, 44.8 -> 47.9 with 4.
+// Requests that never fill a second tile always take one (40 of 3 to 30
+// tokens: 22.3 -> 15.4 us with 1 block, 57.1 -> 51.5 with 7).
+constexpr int kOneTileBlocks = 3;
 
 struct Shape {
-  int32_t per_cta;  // tokens of a CTA's two Q tiles
-  int32_t tiles;    // CTAs along x for the longest request
+  bool one_tile;
+  int32_t tiles;   // CTAs along x for the longest request, without runs
   int32_t n_runs;
   Shape(int32_t batch, int32_t total_extend, int32_t max_extend, int32_t max_prefix, int32_t window, int32_t sinks,
-        int32_t Hq, int32_t Hkv) {
-    per_cta = 2 * (BM / (Hq / Hkv));
-    tiles = (max_extend + per_cta - 1) / per_cta;
-    // tiles with queries: every request's last one may be short
-    int64_t live = (int64_t)total_extend / per_cta + batch;
-    if (live > (int64_t)tiles * batch) live = (int64_t)tiles * batch;
-    // keys of a tile: its queries' positions, the window before them, the sinks
-    const int64_t own = max_extend < per_cta ? max_extend : per_cta;
-    int64_t keys = (int64_t)window - 1 + own + sinks;
+        int32_t Hq, int32_t Hkv, bool kv_fp8) {
+    const int32_t tpt = BM / (Hq / Hkv), pair = 2 * tpt;
+    const auto ceil_div = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+    // CTAs with queries: every request's last one may be short
+    int64_t live = (int64_t)total_extend / pair + batch;
+    const int64_t most = ceil_div(max_extend, pair) * batch;
+    if (live > most) live = most;
+    live *= Hkv;
+    // keys of a pair: its queries' positions, the window before them, the sinks
+    int64_t keys = (int64_t)window - 1 + (max_extend < pair ? max_extend : pair) + sinks;
     if (keys > (int64_t)max_prefix + max_extend) keys = (int64_t)max_prefix + max_extend;
-    int64_t runs = live * Hkv > 0 ? kFillCtas / (live * Hkv) : 1;
-    const int64_t blocks = (keys + BN - 1) / BN;
+    const int64_t blocks = ceil_div(keys, BN);
+    int64_t runs = live > 0 && blocks >= kMinBlocks ? kFillCtas / live : 1;
     if (runs > blocks) runs = blocks;
-    if (blocks < kMinBlocks) runs = 1;
     if (runs > kMaxRuns) runs = kMaxRuns;
     n_runs = runs < 1 ? 1 : (int32_t)runs;
+    one_tile = !kv_fp8 && n_runs == 1 && (max_extend <= tpt || (blocks <= kOneTileBlocks && live > kFillCtas));
+    tiles = (int32_t)ceil_div(max_extend, one_tile ? tpt : pair);
   }
 };
 
@@ -97,13 +108,13 @@ __global__ void __launch_bounds__(128) extend_window_combine_kernel(Params p) {
   for (int e = 0; e < E; ++e) o[lane + 32 * e] = __float2bfloat16_rn(acc[e] * inv);
 }
 
-template <int D, bool kFp8, bool kRuns>
+template <int D, bool kFp8, bool kRuns, int kTiles>
 sgl_status launch(const Params& prm, const ExtendArgs& a, const Shape& s, cudaStream_t stream) {
-  constexpr int kThreads = Roles<kFp8>::kThreads;
-  constexpr int kSmem = smem_bytes<D, kFp8>();
-  auto kern = extend_window_kernel<D, kFp8, kRuns>;
-  if (kernel_blocks_per_sm<extend_window_kernel<D, kFp8, kRuns>>(kSmem, kThreads) < 0) return SGL_ERR_CUDA;
-  if (Roles<kFp8>::kSplitRegs && !kernel_regs_at_least<extend_window_kernel<D, kFp8, kRuns>>(Roles<kFp8>::kLaunchRegs))
+  constexpr int kThreads = Roles<kFp8, kTiles>::kThreads;
+  constexpr int kSmem = smem_bytes<D, kFp8, kTiles>();
+  auto kern = extend_window_kernel<D, kFp8, kRuns, kTiles>;
+  if (kernel_blocks_per_sm<extend_window_kernel<D, kFp8, kRuns, kTiles>>(kSmem, kThreads) < 0) return SGL_ERR_CUDA;
+  if (Roles<kFp8, kTiles>::kSplitRegs && !kernel_regs_at_least<extend_window_kernel<D, kFp8, kRuns, kTiles>>(Roles<kFp8>::kLaunchRegs))
     return SGL_ERR_UNSUPPORTED;
   const dim3 grid((unsigned)(s.tiles * s.n_runs), (unsigned)prm.Hkv, (unsigned)a.batch);
   kern<<<grid, kThreads, kSmem, stream>>>(prm);
@@ -118,7 +129,11 @@ sgl_status launch(const Params& prm, const ExtendArgs& a, const Shape& s, cudaSt
 
 template <int D, bool kFp8>
 sgl_status run(const Params& prm, const ExtendArgs& a, const Shape& s, cudaStream_t stream) {
-  return s.n_runs > 1 ? launch<D, kFp8, true>(prm, a, s, stream) : launch<D, kFp8, false>(prm, a, s, stream);
+  if (s.n_runs > 1) return launch<D, kFp8, true, 2>(prm, a, s, stream);
+  if constexpr (!kFp8) {
+    if (s.one_tile) return launch<D, kFp8, false, 1>(prm, a, s, stream);
+  }
+  return launch<D, kFp8, false, 2>(prm, a, s, stream);
 }
 
 }  // namespace
@@ -128,7 +143,8 @@ size_t extend_window_workspace_bytes(int32_t batch, int32_t total_extend, int32_
   if (batch <= 0 || total_extend <= 0 || max_extend <= 0 || max_prefix < 0 || window <= 0 || sinks < 0 || Hkv <= 0 ||
       Hq < Hkv || Hq / Hkv > BM)
     return extend_workspace_bytes();
-  return layout(Shape(batch, total_extend, max_extend, max_prefix, window, sinks, Hq, Hkv), total_extend, Hq, D,
+  // (the runs, all that the workspace depends on, are the same for either pool type)
+  return layout(Shape(batch, total_extend, max_extend, max_prefix, window, sinks, Hq, Hkv, false), total_extend, Hq, D,
                 nullptr, nullptr);
 }
 
@@ -138,7 +154,7 @@ sgl_status launch_extend_window(const ExtendArgs& a, cudaStream_t stream) {
   const sgl_status st = make_extend_params(a, &prm);
   if (st != SGL_OK) return st;
   const Shape s(a.batch, a.total_extend, a.max_extend, a.max_prefix, a.window, a.sinks, a.num_q_heads,
-                a.num_kv_heads);
+                a.num_kv_heads, a.kv_fp8);
   prm.batch = a.batch;
   prm.n_runs = s.n_runs;
   layout(s, a.total_extend, a.num_q_heads, a.head_dim, a.workspace, &prm);

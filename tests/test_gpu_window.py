@@ -165,19 +165,30 @@ def test_extend_windows_across_blocks(window, sinks, fp8):
     assert_within(W.bf16_bits(case.extend()), want, terms, fp8, rows=tokens)
 
 
-# (Hq, Hkv, D, requests, window, sinks): enough tiles for every SM, so that no
-# tile's keys are dealt to several CTAs (the shapes above are dealt)
-MANY = [(16, 16, 64, 12, 200, 3), (40, 20, 128, 9, 70, 0), (96, 32, 64, 5, 300, 130)]
+# (Hq, Hkv, D, requests, window, sinks, longest extend): enough tiles for every
+# SM, so that no tile's keys are dealt to several CTAs (the shapes above are
+# dealt); requests of one Q tile, of two with few keys (one tile a CTA over
+# bf16 pools) and of two with many (two tiles a CTA)
+MANY = [(16, 16, 64, 12, 200, 3, 25), (40, 20, 128, 9, 70, 0, 25), (96, 32, 64, 5, 300, 130, 25),
+        (40, 40, 64, 5, 90, 2, 150), (80, 40, 128, 4, 100, 0, 100), (40, 40, 64, 5, 600, 4, 150),
+        (80, 40, 128, 4, 500, 20, 100)]
 
 
 @pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
-@pytest.mark.parametrize("shape", MANY, ids=lambda s: f"{s[0]}q{s[1]}kv{s[2]}d_b{s[3]}")
+@pytest.mark.parametrize("shape", MANY, ids=lambda s: f"{s[0]}q{s[1]}kv{s[2]}d_w{s[4]}_e{s[6]}")
 def test_extend_of_many_tiles(shape, fp8):
-    Hq, Hkv, D, n, window, sinks = shape
+    Hq, Hkv, D, n, window, sinks, longest = shape
     g = np.random.default_rng(n)
-    case = Case(attention_case(n, Hq=Hq, Hkv=Hkv, D=D, prefix=g.integers(0, 400, n).tolist(),
-                               ext=g.integers(0, 25, n).tolist(), window=window, sinks=sinks, fp8=fp8))
-    assert_within(W.bf16_bits(case.extend()), *case.want_extend(), fp8, what=str(shape))
+    ext = g.integers(0, longest, n).tolist()
+    ext[1] = longest - 1
+    case = Case(attention_case(n, Hq=Hq, Hkv=Hkv, D=D, prefix=g.integers(0, 800, n).tolist(), ext=ext, window=window,
+                               sinks=sinks, fp8=fp8))
+    total = sum(ext)
+    picked = {0, ext[0], ext[0] + 63, ext[0] + longest - 2, total - 1} | set(g.integers(0, total, 12).tolist())
+    tokens = sorted(t for t in picked if t < total)
+    out = case.extend()
+    assert torch.isfinite(out).all()
+    assert_within(W.bf16_bits(out), *case.want_extend(tokens), fp8, rows=tokens, what=str(shape))
 
 
 def test_extend_full_window_equals_extend():
