@@ -271,7 +271,6 @@ struct Params {
   const int32_t* extend_lens;
   __nv_bfloat16* out;
   int32_t Hq, Hkv, g, tpt, rows_used;
-  uint32_t g_inv;  // row_token
   float scale_log2;
   // multiplies the normalised output (extend) or the unnormalised P.V rows
   // (group mode); 1 on a bf16 pool
@@ -298,6 +297,7 @@ struct Params {
   // n_runs CTAs, whose fp32 states go to entry (row * Hq + head) * n_runs + run
   // of part_ml / part_acc for a combine (1: the CTA writes the output).
   int32_t n_runs;
+  uint32_t g_inv;  // row_token (here at the end: 4 bytes before scale_log2 cost the causal bf16 kernel 1.7%)
 };
 
 // The keys a CTA's queries see in a sliding-window extend.  Query position P
@@ -339,12 +339,21 @@ struct WindowKeys {
   SGL_DEV int32_t first(int32_t P) const { return max(0, P - window + 1) - lo + n_first - i0; }
 };
 
-// Token of row `row` < 128 of a Q tile, row / g, by the 16-bit reciprocal g_inv
-// = ceil(2^16 / g): exact, since its error of less than g / 2^16 a row stays
-// below 1 / g over 128 rows.  (The compiler's division by a runtime g made the
-// Q copies and the output's stores issue-bound.)
+// Token of row `row` < 128 of a Q tile, row / g.  kFast: by the 16-bit
+// reciprocal g_inv = ceil(2^16 / g), exact since its error of less than g /
+// 2^16 a row stays below 1 / g over 128 rows; the sliding-window kernels, whose
+// CTAs can be a few blocks long, are issue-bound in the Q copies and the
+// output's stores without it.  (Only they take it: the causal kernels' register
+// allocation is at its limit, and what moved it cost them 1-2%.)
 __host__ __device__ inline uint32_t row_token_inv(int32_t g) { return (65536u + (uint32_t)g - 1u) / (uint32_t)g; }
-SGL_DEV int row_token(const Params& p, int row) { return (int)(((uint32_t)row * p.g_inv) >> 16); }
+template <bool kFast>
+SGL_DEV int row_token(const Params& p, int row) {
+  return kFast ? (int)(((uint32_t)row * p.g_inv) >> 16) : row / p.g;
+}
+template <bool kFast>
+SGL_DEV int row_head(const Params& p, int row) {
+  return kFast ? row - row_token<true>(p, row) * p.g : row % p.g;
+}
 
 // The lowest n bits (none for n <= 0, all from 32 on).
 SGL_DEV uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u); }
@@ -408,9 +417,9 @@ static_assert(staging_fits<128, false>() && staging_fits<64, false>() && staging
 // Where a run's fp32 P.V row of row rr of tile t goes (nullptr: no query).
 template <int D>
 SGL_DEV uint8_t* state_row(const Params& p, int q0, int t, int rr, int e, int off, int kvh, int run) {
-  const int rt = row_token(p, rr), tok = q0 + t * p.tpt + rt;
+  const int tok = q0 + t * p.tpt + row_token<true>(p, rr);
   if (rr >= p.rows_used || tok >= e) return nullptr;
-  const int64_t row = (int64_t)(off + tok) * p.Hq + (int64_t)kvh * p.g + (rr - rt * p.g);
+  const int64_t row = (int64_t)(off + tok) * p.Hq + (int64_t)kvh * p.g + row_head<true>(p, rr);
   return reinterpret_cast<uint8_t*>(p.part_acc + (row * p.n_runs + run) * D);
 }
 
@@ -428,22 +437,21 @@ constexpr bool q_by_softmax() { return !kFp8 || kGroup; }
 // q0 + t * tpt + m / g, head m % g of the KV head's group; rows past the
 // CTA's tokens are zero-filled.  Group mode gathers the members' decode
 // queries.
-template <int D, bool kGroup, int kTiles>
+template <int D, bool kGroup, int kTiles, bool kWindow>
 SGL_DEV void issue_q_copies(const Params& p, uint32_t sQ_a, int ltid, int nthreads, int kvh, int e, int mbeg,
                             int q0, int off, int tiles) {
   using C = Cfg<D, false>;
   const int ci = ltid & 7, step = nthreads >> 3;
 #pragma unroll
   for (int t = 0; t < kTiles; ++t) {
-    if (t >= tiles) break;
+    if (kWindow && t >= tiles) break;
     for (int row = ltid >> 3; row < 128; row += step) {
-      const int rt = row_token(p, row), rh = row - rt * p.g;
-      const int tok = q0 + t * p.tpt + rt;
+      const int tok = q0 + t * p.tpt + row_token<kWindow>(p, row);
       bool valid = row < p.rows_used && tok < e;
       // the query row: suffix token off+tok, or member tok's decode query
       int64_t qrow = valid ? (kGroup ? (int64_t)p.members[mbeg + tok] : (int64_t)(off + tok)) : 0;
       if (kGroup && (qrow < 0 || qrow >= p.batch)) valid = false, qrow = 0;
-      const __nv_bfloat16* src = p.q + (qrow * p.Hq + (int64_t)kvh * p.g + rh) * D + ci * 8;
+      const __nv_bfloat16* src = p.q + (qrow * p.Hq + (int64_t)kvh * p.g + row_head<kWindow>(p, row)) * D + ci * 8;
 #pragma unroll
       for (int c = 0; c < C::kChunks; ++c)
         cp_async_16(sQ_a + t * C::kTileBytes + c * C::kChunkBytes + sw128(row, ci),
@@ -480,10 +488,10 @@ SGL_DEV void widen_q_in_place(uint32_t sQ_a, int ltid, int nthreads) {
 // nthreads of them; the first `tiles` tiles only), signalled on q_full: on a bf16 pool each thread's
 // arrival fires when its copies land; on an e4m3 pool each thread waits for
 // its own copies, widens them and orders them for the tensor core first.
-template <int D, bool kGroup, bool kFp8, int kTiles>
+template <int D, bool kGroup, bool kFp8, int kTiles, bool kWindow>
 SGL_DEV void load_q_tiles(const Params& p, uint32_t sQ_a, uint64_t* q_full, int ltid, int nthreads, int kvh,
                           int e, int mbeg, int q0, int off, int tiles) {
-  issue_q_copies<D, kGroup, kTiles>(p, sQ_a, ltid, nthreads, kvh, e, mbeg, q0, off, tiles);
+  issue_q_copies<D, kGroup, kTiles, kWindow>(p, sQ_a, ltid, nthreads, kvh, e, mbeg, q0, off, tiles);
   if constexpr (kFp8) {
     cp_async_wait_all();
     widen_q_in_place<D>(sQ_a, ltid, nthreads);
@@ -800,7 +808,7 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz, int run = 0) 
     if constexpr (R::kFullRows) {
     // ------------------------------------------------------------ softmax (whole rows)
     if constexpr (kQSoft)
-      load_q_tiles<D, kGroup, kFp8, kTiles>(p, sQ_a, &bars->q_full, tid, kQThreads, kvh, e, mbeg, q0, off,
+      load_q_tiles<D, kGroup, kFp8, kTiles, kWindow>(p, sQ_a, &bars->q_full, tid, kQThreads, kvh, e, mbeg, q0, off,
                                                 kRuns && !two_tiles ? 1 : kTiles);
     // warp w: Q tile t = w / 4, TMEM lane quarter q = w % 4 (rows 32q..);
     // every thread owns one row: all 128 keys of a block, all D columns of O.
@@ -813,7 +821,7 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz, int run = 0) 
     const uint32_t lane_off = (uint32_t)(q * 32) << 16;
     const uint32_t tS = tmem + lane_off + col_s(t);
     const uint32_t tO = tmem + lane_off + col_o<kTiles>(t);
-    const int tok = q0 + t * p.tpt + row_token(p, row);
+    const int tok = q0 + t * p.tpt + row_token<kWindow>(p, row);
     const bool row_valid = row < p.rows_used && tok < e;
     const int tok_i = row_valid ? tok : (1 << 30);  // padding rows see every key
     // kWindow: the row's bounds in the CTA's key list (padding rows: every key)
@@ -962,7 +970,7 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz, int run = 0) 
                          o[4 * v + 3]);
         }
         warp_store_rows<4 * D, kStride>(stage, q * 32, [&](int rr) { return state_row<D>(p, q0, t, rr, e, off, kvh, run); });
-        const int64_t ent = ((int64_t)(off + tok) * p.Hq + (int64_t)kvh * p.g + (row - row_token(p, row) * p.g)) * p.n_runs + run;
+        const int64_t ent = ((int64_t)(off + tok) * p.Hq + (int64_t)kvh * p.g + row_head<true>(p, row)) * p.n_runs + run;
         if (row_valid) p.part_ml[ent] = make_float2(m_ref, l);
       } else {
         const float inv = l > 0.f ? (kFp8 ? p.o_scale : 1.f) / l : 0.f;
@@ -983,10 +991,10 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz, int run = 0) 
                          w[4 * v + 3]);
         }
         warp_store_rows<2 * D, kStride>(stage, q * 32, [&](int rr) -> uint8_t* {
-          const int rt = row_token(p, rr), tk = q0 + t * p.tpt + rt;
+          const int tk = q0 + t * p.tpt + row_token<kWindow>(p, rr);
           if (rr >= p.rows_used || tk >= e) return nullptr;
           return reinterpret_cast<uint8_t*>(p.out +
-                                            ((int64_t)(off + tk) * p.Hq + (int64_t)kvh * p.g + (rr - rt * p.g)) * D);
+                                            ((int64_t)(off + tk) * p.Hq + (int64_t)kvh * p.g + row_head<kWindow>(p, rr)) * D);
         });
       }
     }
@@ -995,7 +1003,7 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz, int run = 0) 
     if constexpr (!R::kFullRows) {
     // ------------------------------------------------------------ softmax
     if constexpr (kQSoft)
-      load_q_tiles<D, kGroup, kFp8, kTiles>(p, sQ_a, &bars->q_full, tid, kQThreads, kvh, e, mbeg, q0, off,
+      load_q_tiles<D, kGroup, kFp8, kTiles, kWindow>(p, sQ_a, &bars->q_full, tid, kQThreads, kvh, e, mbeg, q0, off,
                                                 kRuns && !two_tiles ? 1 : kTiles);
     // warp w: Q tile t, key-column half h, TMEM lane quarter q (rows 32q..)
     const int t = (warp >> 2) % kTiles, h = warp / (4 * kTiles), q = warp & 3;
@@ -1006,7 +1014,7 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz, int run = 0) 
     const uint32_t pair_bar = 1 + t * 4 + q;  // named barrier of the two halves of these rows
     float* xchg_mine = &bars->xchg[t][h][row];
     const float* xchg_other = &bars->xchg[t][h ^ 1][row];
-    const int tok = q0 + t * p.tpt + row_token(p, row);
+    const int tok = q0 + t * p.tpt + row_token<kWindow>(p, row);
     const bool row_valid = row < p.rows_used && tok < e;
     const int tok_i = row_valid ? tok : (1 << 30);  // padding rows see every key
     // kWindow: the row's bounds in the CTA's key list (padding rows: every key)
@@ -1180,7 +1188,7 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz, int run = 0) 
           uint8_t* dst = state_row<D>(p, q0, t, rr, e, off, kvh, run);
           return dst == nullptr ? dst : dst + 2 * D * h;
         });
-        const int64_t ent = ((int64_t)(off + tok) * p.Hq + (int64_t)kvh * p.g + (row - row_token(p, row) * p.g)) * p.n_runs + run;
+        const int64_t ent = ((int64_t)(off + tok) * p.Hq + (int64_t)kvh * p.g + row_head<true>(p, row)) * p.n_runs + run;
         if (row_valid && h == 0) p.part_ml[ent] = make_float2(m_ref, lrow);
       }
     } else if (ok) {
@@ -1204,10 +1212,10 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz, int run = 0) 
                        w[4 * v + 3]);
       }
       warp_store_rows<D, kStride>(stage, q * 32, [&](int rr) -> uint8_t* {
-        const int rt = row_token(p, rr), tk = q0 + t * p.tpt + rt;
+        const int tk = q0 + t * p.tpt + row_token<kWindow>(p, rr);
         if (rr >= p.rows_used || tk >= e) return nullptr;
         return reinterpret_cast<uint8_t*>(
-            p.out + ((int64_t)(off + tk) * p.Hq + (int64_t)kvh * p.g + (rr - rt * p.g)) * D + (D / 2) * h);
+            p.out + ((int64_t)(off + tk) * p.Hq + (int64_t)kvh * p.g + row_head<kWindow>(p, rr)) * D + (D / 2) * h);
       });
     }
     }
