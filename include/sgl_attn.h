@@ -375,6 +375,9 @@ sgl_status sgl_cascade_decode_attention_fp8(
  *                 never read.
  *     workspace : >= sgl_decode_window_workspace_bytes(batch, max_seq_len,
  *                 window, sinks, dims); scratch, nothing in it outlasts a call.
+ *                 (Both workspace sizes grow with every argument but dims: one
+ *                 for the largest values serves all smaller calls.  Calls whose
+ *                 kernels may overlap need a workspace each.)
  * sgl_extend_attention_window -- the suffix queries of sgl_extend_attention
  *   over those keys (suffix query i is at position prefix_lens[r] + i).  Every
  *   key and value, the suffix's too, is read from the pool through
@@ -442,7 +445,7 @@ sgl_status sgl_extend_attention_window_fp8(const void* q, const void* pool_k, co
  * angle is positions[axis, t] * inv_freq[i], axis = freq_axis[i] (0 with one
  * axis).  Q rows go to q_out, K rows to pool_k[slots[t]], the V rows
  * unchanged to pool_v[slots[t]].  Arithmetic is fp32 with one rounding at the
- * end; angles keep 2^-24 turns at any int32 position.
+ * end; angles keep 2^-24 turns at any int32 position (|inv_freq| up to 2^8).
  *   q            : bf16, token t's Hq rows of D side by side at t * q_stride
  *                  elements; k, v: Hkv rows at t * k_stride, t * v_stride.  The
  *                  strides (multiples of 8, >= the rows) let the three be

@@ -790,6 +790,7 @@ sgl_status extend_window_entry(const void* q, const void* pool_k, const void* po
   a.window = window;
   a.sinks = sinks;
   a.max_prefix = max_prefix;
+  a.workspace_bytes = workspace_bytes;
   return launch_extend_window(a, reinterpret_cast<cudaStream_t>(stream));
 }
 }  // namespace

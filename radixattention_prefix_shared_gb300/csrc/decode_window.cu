@@ -25,13 +25,9 @@ namespace {
 constexpr int kFillUnits = 1824;
 constexpr int kMinRun = 256;
 
-int32_t splits_for(int64_t units, int32_t keys) {
-  const int32_t fill = (int32_t)((kFillUnits + units - 1) / units);
-  const int32_t most = (int32_t)(((int64_t)keys + kMinRun - 1) / kMinRun);
-  const int32_t least = (int32_t)(((int64_t)keys + kItemMax - 1) / kItemMax);
-  const int32_t s = fill < most ? fill : most;
-  return s > least ? s : least;
-}
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int32_t most_runs(int32_t keys) { return (int32_t)ceil_div(keys, kMinRun); }
+int32_t least_runs(int32_t keys) { return (int32_t)ceil_div(keys, kItemMax); }
 
 // Virtual KV heads, and the runs a request is cut into.
 struct Shape {
@@ -44,21 +40,22 @@ struct Shape {
     G = Hq / Hkv;
     const int64_t seen = (int64_t)window + sinks;
     keys = (int32_t)(seen < max_seq_len ? seen : max_seq_len);
-    const int64_t units = (int64_t)batch * (spans_for(Hkv, split, kv_fp8) ? Hkv / kWarps : Hkv);
-    n_splits = splits_for(units, keys);
-    chunk = (int32_t)(((int64_t)keys + n_splits - 1) / n_splits);
+    const int64_t fill = ceil_div(kFillUnits, (int64_t)batch * (spans_for(Hkv, split, kv_fp8) ? Hkv / kWarps : Hkv));
+    n_splits = fill < most_runs(keys) ? (int32_t)fill : most_runs(keys);
+    if (n_splits < least_runs(keys)) n_splits = least_runs(keys);
+    chunk = (int32_t)ceil_div(keys, n_splits);
   }
 };
 
-size_t ws_bytes(int32_t batch, const Shape& s, int32_t D, void* base, Ws* ws) {
-  const size_t n = s.n_splits > 1 ? (size_t)batch * s.n_splits * s.Hkv * s.G : 0;
-  const size_t o_acc = align256(sizeof(float2) * n);
+// (max, sum) and P.V row of every (request, run, query head)
+size_t ws_bytes(int64_t entries, int32_t D, void* base, Ws* ws) {
+  const size_t o_acc = align256(sizeof(float2) * (size_t)entries);
   if (ws != nullptr) {
     char* b = static_cast<char*>(base);
     ws->part_ml = reinterpret_cast<float2*>(b);
     ws->part_acc = reinterpret_cast<float*>(b + o_acc);
   }
-  return o_acc + sizeof(float) * n * D;
+  return o_acc + sizeof(float) * (size_t)entries * D;
 }
 
 // Ring stages: the split kernel's, but four on the CUDA-core path over an e4m3
@@ -211,10 +208,21 @@ sgl_status run_g(int G, const Params& prm, cudaStream_t stream) {
 size_t decode_window_workspace_bytes(int32_t batch, int32_t max_seq_len, int32_t window, int32_t sinks, int32_t Hq,
                                      int32_t Hkv, int32_t D) {
   if (batch <= 0 || max_seq_len <= 0 || window <= 0 || sinks < 0 || Hkv <= 0 || Hq < Hkv) return 256;
-  // (either pool type)
-  const size_t a = ws_bytes(batch, Shape(batch, max_seq_len, window, sinks, Hq, Hkv, false), D, nullptr, nullptr);
-  const size_t b = ws_bytes(batch, Shape(batch, max_seq_len, window, sinks, Hq, Hkv, true), D, nullptr, nullptr);
-  return 256 + (a > b ? a : b);
+  // A bound that grows with every argument, so that a workspace for a server's
+  // largest call serves its smaller ones: fewer requests are cut into more runs
+  // each, and batch x runs is at most the larger of the runs that kItemMax
+  // asks for and of kFillUnits CTAs' over the call's head groups (the e4m3
+  // pool's where it takes fewer) plus one a request, and never past runs of
+  // kMinRun keys.
+  const int64_t seen = (int64_t)window + sinks;
+  const int32_t keys = (int32_t)(seen < max_seq_len ? seen : max_seq_len);
+  if (most_runs(keys) <= 1) return 256;
+  const int32_t split = kv_split_for(Hq / Hkv), heads = Hkv * split;
+  const int64_t fill = ceil_div(kFillUnits, spans_possible(heads, split) ? heads / kWarps : heads) + batch;
+  int64_t runs = (int64_t)batch * least_runs(keys);
+  if (runs < fill) runs = fill;
+  if (runs > (int64_t)batch * most_runs(keys)) runs = (int64_t)batch * most_runs(keys);
+  return 256 + ws_bytes(runs * Hq, D, nullptr, nullptr);
 }
 
 sgl_status launch_decode_window(const DecodeArgs& a, cudaStream_t stream) {
@@ -222,7 +230,8 @@ sgl_status launch_decode_window(const DecodeArgs& a, cudaStream_t stream) {
   if (decode_shape_supported(a.num_q_heads, a.num_kv_heads) != SGL_OK) return SGL_ERR_UNSUPPORTED;
   const Shape s(a.batch, a.max_seq_len, a.window, a.sinks, a.num_q_heads, a.num_kv_heads, a.kv_fp8);
   Params prm = {};
-  if (ws_bytes(a.batch, s, a.head_dim, a.workspace, &prm.ws) > a.workspace_bytes) return SGL_ERR_WORKSPACE;
+  const int64_t entries = s.n_splits > 1 ? (int64_t)a.batch * s.n_splits * a.num_q_heads : 0;
+  if (ws_bytes(entries, a.head_dim, a.workspace, &prm.ws) > a.workspace_bytes) return SGL_ERR_WORKSPACE;
   prm.q = static_cast<const __nv_bfloat16*>(a.q);
   prm.pool_k = static_cast<const uint8_t*>(a.pool_k);
   prm.pool_v = static_cast<const uint8_t*>(a.pool_v);

@@ -295,8 +295,10 @@ struct Params {
   int32_t window, sinks;  // sliding-window extend (WindowKeys)
   // A sliding-window extend of few tiles deals each tile's key blocks to
   // n_runs CTAs, whose fp32 states go to entry (row * Hq + head) * n_runs + run
-  // of part_ml / part_acc for a combine (1: the CTA writes the output).
+  // of part_ml / part_acc for a combine (1: the CTA writes the output).  Rows
+  // from state_rows on (extend lengths above the host's) have no entry.
   int32_t n_runs;
+  int64_t state_rows;  // tokens x Hq
   uint32_t g_inv;  // row_token (here at the end: 4 bytes before scale_log2 cost the causal bf16 kernel 1.7%)
 };
 
@@ -420,6 +422,7 @@ SGL_DEV uint8_t* state_row(const Params& p, int q0, int t, int rr, int e, int of
   const int tok = q0 + t * p.tpt + row_token<true>(p, rr);
   if (rr >= p.rows_used || tok >= e) return nullptr;
   const int64_t row = (int64_t)(off + tok) * p.Hq + (int64_t)kvh * p.g + row_head<true>(p, rr);
+  if (row >= p.state_rows) return nullptr;
   return reinterpret_cast<uint8_t*>(p.part_acc + (row * p.n_runs + run) * D);
 }
 
@@ -747,7 +750,7 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz, int run = 0) 
       for (int o = 16; o > 0; o >>= 1) at += __shfl_xor_sync(0xffffffffu, at, o);
       for (int i = tid; i < (q_end - q0) * p.g; i += (int)blockDim.x) {
         const int64_t row = (int64_t)(at + q0 + i / p.g) * p.Hq + (int64_t)kvh * p.g + i % p.g;
-        p.part_ml[row * p.n_runs + run] = make_float2(-INFINITY, 0.f);
+        if (row < p.state_rows) p.part_ml[row * p.n_runs + run] = make_float2(-INFINITY, 0.f);
       }
       return;
     }
@@ -970,8 +973,8 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz, int run = 0) 
                          o[4 * v + 3]);
         }
         warp_store_rows<4 * D, kStride>(stage, q * 32, [&](int rr) { return state_row<D>(p, q0, t, rr, e, off, kvh, run); });
-        const int64_t ent = ((int64_t)(off + tok) * p.Hq + (int64_t)kvh * p.g + row_head<true>(p, row)) * p.n_runs + run;
-        if (row_valid) p.part_ml[ent] = make_float2(m_ref, l);
+        const int64_t ent = (int64_t)(off + tok) * p.Hq + (int64_t)kvh * p.g + row_head<true>(p, row);
+        if (row_valid && ent < p.state_rows) p.part_ml[ent * p.n_runs + run] = make_float2(m_ref, l);
       } else {
         const float inv = l > 0.f ? (kFp8 ? p.o_scale : 1.f) / l : 0.f;
         constexpr int kStride = out_stride<D>();
@@ -1188,8 +1191,8 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz, int run = 0) 
           uint8_t* dst = state_row<D>(p, q0, t, rr, e, off, kvh, run);
           return dst == nullptr ? dst : dst + 2 * D * h;
         });
-        const int64_t ent = ((int64_t)(off + tok) * p.Hq + (int64_t)kvh * p.g + row_head<true>(p, row)) * p.n_runs + run;
-        if (row_valid && h == 0) p.part_ml[ent] = make_float2(m_ref, lrow);
+        const int64_t ent = (int64_t)(off + tok) * p.Hq + (int64_t)kvh * p.g + row_head<true>(p, row);
+        if (row_valid && h == 0 && ent < p.state_rows) p.part_ml[ent * p.n_runs + run] = make_float2(m_ref, lrow);
       }
     } else if (ok) {
       tc_fence_after();

@@ -27,23 +27,36 @@ constexpr int kMinBlocks = 4;
 // tokens: 22.3 -> 15.4 us with 1 block, 57.1 -> 51.5 with 7).
 constexpr int kOneTileBlocks = 3;
 
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Key blocks of a pair of tiles of `tpt` tokens each: its queries' positions,
+// the window before them, the sinks.
+int64_t key_blocks(int32_t tpt, int32_t max_extend, int32_t max_prefix, int32_t window, int32_t sinks) {
+  int64_t keys = (int64_t)window - 1 + (max_extend < 2 * tpt ? max_extend : 2 * tpt) + sinks;
+  if (keys > (int64_t)max_prefix + max_extend) keys = (int64_t)max_prefix + max_extend;
+  return ceil_div(keys, BN);
+}
+
+int64_t query_rows(int32_t batch, int32_t total_extend, int32_t max_extend) {
+  const int64_t most = (int64_t)batch * max_extend;
+  return total_extend < most ? total_extend : most;
+}
+
 struct Shape {
   bool one_tile;
   int32_t tiles;   // CTAs along x for the longest request, without runs
   int32_t n_runs;
+  int64_t rows;    // tokens that can have queries (total_extend may count padding)
   Shape(int32_t batch, int32_t total_extend, int32_t max_extend, int32_t max_prefix, int32_t window, int32_t sinks,
         int32_t Hq, int32_t Hkv, bool kv_fp8) {
     const int32_t tpt = BM / (Hq / Hkv), pair = 2 * tpt;
-    const auto ceil_div = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+    rows = query_rows(batch, total_extend, max_extend);
     // CTAs with queries: every request's last one may be short
-    int64_t live = (int64_t)total_extend / pair + batch;
+    int64_t live = rows / pair + batch;
     const int64_t most = ceil_div(max_extend, pair) * batch;
     if (live > most) live = most;
     live *= Hkv;
-    // keys of a pair: its queries' positions, the window before them, the sinks
-    int64_t keys = (int64_t)window - 1 + (max_extend < pair ? max_extend : pair) + sinks;
-    if (keys > (int64_t)max_prefix + max_extend) keys = (int64_t)max_prefix + max_extend;
-    const int64_t blocks = ceil_div(keys, BN);
+    const int64_t blocks = key_blocks(tpt, max_extend, max_prefix, window, sinks);
     int64_t runs = live > 0 && blocks >= kMinBlocks ? kFillCtas / live : 1;
     if (runs > blocks) runs = blocks;
     if (runs > kMaxRuns) runs = kMaxRuns;
@@ -53,17 +66,16 @@ struct Shape {
   }
 };
 
-// status word (256 bytes), then (max, sum) and P.V rows of every (token, query
+// status word (256 bytes), then (max, sum) and P.V row of every (token, query
 // head, run)
-size_t layout(const Shape& s, int32_t total_extend, int32_t Hq, int32_t D, void* base, Params* prm) {
-  const size_t entries = s.n_runs > 1 ? (size_t)total_extend * Hq * s.n_runs : 0;
+size_t layout(int64_t entries, int32_t D, void* base, Params* prm) {
   const size_t o_ml = extend_workspace_bytes();
-  const size_t o_acc = o_ml + (entries * sizeof(float2) + 255) / 256 * 256;
+  const size_t o_acc = o_ml + ((size_t)entries * sizeof(float2) + 255) / 256 * 256;
   if (prm != nullptr) {
     prm->part_ml = reinterpret_cast<float2*>(static_cast<char*>(base) + o_ml);
     prm->part_acc = reinterpret_cast<float*>(static_cast<char*>(base) + o_acc);
   }
-  return o_acc + entries * D * sizeof(float);
+  return o_acc + (size_t)entries * D * sizeof(float);
 }
 
 // A warp a (token, query head): lane i holds run i's (max, sum); rows past
@@ -80,7 +92,7 @@ __global__ void __launch_bounds__(128) extend_window_combine_kernel(Params p) {
   // launched dependent on the extend kernel; every warp waits, so that this
   // grid never ends (and what follows it never starts) before that one
   grid_dep_wait();
-  if (row >= tokens * p.Hq) return;
+  if (row >= tokens * p.Hq || row >= p.state_rows) return;
   float2 ml = make_float2(-INFINITY, 0.f);
   if (lane < p.n_runs) ml = p.part_ml[row * p.n_runs + lane];
   float M = ml.x;
@@ -119,8 +131,7 @@ sgl_status launch(const Params& prm, const ExtendArgs& a, const Shape& s, cudaSt
   const dim3 grid((unsigned)(s.tiles * s.n_runs), (unsigned)prm.Hkv, (unsigned)a.batch);
   kern<<<grid, kThreads, kSmem, stream>>>(prm);
   if (kRuns) {
-    const int64_t rows = (int64_t)a.total_extend * prm.Hq;
-    if (launch_dependent(extend_window_combine_kernel<D>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, stream,
+    if (launch_dependent(extend_window_combine_kernel<D>, dim3((unsigned)((prm.state_rows + 3) / 4)), dim3(128), 0, stream,
                          prm) != cudaSuccess)
       return SGL_ERR_CUDA;
   }
@@ -143,9 +154,14 @@ size_t extend_window_workspace_bytes(int32_t batch, int32_t total_extend, int32_
   if (batch <= 0 || total_extend <= 0 || max_extend <= 0 || max_prefix < 0 || window <= 0 || sinks < 0 || Hkv <= 0 ||
       Hq < Hkv || Hq / Hkv > BM)
     return extend_workspace_bytes();
-  // (the runs, all that the workspace depends on, are the same for either pool type)
-  return layout(Shape(batch, total_extend, max_extend, max_prefix, window, sinks, Hq, Hkv, false), total_extend, Hq, D,
-                nullptr, nullptr);
+  // A bound that grows with every argument, so that a workspace for a server's
+  // largest call serves its smaller ones (fewer tiles are dealt to more CTAs
+  // each): live x runs <= kFillCtas, and a pair of tiles has 2 BM rows.
+  const int64_t blocks = key_blocks(BM / (Hq / Hkv), max_extend, max_prefix, window, sinks);
+  if (blocks < kMinBlocks) return extend_workspace_bytes();
+  int64_t entries = query_rows(batch, total_extend, max_extend) * Hq * (blocks < kMaxRuns ? blocks : kMaxRuns);
+  if (entries > (int64_t)kFillCtas * 2 * BM) entries = (int64_t)kFillCtas * 2 * BM;
+  return layout(entries, D, nullptr, nullptr);
 }
 
 sgl_status launch_extend_window(const ExtendArgs& a, cudaStream_t stream) {
@@ -157,7 +173,9 @@ sgl_status launch_extend_window(const ExtendArgs& a, cudaStream_t stream) {
                 a.num_kv_heads, a.kv_fp8);
   prm.batch = a.batch;
   prm.n_runs = s.n_runs;
-  layout(s, a.total_extend, a.num_q_heads, a.head_dim, a.workspace, &prm);
+  prm.state_rows = s.rows * a.num_q_heads;
+  if (layout(s.n_runs > 1 ? prm.state_rows * s.n_runs : 0, a.head_dim, a.workspace, &prm) > a.workspace_bytes)
+    return SGL_ERR_WORKSPACE;
   if (a.head_dim == 128)
     return a.kv_fp8 ? run<128, true>(prm, a, s, stream) : run<128, false>(prm, a, s, stream);
   if (a.head_dim == 64)

@@ -221,6 +221,7 @@ struct ExtendArgs {
   // sliding window (window > 0, launch_extend_window): the suffix is read
   // from the pool on both pool types
   int32_t window = 0, sinks = 0, max_prefix = 0;
+  size_t workspace_bytes = 0;
 };
 size_t extend_workspace_bytes();
 sgl_status launch_extend(const ExtendArgs& a, cudaStream_t stream);

@@ -213,6 +213,16 @@ def test_extend_rows_past_the_suffixes_are_left_alone():
     want, terms = case.want_extend()
     assert_within(W.bf16_bits(out[:9]), want, terms, False)
     assert (out[9:] == -3.5).all()
+    # a padded batch: total_extend counts rows behind the last request (few
+    # tiles of many keys, dealt to several CTAs; then few keys)
+    for window in (700, 4):
+        case = Case(attention_case(25, Hq=4, Hkv=2, D=64, prefix=[900, 9], ext=[6, 3], window=window, sinks=1))
+        case.q = torch.cat([case.q, torch.zeros(3000, 4, 64, dtype=torch.bfloat16, device=DEV)])
+        out = torch.full_like(case.q, -3.5)
+        case.extend(out=out, total_extend=3009)
+        want, terms = case.want_extend()
+        assert_within(W.bf16_bits(out[:9]), want, terms, False)
+        assert (out[9:] == -3.5).all()
 
 
 def test_extend_wide_scores():

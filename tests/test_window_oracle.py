@@ -185,6 +185,23 @@ def test_decode_window_workspace_is_bounded_by_the_window(cuda_lib):
     assert B.decode_window_workspace_bytes(0, 4096, 512, 4, d) > 0
 
 
+def test_workspaces_for_the_largest_call_serve_the_smaller(cuda_lib):
+    g = np.random.default_rng(8)
+    for _ in range(3000):
+        hkv = int(g.choice([1, 2, 3, 4, 8, 32]))
+        d = _dims(num_kv_heads=hkv, num_q_heads=hkv * int(g.choice([1, 2, 4, 5, 8, 17, 32])),
+                  head_dim=int(g.choice([64, 128])))
+        big = [int(np.exp(g.uniform(0, np.log(m)))) for m in (300, 1 << 17, 9000, 300)]
+        small = [int(g.integers(1, m + 1)) for m in big]
+        assert B.decode_window_workspace_bytes(*small, d) <= B.decode_window_workspace_bytes(*big, d), (small, big)
+        # batch, total_extend, max_extend, max_prefix, window, sinks
+        big = [int(np.exp(g.uniform(0, np.log(m)))) for m in (60, 20000, 4000, 30000, 9000, 300)]
+        big[2] = min(big[2], big[1])
+        small = [int(g.integers(1, m + 1)) for m in big]
+        small[2] = min(small[2], small[1])
+        assert B.extend_window_workspace_bytes(*small, d) <= B.extend_window_workspace_bytes(*big, d), (small, big)
+
+
 def test_extend_window_validation(cuda_lib):
     d = _dims()
     need = B.extend_window_workspace_bytes(2, 10, 6, 30, 8, 2, d)
