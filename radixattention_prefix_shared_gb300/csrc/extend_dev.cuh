@@ -299,7 +299,7 @@ struct Params {
   // from state_rows on (extend lengths above the host's) have no entry.
   int32_t n_runs;
   int64_t state_rows;  // tokens x Hq
-  uint32_t g_inv;  // row_token (here at the end: 4 bytes before scale_log2 cost the causal bf16 kernel 1.7%)
+  uint32_t g_inv;  // row_token (at the end: 4 bytes before scale_log2 cost the causal bf16 kernel 1.7%)
 };
 
 // The keys a CTA's queries see in a sliding-window extend.  Query position P
@@ -972,7 +972,8 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz, int run = 0) 
             st_shared_v4(stage + row * kStride + 128 * j + 16 * v, o[4 * v], o[4 * v + 1], o[4 * v + 2],
                          o[4 * v + 3]);
         }
-        warp_store_rows<4 * D, kStride>(stage, q * 32, [&](int rr) { return state_row<D>(p, q0, t, rr, e, off, kvh, run); });
+        warp_store_rows<4 * D, kStride>(stage, q * 32,
+                                        [&](int rr) { return state_row<D>(p, q0, t, rr, e, off, kvh, run); });
         const int64_t ent = (int64_t)(off + tok) * p.Hq + (int64_t)kvh * p.g + row_head<true>(p, row);
         if (row_valid && ent < p.state_rows) p.part_ml[ent * p.n_runs + run] = make_float2(m_ref, l);
       } else {
@@ -997,7 +998,8 @@ SGL_DEV void attend_tiles(const Params& p, int bx, int by, int bz, int run = 0) 
           const int tk = q0 + t * p.tpt + row_token<kWindow>(p, rr);
           if (rr >= p.rows_used || tk >= e) return nullptr;
           return reinterpret_cast<uint8_t*>(p.out +
-                                            ((int64_t)(off + tk) * p.Hq + (int64_t)kvh * p.g + row_head<kWindow>(p, rr)) * D);
+                                            ((int64_t)(off + tk) * p.Hq + (int64_t)kvh * p.g +
+                                             row_head<kWindow>(p, rr)) * D);
         });
       }
     }
