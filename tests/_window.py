@@ -78,5 +78,6 @@ def assert_within(got_bits, want, terms, fp8, rows=None, what=""):
         got, want, bound = got[rows], want[rows], bound[rows]
     assert np.isfinite(got).all(), f"{what}: non-finite output (a hidden position was read?)"
     ratio = np.abs(got - want) / bound
-    assert ratio.max() <= 1.0, f"{what}: error {ratio.max():.3g} of its bound at {np.unravel_index(ratio.argmax(), ratio.shape)}"
+    worst = np.unravel_index(ratio.argmax(), ratio.shape)
+    assert ratio.max() <= 1.0, f"{what}: error {ratio.max():.3g} of its bound at {worst}"
     return float(ratio.max())
