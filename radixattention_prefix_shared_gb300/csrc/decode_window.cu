@@ -168,10 +168,10 @@ sgl_status launch(const Params& prm, cudaStream_t stream) {
   if (kernel_blocks_per_sm<decode_window_kernel<D, G, LPT, KV, kSpans>>((int)smem, kThreads) < 0) return SGL_ERR_CUDA;
   const int64_t heads = kSpans ? prm.Hkv / kWarps : prm.Hkv;
   const int64_t ctas = (int64_t)prm.batch * prm.win.n_splits * heads;
-  if (ctas > 0x7fffffff) return SGL_ERR_UNSUPPORTED;
+  const int64_t rows = (int64_t)prm.batch * prm.Hq;
+  if (ctas > 0x7fffffff || rows > 0x7fffffff) return SGL_ERR_UNSUPPORTED;
   decode_window_kernel<D, G, LPT, KV, kSpans><<<(unsigned)ctas, kThreads, smem, stream>>>(prm);
   if (prm.win.n_splits > 1) {
-    const int64_t rows = (int64_t)prm.batch * prm.Hq;
     if (launch_dependent(window_combine_kernel<D>, dim3((unsigned)rows), dim3(128), 0, stream, prm) != cudaSuccess)
       return SGL_ERR_CUDA;
   }
@@ -255,7 +255,9 @@ sgl_status launch_decode_window(const DecodeArgs& a, cudaStream_t stream) {
   prm.chunk = s.chunk;
   prm.scale_log2 = a.sm_scale * 1.4426950408889634f * (a.kv_fp8 ? a.k_scale : 1.f);
   prm.v_scale = a.kv_fp8 ? a.v_scale : 1.f;
-  prm.win = Window{a.sinks, s.keys, a.max_seq_len, s.n_splits};
+  // (a length past the rows of req_to_token is cut to them as well)
+  const int32_t max_seq = a.max_seq_len < a.rtt_stride ? a.max_seq_len : a.rtt_stride;
+  prm.win = Window{a.sinks, s.keys, max_seq, s.n_splits};
   if (a.head_dim == 128)
     return a.kv_fp8 ? run_g<128, uint8_t>(s.G, prm, stream) : run_g<128, __nv_bfloat16>(s.G, prm, stream);
   if (a.head_dim == 64)
