@@ -22,8 +22,8 @@
 // took each warp some 20 instructions of a pipe that needs 16 cycles each.)
 //
 // Bound by HBM in long prefills: 16,384 tokens of 16 query and 8 KV heads of
-// 128: 47.3 us, 5.7 TB/s (0.84 of the measured copy rate); 8,191 tokens of 32
-// and 8 into an e4m3 pool 35 us, 5.3 TB/s.  64 tokens take 3.1 us.
+// 128: 45.4 us, 5.9 TB/s (0.87 of the measured copy rate); 8,191 tokens of 32
+// and 8 into an e4m3 pool 32.6 us, 5.7 TB/s.  64 tokens take 3.1 us.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -33,12 +33,16 @@ namespace sgl {
 
 namespace {
 
-// Measured on the 16,384-token prefill: 4 warps x 4 blocks 47.3 us, x 5 blocks
-// 50.8; 8 warps x 2 blocks 47.6, x 3 48.2, x 4 (64 registers, spills) 54.5;
-// batches of 2 58.5, of 6 49.5, of 8 52.4 (8 warps x 2 blocks).
-constexpr int kRopeWarps = 4;
+// Measured, 16,384 tokens (and 8,191 into an e4m3 pool): 3 warps x 6 blocks 45.4
+// us (32.6), 2 x 9 46.1 (32.5), 1 x 18 46.1 (32.8), 4 x 4 47.3 (35.4), 8 x 2 47.4
+// (35.9), 4 x 5 51.8 (37.0; 13,000 tokens 38.2 with 3 x 6, 40.0 with 4 x 4, and
+// 4,500 16.6 with either: the rounds' ends differ, 18 warps an SM are as good
+// as any).  Batches of 2, 6, 8 at 8 x 2 blocks: 58.5, 49.5, 52.4 against 47.6.
+// K and V rows in one batch, half each: 47.4 (33.6), though 9.6 us instead of
+// 10.7 with 4 KV heads of 64, whose batches of one section are mostly empty.
+constexpr int kRopeWarps = 3;
 constexpr int kRopeBatch = 4;   // row groups a warp loads at a time
-constexpr int kRopeBlocks = 4;  // resident blocks an SM
+constexpr int kRopeBlocks = 6;  // resident blocks an SM
 
 struct RopeParams {
   const __nv_bfloat16* src[3];  // q, k, v
@@ -347,7 +351,8 @@ sgl_status run(const RopeParams& p, cudaStream_t stream) {
   const int per_sm = kernel_blocks_per_sm<qk_norm_rope_store_kernel<D, kFp8, kInterleaved>>(0, kThreads);
   if (per_sm < 0) return SGL_ERR_CUDA;
   // a token's batches are dealt to several blocks while there are fewer
-  // tokens than the part has warps for
+  // tokens than the part has warps for (and no further: 10,000 tokens dealt to
+  // three warps each, for a fuller last round, took 46.7 us instead of 33.2)
   const int batches = (p.heads[0] + kBatchRows - 1) / kBatchRows + 2 * ((p.heads[1] + kBatchRows - 1) / kBatchRows);
   const int64_t resident = (int64_t)num_sms() * per_sm;
   int64_t parts = (resident * kRopeWarps + p.n - 1) / p.n;
