@@ -36,18 +36,35 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int32_t most_runs(int32_t keys) { return (int32_t)ceil_div(keys, kMinRun); }
 int32_t least_runs(int32_t keys) { return (int32_t)ceil_div(keys, kItemMax); }
 
-// Virtual KV heads, and the runs a request is cut into.
+// Rows of at most 128 bytes (an e4m3 pool's, and bf16 ones of 64 elements)
+// are gathered in spans of kWarps KV heads, a CTA a run of all of them, where
+// that leaves kSpanUnits CTAs of the shortest runs: a span is read at a higher
+// rate than as many rows, but with few CTAs a quarter of them is what counts.
+// Spans and rows: one request of 8 query and 8 e4m3 KV heads of 128, window
+// 4,096 (32 CTAs): 17.5 us, 8.8; 16 x 1,000 (128): 18.2, 13.0; 96 x 511
+// (384): 26.2, 28.7; 32 x 2,048 (512): 30.2, 35.5; 200 x 4,096: 269, 285.
+// bf16 of 64, 16 query and 8 KV heads: 21.2, 9.7; 22.0, 13.0; 27.8, 28.1; 29.8,
+// 33.3; 276, 286; 96 requests of 4 KV heads, 511 (192): 18.7, 11.1; 64 query
+// heads on 8: 128 x 100 (256): 11.8, 14.7.
+constexpr int kSpanUnits = 256;
+constexpr bool short_rows(int32_t D, bool kv_fp8) { return kv_fp8 || D == 64; }
+
+// Virtual KV heads, whether their rows are gathered in spans, and the runs a
+// request is cut into.
 struct Shape {
   int32_t split, Hkv, G;
+  bool spans;
   int32_t keys, n_splits, chunk;
   Shape(int32_t batch, int32_t max_seq_len, int32_t window, int32_t sinks, int32_t Hq, int32_t Hkv_pool,
-        bool kv_fp8) {
+        int32_t D, bool kv_fp8) {
     split = kv_split_for(Hq / Hkv_pool);
     Hkv = Hkv_pool * split;
     G = Hq / Hkv;
     const int64_t seen = (int64_t)window + sinks;
     keys = (int32_t)(seen < max_seq_len ? seen : max_seq_len);
-    const int64_t fill = ceil_div(kFillUnits, (int64_t)batch * (spans_for(Hkv, split, kv_fp8) ? Hkv / kWarps : Hkv));
+    spans = short_rows(D, kv_fp8) && spans_possible(Hkv, split) &&
+            (int64_t)batch * (Hkv / kWarps) * most_runs(keys) >= kSpanUnits;
+    const int64_t fill = ceil_div(kFillUnits, (int64_t)batch * (spans ? Hkv / kWarps : Hkv));
     n_splits = fill < most_runs(keys) ? (int32_t)fill : most_runs(keys);
     if (n_splits < least_runs(keys)) n_splits = least_runs(keys);
     chunk = (int32_t)ceil_div(keys, n_splits);
@@ -179,33 +196,33 @@ sgl_status launch(const Params& prm, cudaStream_t stream) {
 }
 
 template <int D, int G, typename KV>
-sgl_status run(const Params& prm, cudaStream_t stream) {
+sgl_status run(const Params& prm, bool spans, cudaStream_t stream) {
   constexpr int LPT = (D == 128 && G >= 4) ? 16 : 8;
-  if constexpr (sizeof(KV) == 1) {
-    if (spans_for(prm.Hkv, prm.kv_split, true)) return launch<D, G, LPT, KV, true>(prm, stream);
+  if constexpr (short_rows(D, sizeof(KV) == 1)) {
+    if (spans) return launch<D, G, LPT, KV, true>(prm, stream);
   }
   return launch<D, G, LPT, KV, false>(prm, stream);
 }
 
 template <int D, typename KV>
-sgl_status run_g(int G, const Params& prm, cudaStream_t stream) {
+sgl_status run_g(int G, const Params& prm, bool spans, cudaStream_t stream) {
   switch (G) {
-    case 1: return run<D, 1, KV>(prm, stream);
-    case 2: return run<D, 2, KV>(prm, stream);
-    case 3: return run<D, 3, KV>(prm, stream);
-    case 4: return run<D, 4, KV>(prm, stream);
-    case 5: return run<D, 5, KV>(prm, stream);
-    case 6: return run<D, 6, KV>(prm, stream);
-    case 7: return run<D, 7, KV>(prm, stream);
-    case 8: return run<D, 8, KV>(prm, stream);
-    case 9: return run<D, 9, KV>(prm, stream);
-    case 10: return run<D, 10, KV>(prm, stream);
-    case 11: return run<D, 11, KV>(prm, stream);
-    case 12: return run<D, 12, KV>(prm, stream);
-    case 13: return run<D, 13, KV>(prm, stream);
-    case 14: return run<D, 14, KV>(prm, stream);
-    case 15: return run<D, 15, KV>(prm, stream);
-    case 16: return run<D, 16, KV>(prm, stream);
+    case 1: return run<D, 1, KV>(prm, spans, stream);
+    case 2: return run<D, 2, KV>(prm, spans, stream);
+    case 3: return run<D, 3, KV>(prm, spans, stream);
+    case 4: return run<D, 4, KV>(prm, spans, stream);
+    case 5: return run<D, 5, KV>(prm, spans, stream);
+    case 6: return run<D, 6, KV>(prm, spans, stream);
+    case 7: return run<D, 7, KV>(prm, spans, stream);
+    case 8: return run<D, 8, KV>(prm, spans, stream);
+    case 9: return run<D, 9, KV>(prm, spans, stream);
+    case 10: return run<D, 10, KV>(prm, spans, stream);
+    case 11: return run<D, 11, KV>(prm, spans, stream);
+    case 12: return run<D, 12, KV>(prm, spans, stream);
+    case 13: return run<D, 13, KV>(prm, spans, stream);
+    case 14: return run<D, 14, KV>(prm, spans, stream);
+    case 15: return run<D, 15, KV>(prm, spans, stream);
+    case 16: return run<D, 16, KV>(prm, spans, stream);
     default: return SGL_ERR_UNSUPPORTED;
   }
 }
@@ -218,8 +235,8 @@ size_t decode_window_workspace_bytes(int32_t batch, int32_t max_seq_len, int32_t
   // A bound that grows with every argument, so that a workspace for a server's
   // largest call serves its smaller ones: fewer requests are cut into more runs
   // each, and batch x runs is at most the larger of the runs that kItemMax
-  // asks for and of kFillUnits CTAs' over the call's head groups (the e4m3
-  // pool's where it takes fewer) plus one a request, and never past runs of
+  // asks for and of kFillUnits CTAs' over the call's head groups (those of
+  // the gather in spans, which takes fewer) plus one a request, and never past runs of
   // kMinRun keys.
   const int64_t seen = (int64_t)window + sinks;
   const int32_t keys = (int32_t)(seen < max_seq_len ? seen : max_seq_len);
@@ -235,7 +252,8 @@ size_t decode_window_workspace_bytes(int32_t batch, int32_t max_seq_len, int32_t
 sgl_status launch_decode_window(const DecodeArgs& a, cudaStream_t stream) {
   if (a.batch == 0) return SGL_OK;
   if (decode_shape_supported(a.num_q_heads, a.num_kv_heads) != SGL_OK) return SGL_ERR_UNSUPPORTED;
-  const Shape s(a.batch, a.max_seq_len, a.window, a.sinks, a.num_q_heads, a.num_kv_heads, a.kv_fp8);
+  const Shape s(a.batch, a.max_seq_len, a.window, a.sinks, a.num_q_heads, a.num_kv_heads, a.head_dim,
+                a.kv_fp8);
   Params prm = {};
   const int64_t entries = s.n_splits > 1 ? (int64_t)a.batch * s.n_splits * a.num_q_heads : 0;
   if (ws_bytes(entries, a.head_dim, a.workspace, &prm.ws) > a.workspace_bytes) return SGL_ERR_WORKSPACE;
@@ -259,9 +277,11 @@ sgl_status launch_decode_window(const DecodeArgs& a, cudaStream_t stream) {
   const int32_t max_seq = a.max_seq_len < a.rtt_stride ? a.max_seq_len : a.rtt_stride;
   prm.win = Window{a.sinks, s.keys, max_seq, s.n_splits};
   if (a.head_dim == 128)
-    return a.kv_fp8 ? run_g<128, uint8_t>(s.G, prm, stream) : run_g<128, __nv_bfloat16>(s.G, prm, stream);
+    return a.kv_fp8 ? run_g<128, uint8_t>(s.G, prm, s.spans, stream)
+                    : run_g<128, __nv_bfloat16>(s.G, prm, s.spans, stream);
   if (a.head_dim == 64)
-    return a.kv_fp8 ? run_g<64, uint8_t>(s.G, prm, stream) : run_g<64, __nv_bfloat16>(s.G, prm, stream);
+    return a.kv_fp8 ? run_g<64, uint8_t>(s.G, prm, s.spans, stream)
+                    : run_g<64, __nv_bfloat16>(s.G, prm, s.spans, stream);
   return SGL_ERR_UNSUPPORTED;
 }
 

@@ -93,6 +93,22 @@ def test_decode_windows(window, sinks, fp8):
     check_decode(case, case.decode(), f"window {window} sinks {sinks}")
 
 
+# as many requests as fill the device with one CTA a group of 4 KV heads: rows
+# of at most 128 bytes are gathered in spans there; one run a request, and many
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("shape", [(16, 16, 64, 70, 100, 3), (16, 16, 128, 66, 250, 0), (32, 16, 64, 65, 40, 1),
+                                   (64, 16, 64, 16, 1000, 5), (48, 16, 64, 18, 800, 0), (80, 16, 64, 17, 900, 2),
+                                   (32, 16, 128, 16, 1000, 1), (32, 8, 64, 16, 2000, 4), (112, 16, 64, 16, 1021, 0)],
+                         ids=lambda s: f"{s[0]}q{s[1]}kv{s[2]}d_b{s[3]}_w{s[4]}")
+def test_decode_of_many_requests(shape, fp8):
+    Hq, Hkv, D, batch, window, sinks = shape
+    g = np.random.default_rng(batch)
+    seq = [int(n) for n in g.integers(1, window + window // 2, batch)]
+    seq[:5] = [1, 0, window, window + sinks, window + sinks + 1]
+    case = decode_case(Hq + window, seq, Hq=Hq, Hkv=Hkv, D=D, window=window, sinks=sinks, fp8=fp8)
+    check_decode(case, case.decode(max_seq_len=2 * window), f"{shape}")
+
+
 def test_decode_full_window_equals_decode():
     """With a window over everything the call is sgl_decode_attention."""
     case = decode_case(11, [700, 1, 33, 2048], Hq=16, Hkv=8, D=128, window=5000, sinks=0)
