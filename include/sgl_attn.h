@@ -371,8 +371,10 @@ sgl_status sgl_cascade_decode_attention_fp8(
  *   query is at position seq_lens[r] - 1).  Arguments, types and errors as
  *   there, but:
  *     seq_lens  : a length below 1 is a padding row: nothing of it is read and
- *                 its row of out stays as it was.  Keys past max_seq_len are
- *                 never read.
+ *                 its row of out stays as it was.  Of a length above
+ *                 max_seq_len (or rtt_stride) the positions from there on are
+ *                 left out of the keys that its query sees; where that leaves
+ *                 none, its row of out stays as it was.
  *     workspace : >= sgl_decode_window_workspace_bytes(batch, max_seq_len,
  *                 window, sinks, dims); scratch, nothing in it outlasts a call.
  *                 (Both workspace sizes grow with every argument but dims: one

@@ -43,6 +43,7 @@
 
 #include "common.cuh"
 #include "launch.h"
+#include "window_run.h"
 
 namespace sgl {
 namespace dec {
@@ -142,28 +143,6 @@ inline size_t ws_layout(int32_t batch, int64_t max_items, int32_t Hkv, int32_t G
   }
   return off;
 }
-
-// A sliding-window decode.  The query of a request of len keys sees positions
-// [0, sinks) and [len - window, len); in order they are its visible keys
-// 0 .. n - 1, n = min(len, sinks + window), and visible key i sits at
-// position i below `sinks` and at i + (len - n) from there on.  A request's
-// visible keys are cut into at most n_splits near-equal runs; run s of request
-// r is item r * n_splits + s.
-struct Window {
-  int32_t sinks;
-  int32_t max_keys;  // min(max_seq_len, sinks + window)
-  int32_t max_seq;   // longer requests are cut to it
-  int32_t n_splits;  // runs of at most Params::chunk visible keys
-};
-struct WindowRun {
-  int32_t len, n;     // keys of the request, and how many its query sees
-  int32_t ns;         // runs
-  SGL_DEV WindowRun(const Window& w, int32_t chunk, int32_t seq_len) {
-    len = max(0, min(seq_len, w.max_seq));
-    n = min(len, w.max_keys);
-    ns = n > 0 ? 1 + (n - 1) / chunk : 0;
-  }
-};
 
 struct Params {
   const __nv_bfloat16* q;
@@ -1015,8 +994,7 @@ SGL_DEV void split_units(const Params& p, uint8_t* smem, int32_t* s_item, int gt
       const int32_t t0 = run * base + min(run, rem);
       n = base + (run < rem ? 1 : 0);
       const int32_t* rtt = p.req_to_token + (int64_t)row * p.rtt_stride;
-      for (int i = tid; i < n; i += kThreads)
-        s_slots[i] = rtt[t0 + i + (t0 + i >= p.win.sinks ? w.len - w.n : 0)];
+      for (int i = tid; i < n; i += kThreads) s_slots[i] = rtt[w.pos(t0 + i)];
     } else {
       const int2 it = p.ws.items[item];
       r = it.x;

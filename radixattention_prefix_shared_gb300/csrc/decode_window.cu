@@ -273,9 +273,9 @@ sgl_status launch_decode_window(const DecodeArgs& a, cudaStream_t stream) {
   prm.chunk = s.chunk;
   prm.scale_log2 = a.sm_scale * 1.4426950408889634f * (a.kv_fp8 ? a.k_scale : 1.f);
   prm.v_scale = a.kv_fp8 ? a.v_scale : 1.f;
-  // (a length past the rows of req_to_token is cut to them as well)
+  // (positions past the rows of req_to_token are left out as well)
   const int32_t max_seq = a.max_seq_len < a.rtt_stride ? a.max_seq_len : a.rtt_stride;
-  prm.win = Window{a.sinks, s.keys, max_seq, s.n_splits};
+  prm.win = Window{a.sinks, a.window, max_seq, s.n_splits};
   if (a.head_dim == 128)
     return a.kv_fp8 ? run_g<128, uint8_t>(s.G, prm, s.spans, stream)
                     : run_g<128, __nv_bfloat16>(s.G, prm, s.spans, stream);
