@@ -377,6 +377,8 @@ sgl_status sgl_cascade_decode_attention_fp8(
  *                 none, its row of out stays as it was.
  *     workspace : >= sgl_decode_window_workspace_bytes(batch, max_seq_len,
  *                 window, sinks, dims); scratch, nothing in it outlasts a call.
+ *                 Its first 256 bytes are left as they are, so the extend below
+ *                 may share it with its status word in place.
  *                 (Both workspace sizes grow with every argument but dims: one
  *                 for the largest values serves all smaller calls.  Calls whose
  *                 kernels may overlap need a workspace each.)

@@ -71,12 +71,16 @@ struct Shape {
   }
 };
 
-// (max, sum) and P.V row of every (request, run, query head)
+// Bytes in front of the states that a decode leaves as they are: a workspace
+// may serve the window's extend too, whose wait status is its first word.
+constexpr size_t kStatusBytes = 256;
+
+// (max, sum) and P.V row of every (request, run, query head), behind them
 size_t ws_bytes(int64_t entries, int32_t D, void* base, Ws* ws) {
-  const size_t o_acc = align256(sizeof(float2) * (size_t)entries);
+  const size_t o_acc = kStatusBytes + align256(sizeof(float2) * (size_t)entries);
   if (ws != nullptr) {
     char* b = static_cast<char*>(base);
-    ws->part_ml = reinterpret_cast<float2*>(b);
+    ws->part_ml = reinterpret_cast<float2*>(b + kStatusBytes);
     ws->part_acc = reinterpret_cast<float*>(b + o_acc);
   }
   return o_acc + sizeof(float) * (size_t)entries * D;
@@ -231,7 +235,7 @@ sgl_status run_g(int G, const Params& prm, bool spans, cudaStream_t stream) {
 
 size_t decode_window_workspace_bytes(int32_t batch, int32_t max_seq_len, int32_t window, int32_t sinks, int32_t Hq,
                                      int32_t Hkv, int32_t D) {
-  if (batch <= 0 || max_seq_len <= 0 || window <= 0 || sinks < 0 || Hkv <= 0 || Hq < Hkv) return 256;
+  if (batch <= 0 || max_seq_len <= 0 || window <= 0 || sinks < 0 || Hkv <= 0 || Hq < Hkv) return kStatusBytes;
   // A bound that grows with every argument, so that a workspace for a server's
   // largest call serves its smaller ones: fewer requests are cut into more runs
   // each, and batch x runs is at most the larger of the runs that kItemMax
@@ -240,13 +244,13 @@ size_t decode_window_workspace_bytes(int32_t batch, int32_t max_seq_len, int32_t
   // kMinRun keys.
   const int64_t seen = (int64_t)window + sinks;
   const int32_t keys = (int32_t)(seen < max_seq_len ? seen : max_seq_len);
-  if (most_runs(keys) <= 1) return 256;
+  if (most_runs(keys) <= 1) return kStatusBytes;
   const int32_t split = kv_split_for(Hq / Hkv), heads = Hkv * split;
   const int64_t fill = ceil_div(kFillUnits, spans_possible(heads, split) ? heads / kWarps : heads) + batch;
   int64_t runs = (int64_t)batch * least_runs(keys);
   if (runs < fill) runs = fill;
   if (runs > (int64_t)batch * most_runs(keys)) runs = (int64_t)batch * most_runs(keys);
-  return 256 + ws_bytes(runs * Hq, D, nullptr, nullptr);
+  return ws_bytes(runs * Hq, D, nullptr, nullptr);
 }
 
 sgl_status launch_decode_window(const DecodeArgs& a, cudaStream_t stream) {
