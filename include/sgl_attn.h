@@ -397,8 +397,8 @@ sgl_status sgl_cascade_decode_attention_fp8(
  * In both, out may be q itself.  The _fp8 calls are the same over e4m3 pools
  * (values are code * scale; see "FP8 KV pool" above; the extend's query range
  * is sgl_extend_attention_fp8's; the decode with 2 or 4 query heads per KV head
- * rounds softmax weights below 2^-18 of a head's largest to zero, as
- * sgl_decode_attention_fp8 does).
+ * holds softmax weights to 2^-8 of themselves or 2^-23 of a head's largest,
+ * whichever is more, where sgl_decode_attention_fp8 drops those below 2^-18).
  */
 size_t sgl_decode_window_workspace_bytes(int32_t batch, int32_t max_seq_len, int32_t window,
                                          int32_t sinks, const sgl_attn_dims* dims);
