@@ -451,7 +451,9 @@ sgl_status sgl_extend_attention_window_fp8(const void* q, const void* pool_k, co
  * angle is positions[axis, t] * inv_freq[i], axis = freq_axis[i] (0 with one
  * axis).  Q rows go to q_out, K rows to pool_k[slots[t]], the V rows
  * unchanged to pool_v[slots[t]].  Arithmetic is fp32 with one rounding at the
- * end; angles keep 2^-24 turns at any int32 position (|inv_freq| up to 2^8).
+ * end, the norms over every finite row (squares below 2^-126, those of values
+ * below 2^-63, lose bits: an eps of 2^-100 or more outweighs them); angles keep
+ * 2^-24 turns at any int32 position (|inv_freq| up to 2^8).
  *   q            : bf16, token t's Hq rows of D side by side at t * q_stride
  *                  elements; k, v: Hkv rows at t * k_stride, t * v_stride.  The
  *                  strides (multiples of 8, >= the rows) let the three be

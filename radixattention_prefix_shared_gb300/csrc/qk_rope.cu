@@ -126,16 +126,117 @@ SGL_DEV uint64_t turn_fraction(float f) {
   return (bits >> 31) ? 0 - t : t;
 }
 
+// Sum over the D / 8 lanes of a row of the squares of its 8 values.
+template <int D>
+SGL_DEV float row_squares(const float2 (&y0)[2], const float2 (&y1)[2]) {
+  const float2 q = ffma2(y1[1], y1[1], ffma2(y1[0], y1[0], ffma2(y0[1], y0[1], fmul2(y0[0], y0[0]))));
+  float s = q.x + q.y;
+#pragma unroll
+  for (int o = 1; o < D / 8; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
+}
+
+// What turns a lane's values y: y' = y C + other S, other being the pair's other
+// value; the head weights w are in it (null: none).
+template <bool kInterleaved>
+struct Turn {
+  float2 C0[2], C1[2], S0[2], S1[2];
+  bool rotated;
+  SGL_DEV Turn(const __nv_bfloat16* w, const float2* pairs, bool turned, int o0, int o1) : rotated(turned) {
+    float2 w0[2] = {dup(1.f), dup(1.f)}, w1[2] = {dup(1.f), dup(1.f)};
+    if (w != nullptr) {
+      const uint2 a = *reinterpret_cast<const uint2*>(w + o0), c = *reinterpret_cast<const uint2*>(w + o1);
+      unpack4(a.x, a.y, w0);
+      unpack4(c.x, c.y, w1);
+    }
+    float2 v[4] = {make_float2(1.f, 0.f), make_float2(1.f, 0.f), make_float2(1.f, 0.f), make_float2(1.f, 0.f)};
+    if (rotated) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = pairs[e];
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if constexpr (kInterleaved) {  // pair = the two floats of a packed pair
+        C0[j] = fmul2(w0[j], dup(v[j].x));
+        S0[j] = make_float2(-w0[j].y * v[j].y, w0[j].x * v[j].y);
+        C1[j] = fmul2(w1[j], dup(v[2 + j].x));
+        S1[j] = make_float2(-w1[j].y * v[2 + j].y, w1[j].x * v[2 + j].y);
+      } else {  // pair = the same place of the two runs
+        const float2 c = make_float2(v[2 * j].x, v[2 * j + 1].x), sn = make_float2(v[2 * j].y, v[2 * j + 1].y);
+        C0[j] = fmul2(w0[j], c);
+        C1[j] = fmul2(w1[j], c);
+        S1[j] = fmul2(w0[j], sn);
+        S0[j] = fmul2(w1[j], make_float2(-sn.x, -sn.y));
+      }
+    }
+  }
+  // the values turned, times r
+  SGL_DEV void operator()(const float2 (&y0)[2], const float2 (&y1)[2], float r, float2 (&z0)[2], float2 (&z1)[2]) const {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      z0[j] = fmul2(y0[j], C0[j]);
+      z1[j] = fmul2(y1[j], C1[j]);
+      if (rotated) {  // (not + 0 * other: rows that do not turn keep their infinities)
+        z0[j] = ffma2(kInterleaved ? make_float2(y0[j].y, y0[j].x) : y1[j], S0[j], z0[j]);
+        z1[j] = ffma2(kInterleaved ? make_float2(y1[j].y, y1[j].x) : y0[j], S1[j], z1[j]);
+      }
+      z0[j] = fmul2(z0[j], dup(r));
+      z1[j] = fmul2(z1[j], dup(r));
+    }
+  }
+};
+
+// A lane's finished values of row h of token tok (slot `at`): Q (sec 0) to
+// q_out, K to its pool.
+template <int D, bool kFp8, bool kInterleaved>
+SGL_DEV void store_row(const RopeParams& p, int sec, int32_t tok, int64_t at, int h, int o0, int o1,
+                       const float2 (&z0)[2], const float2 (&z1)[2]) {
+  if (kFp8 && sec == 1) {
+    uint8_t* dst = p.pool[0] + (at * p.heads[1] + h) * D;
+    const uint32_t lo = e4m3x4(z0, p.scale[0], p.rcp[0]), hi = e4m3x4(z1, p.scale[0], p.rcp[0]);
+    if constexpr (kInterleaved) {
+      *reinterpret_cast<uint2*>(dst + o0) = make_uint2(lo, hi);
+    } else {
+      *reinterpret_cast<uint32_t*>(dst + o0) = lo;
+      *reinterpret_cast<uint32_t*>(dst + o1) = hi;
+    }
+  } else {
+    __nv_bfloat16* dst = sec == 0 ? p.q_out + ((int64_t)tok * p.heads[0] + h) * D
+                                  : reinterpret_cast<__nv_bfloat16*>(p.pool[0]) + (at * p.heads[1] + h) * D;
+    const uint2 lo = make_uint2(pack_bf16x2(z0[0].x, z0[0].y), pack_bf16x2(z0[1].x, z0[1].y));
+    const uint2 hi = make_uint2(pack_bf16x2(z1[0].x, z1[0].y), pack_bf16x2(z1[1].x, z1[1].y));
+    if constexpr (kInterleaved) {
+      *reinterpret_cast<uint4*>(dst + o0) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+    } else {
+      *reinterpret_cast<uint2*>(dst + o0) = lo;
+      *reinterpret_cast<uint2*>(dst + o1) = hi;
+    }
+  }
+}
+
+// A row whose squares sum up to kFarSquares or more (an RMS from 2^57 on: none in
+// practice, and past fp32 from 2^60 on) is left out; a warp that met one goes over
+// its rows again at the end and finishes those from values at 2^-70 of their
+// size, with eps at 2^-140 of its: r comes out at 2^70 of its size, and neither
+// the squares (a bf16 is below 2^128, so D of them are below 2^123) nor a turned
+// pair's sum overflow.  Leaving them out is a comparison a row: 16,384 tokens 47.9
+// -> 48.3 us, 8,191 with norms into an e4m3 pool 39.8 -> 40.1 (a vote a row in
+// the loop 48.4 and 41.1; a vote a batch and its rows again, 51 to 56 and 50 to
+// 52).  Calls without norms (kNorm false) have no use for it: 33.4 us for 8,191
+// tokens, 34.8 with it.
+constexpr float kFarSquares = 0x1p121f, kFarScale = 0x1p-70f;
+
 // A warp works on batches of kRopeBatch row groups, a group being the 32 / (D /
 // 8) rows (heads of one token) that its lanes hold, 8 values each: lane i < rot
 // / 8 of a row holds pairs 4 i .. 4 i + 3 (8 consecutive values when
 // interleaved, else two runs of 4), the others 8 consecutive values that do
 // not turn.
+// kNorm: some rows have a weight.
 // A token's batches are those of its Q rows, its K rows and its V rows in
 // turn; block y takes an even share of them.  The next batch's rows, and the
 // next token's slot and positions, are loaded before the current batch is
 // worked on.
-template <int D, bool kFp8, bool kInterleaved>
+template <int D, bool kFp8, bool kInterleaved, bool kNorm>
 __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) qk_norm_rope_store_kernel(RopeParams p) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes, kF = D / 64;
   __shared__ float2 s_turn[kRopeWarps][D / 2];  // (cos, sin) of the warp's token
@@ -158,7 +259,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) qk_norm_rope_sto
   const int32_t stride = gridDim.x * kRopeWarps;
   if (t >= p.n) return;
   int b = b0;
-  uint4 raw[kRopeBatch];
+  uint4 raw[kRopeBatch] = {};
   int32_t slot, pos[kF];
   auto section = [&](int bb) { return bb < nq ? 0 : (bb < nq + nk ? 1 : 2); };
   auto load_rows = [&](int32_t tt, int bb) {
@@ -189,8 +290,22 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) qk_norm_rope_sto
         if (lane + 32 * i < nf) pos[i] = fpos[i][tt];
     }
   };
-  load_rows(t, b);
   uint64_t freq[kF];
+  auto fill_turns = [&] {  // of the token whose positions were loaded
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kF; ++i) {
+      const int f = lane + 32 * i;
+      if (f < nf) {
+        const uint64_t a = (uint64_t)(int64_t)pos[i] * freq[i];
+        float sn, cs;
+        sincospif((float)(int32_t)(a >> 32) * 0x1p-31f, &sn, &cs);
+        turn[f] = make_float2(cs, sn);
+      }
+    }
+    __syncwarp();
+  };
+  load_rows(t, b);
 #pragma unroll
   for (int i = 0; i < kF; ++i) {
     const int f = lane + 32 * i;
@@ -204,6 +319,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) qk_norm_rope_sto
   }
   load_token(t);
   bool fresh = true;  // the token's first batch here
+  bool far = false;   // a row was left out
 
   while (true) {
     const int sec = section(b);
@@ -215,20 +331,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) qk_norm_rope_sto
     uint4 cur[kRopeBatch];
 #pragma unroll
     for (int u = 0; u < kRopeBatch; ++u) cur[u] = raw[u];
-    if (fresh && turns) {
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < kF; ++i) {
-        const int f = lane + 32 * i;
-        if (f < nf) {
-          const uint64_t a = (uint64_t)(int64_t)pos[i] * freq[i];
-          float sn, cs;
-          sincospif((float)(int32_t)(a >> 32) * 0x1p-31f, &sn, &cs);
-          turn[f] = make_float2(cs, sn);
-        }
-      }
-      __syncwarp();
-    }
+    if (fresh && turns) fill_turns();
     // on to the next batch
     fresh = ++b == b1;
     if (fresh) {
@@ -242,86 +345,25 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) qk_norm_rope_sto
     }
     if (live) {
       if (sec < 2) {
-        const __nv_bfloat16* w = p.weight[sec];
-        // y' = y C + other S, other being the pair's other value
-        float2 C0[2], C1[2], S0[2], S1[2];
-        {
-          float2 w0[2] = {dup(1.f), dup(1.f)}, w1[2] = {dup(1.f), dup(1.f)};
-          if (w != nullptr) {
-            const uint2 a = *reinterpret_cast<const uint2*>(w + o0), c = *reinterpret_cast<const uint2*>(w + o1);
-            unpack4(a.x, a.y, w0);
-            unpack4(c.x, c.y, w1);
-          }
-          float2 v[4] = {make_float2(1.f, 0.f), make_float2(1.f, 0.f), make_float2(1.f, 0.f), make_float2(1.f, 0.f)};
-          if (rotated) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = turn[4 * li + e];
-          }
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            if constexpr (kInterleaved) {  // pair = the two floats of a packed pair
-              C0[j] = fmul2(w0[j], dup(v[j].x));
-              S0[j] = make_float2(-w0[j].y * v[j].y, w0[j].x * v[j].y);
-              C1[j] = fmul2(w1[j], dup(v[2 + j].x));
-              S1[j] = make_float2(-w1[j].y * v[2 + j].y, w1[j].x * v[2 + j].y);
-            } else {  // pair = the same place of the two runs
-              const float2 c = make_float2(v[2 * j].x, v[2 * j + 1].x), sn = make_float2(v[2 * j].y, v[2 * j + 1].y);
-              C0[j] = fmul2(w0[j], c);
-              C1[j] = fmul2(w1[j], c);
-              S1[j] = fmul2(w0[j], sn);
-              S0[j] = fmul2(w1[j], make_float2(-sn.x, -sn.y));
-            }
-          }
-        }
+        const __nv_bfloat16* w = kNorm ? p.weight[sec] : nullptr;
+        const Turn<kInterleaved> turned(w, turn + 4 * li, rotated, o0, o1);
 #pragma unroll
         for (int u = 0; u < kRopeBatch; ++u) {
           const int h = h0 + u * kRows;
           if (h - sub >= n_heads) break;
-          float2 y0[2], y1[2];
+          float2 y0[2], y1[2], z0[2], z1[2];
           unpack4(cur[u].x, cur[u].y, y0);
           unpack4(cur[u].z, cur[u].w, y1);
           float r = 1.f;
+          bool stored = h < n_heads;
           if (w != nullptr) {
-            const float2 q = ffma2(y1[1], y1[1], ffma2(y1[0], y1[0], ffma2(y0[1], y0[1], fmul2(y0[0], y0[0]))));
-            float q2 = q.x + q.y;
-#pragma unroll
-            for (int o = 1; o < kLanes; o <<= 1) q2 += __shfl_xor_sync(0xffffffffu, q2, o);
-            r = rsqrtf(q2 * (1.f / D) + p.eps);
+            const float s = row_squares<D>(y0, y1);
+            far = far || !(s < kFarSquares);
+            stored = stored && s < kFarSquares;
+            r = rsqrtf(s * (1.f / D) + p.eps);
           }
-          float2 z0[2], z1[2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            z0[j] = fmul2(y0[j], C0[j]);
-            z1[j] = fmul2(y1[j], C1[j]);
-            if (rotated) {  // (not + 0 * other: rows that do not turn keep their infinities)
-              z0[j] = ffma2(kInterleaved ? make_float2(y0[j].y, y0[j].x) : y1[j], S0[j], z0[j]);
-              z1[j] = ffma2(kInterleaved ? make_float2(y1[j].y, y1[j].x) : y0[j], S1[j], z1[j]);
-            }
-            z0[j] = fmul2(z0[j], dup(r));
-            z1[j] = fmul2(z1[j], dup(r));
-          }
-          if (h >= n_heads) continue;
-          if (kFp8 && sec == 1) {
-            uint8_t* dst = p.pool[0] + (at * p.heads[1] + h) * D;
-            const uint32_t lo = e4m3x4(z0, p.scale[0], p.rcp[0]), hi = e4m3x4(z1, p.scale[0], p.rcp[0]);
-            if constexpr (kInterleaved) {
-              *reinterpret_cast<uint2*>(dst + o0) = make_uint2(lo, hi);
-            } else {
-              *reinterpret_cast<uint32_t*>(dst + o0) = lo;
-              *reinterpret_cast<uint32_t*>(dst + o1) = hi;
-            }
-          } else {
-            __nv_bfloat16* dst = sec == 0 ? p.q_out + ((int64_t)tok * p.heads[0] + h) * D
-                                          : reinterpret_cast<__nv_bfloat16*>(p.pool[0]) + (at * p.heads[1] + h) * D;
-            const uint2 lo = make_uint2(pack_bf16x2(z0[0].x, z0[0].y), pack_bf16x2(z0[1].x, z0[1].y));
-            const uint2 hi = make_uint2(pack_bf16x2(z1[0].x, z1[0].y), pack_bf16x2(z1[1].x, z1[1].y));
-            if constexpr (kInterleaved) {
-              *reinterpret_cast<uint4*>(dst + o0) = make_uint4(lo.x, lo.y, hi.x, hi.y);
-            } else {
-              *reinterpret_cast<uint2*>(dst + o0) = lo;
-              *reinterpret_cast<uint2*>(dst + o1) = hi;
-            }
-          }
+          turned(y0, y1, r, z0, z1);
+          if (stored) store_row<D, kFp8, kInterleaved>(p, sec, tok, at, h, o0, o1, z0, z1);
         }
       } else {
 #pragma unroll
@@ -341,14 +383,49 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeBlocks) qk_norm_rope_sto
         }
       }
     }
-    if (!more) return;
+    if (!more) break;
+  }
+  if constexpr (kNorm) {
+    if (!__any_sync(0xffffffffu, far)) return;
+#pragma unroll 1
+    for (t = blockIdx.x * kRopeWarps + warp; t < p.n; t += stride) {
+      load_token(t);
+      if (slot < 0 || slot >= p.pool_size) continue;
+      if (turns) fill_turns();
+#pragma unroll 1
+      for (int bb = b0; bb < b1 && bb < nq + nk; ++bb) {
+        const int sec = section(bb), n_heads = p.heads[sec];
+        const __nv_bfloat16* w = p.weight[sec];
+        if (w == nullptr) continue;
+        const int h0 = (bb - (sec == 0 ? 0 : nq)) * kBatchRows + sub;
+#pragma unroll 1
+        for (int h = h0; h < h0 + kBatchRows && h - sub < n_heads; h += kRows) {
+          float2 y0[2] = {}, y1[2] = {}, z0[2], z1[2];
+          if (h < n_heads) {
+            const __nv_bfloat16* src = p.src[sec] + t * p.stride[sec] + h * D;
+            const uint2 lo = ld_row8(src + o0), hi = ld_row8(src + o1);
+            unpack4(lo.x, lo.y, y0);
+            unpack4(hi.x, hi.y, y1);
+          }
+          const bool mine = !(row_squares<D>(y0, y1) < kFarSquares);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            y0[j] = fmul2(y0[j], dup(kFarScale));
+            y1[j] = fmul2(y1[j], dup(kFarScale));
+          }
+          const float r = rsqrtf(row_squares<D>(y0, y1) * (1.f / D) + p.eps * kFarScale * kFarScale);
+          Turn<kInterleaved>(w, turn + 4 * li, rotated, o0, o1)(y0, y1, r, z0, z1);
+          if (mine) store_row<D, kFp8, kInterleaved>(p, sec, t, slot, h, o0, o1, z0, z1);
+        }
+      }
+    }
   }
 }
 
-template <int D, bool kFp8, bool kInterleaved>
+template <int D, bool kFp8, bool kInterleaved, bool kNorm>
 sgl_status run(const RopeParams& p, cudaStream_t stream) {
   constexpr int kThreads = kRopeWarps * 32, kBatchRows = 32 / (D / 8) * kRopeBatch;
-  const int per_sm = kernel_blocks_per_sm<qk_norm_rope_store_kernel<D, kFp8, kInterleaved>>(0, kThreads);
+  const int per_sm = kernel_blocks_per_sm<qk_norm_rope_store_kernel<D, kFp8, kInterleaved, kNorm>>(0, kThreads);
   if (per_sm < 0) return SGL_ERR_CUDA;
   // a token's batches are dealt to several blocks while there are fewer
   // tokens than the part has warps for (and no further: 10,000 tokens dealt to
@@ -360,15 +437,21 @@ sgl_status run(const RopeParams& p, cudaStream_t stream) {
   int64_t blocks = ((int64_t)p.n + kRopeWarps - 1) / kRopeWarps;
   const int64_t cap = (resident + parts - 1) / parts;
   if (blocks > cap) blocks = cap;
-  qk_norm_rope_store_kernel<D, kFp8, kInterleaved>
+  qk_norm_rope_store_kernel<D, kFp8, kInterleaved, kNorm>
       <<<dim3((unsigned)blocks, (unsigned)parts), kThreads, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? SGL_OK : SGL_ERR_CUDA;
 }
 
+template <int D, bool kFp8, bool kInterleaved>
+sgl_status run_n(const RopeParams& p, cudaStream_t stream) {
+  return p.weight[0] != nullptr || p.weight[1] != nullptr ? run<D, kFp8, kInterleaved, true>(p, stream)
+                                                          : run<D, kFp8, kInterleaved, false>(p, stream);
+}
+
 template <int D>
 sgl_status run_d(const RopeParams& p, bool kv_fp8, cudaStream_t stream) {
-  if (kv_fp8) return p.interleaved ? run<D, true, true>(p, stream) : run<D, true, false>(p, stream);
-  return p.interleaved ? run<D, false, true>(p, stream) : run<D, false, false>(p, stream);
+  if (kv_fp8) return p.interleaved ? run_n<D, true, true>(p, stream) : run_n<D, true, false>(p, stream);
+  return p.interleaved ? run_n<D, false, true>(p, stream) : run_n<D, false, false>(p, stream);
 }
 
 }  // namespace
