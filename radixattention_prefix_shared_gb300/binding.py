@@ -427,6 +427,14 @@ def _raw_stream(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _stream_object(stream):
+    """The torch stream of a call's ``stream`` argument: itself, or the one around a handle."""
+    import torch
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)))
+
+
 def _on(stream):
     """Context whose allocations belong to the stream that a call runs on, so
     that a scratch buffer dropped on return is not handed out again before
@@ -434,11 +442,19 @@ def _on(stream):
     import contextlib
 
     import torch
-    if stream is None:
-        return contextlib.nullcontext()
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)))
-    return torch.cuda.stream(stream)
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(_stream_object(stream))
+
+
+def _in_use(stream, *tensors):
+    """Tensors of a call on a stream of the caller's choice: dropped by the
+    caller, their memory is not handed out again before the call's kernels are
+    done with it.  (That the stream waits for what fills them is the caller's
+    to see to.)"""
+    if stream is not None:
+        s = _stream_object(stream)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(s)
 
 
 def decode_window_workspace_bytes(batch, max_seq_len, window, sinks, dims: sgl_attn_dims) -> int:
@@ -505,6 +521,7 @@ def _decode_window(name, q, pool_k, pool_v, scales, req_to_token, req_pool_idx, 
         req_pool_idx.data_ptr(), seq_lens.data_ptr(), qs[0], int(max_seq_len), int(window), int(sinks), out.data_ptr(),
         workspace.data_ptr(), workspace.nbytes, dims,
         T.current_stream(dev) if stream is None else _raw_stream(stream))
+    _in_use(stream, q, pool_k, pool_v, req_to_token, req_pool_idx, seq_lens, out, workspace)
     if code != 0:
         raise SglError(name, code)
     return out
@@ -564,6 +581,7 @@ def _extend_window(name, q, pool_k, pool_v, scales, req_to_token, req_pool_idx, 
         req_pool_idx.data_ptr(), prefix_lens.data_ptr(), extend_lens.data_ptr(), bs[0], total, int(max_extend),
         int(max_prefix), int(window), int(sinks), out.data_ptr(), workspace.data_ptr(), workspace.nbytes, dims,
         T.current_stream(dev) if stream is None else _raw_stream(stream))
+    _in_use(stream, q, pool_k, pool_v, req_to_token, req_pool_idx, prefix_lens, extend_lens, out, workspace)
     if code != 0:
         raise SglError(name, code)
     return out
@@ -595,6 +613,7 @@ def sgl_check_decode_window_indices(req_to_token, req_pool_idx, seq_lens, *, max
         _ptr(req_to_token), int(req_to_token.shape[0]), int(req_to_token.shape[1]), _ptr(req_pool_idx),
         _ptr(seq_lens), int(req_pool_idx.shape[0]), int(max_seq_len), int(window), int(sinks), int(pool_size),
         _ptr(d_error), _stream(stream)))
+    _in_use(stream, req_to_token, req_pool_idx, seq_lens, d_error)
 
 
 def sgl_check_extend_window_indices(req_to_token, req_pool_idx, prefix_lens, extend_lens, *, total_extend,
@@ -603,6 +622,7 @@ def sgl_check_extend_window_indices(req_to_token, req_pool_idx, prefix_lens, ext
         _ptr(req_to_token), int(req_to_token.shape[0]), int(req_to_token.shape[1]), _ptr(req_pool_idx),
         _ptr(prefix_lens), _ptr(extend_lens), int(req_pool_idx.shape[0]), int(total_extend), int(max_extend),
         int(max_prefix), int(window), int(sinks), int(pool_size), _ptr(d_error), _stream(stream)))
+    _in_use(stream, req_to_token, req_pool_idx, prefix_lens, extend_lens, d_error)
 
 
 # ----------------------------------------------------------------- norms, rotary positions, store
@@ -682,6 +702,7 @@ def _qk_norm_rope_store(name, q, k, v, positions, inv_freq, slots, pool_k, pool_
         freq_axis.data_ptr() if axes > 1 else None, rot, 1 if interleaved else 0, slots.data_ptr(), n,
         q_out.data_ptr(), pool_k.data_ptr(), pool_v.data_ptr(), *scales, _dims_ref(hq, ps[1], d, ps[0], 0.0),
         T.current_stream(dev) if stream is None else _raw_stream(stream))
+    _in_use(stream, q, k, v, positions, inv_freq, slots, pool_k, pool_v, q_weight, k_weight, freq_axis, q_out)
     if code != 0:
         raise SglError(name, code)
     return q_out
