@@ -428,11 +428,13 @@ def _raw_stream(stream):
 
 
 def _stream_object(stream):
-    """The torch stream of a call's ``stream`` argument: itself, or the one around a handle."""
+    """The torch stream of a call's ``stream`` argument: itself, or the one
+    around a handle (0: the default stream, which ExternalStream does not take)."""
     import torch
     if isinstance(stream, torch.cuda.Stream):
         return stream
-    return torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)))
+    handle = int(getattr(stream, "cuda_stream", stream))
+    return torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
 
 
 def _on(stream):

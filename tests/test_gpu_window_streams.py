@@ -118,6 +118,24 @@ def test_dropped_inputs_of_the_checks():
     assert err.tolist() == [0, 0, 0, 0]
 
 
+def test_handle_of_the_default_stream():
+    """Handle 0 is the default stream, for the call and for what it allocates."""
+    assert B._stream_object(0) == torch.cuda.default_stream()
+    side = torch.cuda.Stream()
+    assert B._stream_object(side.cuda_stream).cuda_stream == side.cuda_stream and B._stream_object(side) is side
+    case = decode_case(84, [3000, 900], Hq=8, Hkv=4, D=128, window=2000, sinks=4)
+    case.decode()
+    busy = Busy(torch.cuda.default_stream())
+    busy.fill()
+    with torch.cuda.stream(side):            # the call's own buffers are the default stream's
+        out = case.decode(stream=0)
+        ptr = out.untyped_storage().data_ptr()
+        keep = [torch.zeros_like(out) for _ in range(8)]
+        assert not busy.stream.query() and ptr not in {t.untyped_storage().data_ptr() for t in keep}
+    torch.cuda.synchronize()
+    check_decode(case, out)
+
+
 def test_captured_on_its_own_stream():
     """``stream=`` naming the capturing stream: the graph replays, and the memory
     it was given stays its own."""
