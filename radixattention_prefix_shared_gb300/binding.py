@@ -405,6 +405,15 @@ def _need_dense(name, dtype, **tensors):
             raise ValueError(f"{name}: {arg} must be a dense {dtype} tensor on the current CUDA device")
 
 
+_I32 = 2**31 - 1
+
+
+def _need_i32(name, **values):
+    """Host values that the library takes as int32; ctypes would cut longer ones."""
+    for arg, v in values.items():
+        _need(name, -_I32 <= v <= _I32, f"{arg} = {v} is not an int32")
+
+
 class _Torch:
     """What the calls below look up in torch at every call (bound at the first)."""
 
@@ -460,12 +469,15 @@ def _in_use(stream, *tensors):
 
 
 def decode_window_workspace_bytes(batch, max_seq_len, window, sinks, dims: sgl_attn_dims) -> int:
+    _need_i32("decode_window_workspace_bytes", batch=batch, max_seq_len=max_seq_len, window=window, sinks=sinks)
     return int(lib().sgl_decode_window_workspace_bytes(int(batch), int(max_seq_len), int(window), int(sinks),
                                                        ctypes.byref(dims)))
 
 
 def extend_window_workspace_bytes(batch, total_extend, max_extend, max_prefix, window, sinks,
                                   dims: sgl_attn_dims) -> int:
+    _need_i32("extend_window_workspace_bytes", batch=batch, total_extend=total_extend, max_extend=max_extend,
+              max_prefix=max_prefix, window=window, sinks=sinks)
     return int(lib().sgl_extend_window_workspace_bytes(int(batch), int(total_extend), int(max_extend),
                                                        int(max_prefix), int(window), int(sinks),
                                                        ctypes.byref(dims)))
@@ -510,6 +522,8 @@ def _decode_window(name, q, pool_k, pool_v, scales, req_to_token, req_pool_idx, 
             and (workspace is None or (workspace.is_contiguous() and workspace.get_device() == dev))):
         _refuse_window(name, q, pool_k, pool_v, kv, req_to_token, dict(req_pool_idx=req_pool_idx, seq_lens=seq_lens),
                        out, workspace)
+    if not (-_I32 <= window <= _I32 and -_I32 <= sinks <= _I32 and -_I32 <= max_seq_len <= _I32):
+        _need_i32(name, window=window, sinks=sinks, max_seq_len=max_seq_len)
     dims = _dims_ref(qs[1], ks[1], ks[2], ks[0], float(sm_scale))
     if out is None or workspace is None:
         with _on(stream):
@@ -570,6 +584,9 @@ def _extend_window(name, q, pool_k, pool_v, scales, req_to_token, req_pool_idx, 
                        workspace)
     total = qs[0] if total_extend is None else int(total_extend)
     _need(name, total <= qs[0], "total_extend within q's rows")
+    if not (-_I32 <= window <= _I32 and -_I32 <= sinks <= _I32 and -_I32 <= max_extend <= _I32
+            and -_I32 <= max_prefix <= _I32 and -_I32 <= total):
+        _need_i32(name, window=window, sinks=sinks, max_extend=max_extend, max_prefix=max_prefix, total_extend=total)
     dims = _dims_ref(qs[1], ks[1], ks[2], ks[0], float(sm_scale))
     if out is None or workspace is None:
         with _on(stream):
@@ -611,6 +628,7 @@ def sgl_extend_attention_window_fp8(q, pool_k, pool_v, k_scale, v_scale, req_to_
 
 def sgl_check_decode_window_indices(req_to_token, req_pool_idx, seq_lens, *, max_seq_len, window, sinks=0,
                                     pool_size, d_error, stream=None):
+    _need_i32("sgl_check_decode_window_indices", max_seq_len=max_seq_len, window=window, sinks=sinks)
     _check("sgl_check_decode_window_indices", lib().sgl_check_decode_window_indices(
         _ptr(req_to_token), int(req_to_token.shape[0]), int(req_to_token.shape[1]), _ptr(req_pool_idx),
         _ptr(seq_lens), int(req_pool_idx.shape[0]), int(max_seq_len), int(window), int(sinks), int(pool_size),
@@ -620,6 +638,8 @@ def sgl_check_decode_window_indices(req_to_token, req_pool_idx, seq_lens, *, max
 
 def sgl_check_extend_window_indices(req_to_token, req_pool_idx, prefix_lens, extend_lens, *, total_extend,
                                     max_extend, max_prefix, window, sinks=0, pool_size, d_error, stream=None):
+    _need_i32("sgl_check_extend_window_indices", total_extend=total_extend, max_extend=max_extend,
+              max_prefix=max_prefix, window=window, sinks=sinks)
     _check("sgl_check_extend_window_indices", lib().sgl_check_extend_window_indices(
         _ptr(req_to_token), int(req_to_token.shape[0]), int(req_to_token.shape[1]), _ptr(req_pool_idx),
         _ptr(prefix_lens), _ptr(extend_lens), int(req_pool_idx.shape[0]), int(total_extend), int(max_extend),
