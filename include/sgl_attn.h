@@ -68,8 +68,9 @@ const char* sgl_version(void);
  * and cascade-group kernels (failure detection; the pages have no
  * counterpart).
  *
- * Each stage barrier wait of sgl_extend_attention(_fp8) and of the group
- * pass of sgl_cascade_decode_attention(_fp8) gives up after this much wall
+ * Each stage barrier wait of sgl_extend_attention(_fp8),
+ * sgl_extend_attention_window(_fp8), sgl_mixed_attention and the group pass of
+ * sgl_cascade_decode_attention(_fp8) gives up after this much wall
  * time (default 2 s): the kernel then records a nonzero code (0x5701) in the
  * status word of its workspace, lets its own copies and tensor-core work
  * finish, frees its tensor memory and returns, leaving that call's output
@@ -365,7 +366,8 @@ sgl_status sgl_cascade_decode_attention_fp8(
  * Only positions that some query of the call sees are read, in req_to_token
  * as in the pools: a request's other entries may be stale (their slots freed
  * and serving other requests) or hold anything.  Rows that are read hold
- * finite values, as in every attention call here.
+ * finite values, as in every attention call here (the e4m3 codes 0x7F and 0xFF
+ * are NaN; which calls spread one and which take it for +-480 is not defined).
  *
  * sgl_decode_attention_window -- sgl_decode_attention over those keys (the
  *   query is at position seq_lens[r] - 1).  Arguments, types and errors as
@@ -528,7 +530,8 @@ size_t sgl_cascade_decode_workspace_bytes(int32_t batch, int32_t max_seq_len, in
  * sgl_check_decode_window_indices and sgl_check_extend_window_indices check the
  * positions that the sliding-window calls read (a decode length of 0 is a
  * padding row there, a negative one kind 3).  The slots of
- * sgl_qk_norm_rope_store_kv are checked like a store's, padding left out.
+ * sgl_qk_norm_rope_store_kv are checked with sgl_check_store_kv_indices, which
+ * reports a padding token's as kind 1: give it the other tokens' alone.
  * sgl_check_store_kv_indices needs a scratch bitmap of (pool_size+7)/8 bytes
  * (rounded up to 16) in `bitmap`; it is cleared by the call.
  * sgl_check_cascade_groups needs sgl_check_cascade_scratch_bytes(batch,
