@@ -22,8 +22,8 @@
 // took each warp some 20 instructions of a pipe that needs 16 cycles each.)
 //
 // Bound by HBM in long prefills: 16,384 tokens of 16 query and 8 KV heads of
-// 128: 45.4 us, 5.9 TB/s (0.87 of the measured copy rate); 8,191 tokens of 32
-// and 8 into an e4m3 pool 32.6 us, 5.7 TB/s.  64 tokens take 3.1 us.
+// 128: 46.4 us, 5.8 TB/s (0.85 of the measured copy rate); 8,191 tokens of 32
+// and 8 into an e4m3 pool, without norms, 32.5 us, 5.7 TB/s.  64 tokens take 3.2 us.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -33,8 +33,9 @@ namespace sgl {
 
 namespace {
 
-// Measured, 16,384 tokens (and 8,191 into an e4m3 pool): 3 warps x 6 blocks 45.4
-// us (32.6), 2 x 9 46.1 (32.5), 1 x 18 46.1 (32.8), 4 x 4 47.3 (35.4), 8 x 2 47.4
+// Measured (before rows whose squares overflow were looked for), 16,384 tokens
+// (and 8,191 into an e4m3 pool): 3 warps x 6 blocks 45.4 us (32.6), 2 x 9 46.1
+// (32.5), 1 x 18 46.1 (32.8), 4 x 4 47.3 (35.4), 8 x 2 47.4
 // (35.9), 4 x 5 51.8 (37.0; 13,000 tokens 38.2 with 3 x 6, 40.0 with 4 x 4, and
 // 4,500 16.6 with either: the rounds' ends differ, 18 warps an SM are as good
 // as any).  Batches of 2, 6, 8 at 8 x 2 blocks: 58.5, 49.5, 52.4 against 47.6.
