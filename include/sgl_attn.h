@@ -372,11 +372,12 @@ sgl_status sgl_cascade_decode_attention_fp8(
  * sgl_decode_attention_window -- sgl_decode_attention over those keys (the
  *   query is at position seq_lens[r] - 1).  Arguments, types and errors as
  *   there, but:
- *     seq_lens  : a length below 1 is a padding row: nothing of it is read and
- *                 its row of out stays as it was.  Of a length above
- *                 max_seq_len (or rtt_stride) the positions from there on are
- *                 left out of the keys that its query sees; where that leaves
- *                 none, its row of out stays as it was.
+ *     seq_lens  : a length below 1 is a padding row: neither its req_pool_idx nor
+ *                 anything else of it is used, and its row of out stays as it
+ *                 was.  Of a length above max_seq_len (or rtt_stride) the
+ *                 positions from there on are left out of the keys that its
+ *                 query sees; where that leaves none, its row of out stays as it
+ *                 was.
  *     workspace : >= sgl_decode_window_workspace_bytes(batch, max_seq_len,
  *                 window, sinks, dims); scratch, nothing in it outlasts a call.
  *                 Its first 256 bytes are left as they are, so the extend below
@@ -391,6 +392,7 @@ sgl_status sgl_cascade_decode_attention_fp8(
  *   suffix's slots, already stored (sgl_qk_norm_rope_store_kv or
  *   sgl_store_kv).  Arguments, types and errors as for sgl_extend_attention
  *   without k_new / v_new, but:
+ *     extend_lens: a length of 0 is a padding row, whose req_pool_idx is not used
  *     max_prefix: >= max(prefix_lens) (host value)
  *     workspace : >= sgl_extend_window_workspace_bytes(batch, total_extend,
  *                 max_extend, max_prefix, window, sinks, dims); its first 256
@@ -528,8 +530,9 @@ size_t sgl_cascade_decode_workspace_bytes(int32_t batch, int32_t max_seq_len, in
  * of positions 0..p+e-1 (sgl_extend_attention_fp8 reads the suffix from the
  * pool too).
  * sgl_check_decode_window_indices and sgl_check_extend_window_indices check the
- * positions that the sliding-window calls read (a decode length of 0 is a
- * padding row there, a negative one kind 3).  The slots of
+ * positions that the sliding-window calls read (a decode or extend length of 0 is
+ * a padding row there, whose req_pool_idx may hold anything, a negative one kind
+ * 3).  The slots of
  * sgl_qk_norm_rope_store_kv are checked with sgl_check_store_kv_indices, which
  * reports a padding token's as kind 1: give it the other tokens' alone.
  * sgl_check_store_kv_indices needs a scratch bitmap of (pool_size+7)/8 bytes

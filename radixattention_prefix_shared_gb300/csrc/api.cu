@@ -71,13 +71,18 @@ __global__ void check_store_kernel(const int32_t* __restrict__ slots, int32_t n,
 // mode 1: decode (lens_a = seq).
 // With a window (window > 0, modes 1 and 2) only the positions some query sees
 // are checked: [0, sinks) and those past the first query's position less the
-// window; decode lengths may then be 0 (a padding row).
+// window; decode and extend lengths may then be 0 (a padding row).
 __global__ void check_rows_kernel(const int32_t* __restrict__ rtt, int32_t rtt_rows, int32_t stride,
                                   const int32_t* __restrict__ rpi, const int32_t* __restrict__ lens_a,
                                   const int32_t* __restrict__ lens_b, int32_t mode, int64_t S,
                                   int32_t max_a, int32_t max_b, int32_t window, int32_t sinks,
                                   int32_t* err) {
   const int r = blockIdx.x;
+  if (window > 0 && (mode == 1 ? lens_a[r] : lens_b[r]) == 0) {
+    // a padding row: nothing of it is read, its row of the table either
+    if (mode != 1 && lens_a[r] < 0 && threadIdx.x == 0) report(err, 3, r, 0, lens_a[r]);
+    return;
+  }
   const int32_t row = rpi[r];
   if (row < 0 || row >= rtt_rows) {
     if (threadIdx.x == 0) report(err, 2, r, 0, row);
@@ -99,13 +104,10 @@ __global__ void check_rows_kernel(const int32_t* __restrict__ rtt, int32_t rtt_r
       return;
     }
     n = mode == 2 ? pl + el : pl;
-    if (window > 0) {
-      lo = max(0, pl - window + 1);
-      if (el == 0) n = 0;
-    }
+    if (window > 0) lo = max(0, pl - window + 1);
   } else {
     const int32_t sl = lens_a[r];
-    if (sl < (window > 0 ? 0 : 1)) {
+    if (sl < 1) {
       if (threadIdx.x == 0) report(err, 3, r, 0, sl);
       return;
     }
