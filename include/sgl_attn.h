@@ -532,9 +532,9 @@ size_t sgl_cascade_decode_workspace_bytes(int32_t batch, int32_t max_seq_len, in
  * sgl_check_decode_window_indices and sgl_check_extend_window_indices check the
  * positions that the sliding-window calls read (a decode or extend length of 0 is
  * a padding row there, whose req_pool_idx may hold anything, a negative one kind
- * 3).  The slots of
- * sgl_qk_norm_rope_store_kv are checked with sgl_check_store_kv_indices, which
- * reports a padding token's as kind 1: give it the other tokens' alone.
+ * 3).  The slots of sgl_qk_norm_rope_store_kv are checked with
+ * sgl_check_store_kv_indices, which reports a padding token's as kind 1: give it
+ * the other tokens' alone.
  * sgl_check_store_kv_indices needs a scratch bitmap of (pool_size+7)/8 bytes
  * (rounded up to 16) in `bitmap`; it is cleared by the call.
  * sgl_check_cascade_groups needs sgl_check_cascade_scratch_bytes(batch,
