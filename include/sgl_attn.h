@@ -497,6 +497,116 @@ sgl_status sgl_qk_norm_rope_store_kv_fp8(const void* q, int64_t q_stride, const 
                                          float k_scale, float v_scale, const sgl_attn_dims* dims,
                                          sgl_stream_t stream);
 
+/*
+ * A step over drafted tokens (speculative decoding): a draft model proposes a
+ * tree of tokens for each running request, one pass of the target model computes
+ * them all, the walk down the tree keeps a path, and the path's slots stay.
+ *
+ * Node i (0 <= i < n, n = draft_lens[r]) of request r is token off + i of the
+ * step's [T, ...] tensors, off the sum of draft_lens before r; parents[off + i]
+ * is its parent's index among the request's nodes, below i (a value outside
+ * [0, i): it has none).  At most 64 nodes a request (max_draft above: SGL_ERR_UNSUPPORTED).
+ * A draft_lens entry of 0 (or less) is a padding row: nothing of it is read.
+ *
+ * sgl_verify_attention -- attention of the drafted tokens.  Node i's queries see
+ *   the request's prefix, itself, and the nodes above it (its parent, the
+ *   parent's parent, ...):
+ *     out[off + i, h] = softmax_j(scale q[off + i, h] . K_j) . V_j
+ *   over j < prefix_lens[r] and j = prefix_lens[r] + k, k = i or above i, K_j and V_j
+ *   the pool rows at req_to_token[row, j]: the drafted tokens' K and V are stored
+ *   first, node k's slot at position prefix_lens[r] + k.  A chain (parents i - 1) is
+ *   sgl_extend_attention over the pool.
+ *     parents      : int32 [T]
+ *     prefix_lens  : int32 [batch], >= 0;  draft_lens: int32 [batch]
+ *     total_draft  : T (host value); rows of q and out behind the sum of draft_lens
+ *                    are not read and stay as they were
+ *     max_draft, max_prefix : host values >= the largest length; longer ones are cut.
+ *                    prefix + draft_lens <= rtt_stride
+ *     shared_len   : the batch's rows hold the same slots at positions [0, shared_len)
+ *                    (host value, <= every prefix of a request with tokens; 0: nothing
+ *                    is shared).  Those keys are read once for all requests.
+ *     out          : bf16 [T, Hq, D]; may be q itself (another overlap with q or the
+ *                    pools is SGL_ERR_INVALID_ARG)
+ *     workspace    : >= sgl_verify_workspace_bytes(batch, total_draft, max_draft,
+ *                    max_prefix, shared_len, dims), which grows with every argument;
+ *                    its first 256 bytes zero-filled once before first use (word 0:
+ *                    the bounded-wait status, as for sgl_extend_attention).  Calls
+ *                    whose kernels may overlap need one each.
+ *   Scores, sums and outputs are accumulated in fp32; the weights go to the tensor
+ *   core in bf16 (f16 over e4m3 pools, where the query is widened to f16 as by
+ *   sgl_extend_attention_fp8).
+ *
+ * sgl_verify_drafts -- which drafted tokens the target model keeps, and the token
+ *   after them.  Node 0 is the root: the last token that the request already has,
+ *   always kept (its draft_tokens and coins entries are not used).  Let c be the last
+ *   kept node, R its target row and m = 1.  Nodes 1, 2, ... come in order; node i is
+ *   asked when its parent is c, and kept iff
+ *     R(x) > 0  and  coins[i] * q(x) * m < R(x),      x = draft_tokens[i],
+ *   q(x) = c's draft row at x, or 1 without draft_probs.  A kept node becomes c (R its
+ *   own row, m = 1).  After one that is not kept, R <- max(R / m - q, 0), m <- sum R; or,
+ *   without draft_probs, R(x) <- 0, m <- m - R(x).  The next token is the first v with
+ *   R(0) + ... + R(v) > final_coins[r] * sum R; an R without weight gives way to c's
+ *   target row.  With uniform coins the tokens are distributed as the target's own, if
+ *   drafts were drawn from the draft rows of their parents (independently, one by one), or,
+ *   without draft_probs, picked without chance.
+ *     target_probs : fp32, row of node off + i at (off + i) * target_stride: the
+ *                    target's distribution after that node (rows sum to 1)
+ *     draft_probs  : NULL, or the same of the draft model (draft_stride)
+ *     draft_tokens : int32 [T]; a token outside [0, vocab) is not kept
+ *     coins        : fp32 [T];  final_coins: fp32 [batch]; values in [0, 1)
+ *     accepted     : int32 [batch, max_draft]: the kept nodes, root first, then -1
+ *     num_accepted : int32 [batch]: how many (>= 1)
+ *     next_tokens  : int32 [batch]: -1 where the row has no positive weight
+ *   A padding row gets 0 kept nodes and next token -1.  Weights that are negative,
+ *   infinite or NaN count as 0.  Sums are held in fp64, of partial sums of up to 256
+ *   values in fp32.
+ *
+ * sgl_commit_drafts -- the kept nodes' slots enter the request's row, the others are
+ *   given back:
+ *     req_to_token[row, prefix_lens[r] + k] = slots[off + accepted[r, k]],
+ *     k < num_accepted[r];  seq_lens[r] = prefix_lens[r] + num_accepted[r];
+ *     freed = the slots of all other nodes, request by request in node order,
+ *     *num_freed their number (entries of freed behind it stay as they were).
+ *     slots        : int32 [T], the drafted tokens' slots
+ *     accepted, num_accepted : as sgl_verify_drafts writes them (ascending nodes)
+ *     seq_lens     : int32 [batch];  freed: int32 [T];  num_freed: int32 [1]
+ *   The rows of a batch's requests differ.  Positions outside the row and nodes
+ *   outside the request are skipped.
+ */
+size_t sgl_verify_workspace_bytes(int32_t batch, int32_t total_draft, int32_t max_draft,
+                                  int32_t max_prefix, int32_t shared_len,
+                                  const sgl_attn_dims* dims);
+sgl_status sgl_verify_attention(const void* q, const void* pool_k, const void* pool_v,
+                                const int32_t* req_to_token, int32_t rtt_rows, int32_t rtt_stride,
+                                const int32_t* req_pool_idx, const int32_t* prefix_lens,
+                                const int32_t* draft_lens, const int32_t* parents, int32_t batch,
+                                int32_t total_draft, int32_t max_draft, int32_t max_prefix,
+                                int32_t shared_len, void* out, void* workspace,
+                                size_t workspace_bytes, const sgl_attn_dims* dims,
+                                sgl_stream_t stream);
+sgl_status sgl_verify_attention_fp8(const void* q, const void* pool_k, const void* pool_v,
+                                    float k_scale, float v_scale, const int32_t* req_to_token,
+                                    int32_t rtt_rows, int32_t rtt_stride,
+                                    const int32_t* req_pool_idx, const int32_t* prefix_lens,
+                                    const int32_t* draft_lens, const int32_t* parents,
+                                    int32_t batch, int32_t total_draft, int32_t max_draft,
+                                    int32_t max_prefix, int32_t shared_len, void* out,
+                                    void* workspace, size_t workspace_bytes,
+                                    const sgl_attn_dims* dims, sgl_stream_t stream);
+sgl_status sgl_verify_drafts(const float* target_probs, int64_t target_stride,
+                             const float* draft_probs, int64_t draft_stride, int32_t vocab,
+                             const int32_t* draft_tokens, const int32_t* parents,
+                             const int32_t* draft_lens, int32_t batch, int32_t total_draft,
+                             int32_t max_draft, const float* coins, const float* final_coins,
+                             int32_t* accepted, int32_t* num_accepted, int32_t* next_tokens,
+                             sgl_stream_t stream);
+sgl_status sgl_commit_drafts(int32_t* req_to_token, int32_t rtt_rows, int32_t rtt_stride,
+                             const int32_t* req_pool_idx, const int32_t* prefix_lens,
+                             const int32_t* draft_lens, const int32_t* slots,
+                             const int32_t* accepted, const int32_t* num_accepted, int32_t batch,
+                             int32_t total_draft, int32_t max_draft, int32_t* seq_lens,
+                             int32_t* freed, int32_t* num_freed, sgl_stream_t stream);
+
 /* Workspace sizes (host only; no device call). */
 size_t sgl_extend_workspace_bytes(int32_t batch, int32_t total_extend, const sgl_attn_dims* dims);
 size_t sgl_decode_workspace_bytes(int32_t batch, int32_t max_seq_len, const sgl_attn_dims* dims);
@@ -525,6 +635,11 @@ size_t sgl_cascade_decode_workspace_bytes(int32_t batch, int32_t max_seq_len, in
  *   kind 10: a request's groups do not cover [0, shared_len) back to back
  *           (two groups at one depth, a gap, or a wrong start)
  *                                            a = request, b = depth, c = group / start
+ *   kind 11: a drafted node's parent is neither -1 nor a node before it
+ *                                            a = request, b = node, c = parent
+ *   kind 12: a prefix shorter than shared_len (b = -1, c = prefix), or a slot of the
+ *           shared positions that differs from the first request's
+ *                                            a = request, b = position, c = slot
  * sgl_check_extend_indices checks the slots of positions 0..p-1 of each row
  * (the ones sgl_extend_attention reads); sgl_check_extend_fp8_indices those
  * of positions 0..p+e-1 (sgl_extend_attention_fp8 reads the suffix from the
@@ -535,6 +650,8 @@ size_t sgl_cascade_decode_workspace_bytes(int32_t batch, int32_t max_seq_len, in
  * 3).  The slots of sgl_qk_norm_rope_store_kv are checked with
  * sgl_check_store_kv_indices, which reports a padding token's as kind 1: give it
  * the other tokens' alone.
+ * sgl_check_verify_indices checks what sgl_verify_attention reads: rows, lengths (an
+ * entry of draft_lens of 0 is a padding row), slots, parents and the shared prefix.
  * sgl_check_store_kv_indices needs a scratch bitmap of (pool_size+7)/8 bytes
  * (rounded up to 16) in `bitmap`; it is cleared by the call.
  * sgl_check_cascade_groups needs sgl_check_cascade_scratch_bytes(batch,
@@ -571,6 +688,12 @@ sgl_status sgl_check_extend_window_indices(const int32_t* req_to_token, int32_t 
                                            int32_t batch, int32_t total_extend, int32_t max_extend,
                                            int32_t max_prefix, int32_t window, int32_t sinks,
                                            int64_t pool_size, int32_t* d_error, sgl_stream_t stream);
+sgl_status sgl_check_verify_indices(const int32_t* req_to_token, int32_t rtt_rows,
+                                    int32_t rtt_stride, const int32_t* req_pool_idx,
+                                    const int32_t* prefix_lens, const int32_t* draft_lens,
+                                    const int32_t* parents, int32_t batch, int32_t total_draft,
+                                    int32_t max_draft, int32_t max_prefix, int32_t shared_len,
+                                    int64_t pool_size, int32_t* d_error, sgl_stream_t stream);
 size_t sgl_check_cascade_scratch_bytes(int32_t batch, int32_t max_depth);
 sgl_status sgl_check_cascade_groups(const int32_t* req_to_token, int32_t rtt_rows,
                                     int32_t rtt_stride, const int32_t* req_pool_idx,

@@ -106,6 +106,14 @@ _SIGS = {
     "sgl_qk_norm_rope_store_kv_fp8": (ctypes.c_int, [c_vp, c_i64] * 3
                                       + [c_vp, c_vp, c_f32, c_vp, c_i32, c_vp, c_vp, c_i32, c_i32, c_vp, c_i32,
                                          c_vp, c_vp, c_vp, c_f32, c_f32, _P(sgl_attn_dims), c_vp]),
+    "sgl_verify_workspace_bytes": (c_size, [c_i32] * 5 + [_P(sgl_attn_dims)]),
+    "sgl_verify_attention": (ctypes.c_int, [c_vp] * 4 + [c_i32, c_i32] + [c_vp] * 4 + [c_i32] * 5
+                             + [c_vp, c_vp, c_size, _P(sgl_attn_dims), c_vp]),
+    "sgl_verify_attention_fp8": (ctypes.c_int, [c_vp] * 3 + [c_f32, c_f32, c_vp, c_i32, c_i32] + [c_vp] * 4
+                                 + [c_i32] * 5 + [c_vp, c_vp, c_size, _P(sgl_attn_dims), c_vp]),
+    "sgl_check_verify_indices": (ctypes.c_int, [c_vp, c_i32, c_i32] + [c_vp] * 4 + [c_i32] * 5 + [c_i64, c_vp, c_vp]),
+    "sgl_verify_drafts": (ctypes.c_int, [c_vp, c_i64, c_vp, c_i64, c_i32] + [c_vp] * 3 + [c_i32] * 3 + [c_vp] * 6),
+    "sgl_commit_drafts": (ctypes.c_int, [c_vp, c_i32, c_i32] + [c_vp] * 6 + [c_i32] * 3 + [c_vp] * 4),
     "sgl_check_cascade_scratch_bytes": (c_size, [c_i32, c_i32]),
     "sgl_check_cascade_groups": (ctypes.c_int, [c_vp, c_i32, c_i32, c_vp, c_vp, c_i32, c_vp, c_vp, c_vp,
                                                 c_vp, c_vp, c_i32, c_i32, c_i32, c_vp, c_size, c_vp,
@@ -751,6 +759,226 @@ def sgl_qk_norm_rope_store_kv_fp8(q, k, v, positions, inv_freq, slots, pool_k, p
     return _qk_norm_rope_store("sgl_qk_norm_rope_store_kv_fp8", q, k, v, positions, inv_freq, slots, pool_k, pool_v,
                                (float(k_scale), float(v_scale)), q_weight, k_weight, eps, freq_axis, interleaved,
                                q_out, stream)
+
+
+# ----------------------------------------------------------------- drafted tokens
+
+def verify_workspace_bytes(batch, total_draft, max_draft, max_prefix, shared_len, dims: sgl_attn_dims) -> int:
+    _need_i32("verify_workspace_bytes", batch=batch, total_draft=total_draft, max_draft=max_draft,
+              max_prefix=max_prefix, shared_len=shared_len)
+    return int(lib().sgl_verify_workspace_bytes(int(batch), int(total_draft), int(max_draft), int(max_prefix),
+                                                int(shared_len), ctypes.byref(dims)))
+
+
+def _refuse_verify(name, q, pool_k, pool_v, kv_dtype, req_to_token, req_pool_idx, prefix_lens, draft_lens, parents,
+                   out, workspace):
+    """Names what the call cannot take (its checks failed)."""
+    import torch
+    _need_dense(name, torch.bfloat16, q=q, out=out)
+    _need_dense(name, kv_dtype, pool_k=pool_k, pool_v=pool_v)
+    _need_dense(name, torch.int32, req_to_token=req_to_token, req_pool_idx=req_pool_idx, prefix_lens=prefix_lens,
+                draft_lens=draft_lens, parents=parents)
+    _need(name, q.dim() == 3 and pool_k.dim() == 3 and pool_v.shape == pool_k.shape
+          and q.shape[2] == pool_k.shape[2], "q [T, Hq, D] and pools [S, Hkv, D]")
+    _need(name, req_to_token.dim() == 2, "req_to_token [rows, stride]")
+    _need(name, out is None or out.shape == q.shape, "out of q's shape")
+    _need(name, workspace is None or (workspace.is_contiguous() and workspace.get_device() == q.get_device()),
+          "workspace: a dense buffer on q's device")
+    raise ValueError(f"{name}: one entry a request in req_pool_idx, prefix_lens and draft_lens, one parent a token")
+
+
+def _verify(name, q, pool_k, pool_v, scales, req_to_token, req_pool_idx, prefix_lens, draft_lens, parents, out,
+            max_draft, max_prefix, shared_len, total_draft, workspace, sm_scale, stream):
+    T = _torch()
+    bf16, i32, dev = T.bf16, T.i32, T.current_device()
+    kv = T.u8 if scales else bf16
+    qs, ks, ts, bs = q.shape, pool_k.shape, req_to_token.shape, req_pool_idx.shape
+    if not (q.dtype is bf16 and q.is_contiguous() and q.get_device() == dev and len(qs) == 3
+            and pool_k.dtype is kv and pool_k.is_contiguous() and pool_k.get_device() == dev and len(ks) == 3
+            and pool_v.dtype is kv and pool_v.is_contiguous() and pool_v.get_device() == dev
+            and pool_v.shape == ks and qs[2] == ks[2]
+            and req_to_token.dtype is i32 and req_to_token.is_contiguous() and req_to_token.get_device() == dev
+            and len(ts) == 2
+            and req_pool_idx.dtype is i32 and req_pool_idx.is_contiguous() and req_pool_idx.get_device() == dev
+            and prefix_lens.dtype is i32 and prefix_lens.is_contiguous() and prefix_lens.get_device() == dev
+            and draft_lens.dtype is i32 and draft_lens.is_contiguous() and draft_lens.get_device() == dev
+            and parents.dtype is i32 and parents.is_contiguous() and parents.get_device() == dev
+            and len(bs) == 1 and prefix_lens.shape == bs and draft_lens.shape == bs and parents.shape == qs[:1]
+            and (out is None or (out.dtype is bf16 and out.is_contiguous() and out.get_device() == dev
+                                 and out.shape == qs))
+            and (workspace is None or (workspace.is_contiguous() and workspace.get_device() == dev))):
+        _refuse_verify(name, q, pool_k, pool_v, kv, req_to_token, req_pool_idx, prefix_lens, draft_lens, parents,
+                       out, workspace)
+    total = qs[0] if total_draft is None else int(total_draft)
+    _need(name, total <= qs[0], "total_draft within q's rows")
+    if not (-_I32 <= max_draft <= _I32 and -_I32 <= max_prefix <= _I32 and -_I32 <= shared_len <= _I32
+            and -_I32 <= total):
+        _need_i32(name, max_draft=max_draft, max_prefix=max_prefix, shared_len=shared_len, total_draft=total)
+    dims = _dims_ref(qs[1], ks[1], ks[2], ks[0], float(sm_scale))
+    if out is None or workspace is None:
+        with _on(stream):
+            if out is None:
+                out = T.empty_like(q)
+            if workspace is None:
+                workspace = new_workspace(lib().sgl_verify_workspace_bytes(
+                    bs[0], total, int(max_draft), int(max_prefix), int(shared_len), dims), q.device)
+    code = getattr(lib(), name)(
+        q.data_ptr(), pool_k.data_ptr(), pool_v.data_ptr(), *scales, req_to_token.data_ptr(), ts[0], ts[1],
+        req_pool_idx.data_ptr(), prefix_lens.data_ptr(), draft_lens.data_ptr(), parents.data_ptr(), bs[0], total,
+        int(max_draft), int(max_prefix), int(shared_len), out.data_ptr(), workspace.data_ptr(), workspace.nbytes, dims,
+        T.current_stream(dev) if stream is None else _raw_stream(stream))
+    _in_use(stream, q, pool_k, pool_v, req_to_token, req_pool_idx, prefix_lens, draft_lens, parents, out, workspace)
+    if code != 0:
+        raise SglError(name, code)
+    return out
+
+
+def sgl_verify_attention(q, pool_k, pool_v, req_to_token, req_pool_idx, prefix_lens, draft_lens, parents, out=None, *,
+                         max_draft, max_prefix, shared_len=0, total_draft=None, workspace=None, sm_scale=0.0,
+                         stream=None):
+    """Attention of drafted tokens: each request's nodes see its prefix, themselves
+    and the nodes above them (``parents``: indices among the request's nodes, -1
+    for none).  The drafted tokens' K and V are stored first, at positions prefix,
+    prefix + 1, ... of the request's row.  ``shared_len``: positions whose slots all
+    rows of the batch share, read once."""
+    return _verify("sgl_verify_attention", q, pool_k, pool_v, (), req_to_token, req_pool_idx, prefix_lens, draft_lens,
+                   parents, out, max_draft, max_prefix, shared_len, total_draft, workspace, sm_scale, stream)
+
+
+def sgl_verify_attention_fp8(q, pool_k, pool_v, k_scale, v_scale, req_to_token, req_pool_idx, prefix_lens, draft_lens,
+                             parents, out=None, *, max_draft, max_prefix, shared_len=0, total_draft=None,
+                             workspace=None, sm_scale=0.0, stream=None):
+    """``sgl_verify_attention`` over an e4m3 pool (values are code * scale)."""
+    return _verify("sgl_verify_attention_fp8", q, pool_k, pool_v, (float(k_scale), float(v_scale)), req_to_token,
+                   req_pool_idx, prefix_lens, draft_lens, parents, out, max_draft, max_prefix, shared_len,
+                   total_draft, workspace, sm_scale, stream)
+
+
+def sgl_check_verify_indices(req_to_token, req_pool_idx, prefix_lens, draft_lens, parents, *, total_draft, max_draft,
+                             max_prefix, shared_len=0, pool_size, d_error, stream=None):
+    _need_i32("sgl_check_verify_indices", total_draft=total_draft, max_draft=max_draft, max_prefix=max_prefix,
+              shared_len=shared_len)
+    _check("sgl_check_verify_indices", lib().sgl_check_verify_indices(
+        _ptr(req_to_token), int(req_to_token.shape[0]), int(req_to_token.shape[1]), _ptr(req_pool_idx),
+        _ptr(prefix_lens), _ptr(draft_lens), _ptr(parents), int(req_pool_idx.shape[0]), int(total_draft),
+        int(max_draft), int(max_prefix), int(shared_len), int(pool_size), _ptr(d_error), _stream(stream)))
+    _in_use(stream, req_to_token, req_pool_idx, prefix_lens, draft_lens, parents, d_error)
+
+
+def _refuse_drafts(name, f32, i32):
+    """Names what a call over drafted tokens cannot take (its checks failed)."""
+    import torch
+    dev = torch.cuda.current_device()
+    for arg, t in f32.items():
+        _need(name, t is None or (t.dtype is torch.float32 and t.dim() == 2 and t.stride(1) == 1
+                                  and t.get_device() == dev),
+              f"{arg}: fp32 [T, vocab] with dense rows on the current CUDA device")
+    _need_dense(name, torch.int32, **i32)
+    raise ValueError(f"{name}: one row, token, parent and coin a node; one length and final coin a request; "
+                     "accepted [batch, max_draft]")
+
+
+def sgl_verify_drafts(target_probs, draft_tokens, parents, draft_lens, coins, final_coins, draft_probs=None, *,
+                      max_draft, accepted=None, num_accepted=None, next_tokens=None, stream=None):
+    """The walk down each request's tree of drafted tokens: which nodes the target
+    keeps (``accepted`` [batch, max_draft], root first, then -1; ``num_accepted``)
+    and the token after them (``next_tokens``).
+
+    ``target_probs`` [T, vocab] (and ``draft_probs``, where drafts were drawn from
+    it): the distribution after each node; rows may lie apart.  ``coins`` [T] and
+    ``final_coins`` [batch] are uniform in [0, 1)."""
+    name = "sgl_verify_drafts"
+    T = _torch()
+    i32, f32, dev = T.i32, T.f32, T.current_device()
+    ps, bs, md = target_probs.shape, draft_lens.shape, int(max_draft)
+    rows = ps[:1]
+    ok = (target_probs.dtype is f32 and len(ps) == 2 and target_probs.get_device() == dev
+          and (target_probs.stride(1) == 1 or ps[1] == 1)
+          and draft_tokens.dtype is i32 and draft_tokens.is_contiguous() and draft_tokens.get_device() == dev
+          and draft_tokens.shape == rows
+          and parents.dtype is i32 and parents.is_contiguous() and parents.get_device() == dev
+          and parents.shape == rows
+          and draft_lens.dtype is i32 and draft_lens.is_contiguous() and draft_lens.get_device() == dev
+          and len(bs) == 1
+          and coins.dtype is f32 and coins.is_contiguous() and coins.get_device() == dev and coins.shape == rows
+          and final_coins.dtype is f32 and final_coins.is_contiguous() and final_coins.get_device() == dev
+          and final_coins.shape == bs
+          and (draft_probs is None or (draft_probs.dtype is f32 and draft_probs.shape == ps
+                                       and draft_probs.get_device() == dev
+                                       and (draft_probs.stride(1) == 1 or ps[1] == 1)))
+          and (accepted is None or (accepted.dtype is i32 and accepted.is_contiguous()
+                                    and accepted.get_device() == dev and accepted.shape == (bs[0], md))))
+    if ok:
+        for t in (num_accepted, next_tokens):
+            ok = ok and (t is None or (t.dtype is i32 and t.is_contiguous() and t.get_device() == dev
+                                       and t.shape == bs))
+    if not ok:
+        _refuse_drafts(name, dict(target_probs=target_probs, draft_probs=draft_probs),
+                       dict(draft_tokens=draft_tokens, parents=parents, draft_lens=draft_lens, accepted=accepted,
+                            num_accepted=num_accepted, next_tokens=next_tokens))
+    _need(name, 0 < md <= 64, f"max_draft = {md}: trees of 1 to 64 nodes")
+    if accepted is None or num_accepted is None or next_tokens is None:
+        with _on(stream):
+            if accepted is None:
+                accepted = T.empty((bs[0], md), dtype=i32, device=draft_lens.device)
+            if num_accepted is None:
+                num_accepted = T.empty(bs, dtype=i32, device=draft_lens.device)
+            if next_tokens is None:
+                next_tokens = T.empty(bs, dtype=i32, device=draft_lens.device)
+    # the stride of a single row means nothing
+    pt = target_probs.stride(0) if ps[0] > 1 else ps[1]
+    qt = 0 if draft_probs is None else draft_probs.stride(0) if ps[0] > 1 else ps[1]
+    code = lib().sgl_verify_drafts(
+        target_probs.data_ptr(), pt, None if draft_probs is None else draft_probs.data_ptr(), qt, ps[1],
+        draft_tokens.data_ptr(), parents.data_ptr(), draft_lens.data_ptr(), bs[0], ps[0], md, coins.data_ptr(),
+        final_coins.data_ptr(), accepted.data_ptr(), num_accepted.data_ptr(), next_tokens.data_ptr(),
+        T.current_stream(dev) if stream is None else _raw_stream(stream))
+    _in_use(stream, target_probs, draft_tokens, parents, draft_lens, coins, final_coins, draft_probs, accepted,
+            num_accepted, next_tokens)
+    if code != 0:
+        raise SglError(name, code)
+    return accepted, num_accepted, next_tokens
+
+
+def sgl_commit_drafts(req_to_token, req_pool_idx, prefix_lens, draft_lens, slots, accepted, num_accepted, *,
+                      seq_lens=None, freed=None, num_freed=None, stream=None):
+    """The kept nodes' slots (``slots`` [T]: the drafted tokens') into the requests'
+    rows of ``req_to_token``, behind their prefixes; returns the new ``seq_lens``
+    [batch], the other nodes' slots (``freed`` [T], listed from the front) and their
+    number (``num_freed`` [1])."""
+    name = "sgl_commit_drafts"
+    T = _torch()
+    i32, dev = T.i32, T.current_device()
+    ts, bs, ss, xs = req_to_token.shape, req_pool_idx.shape, slots.shape, accepted.shape
+    ok = len(ts) == 2 and len(bs) == 1 and len(ss) == 1 and len(xs) == 2 and xs[0] == bs[0]
+    for t, shape in ((req_to_token, ts), (req_pool_idx, bs), (prefix_lens, bs), (draft_lens, bs), (slots, ss),
+                     (accepted, xs), (num_accepted, bs), (seq_lens, bs), (freed, ss), (num_freed, (1,))):
+        ok = ok and (t is None or (t.dtype is i32 and t.is_contiguous() and t.get_device() == dev
+                                   and t.shape == shape))
+    if not ok:
+        _need_dense(name, i32, req_to_token=req_to_token, req_pool_idx=req_pool_idx, prefix_lens=prefix_lens,
+                    draft_lens=draft_lens, slots=slots, accepted=accepted, num_accepted=num_accepted,
+                    seq_lens=seq_lens, freed=freed, num_freed=num_freed)
+        raise ValueError(f"{name}: req_to_token [rows, stride], one entry a request in req_pool_idx, prefix_lens, "
+                         "draft_lens, num_accepted and seq_lens, accepted [batch, max_draft], slots and freed [T]")
+    _need(name, xs[1] <= 64, f"max_draft = {xs[1]}: trees of at most 64 nodes")
+    if seq_lens is None or freed is None or num_freed is None:
+        with _on(stream):
+            if seq_lens is None:
+                seq_lens = T.empty(bs, dtype=i32, device=slots.device)
+            if freed is None:
+                freed = T.empty(ss, dtype=i32, device=slots.device)
+            if num_freed is None:
+                num_freed = T.empty((1,), dtype=i32, device=slots.device)
+    code = lib().sgl_commit_drafts(
+        req_to_token.data_ptr(), ts[0], ts[1], req_pool_idx.data_ptr(), prefix_lens.data_ptr(), draft_lens.data_ptr(),
+        slots.data_ptr(), accepted.data_ptr(), num_accepted.data_ptr(), bs[0], ss[0], xs[1], seq_lens.data_ptr(),
+        freed.data_ptr(), num_freed.data_ptr(), T.current_stream(dev) if stream is None else _raw_stream(stream))
+    _in_use(stream, req_to_token, req_pool_idx, prefix_lens, draft_lens, slots, accepted, num_accepted, seq_lens,
+            freed, num_freed)
+    if code != 0:
+        raise SglError(name, code)
+    return seq_lens, freed, num_freed
 
 
 # ----------------------------------------------------------------- radix tree

@@ -146,6 +146,36 @@ __global__ void check_sum_kernel(const int32_t* __restrict__ lens, int32_t batch
   }
 }
 
+// Trees of drafted tokens: parents before their nodes, and rows that hold the
+// shared prefix's slots as the first request with tokens does.  (Rows and
+// lengths are check_rows_kernel's.)
+__global__ void check_trees_kernel(const int32_t* __restrict__ rtt, int32_t rtt_rows, int32_t stride,
+                                   const int32_t* __restrict__ rpi, const int32_t* __restrict__ prefix,
+                                   const int32_t* __restrict__ lens, const int32_t* __restrict__ parents,
+                                   int32_t total, int32_t shared, int32_t* err) {
+  const int r = blockIdx.x;
+  if (lens[r] <= 0) return;
+  int64_t off = 0;
+  int32_t first = r;
+  for (int i = r - 1; i >= 0; --i)
+    if (lens[i] > 0) off += lens[i], first = i;
+  for (int i = threadIdx.x; i < lens[r] && off + i < total; i += blockDim.x) {
+    const int32_t p = parents[off + i];
+    if (p < -1 || p >= i) report(err, 11, r, i, p);
+  }
+  if (shared <= 0) return;
+  if (prefix[r] < shared) {
+    if (threadIdx.x == 0) report(err, 12, r, -1, prefix[r]);
+    return;
+  }
+  const int32_t a = rpi[first], b = rpi[r];
+  if (a < 0 || a >= rtt_rows || b < 0 || b >= rtt_rows) return;
+  for (int j = threadIdx.x; j < shared && j < stride; j += blockDim.x) {
+    const int32_t s = rtt[(int64_t)b * stride + j];
+    if (s != rtt[(int64_t)a * stride + j]) report(err, 12, r, j, s);
+  }
+}
+
 // Cascade groups, one block per group (grid-stride): structure, member
 // ranges, shared slots, and each (request, depth) claimed by one group only.
 __global__ void check_groups_kernel(const int32_t* __restrict__ rtt, int32_t rtt_rows,
@@ -974,6 +1004,179 @@ sgl_status sgl_qk_norm_rope_store_kv_fp8(const void* q, int64_t q_stride, const 
   return qk_rope_entry(q, q_stride, k, k_stride, v, v_stride, q_weight, k_weight, eps, positions, n_axes, inv_freq,
                        freq_axis, rot_dim, interleaved, slots, n, q_out, pool_k, pool_v, true, k_scale, v_scale,
                        dims, stream);
+}
+
+// ---------------------------------------------------------------- drafted tokens
+
+size_t sgl_verify_workspace_bytes(int32_t batch, int32_t total_draft, int32_t max_draft, int32_t max_prefix,
+                                  int32_t shared_len, const sgl_attn_dims* dims) {
+  (void)batch, (void)max_prefix;
+  if (dims == nullptr || dims->num_kv_heads <= 0 || dims->num_q_heads <= 0) return 0;
+  return verify_workspace_bytes(total_draft, max_draft, shared_len, dims->num_q_heads, dims->num_kv_heads,
+                                dims->head_dim);
+}
+
+namespace {
+sgl_status verify_entry(const void* q, const void* pool_k, const void* pool_v, bool kv_fp8, float k_scale,
+                        float v_scale, const int32_t* req_to_token, int32_t rtt_rows, int32_t rtt_stride,
+                        const int32_t* req_pool_idx, const int32_t* prefix_lens, const int32_t* draft_lens,
+                        const int32_t* parents, int32_t batch, int32_t total_draft, int32_t max_draft,
+                        int32_t max_prefix, int32_t shared_len, void* out, void* workspace, size_t workspace_bytes,
+                        const sgl_attn_dims* dims, sgl_stream_t stream) {
+  float scale;
+  const sgl_status st = check_dims(dims, &scale);
+  if (st != SGL_OK) return st;
+  if (batch < 0 || total_draft < 0 || max_draft < 0 || max_prefix < 0 || shared_len < 0 || shared_len > max_prefix)
+    return SGL_ERR_INVALID_ARG;
+  if (dims->num_q_heads / dims->num_kv_heads > 128 || max_draft > kMaxDraft) return SGL_ERR_UNSUPPORTED;
+  if (batch == 0 || total_draft == 0) return SGL_OK;
+  if (max_draft < 1 || max_draft > total_draft) return SGL_ERR_INVALID_ARG;
+  if (!q || !pool_k || !pool_v || !req_to_token || !req_pool_idx || !prefix_lens || !draft_lens || !parents || !out)
+    return SGL_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(pool_k) || !aligned16(pool_v) || !aligned16(out)) return SGL_ERR_INVALID_ARG;
+  if (rtt_rows <= 0 || rtt_stride <= 0 || (int64_t)max_prefix + 1 > rtt_stride) return SGL_ERR_INVALID_ARG;
+  const size_t q_bytes = (size_t)total_draft * dims->num_q_heads * dims->head_dim * 2;
+  const size_t pool_bytes =
+      (size_t)dims->pool_size * dims->num_kv_heads * dims->head_dim * (kv_fp8 ? 1 : 2);
+  if ((out != q && overlaps(out, q_bytes, q, q_bytes)) || overlaps(out, q_bytes, pool_k, pool_bytes) ||
+      overlaps(out, q_bytes, pool_v, pool_bytes))
+    return SGL_ERR_INVALID_ARG;
+  if (workspace == nullptr || !aligned16(workspace) ||
+      workspace_bytes < sgl_verify_workspace_bytes(batch, total_draft, max_draft, max_prefix, shared_len, dims))
+    return SGL_ERR_WORKSPACE;
+  VerifyArgs a;
+  a.q = q;
+  a.pool_k = pool_k;
+  a.pool_v = pool_v;
+  a.req_to_token = req_to_token;
+  a.rtt_stride = rtt_stride;
+  a.req_pool_idx = req_pool_idx;
+  a.prefix_lens = prefix_lens;
+  a.draft_lens = draft_lens;
+  a.parents = parents;
+  a.batch = batch;
+  a.total_draft = total_draft;
+  a.max_draft = max_draft;
+  a.max_prefix = max_prefix;
+  a.shared_len = shared_len;
+  a.out = out;
+  a.workspace = workspace;
+  a.num_q_heads = dims->num_q_heads;
+  a.num_kv_heads = dims->num_kv_heads;
+  a.head_dim = dims->head_dim;
+  a.sm_scale = scale;
+  a.kv_fp8 = kv_fp8;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  return launch_verify(a, reinterpret_cast<cudaStream_t>(stream));
+}
+}  // namespace
+
+sgl_status sgl_verify_attention(const void* q, const void* pool_k, const void* pool_v, const int32_t* req_to_token,
+                                int32_t rtt_rows, int32_t rtt_stride, const int32_t* req_pool_idx,
+                                const int32_t* prefix_lens, const int32_t* draft_lens, const int32_t* parents,
+                                int32_t batch, int32_t total_draft, int32_t max_draft, int32_t max_prefix,
+                                int32_t shared_len, void* out, void* workspace, size_t workspace_bytes,
+                                const sgl_attn_dims* dims, sgl_stream_t stream) {
+  return verify_entry(q, pool_k, pool_v, false, 1.f, 1.f, req_to_token, rtt_rows, rtt_stride, req_pool_idx,
+                      prefix_lens, draft_lens, parents, batch, total_draft, max_draft, max_prefix, shared_len, out,
+                      workspace, workspace_bytes, dims, stream);
+}
+
+sgl_status sgl_verify_attention_fp8(const void* q, const void* pool_k, const void* pool_v, float k_scale,
+                                    float v_scale, const int32_t* req_to_token, int32_t rtt_rows,
+                                    int32_t rtt_stride, const int32_t* req_pool_idx, const int32_t* prefix_lens,
+                                    const int32_t* draft_lens, const int32_t* parents, int32_t batch,
+                                    int32_t total_draft, int32_t max_draft, int32_t max_prefix, int32_t shared_len,
+                                    void* out, void* workspace, size_t workspace_bytes, const sgl_attn_dims* dims,
+                                    sgl_stream_t stream) {
+  if (!valid_kv_scale(k_scale) || !valid_kv_scale(v_scale)) return SGL_ERR_INVALID_ARG;
+  return verify_entry(q, pool_k, pool_v, true, k_scale, v_scale, req_to_token, rtt_rows, rtt_stride, req_pool_idx,
+                      prefix_lens, draft_lens, parents, batch, total_draft, max_draft, max_prefix, shared_len, out,
+                      workspace, workspace_bytes, dims, stream);
+}
+
+sgl_status sgl_check_verify_indices(const int32_t* req_to_token, int32_t rtt_rows, int32_t rtt_stride,
+                                    const int32_t* req_pool_idx, const int32_t* prefix_lens,
+                                    const int32_t* draft_lens, const int32_t* parents, int32_t batch,
+                                    int32_t total_draft, int32_t max_draft, int32_t max_prefix, int32_t shared_len,
+                                    int64_t pool_size, int32_t* d_error, sgl_stream_t stream) {
+  if (shared_len < 0 || shared_len > max_prefix || (batch > 0 && !parents)) return SGL_ERR_INVALID_ARG;
+  const sgl_status st =
+      check_extend(req_to_token, rtt_rows, rtt_stride, req_pool_idx, prefix_lens, draft_lens, batch, total_draft,
+                   max_draft, max_prefix, pool_size, d_error, stream, 2, INT32_MAX, 0);
+  if (st != SGL_OK || batch == 0) return st;
+  check_trees_kernel<<<(unsigned)batch, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+      req_to_token, rtt_rows, rtt_stride, req_pool_idx, prefix_lens, draft_lens, parents, total_draft, shared_len,
+      d_error);
+  return last_launch();
+}
+
+sgl_status sgl_verify_drafts(const float* target_probs, int64_t target_stride, const float* draft_probs,
+                             int64_t draft_stride, int32_t vocab, const int32_t* draft_tokens,
+                             const int32_t* parents, const int32_t* draft_lens, int32_t batch, int32_t total_draft,
+                             int32_t max_draft, const float* coins, const float* final_coins, int32_t* accepted,
+                             int32_t* num_accepted, int32_t* next_tokens, sgl_stream_t stream) {
+  if (batch < 0 || total_draft < 0 || max_draft < 0 || vocab < 1 || target_stride < vocab ||
+      (draft_probs != nullptr && draft_stride < vocab))
+    return SGL_ERR_INVALID_ARG;
+  if (max_draft > kMaxDraft || vocab > (1 << 30) || batch > (1 << 27)) return SGL_ERR_UNSUPPORTED;
+  if (batch == 0) return SGL_OK;
+  if (max_draft < 1 || !draft_lens || !accepted || !num_accepted || !next_tokens) return SGL_ERR_INVALID_ARG;
+  if (total_draft > 0 && (!target_probs || !draft_tokens || !parents || !coins || !final_coins))
+    return SGL_ERR_INVALID_ARG;
+  DraftArgs a;
+  a.target_probs = target_probs;
+  a.target_stride = target_stride;
+  a.draft_probs = draft_probs;
+  a.draft_stride = draft_stride;
+  a.vocab = vocab;
+  a.draft_tokens = draft_tokens;
+  a.parents = parents;
+  a.draft_lens = draft_lens;
+  a.batch = batch;
+  a.total_draft = total_draft;
+  a.max_draft = max_draft;
+  a.coins = coins;
+  a.final_coins = final_coins;
+  a.accepted = accepted;
+  a.num_accepted = num_accepted;
+  a.next_tokens = next_tokens;
+  return launch_verify_drafts(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+sgl_status sgl_commit_drafts(int32_t* req_to_token, int32_t rtt_rows, int32_t rtt_stride,
+                             const int32_t* req_pool_idx, const int32_t* prefix_lens, const int32_t* draft_lens,
+                             const int32_t* slots, const int32_t* accepted, const int32_t* num_accepted,
+                             int32_t batch, int32_t total_draft, int32_t max_draft, int32_t* seq_lens,
+                             int32_t* freed, int32_t* num_freed, sgl_stream_t stream) {
+  if (batch < 0 || total_draft < 0 || max_draft < 0 || rtt_rows <= 0 || rtt_stride <= 0) return SGL_ERR_INVALID_ARG;
+  if (max_draft > kMaxDraft) return SGL_ERR_UNSUPPORTED;
+  if (num_freed == nullptr) return SGL_ERR_INVALID_ARG;
+  if (batch == 0)
+    return cudaMemsetAsync(num_freed, 0, sizeof(int32_t), reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? SGL_OK
+               : SGL_ERR_CUDA;
+  if (max_draft < 1 || !req_to_token || !req_pool_idx || !prefix_lens || !draft_lens || !accepted ||
+      !num_accepted || !seq_lens || (total_draft > 0 && (!slots || !freed)))
+    return SGL_ERR_INVALID_ARG;
+  CommitArgs a;
+  a.req_to_token = req_to_token;
+  a.rtt_rows = rtt_rows;
+  a.rtt_stride = rtt_stride;
+  a.req_pool_idx = req_pool_idx;
+  a.prefix_lens = prefix_lens;
+  a.draft_lens = draft_lens;
+  a.slots = slots;
+  a.accepted = accepted;
+  a.num_accepted = num_accepted;
+  a.batch = batch;
+  a.total_draft = total_draft;
+  a.max_draft = max_draft;
+  a.seq_lens = seq_lens;
+  a.freed = freed;
+  a.num_freed = num_freed;
+  return launch_commit_drafts(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 sgl_status sgl_mixed_attention(

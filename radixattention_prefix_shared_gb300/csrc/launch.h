@@ -230,6 +230,65 @@ size_t extend_window_workspace_bytes(int32_t batch, int32_t total_extend, int32_
                                      int32_t head_dim);
 sgl_status launch_extend_window(const ExtendArgs& a, cudaStream_t stream);
 
+// Attention of drafted tokens (verify.cu); the fields follow sgl_verify_attention.
+struct VerifyArgs {
+  const void* q;
+  const void* pool_k;
+  const void* pool_v;
+  const int32_t* req_to_token;
+  int32_t rtt_stride;
+  const int32_t* req_pool_idx;
+  const int32_t* prefix_lens;
+  const int32_t* draft_lens;
+  const int32_t* parents;
+  int32_t batch, total_draft, max_draft, max_prefix, shared_len;
+  void* out;
+  void* workspace;
+  int32_t num_q_heads, num_kv_heads, head_dim;
+  float sm_scale;
+  bool kv_fp8 = false;
+  float k_scale = 1.f, v_scale = 1.f;
+};
+constexpr int32_t kMaxDraft = 64;  // nodes of a tree (a word of ancestor bits)
+size_t verify_workspace_bytes(int32_t total_draft, int32_t max_draft, int32_t shared_len, int32_t num_q_heads,
+                              int32_t num_kv_heads, int32_t head_dim);
+sgl_status launch_verify(const VerifyArgs& a, cudaStream_t stream);
+
+// The walk down the drafted trees and what becomes of their slots (drafts.cu);
+// the fields follow sgl_verify_drafts and sgl_commit_drafts.
+struct DraftArgs {
+  const float* target_probs;
+  int64_t target_stride;
+  const float* draft_probs;
+  int64_t draft_stride;
+  int32_t vocab;
+  const int32_t* draft_tokens;
+  const int32_t* parents;
+  const int32_t* draft_lens;
+  int32_t batch, total_draft, max_draft;
+  const float* coins;
+  const float* final_coins;
+  int32_t* accepted;
+  int32_t* num_accepted;
+  int32_t* next_tokens;
+};
+sgl_status launch_verify_drafts(const DraftArgs& a, cudaStream_t stream);
+struct CommitArgs {
+  int32_t* req_to_token;
+  int32_t rtt_rows, rtt_stride;
+  const int32_t* req_pool_idx;
+  const int32_t* prefix_lens;
+  const int32_t* draft_lens;
+  const int32_t* slots;
+  const int32_t* accepted;
+  const int32_t* num_accepted;
+  int32_t batch, total_draft, max_draft;
+  int32_t* seq_lens;
+  int32_t* freed;
+  int32_t* num_freed;
+};
+sgl_status launch_commit_drafts(const CommitArgs& a, cudaStream_t stream);
+
 // One launch for an extend batch and a plain decode batch over the same bf16
 // pools (mixed.cu): persistent CTAs, one an SM, the first extend_ctas taking
 // extend tiles first and the rest decode work first.  Shapes the single launch

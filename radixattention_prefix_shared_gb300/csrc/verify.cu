@@ -1,0 +1,1107 @@
+// Attention of drafted tokens (speculative decoding) on tcgen05 tensor cores.
+//
+// A request holds a prefix of p cached tokens and a tree of n drafted ones, all
+// stored in the pool.  Node t's query sees the prefix and, of the tree, itself
+// and the nodes above it:
+//     out[t, h] = softmax_j(scale q[t, h] . K_j) V over j < p and j = p + i,
+//     i in {t, parent(t), parent(parent(t)), ...}.
+//
+// The n g query rows that share a KV head (g = Hq / Hkv) are too few to fill the
+// 128 rows of a tensor-core tile, and the keys are many, so the keys take the
+// tile's rows and the queries its columns:
+//     S^T [128 keys x N] = K Q^T,   O^T [D x N] += V^T P^T,
+// N = 16, 32, 64 or 128 columns.  A tile costs the tensor core what its columns
+// need, K and V enter it as they lie in shared memory (K as a K-major operand,
+// V^T as an MN-major one), and up to 128 query rows read each key once: the call
+// is bound by HBM.  A thread owns a key's row of S^T: it exponentiates N columns
+// and stores them as 16-byte pieces of an MN-major P^T.
+//
+// Softmax: all keys of a block use one reference per column, the maximum of the
+// segment's first block; a later block is accepted while no weight exceeds 2^30
+// (bf16; 2^15 in f16), so maxima over the keys, which lie across the threads, are
+// rare: a butterfly that leaves one column a lane.  Sums are held by column in
+// each thread, in fp32, and added up at the segment's end.
+//
+// Work: (KV head, request, tile of columns) are units of 128-key blocks, laid
+// one after another; every CTA, one an SM, takes an equal run of blocks.  A
+// unit that one CTA holds whole is written as it ends; the pieces of the others
+// leave fp32 states that a second kernel merges.  KV heads are the outermost
+// index, so the CTAs of neighbouring heads walk the same slots at about the same
+// time and their rows share DRAM pages.
+//
+// A prefix that the whole batch shares (shared_len) is a unit of its own, whose
+// columns are the rows of all requests: a launch before that of the rest.
+//
+// Roles: softmax warps (a warpgroup for 32 columns; 64 over e4m3 pools), producer
+// warps (16-byte copies into the swizzled ring; over e4m3 pools the codes go
+// through registers and are widened to f16 there), one thread that issues MMAs.
+// S, P, O and (but for N = 128) Q are held twice, so that the roles meet neither
+// at a block's end nor at a unit's.  Waits are bounded as in the extend kernels.
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "launch.h"
+
+namespace sgl {
+namespace vfy {
+namespace {
+
+constexpr int BN = 128;         // keys of a block
+constexpr int kMaxCtas = 160;   // of a launch (sizes the workspace)
+constexpr int kMaxStages = 12;
+
+template <int D, int N, bool kFp8>
+struct Cfg {
+  static constexpr int kW = N < 32 ? N : 32;  // columns a softmax thread holds at a time
+  static constexpr int kWgs = N <= 32 ? 1 : (kFp8 ? N / 64 : N / 32);
+  static constexpr int kCols = N / kWgs;  // columns of a softmax warpgroup
+  static constexpr int kPasses = kCols / kW;
+  static constexpr int kSoftWarps = 4 * kWgs;
+  static constexpr int kProdWarps = kFp8 ? 8 : 4;
+  static constexpr int kProdThreads = 32 * kProdWarps;
+  static constexpr int kMmaWarp = kSoftWarps + kProdWarps;
+  static constexpr int kThreads = 32 * (kMmaWarp + 1);
+  static constexpr int kChunks = D / 64;         // 128-byte pieces of a row of 16-bit values
+  static constexpr int kChunkBytes = 128 * 128;  // 128 rows of one
+  static constexpr int kTileBytes = kChunks * kChunkBytes;
+  static constexpr int kQChunkBytes = N * 128;
+  static constexpr int kQBytes = kChunks * kQChunkBytes;
+  static constexpr int kQBufs = N == 128 ? 1 : 2;
+  static constexpr int kPBytes = (N + 63) / 64 * kChunkBytes;
+  static constexpr int kMiscBytes = 3072;
+  static constexpr int kFit = (227 * 1024 - kMiscBytes - kQBufs * kQBytes - 2 * kPBytes) / kTileBytes;
+  static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
+  static constexpr int kSmem = kQBufs * kQBytes + 2 * kPBytes + kStages * kTileBytes + kMiscBytes;
+  // largest accepted exponent of a weight, and where the reference puts a
+  // segment's largest: f16 weights start at 2^8, so that they reach down to 2^-32
+  // of it before they round to nothing
+  static constexpr float kAccept = kFp8 ? 15.f : 30.f;
+  static constexpr float kShift = kFp8 ? 8.f : 0.f;
+  static_assert(kStages >= 4 && kStages <= kMaxStages && kSmem <= 227 * 1024, "shared memory");
+  static_assert(4 * N <= 512, "tensor memory");
+};
+
+// A CTA's first block (found by one warp) and what all roles go by.
+struct Start {
+  int32_t kvh, r, tile, off, b, blocks;  // blocks: how many the CTA takes
+  int32_t first_req;                     // first request with tokens
+  int32_t tokens;                        // of the batch
+  int64_t pos, total;                    // first block, blocks of the launch
+};
+
+struct Misc {
+  uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2], pv_done[2], o_full[2], o_free[2], drain;
+  uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
+  uint32_t tmem_base;
+  int abort;
+  Start start;
+  float mcol[128];    // a column's reference
+  float acol[128];    // its rescaling, or what its output is multiplied by
+  int32_t mxcol[128];  // its block maximum, as an ordered integer
+};
+static_assert(sizeof(Misc) <= 3072, "barriers and column states");
+
+struct Params {
+  const __nv_bfloat16* q;
+  const void* pool_k;
+  const void* pool_v;
+  const int32_t* rtt;
+  int64_t rtt_stride;
+  const int32_t* req_pool_idx;
+  const int32_t* prefix_lens;
+  const int32_t* draft_lens;
+  const int32_t* parents;
+  __nv_bfloat16* out;
+  int32_t Hq, Hkv, g, tpt;
+  int32_t batch, total, max_draft, max_prefix, shared;
+  bool shared_pass;  // the launch over the batch's shared prefix
+  float scale_log2, o_scale;
+  int* status;  // word 0: the bounded waits' status; word 1: tokens of the batch
+  uint64_t wait_ns;
+  // states: CTA c's piece of a unit goes to slot 2c + 1 (the unit's first piece)
+  // or 2c, N rows each; whole units' rows go to row_ml / row_acc (nullptr: their
+  // output is written)
+  int4* info;  // per row: first CTA, last CTA, column
+  float2* slot_ml;
+  float* slot_acc;
+  float2* row_ml;
+  float* row_acc;
+};
+
+SGL_DEV int32_t drafts_of(const Params& p, int r) { return max(0, min(__ldg(p.draft_lens + r), p.max_draft)); }
+SGL_DEV int32_t prefix_of(const Params& p, int r) { return max(0, min(__ldg(p.prefix_lens + r), p.max_prefix)); }
+
+// One block after another of a CTA's run.  keys [0, vis) of a unit are seen by
+// every column, keys [vis, vis + n_tree) are its request's tree.
+struct Cursor {
+  int32_t kvh, r, tile, off, n, b, nb, tiles;
+  int32_t k0, vis, n_tree;  // first position; keys
+  SGL_DEV void lens(const Params& p, const Start& s) {
+    if (p.shared_pass) {
+      n = s.tokens;
+      k0 = 0, vis = p.shared, n_tree = 0;
+      tiles = (n + p.tpt - 1) / p.tpt;
+      nb = (vis + BN - 1) / BN;
+    } else {
+      n = drafts_of(p, r);
+      const int32_t pre = prefix_of(p, r);
+      n_tree = (int32_t)min((int64_t)n, p.rtt_stride - pre);  // positions end with the row
+      k0 = min(p.shared, pre);
+      vis = pre - k0;
+      tiles = (n + p.tpt - 1) / p.tpt;
+      nb = n > 0 ? (vis + n_tree + BN - 1) / BN : 0;
+    }
+  }
+  SGL_DEV Cursor(const Params& p, const Start& s) {
+    kvh = s.kvh, r = s.r, tile = s.tile, off = s.off, b = s.b;
+    lens(p, s);
+  }
+  SGL_DEV bool last_of_unit() const { return b + 1 == nb; }
+  // the block after this one (there is one: the caller counts)
+  SGL_DEV void advance(const Params& p, const Start& s) {
+    if (++b < nb) return;
+    b = 0;
+    if (++tile < tiles) return;
+    tile = 0;
+    if (p.shared_pass) {
+      ++kvh;
+      return;
+    }
+    do {
+      off += n;
+      if (++r >= p.batch) r = 0, off = 0, ++kvh;
+      lens(p, s);
+    } while (nb == 0);
+  }
+};
+
+// The CTA whose run of blocks holds block x: runs start at c * total / ctas.
+SGL_DEV int32_t owner(int64_t x, int64_t total, int32_t ctas) { return (int32_t)(((x + 1) * ctas - 1) / total); }
+
+// Finds the CTA's run of blocks (one warp).
+SGL_DEV void find_start(const Params& p, Start* out) {
+  const int lane = threadIdx.x & 31;
+  int64_t blocks = 0;
+  int32_t tokens = 0, first = p.batch;
+  for (int r = lane; r < p.batch; r += 32) {
+    Cursor c = {p, Start{0, r, 0, 0, 0}};
+    if (!p.shared_pass) blocks += (int64_t)c.nb * c.tiles;
+    const int32_t n = drafts_of(p, r);
+    tokens += n;
+    if (n > 0) first = min(first, r);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    blocks += __shfl_xor_sync(0xffffffffu, blocks, o);
+    tokens += __shfl_xor_sync(0xffffffffu, tokens, o);
+    first = min(first, __shfl_xor_sync(0xffffffffu, first, o));
+  }
+  tokens = min(tokens, p.total);
+  Start s = {};
+  s.tokens = tokens;
+  s.first_req = first;
+  if (p.shared_pass) blocks = (int64_t)((tokens + p.tpt - 1) / p.tpt) * ((p.shared + BN - 1) / BN);
+  const int64_t total = blocks * p.Hkv;
+  s.total = total;
+  s.pos = total * blockIdx.x / gridDim.x;
+  s.blocks = (int32_t)(total * (blockIdx.x + 1) / gridDim.x - s.pos);
+  if (s.blocks > 0) {
+    s.kvh = (int32_t)(s.pos / blocks);
+    int64_t rem = s.pos % blocks;
+    if (p.shared_pass) {
+      const int32_t nb = (p.shared + BN - 1) / BN;
+      s.r = first;
+      s.tile = (int32_t)(rem / nb);
+      s.b = (int32_t)(rem % nb);
+    } else {
+      int32_t off = 0;
+      for (int r0 = 0;; r0 += 32) {
+        const int r = r0 + lane;
+        int64_t mine = 0;
+        int32_t n = 0, nb = 1;
+        if (r < p.batch) {
+          const Cursor c = {p, Start{0, r, 0, 0, 0}};
+          n = c.n, nb = max(1, c.nb);
+          mine = (int64_t)c.nb * c.tiles;
+        }
+        int64_t cum = mine;
+        int32_t at = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t a = __shfl_up_sync(0xffffffffu, cum, o);
+          const int32_t t = __shfl_up_sync(0xffffffffu, at, o);
+          if (lane >= o) cum += a, at += t;
+        }
+        const uint32_t hit = __ballot_sync(0xffffffffu, cum > rem);
+        if (hit != 0) {
+          const int w = __ffs(hit) - 1;
+          const int64_t in = rem - __shfl_sync(0xffffffffu, cum - mine, w);
+          const int32_t nbw = __shfl_sync(0xffffffffu, nb, w);
+          s.r = r0 + w;
+          s.off = off + __shfl_sync(0xffffffffu, at - n, w);
+          s.tile = (int32_t)(in / nbw);
+          s.b = (int32_t)(in % nbw);
+          break;
+        }
+        if (r0 + 32 >= p.batch) break;  // (not reached: rem < blocks)
+        rem -= __shfl_sync(0xffffffffu, cum, 31);
+        off += __shfl_sync(0xffffffffu, at, 31);
+      }
+    }
+  }
+  if (lane == 0) *out = s;
+}
+
+SGL_DEV uint32_t sw128(int row, int ci) { return row * 128 + ((ci ^ (row & 7)) << 4); }
+
+SGL_DEV bool warp_wait(uint64_t* bar, uint32_t parity, Misc* m, const Params& p) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) ok = mbar_wait_bounded(bar, parity, &m->abort, p.status, p.wait_ns);
+  return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+}
+
+// floats as integers of the same order
+SGL_DEV int32_t ordered(float x) {
+  const int32_t i = __float_as_int(x);
+  return i < 0 ? i ^ 0x7fffffff : i;
+}
+SGL_DEV float unordered(int32_t i) { return __int_as_float(i < 0 ? i ^ 0x7fffffff : i); }
+
+// v[c] of every lane combined over the warp; lane l is left with column l % W.
+template <int W, typename Op>
+SGL_DEV float columns(float (&v)[W], Op op) {
+  const int lane = threadIdx.x & 31;
+  if constexpr (W == 16) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = op(v[i], __shfl_xor_sync(0xffffffffu, v[i], 16));
+  }
+#pragma unroll
+  for (int s = W / 2; s > 0; s >>= 1) {
+    const bool upper = lane & s;
+#pragma unroll
+    for (int i = 0; i < s; ++i) {
+      const float keep = upper ? v[i + s] : v[i], send = upper ? v[i] : v[i + s];
+      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, s));
+    }
+  }
+  return v[0];
+}
+
+SGL_DEV void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+template <int W>
+SGL_DEV void tmem_ld(uint32_t taddr, uint32_t (&r)[W]) {
+  if constexpr (W == 32) tmem_ld32(taddr, r);
+  else tmem_ld16(taddr, r);
+  tmem_wait_ld();
+}
+template <int W>
+SGL_DEV void tmem_st(uint32_t taddr, const uint32_t (&r)[W]) {
+  if constexpr (W == 32) tmem_st32(taddr, r);
+  else tmem_st16(taddr, r);
+}
+
+// Instruction descriptor, kind::f16, fp32 accumulator, M = 128; S^T = K Q^T has
+// both operands K-major, O^T = V^T P^T both MN-major.
+template <int N, bool kFp8>
+constexpr uint32_t idesc(bool mn_major) {
+  return make_idesc_bf16(128, N, mn_major, kFp8) | ((mn_major ? 1u : 0u) << 15);
+}
+
+// ----------------------------------------------------------------- producers
+
+// A unit's query rows into its Q tile: row m is token tile * tpt + m / g, head m % g.
+template <int D, int N, bool kFp8>
+SGL_DEV void load_q(const Params& p, const Cursor& c, uint32_t sQ, uint64_t* q_full, int ptid) {
+  using C = Cfg<D, N, kFp8>;
+  const int ci = ptid & 7;
+  for (int row = ptid >> 3; row < N; row += C::kProdThreads / 8) {
+    const int k = row / p.g, tok = c.tile * p.tpt + k;
+    const bool valid = k < p.tpt && tok < c.n && c.off + tok < p.total;
+    const int64_t qrow = valid ? (int64_t)(c.off + tok) * p.Hq + (int64_t)c.kvh * p.g + row % p.g : 0;
+    const __nv_bfloat16* src = p.q + qrow * D + ci * 8;
+#pragma unroll
+    for (int h = 0; h < C::kChunks; ++h) {
+      const uint32_t dst = sQ + h * C::kQChunkBytes + sw128(row, ci);
+      if constexpr (kFp8) {
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (valid) w = *reinterpret_cast<const uint4*>(src + 64 * h);
+        float f[8];
+        bf16x8_to_f32(w, f);
+        st_shared_v4(dst, pack_f16x2(f[0], f[1]), pack_f16x2(f[2], f[3]), pack_f16x2(f[4], f[5]),
+                     pack_f16x2(f[6], f[7]));
+      } else {
+        cp_async_16(dst, src + 64 * h, valid ? 16u : 0u);
+      }
+    }
+  }
+  if constexpr (kFp8) {
+    fence_proxy_async_smem();
+    mbar_arrive(q_full);
+  } else {
+    cp_async_mbar_arrive(q_full);
+  }
+}
+
+// The slots of a block's rows first, first + step, ...; -1 where there is no key.
+template <int kRows>
+SGL_DEV void load_slots(const Params& p, const Start& s, const Cursor& c, int first, int step, int32_t (&slot)[kRows]) {
+  const int32_t row = __ldg(p.req_pool_idx + (p.shared_pass ? s.first_req : c.r));
+  const int32_t* t = p.rtt + row * p.rtt_stride + c.k0;
+  const int32_t keys = c.vis + c.n_tree;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int32_t j = c.b * BN + first + step * i;
+    slot[i] = j < keys ? __ldg(t + j) : -1;
+  }
+}
+
+template <int D, int N>
+SGL_DEV void produce(const Params& p, const Start& s, Misc* m, uint32_t sQ, uint32_t sKV, int ptid) {
+  using C = Cfg<D, N, false>;
+  constexpr int kStep = C::kProdThreads / 8, kRows = BN / kStep;
+  const int ci = ptid & 7, rb = ptid >> 3;
+  Cursor c(p, s);
+  int32_t slot[kRows], next[kRows];
+  load_slots(p, s, c, rb, kStep, slot);
+  int seg = 0;
+  auto query = [&]() {
+    const int qb = seg % C::kQBufs, round = seg / C::kQBufs;
+    if (round > 0 && !warp_wait(&m->q_empty[qb], (round - 1) & 1, m, p)) return false;
+    load_q<D, N, false>(p, c, sQ + qb * C::kQBytes, &m->q_full[qb], ptid);
+    return true;
+  };
+  for (int i = 0; i < s.blocks; ++i) {
+    Cursor cn = c;
+    if (i + 1 < s.blocks) {
+      cn.advance(p, s);
+      load_slots(p, s, cn, rb, kStep, next);
+    }
+    const bool opens = i == 0 || c.b == 0;
+    if (opens && C::kQBufs == 2 && !query()) return;
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      const int t = 2 * i + kv, st = t % C::kStages, round = t / C::kStages;
+      if (round > 0 && !warp_wait(&m->kv_empty[st], (round - 1) & 1, m, p)) return;
+      const __nv_bfloat16* pool = static_cast<const __nv_bfloat16*>(kv ? p.pool_v : p.pool_k);
+      const uint32_t dst = sKV + st * C::kTileBytes;
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        const int row = rb + kStep * r;
+        const bool valid = slot[r] >= 0;
+        const __nv_bfloat16* src = pool + ((int64_t)(valid ? slot[r] : 0) * p.Hkv + c.kvh) * D + ci * 8;
+#pragma unroll
+        for (int h = 0; h < C::kChunks; ++h)
+          cp_async_16(dst + h * C::kChunkBytes + sw128(row, ci), src + 64 * h, valid ? 16u : 0u);
+      }
+      cp_async_mbar_arrive(&m->kv_full[st]);
+    }
+    // one Q tile alone: the next unit's waits for the last scores of this one,
+    // and its first keys go ahead of it
+    if (opens && C::kQBufs == 1 && !query()) return;
+    if (c.last_of_unit()) ++seg;
+    c = cn;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) slot[r] = next[r];
+  }
+}
+
+// e4m3 pool: a thread holds its codes of two blocks in registers (64 KB in flight
+// an SM at D = 128) and widens them to f16 as a stage frees.
+template <int D, int N>
+SGL_DEV void produce_fp8(const Params& p, const Start& s, Misc* m, uint32_t sQ, uint32_t sKV, int ptid) {
+  using C = Cfg<D, N, true>;
+  constexpr int kPieces = D / 16;  // 16-byte pieces of a row of codes
+  constexpr int kStep = C::kProdThreads / kPieces, kRows = BN / kStep;
+  struct Held {
+    uint4 k[kRows], v[kRows];
+    int32_t slot[kRows];
+    int32_t kvh;
+  };
+  const int rc = ptid % kPieces, rb = ptid / kPieces;
+  Cursor c(p, s), ahead(p, s);
+  int ahead_i = 0, seg = 0;
+  auto slots = [&](Held& h) {  // of the next block ahead
+    if (ahead_i >= s.blocks) return;
+    if (ahead_i > 0) ahead.advance(p, s);
+    load_slots(p, s, ahead, rb, kStep, h.slot);
+    h.kvh = ahead.kvh;
+    ++ahead_i;
+  };
+  auto codes = [&](Held& h, int i) {  // of block i, whose slots h holds
+    if (i >= s.blocks) return;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const int64_t at = ((int64_t)max(h.slot[r], 0) * p.Hkv + h.kvh) * D + rc * 16;
+      h.k[r] = h.v[r] = make_uint4(0, 0, 0, 0);
+      if (h.slot[r] >= 0) {
+        h.k[r] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.pool_k) + at));
+        h.v[r] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.pool_v) + at));
+      }
+    }
+  };
+  auto widen = [&](const uint4 (&w)[kRows], int st) {
+    const uint32_t dst = sKV + st * C::kTileBytes + (rc >> 2) * C::kChunkBytes;
+    const int piece = 2 * (rc & 3);
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const uint32_t x[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
+      uint32_t o[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x[j] & 0xffffu), __NV_E4M3);
+        const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x[j] >> 16), __NV_E4M3);
+        o[2 * j] = *reinterpret_cast<const uint32_t*>(&a);
+        o[2 * j + 1] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      const int row = rb + kStep * r;
+      st_shared_v4(dst + sw128(row, piece), o[0], o[1], o[2], o[3]);
+      st_shared_v4(dst + sw128(row, piece + 1), o[4], o[5], o[6], o[7]);
+    }
+  };
+  auto query = [&]() {
+    const int qb = seg % C::kQBufs, round = seg / C::kQBufs;
+    if (round > 0 && !warp_wait(&m->q_empty[qb], (round - 1) & 1, m, p)) return false;
+    load_q<D, N, true>(p, c, sQ + qb * C::kQBytes, &m->q_full[qb], ptid);
+    return true;
+  };
+  auto block = [&](Held& h, int i) {
+    if (i > 0) c.advance(p, s);
+    const bool opens = i == 0 || c.b == 0;
+    if (opens && C::kQBufs == 2 && !query()) return false;
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      const int t = 2 * i + kv, st = t % C::kStages, round = t / C::kStages;
+      if (round > 0 && !warp_wait(&m->kv_empty[st], (round - 1) & 1, m, p)) return false;
+      widen(kv ? h.v : h.k, st);
+      fence_proxy_async_smem();
+      mbar_arrive(&m->kv_full[st]);
+    }
+    codes(h, i + 2);
+    slots(h);
+    if (opens && C::kQBufs == 1 && !query()) return false;
+    if (c.last_of_unit()) ++seg;
+    return true;
+  };
+  Held a, b;
+  slots(a);
+  slots(b);
+  codes(a, 0);
+  codes(b, 1);
+  slots(a);
+  slots(b);
+  for (int i = 0; i < s.blocks; i += 2) {
+    if (!block(a, i)) return;
+    if (i + 1 < s.blocks && !block(b, i + 1)) return;
+  }
+}
+
+// ----------------------------------------------------------------- MMA
+
+template <int D, int N, bool kFp8>
+SGL_DEV void issue(const Params& p, const Start& s, Misc* m, uint32_t tmem, uint32_t sQ, uint32_t sP, uint32_t sKV) {
+  using C = Cfg<D, N, kFp8>;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait(bar, parity, 200u)) return true;
+    return mbar_wait_bounded(bar, parity, &m->abort, p.status, p.wait_ns);
+  };
+  Cursor c(p, s);
+  int seg = 0, pv_seg = 0;
+  bool opens = true, pv_opens = true, pv_closes = false;
+  for (int i = 0; i <= s.blocks; ++i) {
+    bool closes = false;
+    if (i < s.blocks) {  // S^T of block i
+      const int t = 2 * i, st = t % C::kStages, qb = seg % C::kQBufs;
+      if (opens && !wait(&m->q_full[qb], (seg / C::kQBufs) & 1)) return;
+      if (!wait(&m->kv_full[st], (t / C::kStages) & 1)) return;
+      fence_proxy_async_smem();
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint64_t a = make_sw128_desc(sKV + st * C::kTileBytes + (kk >> 2) * C::kChunkBytes + (kk & 3) * 32, 16, 1024);
+        const uint64_t b = make_sw128_desc(sQ + qb * C::kQBytes + (kk >> 2) * C::kQChunkBytes + (kk & 3) * 32, 16, 1024);
+        umma_ss(tmem + (i & 1) * N, a, b, idesc<N, kFp8>(false), kk > 0 ? 1u : 0u);
+      }
+      closes = c.last_of_unit() || i + 1 == s.blocks;
+      umma_commit(&m->s_full[i & 1]);
+      umma_commit(&m->kv_empty[st]);
+      if (closes) umma_commit(&m->q_empty[qb]);
+    }
+    if (i > 0) {  // O^T with block i - 1
+      const int j = i - 1, t = 2 * j + 1, st = t % C::kStages, ob = pv_seg & 1;
+      if (pv_opens && pv_seg >= 2 && !wait(&m->o_free[ob], ((pv_seg >> 1) - 1) & 1)) return;
+      if (!wait(&m->kv_full[st], (t / C::kStages) & 1)) return;
+      if (!wait(&m->p_ready[j & 1], (j >> 1) & 1)) return;
+      fence_proxy_async_smem();
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < BN / 16; ++kk) {
+        // 16 keys are 16 rows of 128 bytes in V as in P; 64 dims (or columns) further
+        // on lies the next chunk.  D = 64: the tile's rows 64.. repeat the others.
+        const uint64_t a = make_sw128_desc(sKV + st * C::kTileBytes + kk * 2048, D == 128 ? C::kChunkBytes : 0, 1024);
+        const uint64_t b = make_sw128_desc(sP + (j & 1) * C::kPBytes + kk * 2048, C::kChunkBytes, 1024);
+        umma_ss(tmem + 2 * N + ob * N, a, b, idesc<N, kFp8>(true), (pv_opens && kk == 0) ? 0u : 1u);
+      }
+      umma_commit(&m->kv_empty[st]);
+      umma_commit(&m->pv_done[j & 1]);
+      if (pv_closes) umma_commit(&m->o_full[ob]);
+      pv_opens = pv_closes;
+      if (pv_closes) ++pv_seg;
+    }
+    pv_closes = closes;
+    if (i < s.blocks) {
+      opens = closes;
+      if (closes) ++seg;
+      if (i + 1 < s.blocks) c.advance(p, s);
+    }
+  }
+}
+
+// ----------------------------------------------------------------- softmax
+
+// Which tokens k of the tile see the thread's key, node `node` of the tree: bit
+// k, the node is token tile * tpt + k or above it.  Lanes hold the ancestor sets
+// of nodes lane and lane + 32; each round doubles how far up they reach.
+SGL_DEV uint64_t seen_by(const Params& p, const Cursor& c, int node) {
+  const int lane = threadIdx.x & 31;
+  uint64_t anc[2];
+  int up[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int t = lane + 32 * h;
+    anc[h] = 1ull << t;
+    up[h] = t < c.n && c.off + t < p.total ? __ldg(p.parents + c.off + t) : -1;
+    if (up[h] >= t) up[h] = -1;  // a parent lies before its child
+  }
+  for (int span = 1; span < c.n; span *= 2) {
+    uint64_t a[2];
+    int u[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int src = up[h] & 31;
+      const uint64_t a0 = __shfl_sync(0xffffffffu, anc[0], src), a1 = __shfl_sync(0xffffffffu, anc[1], src);
+      const int u0 = __shfl_sync(0xffffffffu, up[0], src), u1 = __shfl_sync(0xffffffffu, up[1], src);
+      a[h] = up[h] < 0 ? 0ull : up[h] < 32 ? a0 : a1;
+      u[h] = up[h] < 0 ? -1 : up[h] < 32 ? u0 : u1;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) anc[h] |= a[h], up[h] = u[h];
+  }
+  uint64_t seen = 0;
+  const int t0 = c.tile * p.tpt, most = min(p.tpt, c.n - t0);
+  for (int k = 0; k < most; ++k) {
+    const int t = t0 + k;
+    const uint64_t a = __shfl_sync(0xffffffffu, t < 32 ? anc[0] : anc[1], t & 31);
+    if (node >= 0 && node < 64 && (a >> node & 1)) seen |= 1ull << k;
+  }
+  return seen;
+}
+
+template <int D, int N, bool kFp8>
+SGL_DEV void softmax(const Params& p, const Start& s, Misc* m, uint32_t tmem, uint8_t* sP) {
+  using C = Cfg<D, N, kFp8>;
+  constexpr int W = C::kW;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int wg = warp >> 2, q = warp & 3, key = q * 32 + lane, col0 = wg * C::kCols, wt = tid & 127;
+  const uint32_t bar = 1 + wg;
+  const uint32_t lanes = (uint32_t)(q * 32) << 16;
+  const uint32_t sP_a = smem_u32(sP);
+  Cursor c(p, s);
+  int seg = 0;
+  bool opens = true, first_masked = false, ok = true;
+  int32_t b_first = 0;  // the segment's first block in its unit
+  float l[C::kCols];
+  for (int i = 0; i < s.blocks; ++i) {
+    ok = warp_wait(&m->s_full[i & 1], (i >> 1) & 1, m, p) && ok;
+    tc_fence_after();
+    const int node = c.b * BN + key - c.vis;  // of the tree; below 0 a key that all see
+    const bool masked = (c.b + 1) * BN > c.vis;
+    const uint64_t seen = masked && c.n_tree > 0 ? seen_by(p, c, node) : 0ull;
+    if (opens) first_masked = masked, b_first = c.b;
+    const uint32_t tS = tmem + lanes + (i & 1) * N + col0;
+    const uint32_t tO = tmem + lanes + 2 * N + (seg & 1) * N + col0;
+    auto load = [&](int pass, uint32_t (&x)[W]) {
+      tmem_ld<W>(tS + pass * W, x);
+      if (masked && node >= 0) {
+        int k = (col0 + pass * W) / p.g, h = (col0 + pass * W) % p.g;
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          const bool sees = node < c.n_tree && (k >= 64 || (seen >> k & 1));
+          if (!sees) x[e] = __float_as_uint(-INFINITY);
+          if (++h == p.g) h = 0, ++k;
+        }
+      }
+    };
+    const float sc = p.scale_log2;
+    // scores against their columns' references, in units of log 2
+    auto relative = [&](int pass, uint32_t (&x)[W]) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < W; e += 4) {
+        const float4 r = *reinterpret_cast<const float4*>(&m->mcol[col0 + pass * W + e]);
+        const float2 s2 = make_float2(sc, sc);
+        float2 a = ffma2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), s2, make_float2(-r.x, -r.y));
+        float2 b = ffma2(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), s2, make_float2(-r.z, -r.w));
+        x[e] = __float_as_uint(a.x), x[e + 1] = __float_as_uint(a.y);
+        x[e + 2] = __float_as_uint(b.x), x[e + 3] = __float_as_uint(b.y);
+        top = fmax3(top, a.x, a.y);
+        top = fmax3(top, b.x, b.y);
+      }
+      return top;
+    };
+    uint32_t x[W];
+    // a segment's first block sets the references; one whose first block hides
+    // keys (columns may have seen none yet) sets them block by block
+    bool redo = opens || (masked && first_masked);
+    if (!redo) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int pass = 0; pass < C::kPasses; ++pass) {
+        load(pass, x);
+        top = fmaxf(top, relative(pass, x));
+      }
+      redo = top > C::kAccept;
+    }
+    // the warpgroup agrees: lane 0 votes to move the references, lanes 1 to 8
+    // that the warp gave up waiting
+    const bool redo_w = __any_sync(0xffffffffu, redo);
+    const uint32_t votes = bar_red_popc(bar, 128, (lane == 0 && redo_w) || (lane >= 1 && lane <= 8 && !ok));
+    if (votes >= 8) return;
+    if (votes != 0) {
+#pragma unroll
+      for (int pass = 0; pass < C::kPasses; ++pass) {
+        load(pass, x);
+        const float top = columns<W>(*reinterpret_cast<float(*)[W]>(&x), [](float a, float b) { return fmaxf(a, b); });
+        atomicMax(&m->mxcol[col0 + pass * W + (lane & (W - 1))], ordered(top));
+      }
+      named_bar_sync(bar, 128);
+      if (wt < C::kCols) {
+        const int col = col0 + wt;
+        const float before = opens ? -INFINITY : m->mcol[col];
+        const float now = fmaxf(before, unordered(m->mxcol[col]) * sc - C::kShift);
+        m->mxcol[col] = ordered(-INFINITY);
+        m->mcol[col] = now;
+        m->acol[col] = before == -INFINITY ? 0.f : ex2(before - now);
+      }
+      named_bar_sync(bar, 128);
+      if (opens) {
+#pragma unroll
+        for (int e = 0; e < C::kCols; ++e) l[e] = 0.f;
+      } else {
+        ok = warp_wait(&m->pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, m, p) && ok;
+        tc_fence_after();
+#pragma unroll
+        for (int pass = 0; pass < C::kPasses; ++pass) {
+          tmem_ld<W>(tO + pass * W, x);
+#pragma unroll
+          for (int e = 0; e < W; ++e) {
+            const float a = m->acol[col0 + pass * W + e];
+            l[pass * W + e] *= a;
+            x[e] = __float_as_uint(__uint_as_float(x[e]) * a);
+          }
+          tmem_st<W>(tO + pass * W, x);
+        }
+        tmem_wait_st();
+      }
+    }
+    // P^T: this key's row, 8 columns a 16-byte piece; its buffer was last read
+    // with block i - 2
+    if (i >= 2) ok = warp_wait(&m->pv_done[i & 1], ((i >> 1) - 1) & 1, m, p) && ok;
+#pragma unroll
+    for (int pass = 0; pass < C::kPasses; ++pass) {
+      if (C::kPasses > 1 || votes != 0) {
+        load(pass, x);
+        relative(pass, x);
+      }
+      if (votes != 0) {  // a column that has seen no key yet
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+          if (m->mcol[col0 + pass * W + e] == -INFINITY) x[e] = __float_as_uint(-INFINITY);
+      }
+#pragma unroll
+      for (int e = 0; e < W; e += 8) {
+        uint32_t o[4];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          const int at = e + 2 * d;
+          const float2 w = make_float2(ex2(__uint_as_float(x[at])), ex2(__uint_as_float(x[at + 1])));
+          const float2 sum = fadd2(make_float2(l[pass * W + at], l[pass * W + at + 1]), w);
+          l[pass * W + at] = sum.x, l[pass * W + at + 1] = sum.y;
+          o[d] = kFp8 ? pack_f16x2(w.x, w.y) : pack_bf16x2(w.x, w.y);
+        }
+        const int col = col0 + pass * W + e;
+        st_shared_v4(sP_a + (i & 1) * C::kPBytes + (col >> 6) * C::kChunkBytes + sw128(key, (col & 63) >> 3), o[0], o[1],
+                     o[2], o[3]);
+      }
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    mbar_arrive(&m->p_ready[i & 1]);
+    const bool closes = c.last_of_unit() || i + 1 == s.blocks;
+    if (closes) {
+      // the segment's sums and O^T: lane d of warp q is dim 32 q + d
+      ok = warp_wait(&m->o_full[seg & 1], (seg >> 1) & 1, m, p) && ok;
+      tc_fence_after();
+      if (bar_red_or(bar, 128, !ok)) return;
+      // P's rows are free: each warp leaves its 32 keys' sums there, a column a row
+#pragma unroll
+      for (int pass = 0; pass < C::kPasses; ++pass) {
+        const float sum = columns<W>(*reinterpret_cast<float(*)[W]>(&l[pass * W]), [](float a, float b) { return a + b; });
+        float* at = reinterpret_cast<float*>(sP + (i & 1) * C::kPBytes + (col0 >> 6) * C::kChunkBytes +
+                                             sw128(key, (col0 & 63) >> 3));
+        if (lane < W) at[pass] = sum;
+      }
+      named_bar_sync(bar, 128);
+      const bool whole = b_first == 0 && c.last_of_unit();
+      const bool direct = whole && p.row_ml == nullptr;
+      const int64_t slot = (int64_t)(2 * blockIdx.x + (b_first == 0 ? 1 : 0)) * N;
+      auto row_of = [&](int col) -> int64_t {  // of [tokens x Hq], or -1
+        const int k = col / p.g, tok = c.tile * p.tpt + k;
+        if (k >= p.tpt || tok >= c.n || c.off + tok >= p.total) return -1;
+        return (int64_t)(c.off + tok) * p.Hq + (int64_t)c.kvh * p.g + col % p.g;
+      };
+      if (wt < C::kCols) {
+        const int col = col0 + wt;
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+          sum += reinterpret_cast<const float*>(sP + (i & 1) * C::kPBytes + (col0 >> 6) * C::kChunkBytes +
+                                                sw128(w * 32 + wt % W, (col0 & 63) >> 3))[wt / W];
+        m->acol[col] = direct ? p.o_scale / sum : 1.f;
+        const int64_t row = row_of(col);
+        if (row >= 0) {
+          const float2 ml = make_float2(m->mcol[col], sum);
+          if (!whole) p.slot_ml[slot + col] = ml;
+          else if (!direct) p.row_ml[row] = ml;
+          if (b_first == 0) {
+            const int64_t u0 = s.pos + i - c.b;  // the unit's first block
+            p.info[row] = make_int4(blockIdx.x, owner(u0 + c.nb - 1, s.total, gridDim.x), col, 0);
+          }
+        }
+      }
+      named_bar_sync(bar, 128);
+      const int t0 = c.tile * p.tpt;
+      const int most = min(min(p.tpt, c.n - t0), p.total - c.off - t0);  // tokens of the tile
+#pragma unroll
+      for (int pass = 0; pass < C::kPasses; ++pass) {
+        tmem_ld<W>(tO + pass * W, x);
+        const int base = col0 + pass * W;
+        int k = base / p.g, h = base % p.g;
+        int64_t row = (int64_t)(c.off + t0 + k) * p.Hq + (int64_t)c.kvh * p.g + h;
+        if (key < D) {
+#pragma unroll
+          for (int e = 0; e < W; ++e) {
+            if (k < most) {
+              const float o = __uint_as_float(x[e]);
+              if (direct) p.out[row * D + key] = __float2bfloat16_rn(o * m->acol[base + e]);
+              else if (whole) p.row_acc[row * D + key] = o;
+              else p.slot_acc[(slot + base + e) * D + key] = o;
+            }
+            ++row;
+            if (++h == p.g) h = 0, ++k, row += p.Hq - p.g;
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&m->o_free[seg & 1]);
+      ++seg;
+    }
+    opens = closes;
+    if (i + 1 < s.blocks) c.advance(p, s);
+  }
+}
+
+// ----------------------------------------------------------------- kernels
+
+template <int D, int N, bool kFp8>
+__global__ void __launch_bounds__(Cfg<D, N, kFp8>::kThreads, 1) verify_kernel(const Params p) {
+  using C = Cfg<D, N, kFp8>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* sQ = smem;
+  uint8_t* sP = sQ + C::kQBufs * C::kQBytes;
+  uint8_t* sKV = sP + 2 * C::kPBytes;
+  Misc* m = reinterpret_cast<Misc*>(sKV + C::kStages * C::kTileBytes);
+  const int tid = threadIdx.x, warp = tid >> 5;
+  grid_dep_launch();  // what follows waits for this grid's end
+  if (warp == 0) {
+    find_start(p, &m->start);
+  } else if (tid == 32) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&m->q_full[i], C::kProdThreads);
+      mbar_init(&m->q_empty[i], 1);
+      mbar_init(&m->s_full[i], 1);
+      mbar_init(&m->p_ready[i], 32 * C::kSoftWarps);
+      mbar_init(&m->pv_done[i], 1);
+      mbar_init(&m->o_full[i], 1);
+      mbar_init(&m->o_free[i], 32 * C::kSoftWarps);
+    }
+    mbar_init(&m->drain, 1);
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&m->kv_full[i], C::kProdThreads);
+      mbar_init(&m->kv_empty[i], 1);
+    }
+    m->abort = 0;
+    mbar_fence_init();
+  } else if (warp == C::kMmaWarp) {
+    tmem_alloc(&m->tmem_base, 4 * N);
+    tmem_relinquish();
+  }
+  if (tid < 128) m->mxcol[tid] = ordered(-INFINITY);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const Start s = m->start;
+  const uint32_t tmem = m->tmem_base;
+  if (blockIdx.x == 0 && tid == 0) p.status[1] = s.tokens;
+  if (s.blocks > 0) {
+    if (warp < C::kSoftWarps) {
+      softmax<D, N, kFp8>(p, s, m, tmem, sP);
+    } else if (warp < C::kMmaWarp) {
+      const int ptid = tid - 32 * C::kSoftWarps;
+      if constexpr (kFp8) produce_fp8<D, N>(p, s, m, smem_u32(sQ), smem_u32(sKV), ptid);
+      else produce<D, N>(p, s, m, smem_u32(sQ), smem_u32(sKV), ptid);
+    } else if ((tid & 31) == 0) {
+      issue<D, N, kFp8>(p, s, m, tmem, smem_u32(sQ), smem_u32(sP), smem_u32(sKV));
+      // MMAs issued before a wait gave up end before the CTA does
+      umma_commit(&m->drain);
+      mbar_wait_bounded(&m->drain, 0, nullptr, nullptr);
+    }
+  }
+  __syncwarp();
+  cp_async_wait_all();  // nothing of this CTA's shared memory is still being written
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 4 * N);
+  }
+  grid_dep_wait();  // the combine after this grid also finds the one before it ended
+}
+
+// The states of a launch, as the combine reads them.
+struct States {
+  const int4* info;
+  const float2* slot_ml;
+  const float* slot_acc;
+  const float2* row_ml;
+  const float* row_acc;
+  int32_t n;  // columns of a slot
+};
+
+struct CombineParams {
+  States own, shared;  // shared.info == nullptr: no shared prefix
+  __nv_bfloat16* out;
+  const int* status;
+  int32_t Hq;
+  int64_t rows;
+  float o_scale;
+};
+
+template <int D>
+struct Merged {
+  float m = -INFINITY, l = 0.f, acc[D / 32];
+};
+
+// A row's pieces in one launch's states, 32 of them at a time.
+template <int D>
+SGL_DEV void merge(const States& st, int64_t row, const int4& at, Merged<D>* r) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int pieces = at.y - at.x + 1;
+  auto entry = [&](int i) -> int64_t { return (int64_t)(i == 0 ? 2 * at.x + 1 : 2 * (at.x + i)) * st.n + at.z; };
+  for (int i0 = 0; i0 < pieces; i0 += 32) {
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (i0 + lane < pieces) ml = pieces == 1 ? st.row_ml[row] : st.slot_ml[entry(i0 + lane)];
+    if (!(ml.y > 0.f)) ml.x = -INFINITY;
+    float top = ml.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float now = fmaxf(r->m, top);
+    if (now == -INFINITY) continue;  // no keys so far
+    const float keep = ex2(r->m - now), w = ex2(ml.x - now);
+    float sum = ml.y * w;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    r->m = now;
+    r->l = r->l * keep + sum;
+#pragma unroll
+    for (int e = 0; e < E; ++e) r->acc[e] *= keep;
+    const int count = min(32, pieces - i0);
+#pragma unroll 8
+    for (int i = 0; i < count; ++i) {
+      const float f = __shfl_sync(0xffffffffu, w, i);
+      const float* a = (pieces == 1 ? st.row_acc + row * D : st.slot_acc + entry(i0 + i) * D) + lane;
+#pragma unroll
+      for (int e = 0; e < E; ++e) r->acc[e] = fmaf(f, a[32 * e], r->acc[e]);
+    }
+  }
+}
+
+// A warp a (token, query head).
+template <int D>
+__global__ void __launch_bounds__(128) verify_combine_kernel(const CombineParams p) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  grid_dep_wait();
+  if (row >= p.rows || row >= (int64_t)p.status[1] * p.Hq) return;
+  const int4 at = p.own.info[row];
+  if (at.x == at.y && p.own.row_ml == nullptr) return;  // written by the CTA that had its unit whole
+  Merged<D> r;
+#pragma unroll
+  for (int e = 0; e < E; ++e) r.acc[e] = 0.f;
+  merge<D>(p.own, row, at, &r);
+  if (p.shared.info != nullptr) merge<D>(p.shared, row, p.shared.info[row], &r);
+  const float inv = p.o_scale / r.l;
+#pragma unroll
+  for (int e = 0; e < E; ++e) p.out[row * D + lane + 32 * e] = __float2bfloat16_rn(r.acc[e] * inv);
+}
+
+// ----------------------------------------------------------------- host
+
+int columns_for(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Workspace: 256 bytes (status, token count), then per launch the rows' info and
+// the slots; with a shared prefix whole units leave row states too.
+struct Layout {
+  size_t bytes = 256;
+  size_t at(size_t n) {
+    const size_t o = bytes;
+    bytes += round256(n);
+    return o;
+  }
+};
+
+struct Buffers {
+  size_t info, slot_ml, slot_acc, row_ml, row_acc;
+  Buffers(Layout* l, int64_t rows, int n, int D, bool with_rows) {
+    info = l->at((size_t)rows * sizeof(int4));
+    slot_ml = l->at((size_t)2 * kMaxCtas * n * sizeof(float2));
+    slot_acc = l->at((size_t)2 * kMaxCtas * n * D * sizeof(float));
+    row_ml = with_rows ? l->at((size_t)rows * sizeof(float2)) : 0;
+    row_acc = with_rows ? l->at((size_t)rows * D * sizeof(float)) : 0;
+  }
+  void bind(char* base, Params* p) const {
+    p->info = reinterpret_cast<int4*>(base + info);
+    p->slot_ml = reinterpret_cast<float2*>(base + slot_ml);
+    p->slot_acc = reinterpret_cast<float*>(base + slot_acc);
+    p->row_ml = row_ml ? reinterpret_cast<float2*>(base + row_ml) : nullptr;
+    p->row_acc = row_acc ? reinterpret_cast<float*>(base + row_acc) : nullptr;
+  }
+};
+
+template <int D, int N, bool kFp8>
+sgl_status launch_one(const Params& prm, bool dependent, cudaStream_t stream) {
+  using C = Cfg<D, N, kFp8>;
+  auto kern = verify_kernel<D, N, kFp8>;
+  if (kernel_blocks_per_sm<verify_kernel<D, N, kFp8>>(C::kSmem, C::kThreads) < 0) return SGL_ERR_CUDA;
+  const int ctas = num_sms() < kMaxCtas ? num_sms() : kMaxCtas;
+  if (dependent) {
+    if (launch_dependent(kern, dim3(ctas), dim3(C::kThreads), C::kSmem, stream, prm) != cudaSuccess)
+      return SGL_ERR_CUDA;
+  } else {
+    kern<<<ctas, C::kThreads, C::kSmem, stream>>>(prm);
+  }
+  return cudaGetLastError() == cudaSuccess ? SGL_OK : SGL_ERR_CUDA;
+}
+
+template <int D, bool kFp8>
+sgl_status launch_n(const Params& prm, int n, bool dependent, cudaStream_t stream) {
+  if (n == 16) return launch_one<D, 16, kFp8>(prm, dependent, stream);
+  if (n == 32) return launch_one<D, 32, kFp8>(prm, dependent, stream);
+  if (n == 64) return launch_one<D, 64, kFp8>(prm, dependent, stream);
+  return launch_one<D, 128, kFp8>(prm, dependent, stream);
+}
+
+sgl_status launch_pass(const Params& prm, const VerifyArgs& a, int n, bool dependent, cudaStream_t stream) {
+  if (a.head_dim == 128)
+    return a.kv_fp8 ? launch_n<128, true>(prm, n, dependent, stream) : launch_n<128, false>(prm, n, dependent, stream);
+  return a.kv_fp8 ? launch_n<64, true>(prm, n, dependent, stream) : launch_n<64, false>(prm, n, dependent, stream);
+}
+
+States states_of(const Params& p, int n) {
+  return States{p.info, p.slot_ml, p.slot_acc, p.row_ml, p.row_acc, n};
+}
+
+}  // namespace
+}  // namespace vfy
+
+using namespace vfy;
+
+size_t verify_workspace_bytes(int32_t total, int32_t max_draft, int32_t shared_len, int32_t Hq, int32_t Hkv, int32_t D) {
+  Layout l;
+  if (total <= 0 || max_draft <= 0 || Hkv <= 0 || Hq < Hkv) return l.bytes;
+  const int g = Hq / Hkv;
+  const int64_t rows = (int64_t)total * Hq;
+  Buffers own(&l, rows, columns_for((int64_t)max_draft * g), D, shared_len > 0);
+  if (shared_len > 0) Buffers shared(&l, rows, columns_for((int64_t)total * g), D, true);
+  return l.bytes;
+}
+
+sgl_status launch_verify(const VerifyArgs& a, cudaStream_t stream) {
+  const int g = a.num_q_heads / a.num_kv_heads;
+  Params prm = {};
+  prm.q = static_cast<const __nv_bfloat16*>(a.q);
+  prm.pool_k = a.pool_k;
+  prm.pool_v = a.pool_v;
+  prm.rtt = a.req_to_token;
+  prm.rtt_stride = a.rtt_stride;
+  prm.req_pool_idx = a.req_pool_idx;
+  prm.prefix_lens = a.prefix_lens;
+  prm.draft_lens = a.draft_lens;
+  prm.parents = a.parents;
+  prm.out = static_cast<__nv_bfloat16*>(a.out);
+  prm.Hq = a.num_q_heads;
+  prm.Hkv = a.num_kv_heads;
+  prm.g = g;
+  prm.batch = a.batch;
+  prm.total = a.total_draft;
+  prm.max_draft = a.max_draft;
+  prm.max_prefix = a.max_prefix;
+  prm.shared = a.shared_len;
+  prm.scale_log2 = a.sm_scale * 1.4426950408889634f * (a.kv_fp8 ? a.k_scale : 1.f);
+  prm.o_scale = a.kv_fp8 ? a.v_scale : 1.f;
+  prm.status = static_cast<int*>(a.workspace);
+  prm.wait_ns = device_wait_limit_ns();
+  const int64_t rows = (int64_t)a.total_draft * a.num_q_heads;
+  const int n = columns_for((int64_t)a.max_draft * g), ns = columns_for((int64_t)a.total_draft * g);
+  const bool shared = a.shared_len > 0;
+  Layout l;
+  char* base = static_cast<char*>(a.workspace);
+  Buffers(&l, rows, n, a.head_dim, shared).bind(base, &prm);
+  prm.tpt = n / g;
+  CombineParams cp = {};
+  cp.own = states_of(prm, n);
+  if (shared) {
+    Params sp = prm;
+    Buffers(&l, rows, ns, a.head_dim, true).bind(base, &sp);
+    sp.shared_pass = true;
+    sp.tpt = ns / g;
+    cp.shared = states_of(sp, ns);
+    const sgl_status st = launch_pass(sp, a, ns, false, stream);
+    if (st != SGL_OK) return st;
+  }
+  const sgl_status st = launch_pass(prm, a, n, shared, stream);
+  if (st != SGL_OK) return st;
+  cp.out = prm.out;
+  cp.status = prm.status;
+  cp.Hq = prm.Hq;
+  cp.rows = rows;
+  cp.o_scale = prm.o_scale;
+  const dim3 blocks((unsigned)((rows + 3) / 4));
+  const cudaError_t e = a.head_dim == 128
+                            ? launch_dependent(verify_combine_kernel<128>, blocks, dim3(128), 0, stream, cp)
+                            : launch_dependent(verify_combine_kernel<64>, blocks, dim3(128), 0, stream, cp);
+  return e == cudaSuccess ? SGL_OK : SGL_ERR_CUDA;
+}
+
+}  // namespace sgl
