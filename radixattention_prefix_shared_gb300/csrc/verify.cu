@@ -52,33 +52,55 @@ constexpr int kMaxStages = 12;
 
 template <int D, int N, bool kFp8>
 struct Cfg {
-  static constexpr int kW = N < 32 ? N : 32;  // columns a softmax thread holds at a time
-  static constexpr int kWgs = N <= 32 ? 1 : (kFp8 ? N / 64 : N / 32);
-  static constexpr int kCols = N / kWgs;  // columns of a softmax warpgroup
+  static constexpr int kW = N < 32 ? N : 32;       // columns a softmax thread holds at a time
+  static constexpr int kWgs = N <= 32 ? 1 : 2;     // softmax warpgroups
+  static constexpr int kCols = N / kWgs;           // columns of one
   static constexpr int kPasses = kCols / kW;
+  // warps: softmax, epilogue (4), producers, MMA
   static constexpr int kSoftWarps = 4 * kWgs;
-  static constexpr int kProdWarps = kFp8 ? 8 : 4;
+  static constexpr int kProdWarp = kSoftWarps + 4;
+  static constexpr int kProdWarps = kFp8 ? 7 : 3;
   static constexpr int kProdThreads = 32 * kProdWarps;
-  static constexpr int kMmaWarp = kSoftWarps + kProdWarps;
+  static constexpr int kMmaWarp = kProdWarp + kProdWarps;
   static constexpr int kThreads = 32 * (kMmaWarp + 1);
+  // Registers.  12 or 16 warps are launched with up to 168 or 128 a thread; two
+  // softmax warpgroups take some of the others' (setmaxnreg; the sums of the
+  // shares are the launch's registers): 16 warps (bf16) 8 x 160 + 8 x 96 = 16 x
+  // 128, 20 warps (e4m3) 8 x 136 + 4 x 64 + 8 x 72 = 20 x 96.
+  static constexpr bool kSplitRegs = kWgs == 2;
+  static constexpr int kLaunchRegs = kFp8 ? 96 : 128;
+  static constexpr int kSoftRegs = kFp8 ? 136 : 160, kEpiRegs = kFp8 ? 64 : 96, kProdRegs = kFp8 ? 72 : 96;
+  static_assert(!kSplitRegs || (kThreads / 32) * kLaunchRegs >= kSoftWarps * kSoftRegs + 4 * kEpiRegs +
+                                                                    (kProdWarps + 1) * kProdRegs,
+                "register split within the launch's registers");
   static constexpr int kChunks = D / 64;         // 128-byte pieces of a row of 16-bit values
   static constexpr int kChunkBytes = 128 * 128;  // 128 rows of one
   static constexpr int kTileBytes = kChunks * kChunkBytes;
   static constexpr int kQChunkBytes = N * 128;
   static constexpr int kQBytes = kChunks * kQChunkBytes;
   static constexpr int kQBufs = N == 128 ? 1 : 2;
-  static constexpr int kPBytes = (N + 63) / 64 * kChunkBytes;
+  // P^T: a key's row is min(N, 64) values, swizzled over as many bytes
+  static constexpr int kPRow = N >= 64 ? 128 : 2 * N;
+  static constexpr int kPChunkBytes = 128 * kPRow;
+  static constexpr int kPBytes = (N + 63) / 64 * kPChunkBytes;
+  static constexpr uint64_t kPLayout = N >= 64 ? 2 : N == 32 ? 4 : 6;  // 128-, 64-, 32-byte swizzle
   static constexpr int kMiscBytes = 3072;
   static constexpr int kFit = (227 * 1024 - kMiscBytes - kQBufs * kQBytes - 2 * kPBytes) / kTileBytes;
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
+  static constexpr int kK = (kStages + 1) / 2, kV = kStages / 2;  // the K and the V ring
   static constexpr int kSmem = kQBufs * kQBytes + 2 * kPBytes + kStages * kTileBytes + kMiscBytes;
+  // S^T is held so often; a K slot's barrier tells its readers of S too, so there
+  // are no more of those than K slots
+  static constexpr int kSBufs = N == 128 ? 2 : 3;
+  static constexpr int kTmemCols = N == 128 ? 512 : 8 * N;
+  static constexpr int kColO = kSBufs * N;
   // largest accepted exponent of a weight, and where the reference puts a
   // segment's largest: f16 weights start at 2^8, so that they reach down to 2^-32
   // of it before they round to nothing
   static constexpr float kAccept = kFp8 ? 15.f : 30.f;
   static constexpr float kShift = kFp8 ? 8.f : 0.f;
-  static_assert(kStages >= 4 && kStages <= kMaxStages && kSmem <= 227 * 1024, "shared memory");
-  static_assert(4 * N <= 512, "tensor memory");
+  static_assert(kV >= 2 && kK >= kSBufs && kStages <= kMaxStages && kSmem <= 227 * 1024, "shared memory");
+  static_assert(kColO + 2 * N <= kTmemCols && kTmemCols <= 512, "tensor memory");
 };
 
 // A CTA's first block (found by one warp) and what all roles go by.
@@ -90,14 +112,16 @@ struct Start {
 };
 
 struct Misc {
-  uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2], pv_done[2], o_full[2], o_free[2], drain;
-  uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
+  uint64_t q_full[2], q_empty[2], p_ready[2], o_full[2], o_free[2], l_full, l_free, drain;
+  // a slot's copies have landed; it has been read (the MMA that reads it is done,
+  // so what waits for S^T or for P^T's buffer waits for this too)
+  uint64_t k_full[kMaxStages / 2], k_done[kMaxStages / 2], v_full[kMaxStages / 2], v_done[kMaxStages / 2];
   uint32_t tmem_base;
   int abort;
   Start start;
-  float mcol[128];    // a column's reference
-  float acol[128];    // its rescaling, or what its output is multiplied by
-  int32_t mxcol[128];  // its block maximum, as an ordered integer
+  float mcol[128];      // a column's reference
+  int32_t mxcol[128];   // its block maximum, as an ordered integer; then (as a float) its rescaling
+  float lcol[3][128];   // at a segment's end: sums of three warps' keys; then sum, reference, output factor
 };
 static_assert(sizeof(Misc) <= 3072, "barriers and column states");
 
@@ -357,15 +381,15 @@ SGL_DEV void load_slots(const Params& p, const Start& s, const Cursor& c, int fi
   const int32_t keys = c.vis + c.n_tree;
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
-    const int32_t j = c.b * BN + first + step * i;
-    slot[i] = j < keys ? __ldg(t + j) : -1;
+    const int32_t at = first + step * i, j = c.b * BN + at;
+    slot[i] = at < BN && j < keys ? __ldg(t + j) : -1;
   }
 }
 
 template <int D, int N>
 SGL_DEV void produce(const Params& p, const Start& s, Misc* m, uint32_t sQ, uint32_t sKV, int ptid) {
   using C = Cfg<D, N, false>;
-  constexpr int kStep = C::kProdThreads / 8, kRows = BN / kStep;
+  constexpr int kStep = C::kProdThreads / 8, kRows = (BN + kStep - 1) / kStep;
   const int ci = ptid & 7, rb = ptid >> 3;
   Cursor c(p, s);
   int32_t slot[kRows], next[kRows];
@@ -387,20 +411,23 @@ SGL_DEV void produce(const Params& p, const Start& s, Misc* m, uint32_t sQ, uint
     if (opens && C::kQBufs == 2 && !query()) return;
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
-      const int t = 2 * i + kv, st = t % C::kStages, round = t / C::kStages;
-      if (round > 0 && !warp_wait(&m->kv_empty[st], (round - 1) & 1, m, p)) return;
+      const int ring = kv ? C::kV : C::kK, st = i % ring, round = i / ring;
+      uint64_t* full = kv ? m->v_full : m->k_full;
+      uint64_t* done = kv ? m->v_done : m->k_done;
+      if (round > 0 && !warp_wait(&done[st], (round - 1) & 1, m, p)) return;
       const __nv_bfloat16* pool = static_cast<const __nv_bfloat16*>(kv ? p.pool_v : p.pool_k);
-      const uint32_t dst = sKV + st * C::kTileBytes;
+      const uint32_t dst = sKV + (kv ? C::kK + st : st) * C::kTileBytes;
 #pragma unroll
       for (int r = 0; r < kRows; ++r) {
         const int row = rb + kStep * r;
+        if (row >= BN) break;
         const bool valid = slot[r] >= 0;
         const __nv_bfloat16* src = pool + ((int64_t)(valid ? slot[r] : 0) * p.Hkv + c.kvh) * D + ci * 8;
 #pragma unroll
         for (int h = 0; h < C::kChunks; ++h)
           cp_async_16(dst + h * C::kChunkBytes + sw128(row, ci), src + 64 * h, valid ? 16u : 0u);
       }
-      cp_async_mbar_arrive(&m->kv_full[st]);
+      cp_async_mbar_arrive(&full[st]);
     }
     // one Q tile alone: the next unit's waits for the last scores of this one,
     // and its first keys go ahead of it
@@ -412,13 +439,14 @@ SGL_DEV void produce(const Params& p, const Start& s, Misc* m, uint32_t sQ, uint
   }
 }
 
-// e4m3 pool: a thread holds its codes of two blocks in registers (64 KB in flight
-// an SM at D = 128) and widens them to f16 as a stage frees.
+// e4m3 pool: a thread holds its codes of the next kDepth blocks in registers and
+// widens them to f16 as a slot frees.
 template <int D, int N>
 SGL_DEV void produce_fp8(const Params& p, const Start& s, Misc* m, uint32_t sQ, uint32_t sKV, int ptid) {
   using C = Cfg<D, N, true>;
+  constexpr int kDepth = C::kSplitRegs ? 1 : 2;
   constexpr int kPieces = D / 16;  // 16-byte pieces of a row of codes
-  constexpr int kStep = C::kProdThreads / kPieces, kRows = BN / kStep;
+  constexpr int kStep = C::kProdThreads / kPieces, kRows = (BN + kStep - 1) / kStep;
   struct Held {
     uint4 k[kRows], v[kRows];
     int32_t slot[kRows];
@@ -434,23 +462,22 @@ SGL_DEV void produce_fp8(const Params& p, const Start& s, Misc* m, uint32_t sQ, 
     h.kvh = ahead.kvh;
     ++ahead_i;
   };
-  auto codes = [&](Held& h, int i) {  // of block i, whose slots h holds
-    if (i >= s.blocks) return;
+  auto codes = [&](const Held& h, const void* pool, uint4 (&w)[kRows]) {
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-      const int64_t at = ((int64_t)max(h.slot[r], 0) * p.Hkv + h.kvh) * D + rc * 16;
-      h.k[r] = h.v[r] = make_uint4(0, 0, 0, 0);
-      if (h.slot[r] >= 0) {
-        h.k[r] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.pool_k) + at));
-        h.v[r] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.pool_v) + at));
-      }
+      w[r] = make_uint4(0, 0, 0, 0);
+      if (h.slot[r] >= 0)
+        w[r] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(pool) +
+                                                    ((int64_t)h.slot[r] * p.Hkv + h.kvh) * D + rc * 16));
     }
   };
-  auto widen = [&](const uint4 (&w)[kRows], int st) {
-    const uint32_t dst = sKV + st * C::kTileBytes + (rc >> 2) * C::kChunkBytes;
+  auto widen = [&](const uint4 (&w)[kRows], uint32_t tile) {
+    const uint32_t dst = tile + (rc >> 2) * C::kChunkBytes;
     const int piece = 2 * (rc & 3);
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
+      const int row = rb + kStep * r;
+      if (row >= BN) break;
       const uint32_t x[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
       uint32_t o[8];
 #pragma unroll
@@ -460,7 +487,6 @@ SGL_DEV void produce_fp8(const Params& p, const Start& s, Misc* m, uint32_t sQ, 
         o[2 * j] = *reinterpret_cast<const uint32_t*>(&a);
         o[2 * j + 1] = *reinterpret_cast<const uint32_t*>(&b);
       }
-      const int row = rb + kStep * r;
       st_shared_v4(dst + sw128(row, piece), o[0], o[1], o[2], o[3]);
       st_shared_v4(dst + sw128(row, piece + 1), o[4], o[5], o[6], o[7]);
     }
@@ -471,190 +497,243 @@ SGL_DEV void produce_fp8(const Params& p, const Start& s, Misc* m, uint32_t sQ, 
     load_q<D, N, true>(p, c, sQ + qb * C::kQBytes, &m->q_full[qb], ptid);
     return true;
   };
+  // block i out of h, which then takes block i + kDepth (its slots are known) and
+  // the slots of the one after that
   auto block = [&](Held& h, int i) {
     if (i > 0) c.advance(p, s);
     const bool opens = i == 0 || c.b == 0;
     if (opens && C::kQBufs == 2 && !query()) return false;
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
-      const int t = 2 * i + kv, st = t % C::kStages, round = t / C::kStages;
-      if (round > 0 && !warp_wait(&m->kv_empty[st], (round - 1) & 1, m, p)) return false;
-      widen(kv ? h.v : h.k, st);
+      const int ring = kv ? C::kV : C::kK, st = i % ring, round = i / ring;
+      uint64_t* full = kv ? m->v_full : m->k_full;
+      uint64_t* done = kv ? m->v_done : m->k_done;
+      if (round > 0 && !warp_wait(&done[st], (round - 1) & 1, m, p)) return false;
+      widen(kv ? h.v : h.k, sKV + (kv ? C::kK + st : st) * C::kTileBytes);
+      if (i + kDepth < s.blocks) codes(h, kv ? p.pool_v : p.pool_k, kv ? h.v : h.k);
       fence_proxy_async_smem();
-      mbar_arrive(&m->kv_full[st]);
+      mbar_arrive(&full[st]);
     }
-    codes(h, i + 2);
     slots(h);
     if (opens && C::kQBufs == 1 && !query()) return false;
     if (c.last_of_unit()) ++seg;
     return true;
   };
-  Held a, b;
-  slots(a);
-  slots(b);
-  codes(a, 0);
-  codes(b, 1);
-  slots(a);
-  slots(b);
-  for (int i = 0; i < s.blocks; i += 2) {
-    if (!block(a, i)) return;
-    if (i + 1 < s.blocks && !block(b, i + 1)) return;
+  auto start = [&](Held& h, int i) {
+    slots(h);
+    if (i >= s.blocks) return;
+    codes(h, p.pool_k, h.k);
+    codes(h, p.pool_v, h.v);
+  };
+  if constexpr (kDepth == 2) {
+    Held a, b;
+    start(a, 0);
+    start(b, 1);
+    slots(a);
+    slots(b);
+    for (int i = 0; i < s.blocks; i += 2) {
+      if (!block(a, i)) return;
+      if (i + 1 < s.blocks && !block(b, i + 1)) return;
+    }
+  } else {
+    Held a;
+    start(a, 0);
+    slots(a);
+    for (int i = 0; i < s.blocks; ++i)
+      if (!block(a, i)) return;
   }
 }
 
 // ----------------------------------------------------------------- MMA
 
+// The next scores or the next P V, whichever's operands are there first.
 template <int D, int N, bool kFp8>
 SGL_DEV void issue(const Params& p, const Start& s, Misc* m, uint32_t tmem, uint32_t sQ, uint32_t sP, uint32_t sKV) {
   using C = Cfg<D, N, kFp8>;
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try_wait(bar, parity, 200u)) return true;
-    return mbar_wait_bounded(bar, parity, &m->abort, p.status, p.wait_ns);
-  };
-  Cursor c(p, s);
-  int seg = 0, pv_seg = 0;
-  bool opens = true, pv_opens = true, pv_closes = false;
-  for (int i = 0; i <= s.blocks; ++i) {
-    bool closes = false;
-    if (i < s.blocks) {  // S^T of block i
-      const int t = 2 * i, st = t % C::kStages, qb = seg % C::kQBufs;
-      if (opens && !wait(&m->q_full[qb], (seg / C::kQBufs) & 1)) return;
-      if (!wait(&m->kv_full[st], (t / C::kStages) & 1)) return;
-      fence_proxy_async_smem();
-      tc_fence_after();
+  auto there = [&](uint64_t* bar, uint32_t parity) { return mbar_try_wait(bar, parity, 20u); };
+  Cursor c(p, s), cv(p, s);
+  int i = 0, j = 0;  // next block of S^T, of O^T
+  int seg = 0, seg_v = 0;
+  bool opens = true, opens_v = true;
+  uint32_t idle = 0;
+  uint64_t since = 0;
+  while (j < s.blocks) {
+    bool moved = false;
+    if (i < s.blocks && i < j + C::kSBufs) {
+      const int st = i % C::kK, qb = seg % C::kQBufs;
+      if (there(&m->k_full[st], (i / C::kK) & 1) && (!opens || there(&m->q_full[qb], (seg / C::kQBufs) & 1))) {
+        fence_proxy_async_smem();
+        tc_fence_after();
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint64_t a = make_sw128_desc(sKV + st * C::kTileBytes + (kk >> 2) * C::kChunkBytes + (kk & 3) * 32, 16, 1024);
-        const uint64_t b = make_sw128_desc(sQ + qb * C::kQBytes + (kk >> 2) * C::kQChunkBytes + (kk & 3) * 32, 16, 1024);
-        umma_ss(tmem + (i & 1) * N, a, b, idesc<N, kFp8>(false), kk > 0 ? 1u : 0u);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t a = make_sw128_desc(sKV + st * C::kTileBytes + (kk >> 2) * C::kChunkBytes + (kk & 3) * 32, 16, 1024);
+          const uint64_t b = make_sw128_desc(sQ + qb * C::kQBytes + (kk >> 2) * C::kQChunkBytes + (kk & 3) * 32, 16, 1024);
+          umma_ss(tmem + (i % C::kSBufs) * N, a, b, idesc<N, kFp8>(false), kk > 0 ? 1u : 0u);
+        }
+        umma_commit(&m->k_done[st]);
+        opens = c.last_of_unit();
+        if (opens) umma_commit(&m->q_empty[qb]), ++seg;
+        if (++i < s.blocks) c.advance(p, s);
+        moved = true;
       }
-      closes = c.last_of_unit() || i + 1 == s.blocks;
-      umma_commit(&m->s_full[i & 1]);
-      umma_commit(&m->kv_empty[st]);
-      if (closes) umma_commit(&m->q_empty[qb]);
     }
-    if (i > 0) {  // O^T with block i - 1
-      const int j = i - 1, t = 2 * j + 1, st = t % C::kStages, ob = pv_seg & 1;
-      if (pv_opens && pv_seg >= 2 && !wait(&m->o_free[ob], ((pv_seg >> 1) - 1) & 1)) return;
-      if (!wait(&m->kv_full[st], (t / C::kStages) & 1)) return;
-      if (!wait(&m->p_ready[j & 1], (j >> 1) & 1)) return;
-      fence_proxy_async_smem();
-      tc_fence_after();
+    if (j < i) {
+      const int st = j % C::kV, ob = seg_v & 1;
+      if (there(&m->p_ready[j & 1], (j >> 1) & 1) && there(&m->v_full[st], (j / C::kV) & 1) &&
+          (!opens_v || seg_v < 2 || there(&m->o_free[ob], ((seg_v >> 1) - 1) & 1))) {
+        fence_proxy_async_smem();
+        tc_fence_after();
 #pragma unroll
-      for (int kk = 0; kk < BN / 16; ++kk) {
-        // 16 keys are 16 rows of 128 bytes in V as in P; 64 dims (or columns) further
-        // on lies the next chunk.  D = 64: the tile's rows 64.. repeat the others.
-        const uint64_t a = make_sw128_desc(sKV + st * C::kTileBytes + kk * 2048, D == 128 ? C::kChunkBytes : 0, 1024);
-        const uint64_t b = make_sw128_desc(sP + (j & 1) * C::kPBytes + kk * 2048, C::kChunkBytes, 1024);
-        umma_ss(tmem + 2 * N + ob * N, a, b, idesc<N, kFp8>(true), (pv_opens && kk == 0) ? 0u : 1u);
+        for (int kk = 0; kk < BN / 16; ++kk) {
+          // 16 keys are 16 rows in V as in P; 64 dims (or columns) further on lies the
+          // next chunk.  D = 64: the tile's rows 64.. repeat the others.
+          const uint64_t a = make_sw128_desc(sKV + (C::kK + st) * C::kTileBytes + kk * 2048, D == 128 ? C::kChunkBytes : 0, 1024);
+          const uint64_t b = (make_sw128_desc(sP + (j & 1) * C::kPBytes + kk * 16 * C::kPRow, C::kPChunkBytes, 8 * C::kPRow) &
+                              ~((uint64_t)7 << 61)) | (C::kPLayout << 61);
+          umma_ss(tmem + C::kColO + ob * N, a, b, idesc<N, kFp8>(true), (opens_v && kk == 0) ? 0u : 1u);
+        }
+        umma_commit(&m->v_done[st]);
+        opens_v = cv.last_of_unit() || j + 1 == s.blocks;
+        if (opens_v) umma_commit(&m->o_full[ob]), ++seg_v;
+        if (++j < s.blocks) cv.advance(p, s);
+        moved = true;
       }
-      umma_commit(&m->kv_empty[st]);
-      umma_commit(&m->pv_done[j & 1]);
-      if (pv_closes) umma_commit(&m->o_full[ob]);
-      pv_opens = pv_closes;
-      if (pv_closes) ++pv_seg;
     }
-    pv_closes = closes;
-    if (i < s.blocks) {
-      opens = closes;
-      if (closes) ++seg;
-      if (i + 1 < s.blocks) c.advance(p, s);
+    if (moved) {
+      idle = 0;
+    } else if ((++idle & 63u) == 0) {  // bounded, as every wait
+      const uint64_t now = global_timer_ns();
+      if (idle == 64u) since = now;
+      if (m->abort) return;
+      if (now - since > p.wait_ns) {
+        m->abort = 1;
+        atomicExch(p.status, (int)kDevWaitTimeout);
+        return;
+      }
     }
   }
 }
 
 // ----------------------------------------------------------------- softmax
 
-// Which tokens k of the tile see the thread's key, node `node` of the tree: bit
-// k, the node is token tile * tpt + k or above it.  Lanes hold the ancestor sets
-// of nodes lane and lane + 32; each round doubles how far up they reach.
-SGL_DEV uint64_t seen_by(const Params& p, const Cursor& c, int node) {
-  const int lane = threadIdx.x & 31;
-  uint64_t anc[2];
+// A request's tree in a warp: lane l holds the parents of nodes l and l + 32
+// (below 0: none).
+struct Tree {
   int up[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int t = lane + 32 * h;
-    anc[h] = 1ull << t;
-    up[h] = t < c.n && c.off + t < p.total ? __ldg(p.parents + c.off + t) : -1;
-    if (up[h] >= t) up[h] = -1;  // a parent lies before its child
-  }
-  for (int span = 1; span < c.n; span *= 2) {
-    uint64_t a[2];
-    int u[2];
+  SGL_DEV void load(const Params& p, const Cursor& c) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int src = up[h] & 31;
-      const uint64_t a0 = __shfl_sync(0xffffffffu, anc[0], src), a1 = __shfl_sync(0xffffffffu, anc[1], src);
-      const int u0 = __shfl_sync(0xffffffffu, up[0], src), u1 = __shfl_sync(0xffffffffu, up[1], src);
-      a[h] = up[h] < 0 ? 0ull : up[h] < 32 ? a0 : a1;
-      u[h] = up[h] < 0 ? -1 : up[h] < 32 ? u0 : u1;
+      const int t = (threadIdx.x & 31) + 32 * h;
+      up[h] = t < c.n_tree && c.off + t < p.total ? __ldg(p.parents + c.off + t) : -1;
+      if (up[h] >= t) up[h] = -1;  // a parent lies before its child
     }
+  }
+  // Which of W columns from col0 on see the thread's key, node `node`: bit e for
+  // column col0 + e, whose token has that node among itself and those above it.
+  // Ancestor sets grow by doubling: each round adds what the node reached last has
+  // reached.
+  template <int W, int kWords>
+  SGL_DEV void seen(const Params& p, const Cursor& c, int node, int col0, uint32_t (&bits)[kWords]) const {
+    const int lane = threadIdx.x & 31;
+    uint64_t anc[2] = {1ull << lane, 1ull << (lane + 32)};
+    int at[2] = {up[0], up[1]};
+    for (int span = 1; span < c.n_tree; span *= 2) {
+      uint64_t a[2];
+      int u[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) anc[h] |= a[h], up[h] = u[h];
+      for (int h = 0; h < 2; ++h) {
+        const int src = at[h] & 31;
+        const uint64_t a0 = __shfl_sync(0xffffffffu, anc[0], src), a1 = __shfl_sync(0xffffffffu, anc[1], src);
+        const int u0 = __shfl_sync(0xffffffffu, at[0], src), u1 = __shfl_sync(0xffffffffu, at[1], src);
+        a[h] = at[h] < 0 ? 0ull : at[h] < 32 ? a0 : a1;
+        u[h] = at[h] < 0 ? -1 : at[h] < 32 ? u0 : u1;
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) anc[h] |= a[h], at[h] = u[h];
+    }
+    const int t0 = c.tile * p.tpt;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+      const int base = col0 + w * W;
+      bits[w] = 0;
+      for (int k = base / p.g; k * p.g < base + W; ++k) {
+        const int t = t0 + k;  // (uniform; a column past the tile's tokens is not used)
+        if (t >= 64) break;
+        const uint64_t a = __shfl_sync(0xffffffffu, t < 32 ? anc[0] : anc[1], t & 31);
+        const int lo = max(0, k * p.g - base), hi = min(W, (k + 1) * p.g - base);
+        const uint32_t span = (hi - lo >= 32 ? 0xffffffffu : (1u << (hi - lo)) - 1u) << lo;
+        if (node < 0 || (node < c.n_tree && (a >> node & 1))) bits[w] |= span;
+      }
+    }
   }
-  uint64_t seen = 0;
-  const int t0 = c.tile * p.tpt, most = min(p.tpt, c.n - t0);
-  for (int k = 0; k < most; ++k) {
-    const int t = t0 + k;
-    const uint64_t a = __shfl_sync(0xffffffffu, t < 32 ? anc[0] : anc[1], t & 31);
-    if (node >= 0 && node < 64 && (a >> node & 1)) seen |= 1ull << k;
-  }
-  return seen;
+};
+
+// Byte of P^T at (key, column col, a multiple of 8): rows of kPRow bytes whose
+// 16-byte pieces are swizzled.
+template <int N>
+SGL_DEV uint32_t p_at(int key, int col) {
+  if constexpr (N == 16) return key * 32 + (((col >> 3) ^ ((key >> 2) & 1)) << 4);
+  else if constexpr (N == 32) return key * 64 + (((col >> 3) ^ ((key >> 1) & 3)) << 4);
+  else return (col >> 6) * (128 * 128) + sw128(key, (col & 63) >> 3);
 }
 
 template <int D, int N, bool kFp8>
-SGL_DEV void softmax(const Params& p, const Start& s, Misc* m, uint32_t tmem, uint8_t* sP) {
+SGL_DEV void softmax(const Params& p, const Start& s, Misc* m, uint32_t tmem, uint32_t sP) {
   using C = Cfg<D, N, kFp8>;
   constexpr int W = C::kW;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int wg = warp >> 2, q = warp & 3, key = q * 32 + lane, col0 = wg * C::kCols, wt = tid & 127;
   const uint32_t bar = 1 + wg;
   const uint32_t lanes = (uint32_t)(q * 32) << 16;
-  const uint32_t sP_a = smem_u32(sP);
+  const float sc = p.scale_log2;
   Cursor c(p, s);
+  Tree tree;
   int seg = 0;
   bool opens = true, first_masked = false, ok = true;
-  int32_t b_first = 0;  // the segment's first block in its unit
   float l[C::kCols];
   for (int i = 0; i < s.blocks; ++i) {
-    ok = warp_wait(&m->s_full[i & 1], (i >> 1) & 1, m, p) && ok;
-    tc_fence_after();
-    const int node = c.b * BN + key - c.vis;  // of the tree; below 0 a key that all see
     const bool masked = (c.b + 1) * BN > c.vis;
-    const uint64_t seen = masked && c.n_tree > 0 ? seen_by(p, c, node) : 0ull;
-    if (opens) first_masked = masked, b_first = c.b;
-    const uint32_t tS = tmem + lanes + (i & 1) * N + col0;
-    const uint32_t tO = tmem + lanes + 2 * N + (seg & 1) * N + col0;
+    if (opens) {
+      first_masked = masked;
+      tree.load(p, c);
+    }
+    const int node = c.b * BN + key - c.vis;  // of the tree; below 0 a key that all see
+    uint32_t bits[C::kPasses];
+    if (masked) {
+      if (c.n_tree > 0) {
+        tree.seen<W>(p, c, node, col0, bits);
+      } else {
+#pragma unroll
+        for (int w = 0; w < C::kPasses; ++w) bits[w] = node < 0 ? 0xffffffffu : 0u;
+      }
+    }
+    ok = warp_wait(&m->k_done[i % C::kK], (i / C::kK) & 1, m, p) && ok;  // S^T is there
+    tc_fence_after();
+    const uint32_t tS = tmem + lanes + (i % C::kSBufs) * N + col0;
+    const uint32_t tO = tmem + lanes + C::kColO + (seg & 1) * N + col0;
     auto load = [&](int pass, uint32_t (&x)[W]) {
       tmem_ld<W>(tS + pass * W, x);
-      if (masked && node >= 0) {
-        int k = (col0 + pass * W) / p.g, h = (col0 + pass * W) % p.g;
+      if (masked) {
 #pragma unroll
-        for (int e = 0; e < W; ++e) {
-          const bool sees = node < c.n_tree && (k >= 64 || (seen >> k & 1));
-          if (!sees) x[e] = __float_as_uint(-INFINITY);
-          if (++h == p.g) h = 0, ++k;
-        }
+        for (int e = 0; e < W; ++e)
+          if (!(bits[pass] >> e & 1)) x[e] = __float_as_uint(-INFINITY);
       }
     };
-    const float sc = p.scale_log2;
     // scores against their columns' references, in units of log 2
     auto relative = [&](int pass, uint32_t (&x)[W]) {
-      float top = -INFINITY;
+      float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      const float2 s2 = make_float2(sc, sc);
 #pragma unroll
       for (int e = 0; e < W; e += 4) {
         const float4 r = *reinterpret_cast<const float4*>(&m->mcol[col0 + pass * W + e]);
-        const float2 s2 = make_float2(sc, sc);
         float2 a = ffma2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), s2, make_float2(-r.x, -r.y));
         float2 b = ffma2(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), s2, make_float2(-r.z, -r.w));
         x[e] = __float_as_uint(a.x), x[e + 1] = __float_as_uint(a.y);
         x[e + 2] = __float_as_uint(b.x), x[e + 3] = __float_as_uint(b.y);
-        top = fmax3(top, a.x, a.y);
-        top = fmax3(top, b.x, b.y);
+        top[(e >> 1) & 3] = fmax3(top[(e >> 1) & 3], a.x, a.y);
+        top[((e >> 1) + 1) & 3] = fmax3(top[((e >> 1) + 1) & 3], b.x, b.y);
       }
-      return top;
+      return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
     };
     uint32_t x[W];
     // a segment's first block sets the references; one whose first block hides
@@ -675,6 +754,8 @@ SGL_DEV void softmax(const Params& p, const Start& s, Misc* m, uint32_t tmem, ui
     const uint32_t votes = bar_red_popc(bar, 128, (lane == 0 && redo_w) || (lane >= 1 && lane <= 8 && !ok));
     if (votes >= 8) return;
     if (votes != 0) {
+      if (wt < C::kCols) m->mxcol[col0 + wt] = ordered(-INFINITY);
+      named_bar_sync(bar, 128);
 #pragma unroll
       for (int pass = 0; pass < C::kPasses; ++pass) {
         load(pass, x);
@@ -686,23 +767,23 @@ SGL_DEV void softmax(const Params& p, const Start& s, Misc* m, uint32_t tmem, ui
         const int col = col0 + wt;
         const float before = opens ? -INFINITY : m->mcol[col];
         const float now = fmaxf(before, unordered(m->mxcol[col]) * sc - C::kShift);
-        m->mxcol[col] = ordered(-INFINITY);
         m->mcol[col] = now;
-        m->acol[col] = before == -INFINITY ? 0.f : ex2(before - now);
+        m->mxcol[col] = __float_as_int(before == -INFINITY ? 0.f : ex2(before - now));
       }
       named_bar_sync(bar, 128);
       if (opens) {
 #pragma unroll
         for (int e = 0; e < C::kCols; ++e) l[e] = 0.f;
       } else {
-        ok = warp_wait(&m->pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, m, p) && ok;
+        // O^T of the blocks before comes to the new references
+        ok = warp_wait(&m->v_done[(i - 1) % C::kV], ((i - 1) / C::kV) & 1, m, p) && ok;
         tc_fence_after();
 #pragma unroll
         for (int pass = 0; pass < C::kPasses; ++pass) {
           tmem_ld<W>(tO + pass * W, x);
 #pragma unroll
           for (int e = 0; e < W; ++e) {
-            const float a = m->acol[col0 + pass * W + e];
+            const float a = __int_as_float(m->mxcol[col0 + pass * W + e]);
             l[pass * W + e] *= a;
             x[e] = __float_as_uint(__uint_as_float(x[e]) * a);
           }
@@ -713,7 +794,8 @@ SGL_DEV void softmax(const Params& p, const Start& s, Misc* m, uint32_t tmem, ui
     }
     // P^T: this key's row, 8 columns a 16-byte piece; its buffer was last read
     // with block i - 2
-    if (i >= 2) ok = warp_wait(&m->pv_done[i & 1], ((i >> 1) - 1) & 1, m, p) && ok;
+    if (i >= 2) ok = warp_wait(&m->v_done[(i - 2) % C::kV], ((i - 2) / C::kV) & 1, m, p) && ok;
+    const uint32_t pbuf = sP + (i & 1) * C::kPBytes;
 #pragma unroll
     for (int pass = 0; pass < C::kPasses; ++pass) {
       if (C::kPasses > 1 || votes != 0) {
@@ -736,85 +818,114 @@ SGL_DEV void softmax(const Params& p, const Start& s, Misc* m, uint32_t tmem, ui
           l[pass * W + at] = sum.x, l[pass * W + at + 1] = sum.y;
           o[d] = kFp8 ? pack_f16x2(w.x, w.y) : pack_bf16x2(w.x, w.y);
         }
-        const int col = col0 + pass * W + e;
-        st_shared_v4(sP_a + (i & 1) * C::kPBytes + (col >> 6) * C::kChunkBytes + sw128(key, (col & 63) >> 3), o[0], o[1],
-                     o[2], o[3]);
+        st_shared_v4(pbuf + p_at<N>(key, col0 + pass * W + e), o[0], o[1], o[2], o[3]);
       }
     }
     fence_proxy_async_smem();
     tc_fence_before();
     mbar_arrive(&m->p_ready[i & 1]);
-    const bool closes = c.last_of_unit() || i + 1 == s.blocks;
-    if (closes) {
-      // the segment's sums and O^T: lane d of warp q is dim 32 q + d
-      ok = warp_wait(&m->o_full[seg & 1], (seg >> 1) & 1, m, p) && ok;
-      tc_fence_after();
-      if (bar_red_or(bar, 128, !ok)) return;
-      // P's rows are free: each warp leaves its 32 keys' sums there, a column a row
+    opens = c.last_of_unit() || i + 1 == s.blocks;
+    if (opens) {
+      // the segment's sums and references go to the epilogue warps
+      if (seg > 0) ok = warp_wait(&m->l_free, (seg - 1) & 1, m, p) && ok;
 #pragma unroll
       for (int pass = 0; pass < C::kPasses; ++pass) {
         const float sum = columns<W>(*reinterpret_cast<float(*)[W]>(&l[pass * W]), [](float a, float b) { return a + b; });
-        float* at = reinterpret_cast<float*>(sP + (i & 1) * C::kPBytes + (col0 >> 6) * C::kChunkBytes +
-                                             sw128(key, (col0 & 63) >> 3));
-        if (lane < W) at[pass] = sum;
+        if (q > 0 && lane < W) m->lcol[q - 1][col0 + pass * W + lane] = sum;
+        l[pass] = sum;
       }
-      named_bar_sync(bar, 128);
-      const bool whole = b_first == 0 && c.last_of_unit();
-      const bool direct = whole && p.row_ml == nullptr;
-      const int64_t slot = (int64_t)(2 * blockIdx.x + (b_first == 0 ? 1 : 0)) * N;
-      auto row_of = [&](int col) -> int64_t {  // of [tokens x Hq], or -1
-        const int k = col / p.g, tok = c.tile * p.tpt + k;
-        if (k >= p.tpt || tok >= c.n || c.off + tok >= p.total) return -1;
-        return (int64_t)(c.off + tok) * p.Hq + (int64_t)c.kvh * p.g + col % p.g;
-      };
-      if (wt < C::kCols) {
-        const int col = col0 + wt;
-        float sum = 0.f;
+      if (bar_red_or(bar, 128, !ok)) return;
+      if (q == 0) {
 #pragma unroll
-        for (int w = 0; w < 4; ++w)
-          sum += reinterpret_cast<const float*>(sP + (i & 1) * C::kPBytes + (col0 >> 6) * C::kChunkBytes +
-                                                sw128(w * 32 + wt % W, (col0 & 63) >> 3))[wt / W];
-        m->acol[col] = direct ? p.o_scale / sum : 1.f;
-        const int64_t row = row_of(col);
-        if (row >= 0) {
-          const float2 ml = make_float2(m->mcol[col], sum);
-          if (!whole) p.slot_ml[slot + col] = ml;
-          else if (!direct) p.row_ml[row] = ml;
-          if (b_first == 0) {
-            const int64_t u0 = s.pos + i - c.b;  // the unit's first block
-            p.info[row] = make_int4(blockIdx.x, owner(u0 + c.nb - 1, s.total, gridDim.x), col, 0);
+        for (int pass = 0; pass < C::kPasses; ++pass) {
+          const int col = col0 + pass * W + lane;
+          if (lane < W) {
+            const float sum = (l[pass] + m->lcol[0][col]) + (m->lcol[1][col] + m->lcol[2][col]);
+            m->lcol[0][col] = sum;
+            m->lcol[1][col] = m->mcol[col];
           }
         }
+        mbar_arrive(&m->l_full);
       }
-      named_bar_sync(bar, 128);
-      const int t0 = c.tile * p.tpt;
-      const int most = min(min(p.tpt, c.n - t0), p.total - c.off - t0);  // tokens of the tile
-#pragma unroll
-      for (int pass = 0; pass < C::kPasses; ++pass) {
-        tmem_ld<W>(tO + pass * W, x);
-        const int base = col0 + pass * W;
-        int k = base / p.g, h = base % p.g;
-        int64_t row = (int64_t)(c.off + t0 + k) * p.Hq + (int64_t)c.kvh * p.g + h;
-        if (key < D) {
-#pragma unroll
-          for (int e = 0; e < W; ++e) {
-            if (k < most) {
-              const float o = __uint_as_float(x[e]);
-              if (direct) p.out[row * D + key] = __float2bfloat16_rn(o * m->acol[base + e]);
-              else if (whole) p.row_acc[row * D + key] = o;
-              else p.slot_acc[(slot + base + e) * D + key] = o;
-            }
-            ++row;
-            if (++h == p.g) h = 0, ++k, row += p.Hq - p.g;
-          }
-        }
-      }
-      tc_fence_before();
-      mbar_arrive(&m->o_free[seg & 1]);
       ++seg;
     }
-    opens = closes;
     if (i + 1 < s.blocks) c.advance(p, s);
+  }
+}
+
+// ----------------------------------------------------------------- epilogue
+
+// A segment's O^T: lane d of warp q holds dim 32 q + d of every column.
+template <int D, int N, bool kFp8>
+SGL_DEV void epilogue(const Params& p, const Start& s, Misc* m, uint32_t tmem, int et) {
+  using C = Cfg<D, N, kFp8>;
+  constexpr int W = C::kW;
+  const int q = et >> 5;
+  const uint32_t bar = 1 + C::kWgs;
+  Cursor c(p, s);
+  int i = 0;
+  for (int seg = 0; i < s.blocks; ++seg) {
+    const int b0 = c.b, take = min(c.nb - b0, s.blocks - i);  // the segment's blocks of the unit
+    const bool whole = take == c.nb, direct = whole && p.row_ml == nullptr;
+    const int64_t slot = (int64_t)(2 * blockIdx.x + (b0 == 0 ? 1 : 0)) * N;
+    const int t0 = c.tile * p.tpt;
+    const int most = min(min(p.tpt, c.n - t0), p.total - c.off - t0);  // tokens of the tile
+    const int64_t row0 = (int64_t)(c.off + t0) * p.Hq + (int64_t)c.kvh * p.g;
+    bool ok = warp_wait(&m->l_full, seg & 1, m, p);
+    if (et < N) {
+      const float sum = m->lcol[0][et];
+      m->lcol[2][et] = p.o_scale / sum;
+      const int k = et / p.g;
+      if (k < most) {
+        const int64_t row = row0 + (int64_t)k * p.Hq + et % p.g;
+        const float2 ml = make_float2(m->lcol[1][et], sum);
+        if (!whole) p.slot_ml[slot + et] = ml;
+        else if (!direct) p.row_ml[row] = ml;
+        // (pos + i - b0 + nb - 1: the unit's last block)
+        if (b0 == 0)
+          p.info[row] = make_int4(blockIdx.x, whole ? (int)blockIdx.x : owner(s.pos + i + c.nb - 1, s.total, gridDim.x), et, 0);
+      }
+    }
+    ok = warp_wait(&m->o_full[seg & 1], (seg >> 1) & 1, m, p) && ok;
+    tc_fence_after();
+    if (bar_red_or(bar, 128, !ok)) return;
+    const uint32_t tO = tmem + ((uint32_t)(q * 32) << 16) + C::kColO + (seg & 1) * N;
+    int k = 0, h = 0;
+    int64_t row = row0;
+#pragma unroll 1
+    for (int w = 0; w < N / W; ++w) {
+      uint32_t x[W];
+      tmem_ld<W>(tO + w * W, x);
+      if (et >= D || k >= most) continue;  // (a warp's lanes alike; k >= most from here on)
+      // the destination of column e: consecutive for states, rows of a token's
+      // heads else
+      if (whole) {
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          if (k < most) {
+            const float o = __uint_as_float(x[e]);
+            if (direct) p.out[row * D + et] = __float2bfloat16_rn(o * m->lcol[2][w * W + e]);
+            else p.row_acc[row * D + et] = o;
+          }
+          ++row;
+          if (++h == p.g) h = 0, ++k, row += p.Hq - p.g;
+        }
+      } else {
+        float* to = p.slot_acc + (slot + w * W) * D + et;
+        const int live = most * p.g - w * W;
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+          if (e < live) to[e * D] = __uint_as_float(x[e]);
+      }
+    }
+    tc_fence_before();
+    mbar_arrive(&m->o_free[seg & 1]);
+    mbar_arrive(&m->l_free);
+    i += take;
+    if (i < s.blocks) {
+      c.b = c.nb - 1;
+      c.advance(p, s);
+    }
   }
 }
 
@@ -836,35 +947,47 @@ __global__ void __launch_bounds__(Cfg<D, N, kFp8>::kThreads, 1) verify_kernel(co
     for (int i = 0; i < 2; ++i) {
       mbar_init(&m->q_full[i], C::kProdThreads);
       mbar_init(&m->q_empty[i], 1);
-      mbar_init(&m->s_full[i], 1);
       mbar_init(&m->p_ready[i], 32 * C::kSoftWarps);
-      mbar_init(&m->pv_done[i], 1);
       mbar_init(&m->o_full[i], 1);
-      mbar_init(&m->o_free[i], 32 * C::kSoftWarps);
+      mbar_init(&m->o_free[i], 128);
     }
+    mbar_init(&m->l_full, 32 * C::kWgs);
+    mbar_init(&m->l_free, 128);
     mbar_init(&m->drain, 1);
-    for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(&m->kv_full[i], C::kProdThreads);
-      mbar_init(&m->kv_empty[i], 1);
+    for (int i = 0; i < C::kK; ++i) {
+      mbar_init(&m->k_full[i], C::kProdThreads);
+      mbar_init(&m->k_done[i], 1);
+    }
+    for (int i = 0; i < C::kV; ++i) {
+      mbar_init(&m->v_full[i], C::kProdThreads);
+      mbar_init(&m->v_done[i], 1);
     }
     m->abort = 0;
     mbar_fence_init();
   } else if (warp == C::kMmaWarp) {
-    tmem_alloc(&m->tmem_base, 4 * N);
+    tmem_alloc(&m->tmem_base, C::kTmemCols);
     tmem_relinquish();
   }
-  if (tid < 128) m->mxcol[tid] = ordered(-INFINITY);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const Start s = m->start;
   const uint32_t tmem = m->tmem_base;
   if (blockIdx.x == 0 && tid == 0) p.status[1] = s.tokens;
+  if constexpr (C::kSplitRegs) {
+    // every warp of a warpgroup together
+    static_assert(C::kProdWarp % 4 == 0 && (C::kMmaWarp + 1) % 4 == 0, "whole warpgroups");
+    if (warp < C::kSoftWarps) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
+    else if (warp < C::kProdWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kEpiRegs));
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kProdRegs));
+  }
   if (s.blocks > 0) {
     if (warp < C::kSoftWarps) {
-      softmax<D, N, kFp8>(p, s, m, tmem, sP);
+      softmax<D, N, kFp8>(p, s, m, tmem, smem_u32(sP));
+    } else if (warp < C::kProdWarp) {
+      epilogue<D, N, kFp8>(p, s, m, tmem, tid - 32 * C::kSoftWarps);
     } else if (warp < C::kMmaWarp) {
-      const int ptid = tid - 32 * C::kSoftWarps;
+      const int ptid = tid - 32 * C::kProdWarp;
       if constexpr (kFp8) produce_fp8<D, N>(p, s, m, smem_u32(sQ), smem_u32(sKV), ptid);
       else produce<D, N>(p, s, m, smem_u32(sQ), smem_u32(sKV), ptid);
     } else if ((tid & 31) == 0) {
@@ -880,7 +1003,7 @@ __global__ void __launch_bounds__(Cfg<D, N, kFp8>::kThreads, 1) verify_kernel(co
   __syncthreads();
   if (warp == C::kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem, 4 * N);
+    tmem_dealloc(tmem, C::kTmemCols);
   }
   grid_dep_wait();  // the combine after this grid also finds the one before it ended
 }
@@ -1004,6 +1127,7 @@ sgl_status launch_one(const Params& prm, bool dependent, cudaStream_t stream) {
   using C = Cfg<D, N, kFp8>;
   auto kern = verify_kernel<D, N, kFp8>;
   if (kernel_blocks_per_sm<verify_kernel<D, N, kFp8>>(C::kSmem, C::kThreads) < 0) return SGL_ERR_CUDA;
+  if (C::kSplitRegs && !kernel_regs_at_least<verify_kernel<D, N, kFp8>>(C::kLaunchRegs)) return SGL_ERR_UNSUPPORTED;
   const int ctas = num_sms() < kMaxCtas ? num_sms() : kMaxCtas;
   if (dependent) {
     if (launch_dependent(kern, dim3(ctas), dim3(C::kThreads), C::kSmem, stream, prm) != cudaSuccess)
