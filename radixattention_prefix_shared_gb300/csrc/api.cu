@@ -1029,6 +1029,7 @@ sgl_status verify_entry(const void* q, const void* pool_k, const void* pool_v, b
   if (batch < 0 || total_draft < 0 || max_draft < 0 || max_prefix < 0 || shared_len < 0 || shared_len > max_prefix)
     return SGL_ERR_INVALID_ARG;
   if (dims->num_q_heads / dims->num_kv_heads > 128 || max_draft > kMaxDraft) return SGL_ERR_UNSUPPORTED;
+  if ((int64_t)total_draft * dims->num_q_heads > INT32_MAX) return SGL_ERR_UNSUPPORTED;
   if (batch == 0 || total_draft == 0) return SGL_OK;
   if (max_draft < 1 || max_draft > total_draft) return SGL_ERR_INVALID_ARG;
   if (!q || !pool_k || !pool_v || !req_to_token || !req_pool_idx || !prefix_lens || !draft_lens || !parents || !out)

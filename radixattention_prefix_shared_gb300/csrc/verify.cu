@@ -52,24 +52,24 @@ constexpr int kMaxStages = 12;
 
 template <int D, int N, bool kFp8>
 struct Cfg {
-  static constexpr int kW = N < 32 ? N : 32;       // columns a softmax thread holds at a time
-  static constexpr int kWgs = N <= 32 ? 1 : 2;     // softmax warpgroups
-  static constexpr int kCols = N / kWgs;           // columns of one
-  static constexpr int kPasses = kCols / kW;
+  static_assert(N <= (kFp8 ? 64 : 128), "columns");
+  static constexpr int kCols = N < 32 ? N : 32;  // columns of a softmax warpgroup: a thread holds them all
+  static constexpr int kWgs = N / kCols;
   // warps: softmax, epilogue (4), producers, MMA
   static constexpr int kSoftWarps = 4 * kWgs;
   static constexpr int kProdWarp = kSoftWarps + 4;
-  static constexpr int kProdWarps = kFp8 ? 7 : 3;
+  static constexpr int kProdWarps = N == 128 ? 3 : 7;
   static constexpr int kProdThreads = 32 * kProdWarps;
   static constexpr int kMmaWarp = kProdWarp + kProdWarps;
   static constexpr int kThreads = 32 * (kMmaWarp + 1);
-  // Registers.  12 or 16 warps are launched with up to 168 or 128 a thread; two
-  // softmax warpgroups take some of the others' (setmaxnreg; the sums of the
-  // shares are the launch's registers): 16 warps (bf16) 8 x 160 + 8 x 96 = 16 x
-  // 128, 20 warps (e4m3) 8 x 136 + 4 x 64 + 8 x 72 = 20 x 96.
-  static constexpr bool kSplitRegs = kWgs == 2;
-  static constexpr int kLaunchRegs = kFp8 ? 96 : 128;
-  static constexpr int kSoftRegs = kFp8 ? 136 : 160, kEpiRegs = kFp8 ? 64 : 96, kProdRegs = kFp8 ? 72 : 96;
+  // Registers.  16 warps are launched with 128 a thread; with more, the softmax
+  // warps take some of the others' (setmaxnreg; the shares add up to the launch's
+  // registers): 20 warps 8 x 128 + 4 x 64 + 8 x 80 = 20 x 96, 24 warps 16 x 88 +
+  // 8 x 64 = 24 x 80.
+  static constexpr bool kSplitRegs = kWgs > 1;
+  static constexpr int kLaunchRegs = N == 128 ? 80 : 96;
+  static constexpr int kSoftRegs = N == 128 ? 88 : 128, kEpiRegs = 64;
+  static constexpr int kProdRegs = N == 128 ? 64 : 80;
   static_assert(!kSplitRegs || (kThreads / 32) * kLaunchRegs >= kSoftWarps * kSoftRegs + 4 * kEpiRegs +
                                                                     (kProdWarps + 1) * kProdRegs,
                 "register split within the launch's registers");
@@ -111,17 +111,30 @@ struct Start {
   int64_t pos, total;                    // first block, blocks of the launch
 };
 
+// What the softmax and the epilogue go by in a segment (the blocks of a unit that
+// a CTA takes).  The epilogue's first warp writes it, two segments ahead, so that
+// no softmax warp waits for a load from global memory.
+struct Segment {
+  int32_t b0, take, nb;      // first block, blocks of it; blocks of the unit
+  int32_t vis, n_tree;       // keys that all see; the tree's nodes behind them
+  int32_t t0, h0, live;      // token and head of the tile's first column, columns of it
+  int32_t off, kvh;          // the request's first token among the step's
+  int8_t up[kMaxDraft];      // parents (below 0: none)
+};
+
 struct Misc {
-  uint64_t q_full[2], q_empty[2], p_ready[2], o_full[2], o_free[2], l_full, l_free, drain;
+  uint64_t q_full[2], q_empty[2], p_ready[2], o_full[2], o_free[2], u_full[2], l_full, l_free, drain;
   // a slot's copies have landed; it has been read (the MMA that reads it is done,
   // so what waits for S^T or for P^T's buffer waits for this too)
   uint64_t k_full[kMaxStages / 2], k_done[kMaxStages / 2], v_full[kMaxStages / 2], v_done[kMaxStages / 2];
+  int32_t k_last[kMaxStages / 2];  // the slot's block is its segment's last
   uint32_t tmem_base;
   int abort;
   Start start;
-  float mcol[128];      // a column's reference
-  int32_t mxcol[128];   // its block maximum, as an ordered integer; then (as a float) its rescaling
-  float lcol[3][128];   // at a segment's end: sums of three warps' keys; then sum, reference, output factor
+  Segment seg[2];
+  alignas(16) float mcol[128];  // a column's reference (read four at a time)
+  int32_t mxcol[128];  // its block maximum, as an ordered integer; then (as a float) its rescaling
+  float lcol[2][128];  // at a segment's end: sums over the keys, references (then output factors)
 };
 static_assert(sizeof(Misc) <= 3072, "barriers and column states");
 
@@ -136,7 +149,7 @@ struct Params {
   const int32_t* draft_lens;
   const int32_t* parents;
   __nv_bfloat16* out;
-  int32_t Hq, Hkv, g, tpt;
+  int32_t Hq, Hkv, g, cols;
   int32_t batch, total, max_draft, max_prefix, shared;
   bool shared_pass;  // the launch over the batch's shared prefix
   float scale_log2, o_scale;
@@ -155,35 +168,63 @@ struct Params {
 SGL_DEV int32_t drafts_of(const Params& p, int r) { return max(0, min(__ldg(p.draft_lens + r), p.max_draft)); }
 SGL_DEV int32_t prefix_of(const Params& p, int r) { return max(0, min(__ldg(p.prefix_lens + r), p.max_prefix)); }
 
+// The requests that a CTA comes to, in order, from the one it starts with: a warp
+// holds the lengths of 64 (lane l those of numbers base + l and base + 32 + l), the
+// later half on its way while the first is used: a load that waits behind the
+// copies takes 2 us.
+struct Requests {
+  int32_t n[2], pre[2], row[2], base, first;
+  SGL_DEV void fill(const Params& p, int h) {
+    const int r = (int)(((int64_t)first + base + 32 * h + (threadIdx.x & 31)) % p.batch);
+    n[h] = drafts_of(p, r), pre[h] = prefix_of(p, r), row[h] = __ldg(p.req_pool_idx + r);
+  }
+  SGL_DEV Requests(const Params& p, const Start& s) : base(0), first(s.r) {
+    fill(p, 0);
+    fill(p, 1);
+  }
+  SGL_DEV void get(const Params& p, int u, int32_t* nn, int32_t* pp, int32_t* rr) {
+    while (u - base >= 32) {
+      n[0] = n[1], pre[0] = pre[1], row[0] = row[1];
+      base += 32;
+      fill(p, 1);
+    }
+    *nn = __shfl_sync(0xffffffffu, n[0], u - base);
+    *pp = __shfl_sync(0xffffffffu, pre[0], u - base);
+    *rr = __shfl_sync(0xffffffffu, row[0], u - base);
+  }
+};
+
 // One block after another of a CTA's run.  keys [0, vis) of a unit are seen by
 // every column, keys [vis, vis + n_tree) are its request's tree.
 struct Cursor {
-  int32_t kvh, r, tile, off, n, b, nb, tiles;
-  int32_t k0, vis, n_tree;  // first position; keys
-  SGL_DEV void lens(const Params& p, const Start& s) {
+  int32_t kvh, r, u, tile, off, n, b, nb, tiles;
+  int32_t k0, vis, n_tree, row;  // first position; keys; row of the table
+  SGL_DEV void lens(const Params& p, int32_t n_, int32_t pre, int32_t row_) {
+    n = n_, row = row_;
+    n_tree = (int32_t)min((int64_t)n, p.rtt_stride - pre);  // positions end with the row
+    k0 = min(p.shared, pre);
+    vis = pre - k0;
+    tiles = (n * p.g + p.cols - 1) / p.cols;
+    nb = n > 0 ? (vis + n_tree + BN - 1) / BN : 0;
+  }
+  SGL_DEV Cursor() {}
+  SGL_DEV Cursor(const Params& p, const Start& s, Requests& q) {
+    kvh = s.kvh, r = s.r, u = 0, tile = s.tile, off = s.off, b = s.b;
     if (p.shared_pass) {
       n = s.tokens;
       k0 = 0, vis = p.shared, n_tree = 0;
-      tiles = (n + p.tpt - 1) / p.tpt;
+      row = __ldg(p.req_pool_idx + s.first_req);
+      tiles = (n * p.g + p.cols - 1) / p.cols;
       nb = (vis + BN - 1) / BN;
     } else {
-      n = drafts_of(p, r);
-      const int32_t pre = prefix_of(p, r);
-      n_tree = (int32_t)min((int64_t)n, p.rtt_stride - pre);  // positions end with the row
-      k0 = min(p.shared, pre);
-      vis = pre - k0;
-      tiles = (n + p.tpt - 1) / p.tpt;
-      nb = n > 0 ? (vis + n_tree + BN - 1) / BN : 0;
+      int32_t n_, pre, row_;
+      q.get(p, 0, &n_, &pre, &row_);
+      lens(p, n_, pre, row_);
     }
   }
-  SGL_DEV Cursor(const Params& p, const Start& s) {
-    kvh = s.kvh, r = s.r, tile = s.tile, off = s.off, b = s.b;
-    lens(p, s);
-  }
   SGL_DEV bool last_of_unit() const { return b + 1 == nb; }
-  // the block after this one (there is one: the caller counts)
-  SGL_DEV void advance(const Params& p, const Start& s) {
-    if (++b < nb) return;
+  // the first block of the next unit (there is one: the caller counts blocks)
+  SGL_DEV void next_unit(const Params& p, Requests& q) {
     b = 0;
     if (++tile < tiles) return;
     tile = 0;
@@ -193,9 +234,15 @@ struct Cursor {
     }
     do {
       off += n;
+      ++u;
       if (++r >= p.batch) r = 0, off = 0, ++kvh;
-      lens(p, s);
+      int32_t n_, pre, row_;
+      q.get(p, u, &n_, &pre, &row_);
+      lens(p, n_, pre, row_);
     } while (nb == 0);
+  }
+  SGL_DEV void advance(const Params& p, Requests& q) {
+    if (++b == nb) next_unit(p, q);
   }
 };
 
@@ -208,11 +255,11 @@ SGL_DEV void find_start(const Params& p, Start* out) {
   int64_t blocks = 0;
   int32_t tokens = 0, first = p.batch;
   for (int r = lane; r < p.batch; r += 32) {
-    Cursor c = {p, Start{0, r, 0, 0, 0}};
+    Cursor c;
+    c.lens(p, drafts_of(p, r), prefix_of(p, r), 0);
     if (!p.shared_pass) blocks += (int64_t)c.nb * c.tiles;
-    const int32_t n = drafts_of(p, r);
-    tokens += n;
-    if (n > 0) first = min(first, r);
+    tokens += c.n;
+    if (c.n > 0) first = min(first, r);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -224,7 +271,7 @@ SGL_DEV void find_start(const Params& p, Start* out) {
   Start s = {};
   s.tokens = tokens;
   s.first_req = first;
-  if (p.shared_pass) blocks = (int64_t)((tokens + p.tpt - 1) / p.tpt) * ((p.shared + BN - 1) / BN);
+  if (p.shared_pass) blocks = (int64_t)((tokens * p.g + p.cols - 1) / p.cols) * ((p.shared + BN - 1) / BN);
   const int64_t total = blocks * p.Hkv;
   s.total = total;
   s.pos = total * blockIdx.x / gridDim.x;
@@ -244,7 +291,8 @@ SGL_DEV void find_start(const Params& p, Start* out) {
         int64_t mine = 0;
         int32_t n = 0, nb = 1;
         if (r < p.batch) {
-          const Cursor c = {p, Start{0, r, 0, 0, 0}};
+          Cursor c;
+          c.lens(p, drafts_of(p, r), prefix_of(p, r), 0);
           n = c.n, nb = max(1, c.nb);
           mine = (int64_t)c.nb * c.tiles;
         }
@@ -340,50 +388,46 @@ constexpr uint32_t idesc(bool mn_major) {
 
 // ----------------------------------------------------------------- producers
 
-// A unit's query rows into its Q tile: row m is token tile * tpt + m / g, head m % g.
+// A unit's query rows into its Q tile: a request's rows are (token, head of the KV
+// head's group), tile t holds rows t N .. t N + N - 1.
 template <int D, int N, bool kFp8>
-SGL_DEV void load_q(const Params& p, const Cursor& c, uint32_t sQ, uint64_t* q_full, int ptid) {
+SGL_DEV void copy_q(const Params& p, const Cursor& c, uint32_t sQ, int ptid) {
   using C = Cfg<D, N, kFp8>;
   const int ci = ptid & 7;
   for (int row = ptid >> 3; row < N; row += C::kProdThreads / 8) {
-    const int k = row / p.g, tok = c.tile * p.tpt + k;
-    const bool valid = k < p.tpt && tok < c.n && c.off + tok < p.total;
-    const int64_t qrow = valid ? (int64_t)(c.off + tok) * p.Hq + (int64_t)c.kvh * p.g + row % p.g : 0;
+    const int r = c.tile * N + row, tok = r / p.g;
+    const bool valid = tok < c.n && c.off + tok < p.total;
+    const int64_t qrow = valid ? (int64_t)(c.off + tok) * p.Hq + (int64_t)c.kvh * p.g + r % p.g : 0;
     const __nv_bfloat16* src = p.q + qrow * D + ci * 8;
 #pragma unroll
-    for (int h = 0; h < C::kChunks; ++h) {
-      const uint32_t dst = sQ + h * C::kQChunkBytes + sw128(row, ci);
-      if constexpr (kFp8) {
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (valid) w = *reinterpret_cast<const uint4*>(src + 64 * h);
-        float f[8];
-        bf16x8_to_f32(w, f);
-        st_shared_v4(dst, pack_f16x2(f[0], f[1]), pack_f16x2(f[2], f[3]), pack_f16x2(f[4], f[5]),
-                     pack_f16x2(f[6], f[7]));
-      } else {
-        cp_async_16(dst, src + 64 * h, valid ? 16u : 0u);
-      }
-    }
+    for (int h = 0; h < C::kChunks; ++h)
+      cp_async_16(sQ + h * C::kQChunkBytes + sw128(row, ci), src + 64 * h, valid ? 16u : 0u);
   }
-  if constexpr (kFp8) {
-    fence_proxy_async_smem();
-    mbar_arrive(q_full);
-  } else {
-    cp_async_mbar_arrive(q_full);
+}
+// The thread's own pieces of it, landed, from bf16 to f16 (e4m3 pools).
+template <int D, int N>
+SGL_DEV void widen_q(uint32_t sQ, int ptid) {
+  using C = Cfg<D, N, true>;
+  const int ci = ptid & 7;
+  for (int row = ptid >> 3; row < N; row += C::kProdThreads / 8) {
+#pragma unroll
+    for (int h = 0; h < C::kChunks; ++h) {
+      const uint32_t at = sQ + h * C::kQChunkBytes + sw128(row, ci);
+      float f[8];
+      bf16x8_to_f32(ld_shared_v4(at), f);
+      st_shared_v4(at, pack_f16x2(f[0], f[1]), pack_f16x2(f[2], f[3]), pack_f16x2(f[4], f[5]),
+                   pack_f16x2(f[6], f[7]));
+    }
   }
 }
 
 // The slots of a block's rows first, first + step, ...; -1 where there is no key.
 template <int kRows>
-SGL_DEV void load_slots(const Params& p, const Start& s, const Cursor& c, int first, int step, int32_t (&slot)[kRows]) {
-  const int32_t row = __ldg(p.req_pool_idx + (p.shared_pass ? s.first_req : c.r));
-  const int32_t* t = p.rtt + row * p.rtt_stride + c.k0;
-  const int32_t keys = c.vis + c.n_tree;
+SGL_DEV void load_slots(const Params& p, const Cursor& c, int first, int step, int32_t (&slot)[kRows]) {
+  const int32_t* t = p.rtt + c.row * p.rtt_stride + c.k0 + c.b * BN + first;
+  const int32_t keys = min(c.vis + c.n_tree - c.b * BN, BN);
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const int32_t at = first + step * i, j = c.b * BN + at;
-    slot[i] = at < BN && j < keys ? __ldg(t + j) : -1;
-  }
+  for (int i = 0; i < kRows; ++i) slot[i] = first + step * i < keys ? __ldg(t + step * i) : -1;
 }
 
 template <int D, int N>
@@ -391,21 +435,23 @@ SGL_DEV void produce(const Params& p, const Start& s, Misc* m, uint32_t sQ, uint
   using C = Cfg<D, N, false>;
   constexpr int kStep = C::kProdThreads / 8, kRows = (BN + kStep - 1) / kStep;
   const int ci = ptid & 7, rb = ptid >> 3;
-  Cursor c(p, s);
+  Requests req(p, s);
+  Cursor c(p, s, req);
   int32_t slot[kRows], next[kRows];
-  load_slots(p, s, c, rb, kStep, slot);
+  load_slots(p, c, rb, kStep, slot);
   int seg = 0;
   auto query = [&]() {
     const int qb = seg % C::kQBufs, round = seg / C::kQBufs;
     if (round > 0 && !warp_wait(&m->q_empty[qb], (round - 1) & 1, m, p)) return false;
-    load_q<D, N, false>(p, c, sQ + qb * C::kQBytes, &m->q_full[qb], ptid);
+    copy_q<D, N, false>(p, c, sQ + qb * C::kQBytes, ptid);
+    cp_async_mbar_arrive(&m->q_full[qb]);
     return true;
   };
   for (int i = 0; i < s.blocks; ++i) {
     Cursor cn = c;
     if (i + 1 < s.blocks) {
-      cn.advance(p, s);
-      load_slots(p, s, cn, rb, kStep, next);
+      cn.advance(p, req);
+      load_slots(p, cn, rb, kStep, next);
     }
     const bool opens = i == 0 || c.b == 0;
     if (opens && C::kQBufs == 2 && !query()) return;
@@ -428,6 +474,10 @@ SGL_DEV void produce(const Params& p, const Start& s, Misc* m, uint32_t sQ, uint
           cp_async_16(dst + h * C::kChunkBytes + sw128(row, ci), src + 64 * h, valid ? 16u : 0u);
       }
       cp_async_mbar_arrive(&full[st]);
+      if (kv == 0 && ptid == 0) {
+        m->k_last[st] = c.last_of_unit() || i + 1 == s.blocks;
+        mbar_arrive(&full[st]);
+      }
     }
     // one Q tile alone: the next unit's waits for the last scores of this one,
     // and its first keys go ahead of it
@@ -439,39 +489,92 @@ SGL_DEV void produce(const Params& p, const Start& s, Misc* m, uint32_t sQ, uint
   }
 }
 
-// e4m3 pool: a thread holds its codes of the next kDepth blocks in registers and
-// widens them to f16 as a slot frees.
+// e4m3 pool: a row's codes are copied into the second half of its place in the slot
+// and widened to f16 from there, by the threads of the warp that copied them, so
+// every free slot has codes on their way and no staging of its own.  A warp goes on
+// with what it can: a copy when a slot is free, else the oldest tile that it has
+// not widened.  (Codes held in registers instead, one block ahead: 1,328 us on 48
+// requests of up to 16,000 tokens, 32 drafts, 32 query heads on 8.)
 template <int D, int N>
 SGL_DEV void produce_fp8(const Params& p, const Start& s, Misc* m, uint32_t sQ, uint32_t sKV, int ptid) {
   using C = Cfg<D, N, true>;
-  constexpr int kDepth = C::kSplitRegs ? 1 : 2;
   constexpr int kPieces = D / 16;  // 16-byte pieces of a row of codes
   constexpr int kStep = C::kProdThreads / kPieces, kRows = (BN + kStep - 1) / kStep;
-  struct Held {
-    uint4 k[kRows], v[kRows];
-    int32_t slot[kRows];
-    int32_t kvh;
-  };
+  constexpr int kAhead = 4;  // tiles copied and not widened
   const int rc = ptid % kPieces, rb = ptid / kPieces;
-  Cursor c(p, s), ahead(p, s);
-  int ahead_i = 0, seg = 0;
-  auto slots = [&](Held& h) {  // of the next block ahead
-    if (ahead_i >= s.blocks) return;
-    if (ahead_i > 0) ahead.advance(p, s);
-    load_slots(p, s, ahead, rb, kStep, h.slot);
-    h.kvh = ahead.kvh;
-    ++ahead_i;
+  const int raw = (D == 128 ? C::kChunkBytes : 64) + rc * 16;  // the thread's codes in a row's place
+  Requests req(p, s);
+  Cursor c(p, s, req);  // of the next block to copy
+  int32_t slot[kRows], next[kRows];
+  load_slots(p, c, rb, kStep, slot);
+  Cursor cn = c;
+  const int tiles = 2 * s.blocks;
+  int copied = 0, widened = 0, seg = 0, seg_w = 0;
+  bool opens = true;
+  uint32_t firsts = 0, lasts = 0;  // bit b % 32: block b is its segment's first, last
+  // the barriers that the next copy waits for: its slot's and, with a segment's
+  // first keys, its Q tile's
+  auto slot_bar = [&](int t) {
+    const int i = t >> 1, st = i % ((t & 1) ? C::kV : C::kK);
+    return (t & 1) ? &m->v_done[st] : &m->k_done[st];
   };
-  auto codes = [&](const Held& h, const void* pool, uint4 (&w)[kRows]) {
+  auto round_of = [&](int t) { return (t >> 1) / ((t & 1) ? C::kV : C::kK); };
+  auto free = [&]() {
+    const int round = round_of(copied);
+    bool ok = round == 0 || mbar_try_wait(slot_bar(copied), (round - 1) & 1, 20u);
+    if (!(copied & 1) && opens && seg >= 2) ok = ok && mbar_try_wait(&m->q_empty[seg & 1], ((seg >> 1) - 1) & 1, 20u);
+    return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+  };
+  auto copy = [&]() {
+    const int t = copied, i = t >> 1, kv = t & 1, st = i % (kv ? C::kV : C::kK);
+    if (!kv) {
+      const bool last = c.last_of_unit() || i + 1 == s.blocks;
+      const uint32_t bit = 1u << (i & 31);
+      firsts = opens ? firsts | bit : firsts & ~bit;
+      lasts = last ? lasts | bit : lasts & ~bit;
+      if (opens) copy_q<D, N, true>(p, c, sQ + (seg & 1) * C::kQBytes, ptid);
+      if (last) ++seg;
+      opens = last;
+      cn = c;
+      if (i + 1 < s.blocks) {  // the next block's slots
+        cn.advance(p, req);
+        load_slots(p, cn, rb, kStep, next);
+      }
+    }
+    const uint8_t* pool = static_cast<const uint8_t*>(kv ? p.pool_v : p.pool_k);
+    const uint32_t dst = sKV + (kv ? C::kK + st : st) * C::kTileBytes + raw;
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-      w[r] = make_uint4(0, 0, 0, 0);
-      if (h.slot[r] >= 0)
-        w[r] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(pool) +
-                                                    ((int64_t)h.slot[r] * p.Hkv + h.kvh) * D + rc * 16));
+      const int row = rb + kStep * r;
+      if (row >= BN) break;
+      const bool valid = slot[r] >= 0;
+      cp_async_16(dst + row * 128, pool + ((int64_t)(valid ? slot[r] : 0) * p.Hkv + c.kvh) * D + rc * 16,
+                  valid ? 16u : 0u);
     }
+    cp_async_commit();
+    if (kv) {
+      c = cn;
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) slot[r] = next[r];
+    }
+    ++copied;
   };
-  auto widen = [&](const uint4 (&w)[kRows], uint32_t tile) {
+  auto widen = [&]() {
+    const int t = widened, i = t >> 1, kv = t & 1, st = i % (kv ? C::kV : C::kK);
+    switch (copied - widened) {  // the thread's copies of tile t have landed
+      case 1: cp_async_wait<0>(); break;
+      case 2: cp_async_wait<1>(); break;
+      case 3: cp_async_wait<2>(); break;
+      default: cp_async_wait<3>(); break;
+    }
+    const uint32_t tile = sKV + (kv ? C::kK + st : st) * C::kTileBytes;
+    uint4 w[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const int row = rb + kStep * r;
+      if (row < BN) w[r] = ld_shared_v4(tile + raw + row * 128);
+    }
+    __syncwarp();  // a row's codes have been read by all its threads
     const uint32_t dst = tile + (rc >> 2) * C::kChunkBytes;
     const int piece = 2 * (rc & 3);
 #pragma unroll
@@ -490,57 +593,28 @@ SGL_DEV void produce_fp8(const Params& p, const Start& s, Misc* m, uint32_t sQ, 
       st_shared_v4(dst + sw128(row, piece), o[0], o[1], o[2], o[3]);
       st_shared_v4(dst + sw128(row, piece + 1), o[4], o[5], o[6], o[7]);
     }
-  };
-  auto query = [&]() {
-    const int qb = seg % C::kQBufs, round = seg / C::kQBufs;
-    if (round > 0 && !warp_wait(&m->q_empty[qb], (round - 1) & 1, m, p)) return false;
-    load_q<D, N, true>(p, c, sQ + qb * C::kQBytes, &m->q_full[qb], ptid);
-    return true;
-  };
-  // block i out of h, which then takes block i + kDepth (its slots are known) and
-  // the slots of the one after that
-  auto block = [&](Held& h, int i) {
-    if (i > 0) c.advance(p, s);
-    const bool opens = i == 0 || c.b == 0;
-    if (opens && C::kQBufs == 2 && !query()) return false;
-#pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      const int ring = kv ? C::kV : C::kK, st = i % ring, round = i / ring;
-      uint64_t* full = kv ? m->v_full : m->k_full;
-      uint64_t* done = kv ? m->v_done : m->k_done;
-      if (round > 0 && !warp_wait(&done[st], (round - 1) & 1, m, p)) return false;
-      widen(kv ? h.v : h.k, sKV + (kv ? C::kK + st : st) * C::kTileBytes);
-      if (i + kDepth < s.blocks) codes(h, kv ? p.pool_v : p.pool_k, kv ? h.v : h.k);
-      fence_proxy_async_smem();
-      mbar_arrive(&full[st]);
+    const bool first = !kv && (firsts >> (i & 31) & 1);
+    if (first) widen_q<D, N>(sQ + (seg_w & 1) * C::kQBytes, ptid);
+    fence_proxy_async_smem();
+    if (first) mbar_arrive(&m->q_full[seg_w & 1]), ++seg_w;
+    uint64_t* full = kv ? &m->v_full[st] : &m->k_full[st];
+    if (!kv && ptid == 0) {
+      m->k_last[st] = lasts >> (i & 31) & 1;
+      mbar_arrive(full);
     }
-    slots(h);
-    if (opens && C::kQBufs == 1 && !query()) return false;
-    if (c.last_of_unit()) ++seg;
-    return true;
+    mbar_arrive(full);
+    ++widened;
   };
-  auto start = [&](Held& h, int i) {
-    slots(h);
-    if (i >= s.blocks) return;
-    codes(h, p.pool_k, h.k);
-    codes(h, p.pool_v, h.v);
-  };
-  if constexpr (kDepth == 2) {
-    Held a, b;
-    start(a, 0);
-    start(b, 1);
-    slots(a);
-    slots(b);
-    for (int i = 0; i < s.blocks; i += 2) {
-      if (!block(a, i)) return;
-      if (i + 1 < s.blocks && !block(b, i + 1)) return;
+  while (widened < tiles) {
+    if (copied < tiles && copied - widened < kAhead && free()) {
+      copy();
+    } else if (copied > widened) {
+      widen();
+    } else {
+      const int round = round_of(copied);
+      if (round > 0 && !warp_wait(slot_bar(copied), (round - 1) & 1, m, p)) return;
+      if (!(copied & 1) && opens && seg >= 2 && !warp_wait(&m->q_empty[seg & 1], ((seg >> 1) - 1) & 1, m, p)) return;
     }
-  } else {
-    Held a;
-    start(a, 0);
-    slots(a);
-    for (int i = 0; i < s.blocks; ++i)
-      if (!block(a, i)) return;
   }
 }
 
@@ -551,8 +625,8 @@ template <int D, int N, bool kFp8>
 SGL_DEV void issue(const Params& p, const Start& s, Misc* m, uint32_t tmem, uint32_t sQ, uint32_t sP, uint32_t sKV) {
   using C = Cfg<D, N, kFp8>;
   auto there = [&](uint64_t* bar, uint32_t parity) { return mbar_try_wait(bar, parity, 20u); };
-  Cursor c(p, s), cv(p, s);
   int i = 0, j = 0;  // next block of S^T, of O^T
+  uint32_t lasts = 0;  // bit b % 32: block b is its segment's last
   int seg = 0, seg_v = 0;
   bool opens = true, opens_v = true;
   uint32_t idle = 0;
@@ -570,10 +644,11 @@ SGL_DEV void issue(const Params& p, const Start& s, Misc* m, uint32_t tmem, uint
           const uint64_t b = make_sw128_desc(sQ + qb * C::kQBytes + (kk >> 2) * C::kQChunkBytes + (kk & 3) * 32, 16, 1024);
           umma_ss(tmem + (i % C::kSBufs) * N, a, b, idesc<N, kFp8>(false), kk > 0 ? 1u : 0u);
         }
+        opens = m->k_last[st] != 0;
+        lasts = (lasts & ~(1u << (i & 31))) | ((opens ? 1u : 0u) << (i & 31));
         umma_commit(&m->k_done[st]);
-        opens = c.last_of_unit();
         if (opens) umma_commit(&m->q_empty[qb]), ++seg;
-        if (++i < s.blocks) c.advance(p, s);
+        ++i;
         moved = true;
       }
     }
@@ -593,9 +668,9 @@ SGL_DEV void issue(const Params& p, const Start& s, Misc* m, uint32_t tmem, uint
           umma_ss(tmem + C::kColO + ob * N, a, b, idesc<N, kFp8>(true), (opens_v && kk == 0) ? 0u : 1u);
         }
         umma_commit(&m->v_done[st]);
-        opens_v = cv.last_of_unit() || j + 1 == s.blocks;
+        opens_v = lasts >> (j & 31) & 1;
         if (opens_v) umma_commit(&m->o_full[ob]), ++seg_v;
-        if (++j < s.blocks) cv.advance(p, s);
+        ++j;
         moved = true;
       }
     }
@@ -616,57 +691,41 @@ SGL_DEV void issue(const Params& p, const Start& s, Misc* m, uint32_t tmem, uint
 
 // ----------------------------------------------------------------- softmax
 
-// A request's tree in a warp: lane l holds the parents of nodes l and l + 32
-// (below 0: none).
-struct Tree {
-  int up[2];
-  SGL_DEV void load(const Params& p, const Cursor& c) {
+// Which of the W columns from col0 on see the thread's key, node `node` of the
+// tree (below 0: a key that all see): bit e for column col0 + e, whose token has
+// that node among itself and those above it.  Lanes hold the ancestor sets of
+// nodes lane and lane + 32, which grow by doubling: each round adds what the node
+// reached last has reached.
+template <int W>
+SGL_DEV uint32_t seen_by(const Params& p, const Segment& g, int node, int col0) {
+  const int lane = threadIdx.x & 31;
+  if (g.n_tree == 0) return node < 0 ? 0xffffffffu : 0u;
+  uint64_t anc[2] = {1ull << lane, 1ull << (lane + 32)};
+  int at[2] = {g.up[lane], g.up[lane + 32]};
+  for (int span = 1; span < g.n_tree; span *= 2) {
+    uint64_t a[2];
+    int u[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int t = (threadIdx.x & 31) + 32 * h;
-      up[h] = t < c.n_tree && c.off + t < p.total ? __ldg(p.parents + c.off + t) : -1;
-      if (up[h] >= t) up[h] = -1;  // a parent lies before its child
+      const int src = at[h] & 31;
+      const uint64_t a0 = __shfl_sync(0xffffffffu, anc[0], src), a1 = __shfl_sync(0xffffffffu, anc[1], src);
+      const int u0 = __shfl_sync(0xffffffffu, at[0], src), u1 = __shfl_sync(0xffffffffu, at[1], src);
+      a[h] = at[h] < 0 ? 0ull : at[h] < 32 ? a0 : a1;
+      u[h] = at[h] < 0 ? -1 : at[h] < 32 ? u0 : u1;
     }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) anc[h] |= a[h], at[h] = u[h];
   }
-  // Which of W columns from col0 on see the thread's key, node `node`: bit e for
-  // column col0 + e, whose token has that node among itself and those above it.
-  // Ancestor sets grow by doubling: each round adds what the node reached last has
-  // reached.
-  template <int W, int kWords>
-  SGL_DEV void seen(const Params& p, const Cursor& c, int node, int col0, uint32_t (&bits)[kWords]) const {
-    const int lane = threadIdx.x & 31;
-    uint64_t anc[2] = {1ull << lane, 1ull << (lane + 32)};
-    int at[2] = {up[0], up[1]};
-    for (int span = 1; span < c.n_tree; span *= 2) {
-      uint64_t a[2];
-      int u[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int src = at[h] & 31;
-        const uint64_t a0 = __shfl_sync(0xffffffffu, anc[0], src), a1 = __shfl_sync(0xffffffffu, anc[1], src);
-        const int u0 = __shfl_sync(0xffffffffu, at[0], src), u1 = __shfl_sync(0xffffffffu, at[1], src);
-        a[h] = at[h] < 0 ? 0ull : at[h] < 32 ? a0 : a1;
-        u[h] = at[h] < 0 ? -1 : at[h] < 32 ? u0 : u1;
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) anc[h] |= a[h], at[h] = u[h];
-    }
-    const int t0 = c.tile * p.tpt;
-#pragma unroll
-    for (int w = 0; w < kWords; ++w) {
-      const int base = col0 + w * W;
-      bits[w] = 0;
-      for (int k = base / p.g; k * p.g < base + W; ++k) {
-        const int t = t0 + k;  // (uniform; a column past the tile's tokens is not used)
-        if (t >= 64) break;
-        const uint64_t a = __shfl_sync(0xffffffffu, t < 32 ? anc[0] : anc[1], t & 31);
-        const int lo = max(0, k * p.g - base), hi = min(W, (k + 1) * p.g - base);
-        const uint32_t span = (hi - lo >= 32 ? 0xffffffffu : (1u << (hi - lo)) - 1u) << lo;
-        if (node < 0 || (node < c.n_tree && (a >> node & 1))) bits[w] |= span;
-      }
-    }
+  uint32_t bits = 0;
+  int t = g.t0 + (g.h0 + col0) / p.g, lo = -((g.h0 + col0) % p.g);  // token, its first column
+  for (; lo < W && t < 64; ++t, lo += p.g) {  // (columns past the tile's are not used)
+    const uint64_t a = __shfl_sync(0xffffffffu, t < 32 ? anc[0] : anc[1], t & 31);
+    const int c0 = max(0, lo), c1 = min(W, lo + p.g);
+    const uint32_t span = (c1 - c0 >= 32 ? 0xffffffffu : (1u << (c1 - c0)) - 1u) << c0;
+    if (node < 0 || (node < g.n_tree && (a >> node & 1))) bits |= span;
   }
-};
+  return bits;
+}
 
 // Byte of P^T at (key, column col, a multiple of 8): rows of kPRow bytes whose
 // 16-byte pieces are swizzled.
@@ -680,133 +739,109 @@ SGL_DEV uint32_t p_at(int key, int col) {
 template <int D, int N, bool kFp8>
 SGL_DEV void softmax(const Params& p, const Start& s, Misc* m, uint32_t tmem, uint32_t sP) {
   using C = Cfg<D, N, kFp8>;
-  constexpr int W = C::kW;
+  constexpr int W = C::kCols;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int wg = warp >> 2, q = warp & 3, key = q * 32 + lane, col0 = wg * C::kCols, wt = tid & 127;
+  const int wg = warp >> 2, q = warp & 3, key = q * 32 + lane, col0 = wg * W, wt = tid & 127;
   const uint32_t bar = 1 + wg;
   const uint32_t lanes = (uint32_t)(q * 32) << 16;
   const float sc = p.scale_log2;
-  Cursor c(p, s);
-  Tree tree;
-  int seg = 0;
-  bool opens = true, first_masked = false, ok = true;
-  float l[C::kCols];
-  for (int i = 0; i < s.blocks; ++i) {
-    const bool masked = (c.b + 1) * BN > c.vis;
-    if (opens) {
-      first_masked = masked;
-      tree.load(p, c);
-    }
-    const int node = c.b * BN + key - c.vis;  // of the tree; below 0 a key that all see
-    uint32_t bits[C::kPasses];
-    if (masked) {
-      if (c.n_tree > 0) {
-        tree.seen<W>(p, c, node, col0, bits);
-      } else {
-#pragma unroll
-        for (int w = 0; w < C::kPasses; ++w) bits[w] = node < 0 ? 0xffffffffu : 0u;
-      }
-    }
-    ok = warp_wait(&m->k_done[i % C::kK], (i / C::kK) & 1, m, p) && ok;  // S^T is there
-    tc_fence_after();
-    const uint32_t tS = tmem + lanes + (i % C::kSBufs) * N + col0;
+  int i = 0;
+  bool ok = true;
+  float l[W];
+  for (int seg = 0; i < s.blocks; ++seg) {
+    const Segment& g = m->seg[seg & 1];
+    ok = warp_wait(&m->u_full[seg & 1], (seg >> 1) & 1, m, p) && ok;
+    if (bar_red_or(bar, 128, !ok)) return;
+    const int take = g.take;
+    int node = g.b0 * BN + key - g.vis;  // of the tree; below 0 a key that all see
+    const bool first_masked = (g.b0 + 1) * BN > g.vis;
+    const int hidden_from = g.vis / BN - g.b0;  // first block of the segment with keys that some do not see
     const uint32_t tO = tmem + lanes + C::kColO + (seg & 1) * N + col0;
-    auto load = [&](int pass, uint32_t (&x)[W]) {
-      tmem_ld<W>(tS + pass * W, x);
-      if (masked) {
 #pragma unroll
-        for (int e = 0; e < W; ++e)
-          if (!(bits[pass] >> e & 1)) x[e] = __float_as_uint(-INFINITY);
+    for (int e = 0; e < W; ++e) l[e] = 0.f;
+    for (int b = 0; b < take; ++b, ++i, node += BN) {
+      const bool masked = b >= hidden_from, opens = b == 0;
+      uint32_t bits = 0;
+      if (masked) bits = seen_by<W>(p, g, node, col0);
+      ok = warp_wait(&m->k_done[i % C::kK], (i / C::kK) & 1, m, p) && ok;  // S^T is there
+      tc_fence_after();
+      const uint32_t tS = tmem + lanes + (i % C::kSBufs) * N + col0;
+      uint32_t x[W];
+      auto load = [&]() {
+        tmem_ld<W>(tS, x);
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < W; ++e)
+            if (!(bits >> e & 1)) x[e] = __float_as_uint(-INFINITY);
+        }
+      };
+      // scores against their columns' references, in units of log 2
+      auto relative = [&]() {
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        const float2 s2 = make_float2(sc, sc);
+#pragma unroll
+        for (int e = 0; e < W; e += 4) {
+          const float4 r = *reinterpret_cast<const float4*>(&m->mcol[col0 + e]);
+          const float2 a = ffma2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), s2, make_float2(-r.x, -r.y));
+          const float2 c = ffma2(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), s2, make_float2(-r.z, -r.w));
+          x[e] = __float_as_uint(a.x), x[e + 1] = __float_as_uint(a.y);
+          x[e + 2] = __float_as_uint(c.x), x[e + 3] = __float_as_uint(c.y);
+          top[(e >> 1) & 3] = fmax3(top[(e >> 1) & 3], a.x, a.y);
+          top[((e >> 1) + 1) & 3] = fmax3(top[((e >> 1) + 1) & 3], c.x, c.y);
+        }
+        return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+      };
+      // a segment's first block sets the references; one whose first block hides
+      // keys (columns may have seen none yet) sets them block by block
+      bool redo = opens || (masked && first_masked);
+      if (!redo) {
+        load();
+        redo = relative() > C::kAccept;
       }
-    };
-    // scores against their columns' references, in units of log 2
-    auto relative = [&](int pass, uint32_t (&x)[W]) {
-      float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      const float2 s2 = make_float2(sc, sc);
-#pragma unroll
-      for (int e = 0; e < W; e += 4) {
-        const float4 r = *reinterpret_cast<const float4*>(&m->mcol[col0 + pass * W + e]);
-        float2 a = ffma2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), s2, make_float2(-r.x, -r.y));
-        float2 b = ffma2(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), s2, make_float2(-r.z, -r.w));
-        x[e] = __float_as_uint(a.x), x[e + 1] = __float_as_uint(a.y);
-        x[e + 2] = __float_as_uint(b.x), x[e + 3] = __float_as_uint(b.y);
-        top[(e >> 1) & 3] = fmax3(top[(e >> 1) & 3], a.x, a.y);
-        top[((e >> 1) + 1) & 3] = fmax3(top[((e >> 1) + 1) & 3], b.x, b.y);
-      }
-      return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-    };
-    uint32_t x[W];
-    // a segment's first block sets the references; one whose first block hides
-    // keys (columns may have seen none yet) sets them block by block
-    bool redo = opens || (masked && first_masked);
-    if (!redo) {
-      float top = -INFINITY;
-#pragma unroll
-      for (int pass = 0; pass < C::kPasses; ++pass) {
-        load(pass, x);
-        top = fmaxf(top, relative(pass, x));
-      }
-      redo = top > C::kAccept;
-    }
-    // the warpgroup agrees: lane 0 votes to move the references, lanes 1 to 8
-    // that the warp gave up waiting
-    const bool redo_w = __any_sync(0xffffffffu, redo);
-    const uint32_t votes = bar_red_popc(bar, 128, (lane == 0 && redo_w) || (lane >= 1 && lane <= 8 && !ok));
-    if (votes >= 8) return;
-    if (votes != 0) {
-      if (wt < C::kCols) m->mxcol[col0 + wt] = ordered(-INFINITY);
-      named_bar_sync(bar, 128);
-#pragma unroll
-      for (int pass = 0; pass < C::kPasses; ++pass) {
-        load(pass, x);
-        const float top = columns<W>(*reinterpret_cast<float(*)[W]>(&x), [](float a, float b) { return fmaxf(a, b); });
-        atomicMax(&m->mxcol[col0 + pass * W + (lane & (W - 1))], ordered(top));
-      }
-      named_bar_sync(bar, 128);
-      if (wt < C::kCols) {
-        const int col = col0 + wt;
-        const float before = opens ? -INFINITY : m->mcol[col];
-        const float now = fmaxf(before, unordered(m->mxcol[col]) * sc - C::kShift);
-        m->mcol[col] = now;
-        m->mxcol[col] = __float_as_int(before == -INFINITY ? 0.f : ex2(before - now));
-      }
-      named_bar_sync(bar, 128);
-      if (opens) {
-#pragma unroll
-        for (int e = 0; e < C::kCols; ++e) l[e] = 0.f;
-      } else {
-        // O^T of the blocks before comes to the new references
-        ok = warp_wait(&m->v_done[(i - 1) % C::kV], ((i - 1) / C::kV) & 1, m, p) && ok;
-        tc_fence_after();
-#pragma unroll
-        for (int pass = 0; pass < C::kPasses; ++pass) {
-          tmem_ld<W>(tO + pass * W, x);
+      // the warpgroup agrees: lane 0 votes to move the references, lanes 1 to 8
+      // that the warp gave up waiting
+      const bool redo_w = __any_sync(0xffffffffu, redo);
+      const uint32_t votes = bar_red_popc(bar, 128, (lane == 0 && redo_w) || (lane >= 1 && lane <= 8 && !ok));
+      if (votes >= 8) return;
+      if (votes != 0) {
+        if (wt < W) m->mxcol[col0 + wt] = ordered(-INFINITY);
+        named_bar_sync(bar, 128);
+        load();
+        const float top = columns<W>(*reinterpret_cast<float(*)[W]>(&x), [](float a, float c) { return fmaxf(a, c); });
+        atomicMax(&m->mxcol[col0 + (lane & (W - 1))], ordered(top));
+        named_bar_sync(bar, 128);
+        if (wt < W) {
+          const int col = col0 + wt;
+          const float before = opens ? -INFINITY : m->mcol[col];
+          const float now = fmaxf(before, unordered(m->mxcol[col]) * sc - C::kShift);
+          m->mcol[col] = now;
+          m->mxcol[col] = __float_as_int(before == -INFINITY ? 0.f : ex2(before - now));
+        }
+        named_bar_sync(bar, 128);
+        if (!opens) {
+          // O^T of the blocks before comes to the new references
+          ok = warp_wait(&m->v_done[(i - 1) % C::kV], ((i - 1) / C::kV) & 1, m, p) && ok;
+          tc_fence_after();
+          tmem_ld<W>(tO, x);
 #pragma unroll
           for (int e = 0; e < W; ++e) {
-            const float a = __int_as_float(m->mxcol[col0 + pass * W + e]);
-            l[pass * W + e] *= a;
+            const float a = __int_as_float(m->mxcol[col0 + e]);
+            l[e] *= a;
             x[e] = __float_as_uint(__uint_as_float(x[e]) * a);
           }
-          tmem_st<W>(tO + pass * W, x);
+          tmem_st<W>(tO, x);
+          tmem_wait_st();
         }
-        tmem_wait_st();
-      }
-    }
-    // P^T: this key's row, 8 columns a 16-byte piece; its buffer was last read
-    // with block i - 2
-    if (i >= 2) ok = warp_wait(&m->v_done[(i - 2) % C::kV], ((i - 2) / C::kV) & 1, m, p) && ok;
-    const uint32_t pbuf = sP + (i & 1) * C::kPBytes;
+        load();
+        relative();
 #pragma unroll
-    for (int pass = 0; pass < C::kPasses; ++pass) {
-      if (C::kPasses > 1 || votes != 0) {
-        load(pass, x);
-        relative(pass, x);
+        for (int e = 0; e < W; ++e)  // a column that has seen no key yet
+          if (m->mcol[col0 + e] == -INFINITY) x[e] = __float_as_uint(-INFINITY);
       }
-      if (votes != 0) {  // a column that has seen no key yet
-#pragma unroll
-        for (int e = 0; e < W; ++e)
-          if (m->mcol[col0 + pass * W + e] == -INFINITY) x[e] = __float_as_uint(-INFINITY);
-      }
+      // P^T: this key's row, 8 columns a 16-byte piece; its buffer was last read
+      // with block i - 2
+      if (i >= 2) ok = warp_wait(&m->v_done[(i - 2) % C::kV], ((i - 2) / C::kV) & 1, m, p) && ok;
+      const uint32_t pbuf = sP + (i & 1) * C::kPBytes;
 #pragma unroll
       for (int e = 0; e < W; e += 8) {
         uint32_t o[4];
@@ -814,42 +849,29 @@ SGL_DEV void softmax(const Params& p, const Start& s, Misc* m, uint32_t tmem, ui
         for (int d = 0; d < 4; ++d) {
           const int at = e + 2 * d;
           const float2 w = make_float2(ex2(__uint_as_float(x[at])), ex2(__uint_as_float(x[at + 1])));
-          const float2 sum = fadd2(make_float2(l[pass * W + at], l[pass * W + at + 1]), w);
-          l[pass * W + at] = sum.x, l[pass * W + at + 1] = sum.y;
+          const float2 sum = fadd2(make_float2(l[at], l[at + 1]), w);
+          l[at] = sum.x, l[at + 1] = sum.y;
           o[d] = kFp8 ? pack_f16x2(w.x, w.y) : pack_bf16x2(w.x, w.y);
         }
-        st_shared_v4(pbuf + p_at<N>(key, col0 + pass * W + e), o[0], o[1], o[2], o[3]);
+        st_shared_v4(pbuf + p_at<N>(key, col0 + e), o[0], o[1], o[2], o[3]);
       }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      mbar_arrive(&m->p_ready[i & 1]);
     }
-    fence_proxy_async_smem();
-    tc_fence_before();
-    mbar_arrive(&m->p_ready[i & 1]);
-    opens = c.last_of_unit() || i + 1 == s.blocks;
-    if (opens) {
-      // the segment's sums and references go to the epilogue warps
-      if (seg > 0) ok = warp_wait(&m->l_free, (seg - 1) & 1, m, p) && ok;
-#pragma unroll
-      for (int pass = 0; pass < C::kPasses; ++pass) {
-        const float sum = columns<W>(*reinterpret_cast<float(*)[W]>(&l[pass * W]), [](float a, float b) { return a + b; });
-        if (q > 0 && lane < W) m->lcol[q - 1][col0 + pass * W + lane] = sum;
-        l[pass] = sum;
+    // the segment's sums and references go to the epilogue warps
+    if (seg > 0) ok = warp_wait(&m->l_free, (seg - 1) & 1, m, p) && ok;
+    float sum = columns<W>(l, [](float a, float c) { return a + c; });
+    const int col = col0 + lane;
+    if (q > 0 && lane < W) (q == 1 ? m->lcol[0] : q == 2 ? m->lcol[1] : reinterpret_cast<float*>(m->mxcol))[col] = sum;
+    if (bar_red_or(bar, 128, !ok)) return;
+    if (q == 0) {
+      if (lane < W) {
+        m->lcol[0][col] = (sum + m->lcol[0][col]) + (m->lcol[1][col] + __int_as_float(m->mxcol[col]));
+        m->lcol[1][col] = m->mcol[col];
       }
-      if (bar_red_or(bar, 128, !ok)) return;
-      if (q == 0) {
-#pragma unroll
-        for (int pass = 0; pass < C::kPasses; ++pass) {
-          const int col = col0 + pass * W + lane;
-          if (lane < W) {
-            const float sum = (l[pass] + m->lcol[0][col]) + (m->lcol[1][col] + m->lcol[2][col]);
-            m->lcol[0][col] = sum;
-            m->lcol[1][col] = m->mcol[col];
-          }
-        }
-        mbar_arrive(&m->l_full);
-      }
-      ++seg;
+      mbar_arrive(&m->l_full);
     }
-    if (i + 1 < s.blocks) c.advance(p, s);
   }
 }
 
@@ -859,73 +881,99 @@ SGL_DEV void softmax(const Params& p, const Start& s, Misc* m, uint32_t tmem, ui
 template <int D, int N, bool kFp8>
 SGL_DEV void epilogue(const Params& p, const Start& s, Misc* m, uint32_t tmem, int et) {
   using C = Cfg<D, N, kFp8>;
-  constexpr int W = C::kW;
-  const int q = et >> 5;
+  constexpr int W = 16;
+  const int q = et >> 5, lane = et & 31;
   const uint32_t bar = 1 + C::kWgs;
-  Cursor c(p, s);
+  // the first warp lists the segments; the parents of the one after next are on
+  // their way meanwhile
+  Requests req(p, s);
+  Cursor c(p, s, req);
+  int listed = 0, n_listed = 0;  // blocks, segments
+  auto list = [&]() {
+    if (listed >= s.blocks) return;
+    Segment& g = m->seg[n_listed & 1];
+    const int take = min(c.nb - c.b, s.blocks - listed), r0 = c.tile * N;
+    int up[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int t = lane + 32 * h;
+      up[h] = t < c.n_tree && c.off + t < p.total ? __ldg(p.parents + c.off + t) : -1;
+      if (up[h] < 0 || up[h] >= t) up[h] = -1;  // a parent lies before its child
+      g.up[t] = (int8_t)up[h];
+    }
+    if (lane == 0) {
+      g.b0 = c.b, g.take = take, g.nb = c.nb, g.vis = c.vis, g.n_tree = c.n_tree, g.kvh = c.kvh;
+      g.t0 = r0 / p.g, g.h0 = r0 % p.g, g.off = c.off;
+      g.live = min(N, min(c.n, p.total - c.off) * p.g - r0);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&m->u_full[n_listed & 1]);
+    listed += take;
+    ++n_listed;
+    if (listed < s.blocks) c.next_unit(p, req);
+  };
+  if (q == 0) {
+    list();
+    list();
+  }
   int i = 0;
   for (int seg = 0; i < s.blocks; ++seg) {
-    const int b0 = c.b, take = min(c.nb - b0, s.blocks - i);  // the segment's blocks of the unit
-    const bool whole = take == c.nb, direct = whole && p.row_ml == nullptr;
+    bool ok = q == 0 || warp_wait(&m->u_full[seg & 1], (seg >> 1) & 1, m, p);
+    const Segment& g = m->seg[seg & 1];
+    const int b0 = g.b0, take = g.take, nb = g.nb, live = g.live, h0 = g.h0;
+    const int64_t row0 = (int64_t)(g.off + g.t0) * p.Hq + (int64_t)g.kvh * p.g;  // of the token's first head
+    const bool whole = take == nb, direct = whole && p.row_ml == nullptr;
     const int64_t slot = (int64_t)(2 * blockIdx.x + (b0 == 0 ? 1 : 0)) * N;
-    const int t0 = c.tile * p.tpt;
-    const int most = min(min(p.tpt, c.n - t0), p.total - c.off - t0);  // tokens of the tile
-    const int64_t row0 = (int64_t)(c.off + t0) * p.Hq + (int64_t)c.kvh * p.g;
-    bool ok = warp_wait(&m->l_full, seg & 1, m, p);
+    ok = warp_wait(&m->l_full, seg & 1, m, p) && ok;
+    if (bar_red_or(bar, 128, !ok)) return;  // (and all have read the segment)
+    if (q == 0) list();
     if (et < N) {
-      const float sum = m->lcol[0][et];
-      m->lcol[2][et] = p.o_scale / sum;
-      const int k = et / p.g;
-      if (k < most) {
-        const int64_t row = row0 + (int64_t)k * p.Hq + et % p.g;
-        const float2 ml = make_float2(m->lcol[1][et], sum);
+      const float sum = m->lcol[0][et], ref = m->lcol[1][et];
+      m->lcol[1][et] = p.o_scale / sum;
+      if (et < live) {
+        const int64_t row = row0 + (int64_t)((h0 + et) / p.g) * p.Hq + (h0 + et) % p.g;
+        const float2 ml = make_float2(ref, sum);
         if (!whole) p.slot_ml[slot + et] = ml;
         else if (!direct) p.row_ml[row] = ml;
         // (pos + i - b0 + nb - 1: the unit's last block)
         if (b0 == 0)
-          p.info[row] = make_int4(blockIdx.x, whole ? (int)blockIdx.x : owner(s.pos + i + c.nb - 1, s.total, gridDim.x), et, 0);
+          p.info[row] = make_int4(blockIdx.x, whole ? (int)blockIdx.x : owner(s.pos + i + nb - 1, s.total, gridDim.x), et, 0);
       }
     }
-    ok = warp_wait(&m->o_full[seg & 1], (seg >> 1) & 1, m, p) && ok;
+    ok = warp_wait(&m->o_full[seg & 1], (seg >> 1) & 1, m, p);
     tc_fence_after();
     if (bar_red_or(bar, 128, !ok)) return;
     const uint32_t tO = tmem + ((uint32_t)(q * 32) << 16) + C::kColO + (seg & 1) * N;
-    int k = 0, h = 0;
-    int64_t row = row0;
+    int h = h0;
+    int64_t row = row0 + h0;
 #pragma unroll 1
     for (int w = 0; w < N / W; ++w) {
+      if (w * W >= live) break;
       uint32_t x[W];
       tmem_ld<W>(tO + w * W, x);
-      if (et >= D || k >= most) continue;  // (a warp's lanes alike; k >= most from here on)
-      // the destination of column e: consecutive for states, rows of a token's
-      // heads else
-      if (whole) {
+      if (et >= D) continue;  // (a warp's lanes alike)
+      if (whole) {  // rows of a token's heads
 #pragma unroll
         for (int e = 0; e < W; ++e) {
-          if (k < most) {
+          if (w * W + e < live) {
             const float o = __uint_as_float(x[e]);
-            if (direct) p.out[row * D + et] = __float2bfloat16_rn(o * m->lcol[2][w * W + e]);
+            if (direct) p.out[row * D + et] = __float2bfloat16_rn(o * m->lcol[1][w * W + e]);
             else p.row_acc[row * D + et] = o;
           }
           ++row;
-          if (++h == p.g) h = 0, ++k, row += p.Hq - p.g;
+          if (++h == p.g) h = 0, row += p.Hq - p.g;
         }
       } else {
         float* to = p.slot_acc + (slot + w * W) * D + et;
-        const int live = most * p.g - w * W;
 #pragma unroll
         for (int e = 0; e < W; ++e)
-          if (e < live) to[e * D] = __uint_as_float(x[e]);
+          if (w * W + e < live) to[e * D] = __uint_as_float(x[e]);
       }
     }
     tc_fence_before();
     mbar_arrive(&m->o_free[seg & 1]);
     mbar_arrive(&m->l_free);
     i += take;
-    if (i < s.blocks) {
-      c.b = c.nb - 1;
-      c.advance(p, s);
-    }
   }
 }
 
@@ -950,12 +998,13 @@ __global__ void __launch_bounds__(Cfg<D, N, kFp8>::kThreads, 1) verify_kernel(co
       mbar_init(&m->p_ready[i], 32 * C::kSoftWarps);
       mbar_init(&m->o_full[i], 1);
       mbar_init(&m->o_free[i], 128);
+      mbar_init(&m->u_full[i], 1);
     }
     mbar_init(&m->l_full, 32 * C::kWgs);
     mbar_init(&m->l_free, 128);
     mbar_init(&m->drain, 1);
     for (int i = 0; i < C::kK; ++i) {
-      mbar_init(&m->k_full[i], C::kProdThreads);
+      mbar_init(&m->k_full[i], C::kProdThreads + 1);  // and the thread that writes k_last
       mbar_init(&m->k_done[i], 1);
     }
     for (int i = 0; i < C::kV; ++i) {
@@ -1089,7 +1138,11 @@ __global__ void __launch_bounds__(128) verify_combine_kernel(const CombineParams
 
 // ----------------------------------------------------------------- host
 
-int columns_for(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+// Columns of a tile for so many query rows a KV head.  (128 over an e4m3 pool left
+// the softmax and the producers too few registers.)
+int columns_for(int64_t rows, bool kv_fp8) {
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 || kv_fp8 ? 64 : 128;
+}
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -1142,8 +1195,10 @@ template <int D, bool kFp8>
 sgl_status launch_n(const Params& prm, int n, bool dependent, cudaStream_t stream) {
   if (n == 16) return launch_one<D, 16, kFp8>(prm, dependent, stream);
   if (n == 32) return launch_one<D, 32, kFp8>(prm, dependent, stream);
-  if (n == 64) return launch_one<D, 64, kFp8>(prm, dependent, stream);
-  return launch_one<D, 128, kFp8>(prm, dependent, stream);
+  if constexpr (!kFp8) {
+    if (n == 128) return launch_one<D, 128, kFp8>(prm, dependent, stream);
+  }
+  return launch_one<D, 64, kFp8>(prm, dependent, stream);
 }
 
 sgl_status launch_pass(const Params& prm, const VerifyArgs& a, int n, bool dependent, cudaStream_t stream) {
@@ -1166,8 +1221,9 @@ size_t verify_workspace_bytes(int32_t total, int32_t max_draft, int32_t shared_l
   if (total <= 0 || max_draft <= 0 || Hkv <= 0 || Hq < Hkv) return l.bytes;
   const int g = Hq / Hkv;
   const int64_t rows = (int64_t)total * Hq;
-  Buffers own(&l, rows, columns_for((int64_t)max_draft * g), D, shared_len > 0);
-  if (shared_len > 0) Buffers shared(&l, rows, columns_for((int64_t)total * g), D, true);
+  // (sized as over a bf16 pool: one size for both)
+  Buffers own(&l, rows, columns_for((int64_t)max_draft * g, false), D, shared_len > 0);
+  if (shared_len > 0) Buffers shared(&l, rows, columns_for((int64_t)total * g, false), D, true);
   return l.bytes;
 }
 
@@ -1197,19 +1253,19 @@ sgl_status launch_verify(const VerifyArgs& a, cudaStream_t stream) {
   prm.status = static_cast<int*>(a.workspace);
   prm.wait_ns = device_wait_limit_ns();
   const int64_t rows = (int64_t)a.total_draft * a.num_q_heads;
-  const int n = columns_for((int64_t)a.max_draft * g), ns = columns_for((int64_t)a.total_draft * g);
+  const int n = columns_for((int64_t)a.max_draft * g, a.kv_fp8), ns = columns_for((int64_t)a.total_draft * g, a.kv_fp8);
   const bool shared = a.shared_len > 0;
   Layout l;
   char* base = static_cast<char*>(a.workspace);
   Buffers(&l, rows, n, a.head_dim, shared).bind(base, &prm);
-  prm.tpt = n / g;
+  prm.cols = n;
   CombineParams cp = {};
   cp.own = states_of(prm, n);
   if (shared) {
     Params sp = prm;
     Buffers(&l, rows, ns, a.head_dim, true).bind(base, &sp);
     sp.shared_pass = true;
-    sp.tpt = ns / g;
+    sp.cols = ns;
     cp.shared = states_of(sp, ns);
     const sgl_status st = launch_pass(sp, a, ns, false, stream);
     if (st != SGL_OK) return st;
