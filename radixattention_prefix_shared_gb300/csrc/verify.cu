@@ -58,20 +58,22 @@ struct Cfg {
   // warps: softmax, epilogue (4), producers, MMA
   static constexpr int kSoftWarps = 4 * kWgs;
   static constexpr int kProdWarp = kSoftWarps + 4;
-  static constexpr int kProdWarps = N == 128 ? 3 : 7;
+  static constexpr int kProdWarps = kFp8 ? 11 : N == 128 ? 3 : 7;
   static constexpr int kProdThreads = 32 * kProdWarps;
   static constexpr int kMmaWarp = kProdWarp + kProdWarps;
   static constexpr int kThreads = 32 * (kMmaWarp + 1);
   // Registers.  16 warps are launched with 128 a thread; with more, the softmax
   // warps take some of the others' (setmaxnreg; the shares add up to the launch's
-  // registers): 20 warps 8 x 128 + 4 x 64 + 8 x 80 = 20 x 96, 24 warps 16 x 88 +
-  // 8 x 64 = 24 x 80.
-  static constexpr bool kSplitRegs = kWgs > 1;
-  static constexpr int kLaunchRegs = N == 128 ? 80 : 96;
-  static constexpr int kSoftRegs = N == 128 ? 88 : 128, kEpiRegs = 64;
-  static constexpr int kProdRegs = N == 128 ? 64 : 80;
-  static_assert(!kSplitRegs || (kThreads / 32) * kLaunchRegs >= kSoftWarps * kSoftRegs + 4 * kEpiRegs +
-                                                                    (kProdWarps + 1) * kProdRegs,
+  // registers).  A register that does not fit costs much here: its load waits behind
+  // the copies.
+  static constexpr int kWarps = kThreads / 32;
+  static constexpr bool kSplitRegs = kWarps > 16;
+  static constexpr int kLaunchRegs = kWarps == 24 ? 80 : 96;
+  static constexpr int kSoftRegs = kFp8 ? (N == 64 ? 104 : 128) : (N == 128 ? 88 : 112);
+  static constexpr int kEpiRegs = kFp8 && N == 64 ? 56 : 64;
+  static constexpr int kProdRegs = kFp8 ? (N == 64 ? 72 : 96) : (N == 128 ? 64 : 96);
+  static_assert(!kSplitRegs || kWarps * kLaunchRegs >= kSoftWarps * kSoftRegs + 4 * kEpiRegs +
+                                                           (kProdWarps + 1) * kProdRegs,
                 "register split within the launch's registers");
   static constexpr int kChunks = D / 64;         // 128-byte pieces of a row of 16-bit values
   static constexpr int kChunkBytes = 128 * 128;  // 128 rows of one
@@ -388,10 +390,16 @@ constexpr uint32_t idesc(bool mn_major) {
 
 // ----------------------------------------------------------------- producers
 
+// What is left of a unit when the cursor has gone on.
+struct Unit {
+  int32_t kvh, tile, off, n;
+  SGL_DEV explicit Unit(const Cursor& c) : kvh(c.kvh), tile(c.tile), off(c.off), n(c.n) {}
+};
+
 // A unit's query rows into its Q tile: a request's rows are (token, head of the KV
 // head's group), tile t holds rows t N .. t N + N - 1.
 template <int D, int N, bool kFp8>
-SGL_DEV void copy_q(const Params& p, const Cursor& c, uint32_t sQ, int ptid) {
+SGL_DEV void copy_q(const Params& p, const Unit& c, uint32_t sQ, int ptid) {
   using C = Cfg<D, N, kFp8>;
   const int ci = ptid & 7;
   for (int row = ptid >> 3; row < N; row += C::kProdThreads / 8) {
@@ -422,12 +430,20 @@ SGL_DEV void widen_q(uint32_t sQ, int ptid) {
 }
 
 // The slots of a block's rows first, first + step, ...; -1 where there is no key.
+// Those of later blocks are called into the L2: behind a ring full of copies a load
+// that goes to memory takes as long as the ring lasts.
+constexpr int kSlotsAhead = 6;
 template <int kRows>
 SGL_DEV void load_slots(const Params& p, const Cursor& c, int first, int step, int32_t (&slot)[kRows]) {
-  const int32_t* t = p.rtt + c.row * p.rtt_stride + c.k0 + c.b * BN + first;
-  const int32_t keys = min(c.vis + c.n_tree - c.b * BN, BN);
+  const int32_t at = c.b * BN;
+  const int32_t* t = p.rtt + c.row * p.rtt_stride + c.k0;
+  const int32_t all = c.vis + c.n_tree, keys = min(all - at, BN);
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) slot[i] = first + step * i < keys ? __ldg(t + step * i) : -1;
+  for (int i = 0; i < kRows; ++i) slot[i] = first + step * i < keys ? __ldg(t + at + first + step * i) : -1;
+  // one warp's threads, a line of 32 slots each: at a unit's start kSlotsAhead blocks
+  const int ahead = at + (c.b == 0 ? first * 32 : kSlotsAhead * BN + first * 32);
+  if (first < (c.b == 0 ? 4 * (kSlotsAhead + 1) : 4) && ahead < all)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(t + ahead));
 }
 
 template <int D, int N>
@@ -436,24 +452,25 @@ SGL_DEV void produce(const Params& p, const Start& s, Misc* m, uint32_t sQ, uint
   constexpr int kStep = C::kProdThreads / 8, kRows = (BN + kStep - 1) / kStep;
   const int ci = ptid & 7, rb = ptid >> 3;
   Requests req(p, s);
-  Cursor c(p, s, req);
+  Cursor c(p, s, req);  // one block ahead: its slots are on their way
+  Unit now(c);
   int32_t slot[kRows], next[kRows];
   load_slots(p, c, rb, kStep, slot);
   int seg = 0;
+  bool opens = true;
   auto query = [&]() {
     const int qb = seg % C::kQBufs, round = seg / C::kQBufs;
     if (round > 0 && !warp_wait(&m->q_empty[qb], (round - 1) & 1, m, p)) return false;
-    copy_q<D, N, false>(p, c, sQ + qb * C::kQBytes, ptid);
+    copy_q<D, N, false>(p, now, sQ + qb * C::kQBytes, ptid);
     cp_async_mbar_arrive(&m->q_full[qb]);
     return true;
   };
   for (int i = 0; i < s.blocks; ++i) {
-    Cursor cn = c;
+    const bool last = c.last_of_unit() || i + 1 == s.blocks;
     if (i + 1 < s.blocks) {
-      cn.advance(p, req);
-      load_slots(p, cn, rb, kStep, next);
+      c.advance(p, req);
+      load_slots(p, c, rb, kStep, next);
     }
-    const bool opens = i == 0 || c.b == 0;
     if (opens && C::kQBufs == 2 && !query()) return;
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
@@ -468,22 +485,22 @@ SGL_DEV void produce(const Params& p, const Start& s, Misc* m, uint32_t sQ, uint
         const int row = rb + kStep * r;
         if (row >= BN) break;
         const bool valid = slot[r] >= 0;
-        const __nv_bfloat16* src = pool + ((int64_t)(valid ? slot[r] : 0) * p.Hkv + c.kvh) * D + ci * 8;
+        const __nv_bfloat16* src = pool + ((int64_t)(valid ? slot[r] : 0) * p.Hkv + now.kvh) * D + ci * 8;
 #pragma unroll
         for (int h = 0; h < C::kChunks; ++h)
           cp_async_16(dst + h * C::kChunkBytes + sw128(row, ci), src + 64 * h, valid ? 16u : 0u);
       }
       cp_async_mbar_arrive(&full[st]);
       if (kv == 0 && ptid == 0) {
-        m->k_last[st] = c.last_of_unit() || i + 1 == s.blocks;
+        m->k_last[st] = last;
         mbar_arrive(&full[st]);
       }
     }
     // one Q tile alone: the next unit's waits for the last scores of this one,
     // and its first keys go ahead of it
     if (opens && C::kQBufs == 1 && !query()) return;
-    if (c.last_of_unit()) ++seg;
-    c = cn;
+    opens = last;
+    if (last) ++seg, now = Unit(c);
 #pragma unroll
     for (int r = 0; r < kRows; ++r) slot[r] = next[r];
   }
@@ -491,56 +508,43 @@ SGL_DEV void produce(const Params& p, const Start& s, Misc* m, uint32_t sQ, uint
 
 // e4m3 pool: a row's codes are copied into the second half of its place in the slot
 // and widened to f16 from there, by the threads of the warp that copied them, so
-// every free slot has codes on their way and no staging of its own.  A warp goes on
-// with what it can: a copy when a slot is free, else the oldest tile that it has
-// not widened.  (Codes held in registers instead, one block ahead: 1,328 us on 48
-// requests of up to 16,000 tokens, 32 drafts, 32 query heads on 8.)
+// every free slot has codes on their way and no staging of its own.  Tiles (K and V
+// in turn) are copied kLag ahead of the one that is widened: as many as leave the
+// MMAs a slot of each ring besides.  (Codes held in registers instead, one block
+// ahead: 1,328 us on 48 requests of up to 16,000 tokens, 32 drafts, 32 heads on 8.)
 template <int D, int N>
 SGL_DEV void produce_fp8(const Params& p, const Start& s, Misc* m, uint32_t sQ, uint32_t sKV, int ptid) {
   using C = Cfg<D, N, true>;
   constexpr int kPieces = D / 16;  // 16-byte pieces of a row of codes
   constexpr int kStep = C::kProdThreads / kPieces, kRows = (BN + kStep - 1) / kStep;
-  constexpr int kAhead = 4;  // tiles copied and not widened
+  constexpr int kLag = C::kV == 2 ? 2 : C::kV == 3 ? 3 : 5;  // at most 2 kV - 1 (a wait for a slot ends)
   const int rc = ptid % kPieces, rb = ptid / kPieces;
   const int raw = (D == 128 ? C::kChunkBytes : 64) + rc * 16;  // the thread's codes in a row's place
   Requests req(p, s);
-  Cursor c(p, s, req);  // of the next block to copy
+  Cursor c(p, s, req);  // one block ahead of the copies
+  Unit now(c);
   int32_t slot[kRows], next[kRows];
   load_slots(p, c, rb, kStep, slot);
-  Cursor cn = c;
-  const int tiles = 2 * s.blocks;
-  int copied = 0, widened = 0, seg = 0, seg_w = 0;
-  bool opens = true;
+  int seg = 0, seg_w = 0;
+  bool opens = true, last = false;
   uint32_t firsts = 0, lasts = 0;  // bit b % 32: block b is its segment's first, last
-  // the barriers that the next copy waits for: its slot's and, with a segment's
-  // first keys, its Q tile's
-  auto slot_bar = [&](int t) {
-    const int i = t >> 1, st = i % ((t & 1) ? C::kV : C::kK);
-    return (t & 1) ? &m->v_done[st] : &m->k_done[st];
-  };
-  auto round_of = [&](int t) { return (t >> 1) / ((t & 1) ? C::kV : C::kK); };
-  auto free = [&]() {
-    const int round = round_of(copied);
-    bool ok = round == 0 || mbar_try_wait(slot_bar(copied), (round - 1) & 1, 20u);
-    if (!(copied & 1) && opens && seg >= 2) ok = ok && mbar_try_wait(&m->q_empty[seg & 1], ((seg >> 1) - 1) & 1, 20u);
-    return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-  };
-  auto copy = [&]() {
-    const int t = copied, i = t >> 1, kv = t & 1, st = i % (kv ? C::kV : C::kK);
+  auto copy = [&](int i, int kv) {
+    const int ring = kv ? C::kV : C::kK, st = i % ring, round = i / ring;
     if (!kv) {
-      const bool last = c.last_of_unit() || i + 1 == s.blocks;
+      last = c.last_of_unit() || i + 1 == s.blocks;
       const uint32_t bit = 1u << (i & 31);
       firsts = opens ? firsts | bit : firsts & ~bit;
       lasts = last ? lasts | bit : lasts & ~bit;
-      if (opens) copy_q<D, N, true>(p, c, sQ + (seg & 1) * C::kQBytes, ptid);
-      if (last) ++seg;
-      opens = last;
-      cn = c;
-      if (i + 1 < s.blocks) {  // the next block's slots
-        cn.advance(p, req);
-        load_slots(p, cn, rb, kStep, next);
+      if (i + 1 < s.blocks) {
+        c.advance(p, req);
+        load_slots(p, c, rb, kStep, next);
+      }
+      if (opens) {
+        if (seg >= 2 && !warp_wait(&m->q_empty[seg & 1], ((seg >> 1) - 1) & 1, m, p)) return false;
+        copy_q<D, N, true>(p, now, sQ + (seg & 1) * C::kQBytes, ptid);
       }
     }
+    if (round > 0 && !warp_wait(kv ? &m->v_done[st] : &m->k_done[st], (round - 1) & 1, m, p)) return false;
     const uint8_t* pool = static_cast<const uint8_t*>(kv ? p.pool_v : p.pool_k);
     const uint32_t dst = sKV + (kv ? C::kK + st : st) * C::kTileBytes + raw;
 #pragma unroll
@@ -548,25 +552,19 @@ SGL_DEV void produce_fp8(const Params& p, const Start& s, Misc* m, uint32_t sQ, 
       const int row = rb + kStep * r;
       if (row >= BN) break;
       const bool valid = slot[r] >= 0;
-      cp_async_16(dst + row * 128, pool + ((int64_t)(valid ? slot[r] : 0) * p.Hkv + c.kvh) * D + rc * 16,
+      cp_async_16(dst + row * 128, pool + ((int64_t)(valid ? slot[r] : 0) * p.Hkv + now.kvh) * D + rc * 16,
                   valid ? 16u : 0u);
     }
-    cp_async_commit();
     if (kv) {
-      c = cn;
+      opens = last;
+      if (last) ++seg, now = Unit(c);
 #pragma unroll
       for (int r = 0; r < kRows; ++r) slot[r] = next[r];
     }
-    ++copied;
+    return true;
   };
-  auto widen = [&]() {
-    const int t = widened, i = t >> 1, kv = t & 1, st = i % (kv ? C::kV : C::kK);
-    switch (copied - widened) {  // the thread's copies of tile t have landed
-      case 1: cp_async_wait<0>(); break;
-      case 2: cp_async_wait<1>(); break;
-      case 3: cp_async_wait<2>(); break;
-      default: cp_async_wait<3>(); break;
-    }
+  auto widen = [&](int i, int kv) {
+    const int st = i % (kv ? C::kV : C::kK);
     const uint32_t tile = sKV + (kv ? C::kK + st : st) * C::kTileBytes;
     uint4 w[kRows];
 #pragma unroll
@@ -603,17 +601,14 @@ SGL_DEV void produce_fp8(const Params& p, const Start& s, Misc* m, uint32_t sQ, 
       mbar_arrive(full);
     }
     mbar_arrive(full);
-    ++widened;
   };
-  while (widened < tiles) {
-    if (copied < tiles && copied - widened < kAhead && free()) {
-      copy();
-    } else if (copied > widened) {
-      widen();
-    } else {
-      const int round = round_of(copied);
-      if (round > 0 && !warp_wait(slot_bar(copied), (round - 1) & 1, m, p)) return;
-      if (!(copied & 1) && opens && seg >= 2 && !warp_wait(&m->q_empty[seg & 1], ((seg >> 1) - 1) & 1, m, p)) return;
+  const int tiles = 2 * s.blocks;
+  for (int t = 0; t < tiles + kLag; ++t) {
+    if (t < tiles && !copy(t >> 1, t & 1)) return;
+    cp_async_commit();  // one group a tile (an empty one past the last)
+    if (t >= kLag) {
+      cp_async_wait<kLag>();  // the thread's copies of tile t - kLag have landed
+      widen((t - kLag) >> 1, (t - kLag) & 1);
     }
   }
 }
@@ -1023,23 +1018,22 @@ __global__ void __launch_bounds__(Cfg<D, N, kFp8>::kThreads, 1) verify_kernel(co
   const Start s = m->start;
   const uint32_t tmem = m->tmem_base;
   if (blockIdx.x == 0 && tid == 0) p.status[1] = s.tokens;
-  if constexpr (C::kSplitRegs) {
-    // every warp of a warpgroup together
-    static_assert(C::kProdWarp % 4 == 0 && (C::kMmaWarp + 1) % 4 == 0, "whole warpgroups");
-    if (warp < C::kSoftWarps) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
-    else if (warp < C::kProdWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kEpiRegs));
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kProdRegs));
-  }
-  if (s.blocks > 0) {
-    if (warp < C::kSoftWarps) {
-      softmax<D, N, kFp8>(p, s, m, tmem, smem_u32(sP));
-    } else if (warp < C::kProdWarp) {
-      epilogue<D, N, kFp8>(p, s, m, tmem, tid - 32 * C::kSoftWarps);
-    } else if (warp < C::kMmaWarp) {
+  // Registers move between whole warpgroups, inside the roles' branches: the
+  // compiler gives all code behind a change the smallest share that reaches it.
+  static_assert(C::kProdWarp % 4 == 0 && (C::kMmaWarp + 1) % 4 == 0, "whole warpgroups");
+  if (warp < C::kSoftWarps) {
+    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
+    if (s.blocks > 0) softmax<D, N, kFp8>(p, s, m, tmem, smem_u32(sP));
+  } else if (warp < C::kProdWarp) {
+    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kEpiRegs));
+    if (s.blocks > 0) epilogue<D, N, kFp8>(p, s, m, tmem, tid - 32 * C::kSoftWarps);
+  } else {
+    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kProdRegs));
+    if (s.blocks > 0 && warp < C::kMmaWarp) {
       const int ptid = tid - 32 * C::kProdWarp;
       if constexpr (kFp8) produce_fp8<D, N>(p, s, m, smem_u32(sQ), smem_u32(sKV), ptid);
       else produce<D, N>(p, s, m, smem_u32(sQ), smem_u32(sKV), ptid);
-    } else if ((tid & 31) == 0) {
+    } else if (s.blocks > 0 && (tid & 31) == 0) {
       issue<D, N, kFp8>(p, s, m, tmem, smem_u32(sQ), smem_u32(sP), smem_u32(sKV));
       // MMAs issued before a wait gave up end before the CTA does
       umma_commit(&m->drain);
