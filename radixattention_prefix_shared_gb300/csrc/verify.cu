@@ -224,7 +224,6 @@ struct Cursor {
       lens(p, n_, pre, row_);
     }
   }
-  SGL_DEV bool last_of_unit() const { return b + 1 == nb; }
   // the first block of the next unit (there is one: the caller counts blocks)
   SGL_DEV void next_unit(const Params& p, Requests& q) {
     b = 0;
@@ -390,23 +389,17 @@ constexpr uint32_t idesc(bool mn_major) {
 
 // ----------------------------------------------------------------- producers
 
-// What is left of a unit when the cursor has gone on.
-struct Unit {
-  int32_t kvh, tile, off, n;
-  SGL_DEV explicit Unit(const Cursor& c) : kvh(c.kvh), tile(c.tile), off(c.off), n(c.n) {}
-};
-
 // A unit's query rows into its Q tile: a request's rows are (token, head of the KV
 // head's group), tile t holds rows t N .. t N + N - 1.
 template <int D, int N, bool kFp8>
-SGL_DEV void copy_q(const Params& p, const Unit& c, uint32_t sQ, int ptid) {
+SGL_DEV void copy_q(const Params& p, const Segment& g, uint32_t sQ, int ptid) {
   using C = Cfg<D, N, kFp8>;
   const int ci = ptid & 7;
+  const int64_t row0 = (int64_t)(g.off + g.t0) * p.Hq + (int64_t)g.kvh * p.g;
   for (int row = ptid >> 3; row < N; row += C::kProdThreads / 8) {
-    const int r = c.tile * N + row, tok = r / p.g;
-    const bool valid = tok < c.n && c.off + tok < p.total;
-    const int64_t qrow = valid ? (int64_t)(c.off + tok) * p.Hq + (int64_t)c.kvh * p.g + r % p.g : 0;
-    const __nv_bfloat16* src = p.q + qrow * D + ci * 8;
+    const bool valid = row < g.live;
+    const int r = g.h0 + row;
+    const __nv_bfloat16* src = p.q + (valid ? (row0 + (int64_t)(r / p.g) * p.Hq + r % p.g) * D : 0) + ci * 8;
 #pragma unroll
     for (int h = 0; h < C::kChunks; ++h)
       cp_async_16(sQ + h * C::kQChunkBytes + sw128(row, ci), src + 64 * h, valid ? 16u : 0u);
@@ -446,6 +439,22 @@ SGL_DEV void load_slots(const Params& p, const Cursor& c, int first, int step, i
     asm volatile("prefetch.global.L2 [%0];" ::"l"(t + ahead));
 }
 
+// Where the producers are in the segments (every thread for itself).
+struct Place {
+  int seg = -1, left = 0;
+  bool opens;
+  SGL_DEV bool step(Misc* m, const Params& p) {
+    opens = left == 0;
+    if (opens) {
+      ++seg;
+      if (!warp_wait(&m->u_full[seg & 1], (seg >> 1) & 1, m, p)) return false;
+      left = m->seg[seg & 1].take;
+    }
+    --left;
+    return true;
+  }
+};
+
 template <int D, int N>
 SGL_DEV void produce(const Params& p, const Start& s, Misc* m, uint32_t sQ, uint32_t sKV, int ptid) {
   using C = Cfg<D, N, false>;
@@ -453,25 +462,24 @@ SGL_DEV void produce(const Params& p, const Start& s, Misc* m, uint32_t sQ, uint
   const int ci = ptid & 7, rb = ptid >> 3;
   Requests req(p, s);
   Cursor c(p, s, req);  // one block ahead: its slots are on their way
-  Unit now(c);
   int32_t slot[kRows], next[kRows];
   load_slots(p, c, rb, kStep, slot);
-  int seg = 0;
-  bool opens = true;
+  Place at;
   auto query = [&]() {
-    const int qb = seg % C::kQBufs, round = seg / C::kQBufs;
+    const int qb = at.seg % C::kQBufs, round = at.seg / C::kQBufs;
     if (round > 0 && !warp_wait(&m->q_empty[qb], (round - 1) & 1, m, p)) return false;
-    copy_q<D, N, false>(p, now, sQ + qb * C::kQBytes, ptid);
+    copy_q<D, N, false>(p, m->seg[at.seg & 1], sQ + qb * C::kQBytes, ptid);
     cp_async_mbar_arrive(&m->q_full[qb]);
     return true;
   };
   for (int i = 0; i < s.blocks; ++i) {
-    const bool last = c.last_of_unit() || i + 1 == s.blocks;
+    if (!at.step(m, p)) return;
+    const int32_t kvh = m->seg[at.seg & 1].kvh;
     if (i + 1 < s.blocks) {
       c.advance(p, req);
       load_slots(p, c, rb, kStep, next);
     }
-    if (opens && C::kQBufs == 2 && !query()) return;
+    if (at.opens && C::kQBufs == 2 && !query()) return;
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
       const int ring = kv ? C::kV : C::kK, st = i % ring, round = i / ring;
@@ -485,22 +493,20 @@ SGL_DEV void produce(const Params& p, const Start& s, Misc* m, uint32_t sQ, uint
         const int row = rb + kStep * r;
         if (row >= BN) break;
         const bool valid = slot[r] >= 0;
-        const __nv_bfloat16* src = pool + ((int64_t)(valid ? slot[r] : 0) * p.Hkv + now.kvh) * D + ci * 8;
+        const __nv_bfloat16* src = pool + ((int64_t)(valid ? slot[r] : 0) * p.Hkv + kvh) * D + ci * 8;
 #pragma unroll
         for (int h = 0; h < C::kChunks; ++h)
           cp_async_16(dst + h * C::kChunkBytes + sw128(row, ci), src + 64 * h, valid ? 16u : 0u);
       }
       cp_async_mbar_arrive(&full[st]);
       if (kv == 0 && ptid == 0) {
-        m->k_last[st] = last;
+        m->k_last[st] = at.left == 0;
         mbar_arrive(&full[st]);
       }
     }
     // one Q tile alone: the next unit's waits for the last scores of this one,
     // and its first keys go ahead of it
-    if (opens && C::kQBufs == 1 && !query()) return;
-    opens = last;
-    if (last) ++seg, now = Unit(c);
+    if (at.opens && C::kQBufs == 1 && !query()) return;
 #pragma unroll
     for (int r = 0; r < kRows; ++r) slot[r] = next[r];
   }
@@ -522,26 +528,28 @@ SGL_DEV void produce_fp8(const Params& p, const Start& s, Misc* m, uint32_t sQ, 
   const int raw = (D == 128 ? C::kChunkBytes : 64) + rc * 16;  // the thread's codes in a row's place
   Requests req(p, s);
   Cursor c(p, s, req);  // one block ahead of the copies
-  Unit now(c);
   int32_t slot[kRows], next[kRows];
   load_slots(p, c, rb, kStep, slot);
-  int seg = 0, seg_w = 0;
-  bool opens = true, last = false;
+  Place at;
+  int seg_w = 0;
+  int32_t kvh = 0;
   uint32_t firsts = 0, lasts = 0;  // bit b % 32: block b is its segment's first, last
   auto copy = [&](int i, int kv) {
     const int ring = kv ? C::kV : C::kK, st = i % ring, round = i / ring;
     if (!kv) {
-      last = c.last_of_unit() || i + 1 == s.blocks;
+      if (!at.step(m, p)) return false;
       const uint32_t bit = 1u << (i & 31);
-      firsts = opens ? firsts | bit : firsts & ~bit;
-      lasts = last ? lasts | bit : lasts & ~bit;
+      firsts = at.opens ? firsts | bit : firsts & ~bit;
+      lasts = at.left == 0 ? lasts | bit : lasts & ~bit;
       if (i + 1 < s.blocks) {
         c.advance(p, req);
         load_slots(p, c, rb, kStep, next);
       }
-      if (opens) {
+      if (at.opens) {
+        const int seg = at.seg;
+        kvh = m->seg[seg & 1].kvh;
         if (seg >= 2 && !warp_wait(&m->q_empty[seg & 1], ((seg >> 1) - 1) & 1, m, p)) return false;
-        copy_q<D, N, true>(p, now, sQ + (seg & 1) * C::kQBytes, ptid);
+        copy_q<D, N, true>(p, m->seg[seg & 1], sQ + (seg & 1) * C::kQBytes, ptid);
       }
     }
     if (round > 0 && !warp_wait(kv ? &m->v_done[st] : &m->k_done[st], (round - 1) & 1, m, p)) return false;
@@ -552,12 +560,10 @@ SGL_DEV void produce_fp8(const Params& p, const Start& s, Misc* m, uint32_t sQ, 
       const int row = rb + kStep * r;
       if (row >= BN) break;
       const bool valid = slot[r] >= 0;
-      cp_async_16(dst + row * 128, pool + ((int64_t)(valid ? slot[r] : 0) * p.Hkv + now.kvh) * D + rc * 16,
+      cp_async_16(dst + row * 128, pool + ((int64_t)(valid ? slot[r] : 0) * p.Hkv + kvh) * D + rc * 16,
                   valid ? 16u : 0u);
     }
     if (kv) {
-      opens = last;
-      if (last) ++seg, now = Unit(c);
 #pragma unroll
       for (int r = 0; r < kRows; ++r) slot[r] = next[r];
     }
@@ -588,8 +594,13 @@ SGL_DEV void produce_fp8(const Params& p, const Start& s, Misc* m, uint32_t sQ, 
         o[2 * j] = *reinterpret_cast<const uint32_t*>(&a);
         o[2 * j + 1] = *reinterpret_cast<const uint32_t*>(&b);
       }
-      st_shared_v4(dst + sw128(row, piece), o[0], o[1], o[2], o[3]);
-      st_shared_v4(dst + sw128(row, piece + 1), o[4], o[5], o[6], o[7]);
+      // (a row's two halves lie 16 KB apart, on the same banks: their threads store
+      // their pieces in opposite order)
+      const int swap = rc >> 2;
+      st_shared_v4(dst + sw128(row, piece + swap), swap ? o[4] : o[0], swap ? o[5] : o[1], swap ? o[6] : o[2],
+                   swap ? o[7] : o[3]);
+      st_shared_v4(dst + sw128(row, piece + 1 - swap), swap ? o[0] : o[4], swap ? o[1] : o[5], swap ? o[2] : o[6],
+                   swap ? o[3] : o[7]);
     }
     const bool first = !kv && (firsts >> (i & 31) & 1);
     if (first) widen_q<D, N>(sQ + (seg_w & 1) * C::kQBytes, ptid);
