@@ -12,19 +12,23 @@
 //
 // Work: a cluster of CTAs a request, the vocabulary dealt out in contiguous spans
 // to the CTAs and their warps.  All weights that the walk can ask for are gathered
-// at once (one dependent load after the tokens); every CTA then walks by itself
-// and they meet only for sums over a row: one a second child that is asked (with
-// draft rows), one at the end.  R is never stored: a pass recomputes it from the
-// target and the draft row.  The CTA and the warp in whose span the drawn token
-// lies read that span once more.
+// at once (one dependent load after the tokens); each CTA's first warp then walks,
+// nodes in its lanes, and the cluster meets only for sums over a row: one a second
+// child that is asked (with draft rows), one at the end.  R is never stored: a pass
+// recomputes it from the target and the draft row.  The warp in whose span the
+// drawn token lies reads that span once more.
 //
-// Bound: HBM (one row, two with draft rows) for large batches, a chain of some
-// six dependent loads and two cluster barriers for small ones.
+// Bound: HBM (one row, two with draft rows) for large batches, a chain of five
+// dependent loads and a cluster barrier for small ones.
 //
-// Sums: up to 256 values are added in fp32 (a weight's own rounding included,
-// some 2^-22 of the sum), all else in fp64, whose adds this part makes at 1 / 64 of
-// the fp32 rate.
+// Sums: most of a vocabulary's weights are some 1e-8 of the sum, so an error of that
+// size moves the drawn token; but this part makes fp64 sums at 1 / 64 of the fp32
+// rate.  Values of R and their sums are held as two fp32 numbers (the second what
+// the first has lost), some 45 bits, up to a warp's sum, and in fp64 from there on, in
+// one warp of a CTA (all eight of them: 20 us of 82, 64 chains over 131,072 tokens).
 #include <cooperative_groups.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "launch.h"
@@ -34,12 +38,16 @@ namespace cg = cooperative_groups;
 namespace sgl {
 namespace {
 
-constexpr int kWarps = 16;
+constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxCluster = 8;
+// 16-byte vectors of a row that a lane holds at a time (8: the unrolled arithmetic
+// outgrows the instruction cache, 75 us against 27 on 64 chains over 131,072 tokens)
+constexpr int kVecs = 4;
 
+// A row as 16-byte vectors: vector k is values 4 k - shift .. + 3.
 struct Row {
-  const float* p;  // aligned to 16 bytes, `shift` values before the row
+  const float* p;
   int shift;
 };
 SGL_DEV Row row_at(const float* base, int64_t stride, int64_t r) {
@@ -47,20 +55,8 @@ SGL_DEV Row row_at(const float* base, int64_t stride, int64_t r) {
   const int shift = (int)((reinterpret_cast<uintptr_t>(p) >> 2) & 3);
   return Row{p - shift, shift};
 }
-// Values 4 k - shift .. + 3 of a row of V (those outside it are 0).
-SGL_DEV float4 load4(const Row& r, int k, int V) {
-  const int at = 4 * k - r.shift;
-  if (at >= 0 && at + 3 < V) return __ldg(reinterpret_cast<const float4*>(r.p) + k);
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (at >= 0 && at < V) v.x = __ldg(r.p + 4 * k);
-  if (at + 1 >= 0 && at + 1 < V) v.y = __ldg(r.p + 4 * k + 1);
-  if (at + 2 >= 0 && at + 2 < V) v.z = __ldg(r.p + 4 * k + 2);
-  if (at + 3 >= 0 && at + 3 < V) v.w = __ldg(r.p + 4 * k + 3);
-  return v;
-}
-// The same values of a row that lies otherwise against 16 bytes (`shift` of the
-// first row's).
-SGL_DEV float4 load4_at(const float* row, int at, int V) {
+// Values at .. at + 3 of a row, one by one; 0 outside it.
+__device__ __noinline__ float4 load_each(const float* row, int at, int V) {
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   if (at >= 0 && at < V) v.x = __ldg(row + at);
   if (at + 1 >= 0 && at + 1 < V) v.y = __ldg(row + at + 1);
@@ -70,53 +66,88 @@ SGL_DEV float4 load4_at(const float* row, int at, int V) {
 }
 
 // What is not a positive finite weight counts as none.
-SGL_DEV float weight(float x) { return x > 0.f && x <= 3.402823466e38f ? x : 0.f; }
+SGL_DEV float weight(float x) {
+  x = fmaxf(x, 0.f);  // NaN, too
+  return x <= 3.402823466e38f ? x : 0.f;
+}
+SGL_DEV float4 weight4(const float4& v) { return make_float4(weight(v.x), weight(v.y), weight(v.z), weight(v.w)); }
+
+// h + l, l what h has lost.  (No contraction or reordering: the sums are exact.)
+struct Pair {
+  float h = 0.f, l = 0.f;
+  SGL_DEV void add(float h2, float l2) {
+    const float s = __fadd_rn(h, h2), b = __fsub_rn(s, h);
+    const float e = __fadd_rn(__fsub_rn(h, __fsub_rn(s, b)), __fsub_rn(h2, b));
+    h = s, l = __fadd_rn(l, __fadd_rn(e, l2));
+  }
+  SGL_DEV void tidy() {  // |l| below a step of h again
+    const float s = __fadd_rn(h, l);
+    l = __fsub_rn(l, __fsub_rn(s, h)), h = s;
+  }
+  SGL_DEV double value() const { return (double)h + (double)l; }
+};
+SGL_DEV Pair warp_total(Pair p) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    p.tidy();
+    p.add(__shfl_xor_sync(0xffffffffu, p.h, o), __shfl_xor_sync(0xffffffffu, p.l, o));
+  }
+  return p;
+}
+
+SGL_DEV int pick(const int (&x)[2], int i) {
+  const int a = __shfl_sync(0xffffffffu, x[0], i & 31), b = __shfl_sync(0xffffffffu, x[1], i & 31);
+  return i < 32 ? a : b;
+}
+SGL_DEV float pick(const float (&x)[2], int i) {
+  const float a = __shfl_sync(0xffffffffu, x[0], i & 31), b = __shfl_sync(0xffffffffu, x[1], i & 31);
+  return i < 32 ? a : b;
+}
+SGL_DEV double pick(const double (&x)[2], int i) {
+  const double a = __shfl_sync(0xffffffffu, x[0], i & 31), b = __shfl_sync(0xffffffffu, x[1], i & 31);
+  return i < 32 ? a : b;
+}
+// Bit i: node i (lane i % 32's) has it.
+SGL_DEV uint64_t nodes(bool lo, bool hi) {
+  return (uint64_t)__ballot_sync(0xffffffffu, hi) << 32 | __ballot_sync(0xffffffffu, lo);
+}
 
 struct Shared {
-  int parent[kMaxDraft], token[kMaxDraft];
-  float coin[kMaxDraft];
-  float px[kMaxDraft], qx[kMaxDraft];  // target and draft weight of a node's token at its parent
-  double mass[kMaxDraft + 1];          // m after j rejections at the node
-  int gone[kMaxDraft];                 // tokens rejected there (without draft rows)
-  int path[kMaxDraft];
-  int at, next, rejected, accepted, asks;  // asks: the walk stands before a sum
-  int part[kWarps];
+  // what the warps go by in a pass: the node, its rejections, which nodes those were
+  int at, rej, more;  // more: another pass follows this one
+  uint64_t gone;
+  int token[kMaxDraft];
+  float inv_h[kMaxDraft], inv_l[kMaxDraft];  // 1 / m after j rejections, j >= 1
   double warp_sum[kWarps];
   double cta_sum[2][kMaxCluster];  // by pass parity: the cluster's CTAs write here
+  // where the drawn token lies: the warp (below 0: not in this CTA), what lies before
+  int found, past;
+  double cum, bound;
 };
 
-// Four values of R at vector k of a row.
-template <bool kDraft>
-SGL_DEV float4 residual4(const Row& t, const Row& d, bool same, const float* drow, int k, int V, int rej, float inv1,
-                         const Shared* s) {
-  float4 v = load4(t, k, V);
-  v = make_float4(weight(v.x), weight(v.y), weight(v.z), weight(v.w));
-  if (rej == 0) return v;
-  if constexpr (kDraft) {
-    float4 q = same ? load4(d, k, V) : load4_at(drow, 4 * k - t.shift, V);
-    q = make_float4(weight(q.x), weight(q.y), weight(q.z), weight(q.w));
-    v = make_float4(fmaxf(v.x - q.x, 0.f), fmaxf(v.y - q.y, 0.f), fmaxf(v.z - q.z, 0.f), fmaxf(v.w - q.w, 0.f));
-    for (int j = 1; j < rej; ++j) {
-      const float inv = j == 1 ? inv1 : (float)(1.0 / s->mass[j]);
-      v = make_float4(fmaxf(fmaf(v.x, inv, -q.x), 0.f), fmaxf(fmaf(v.y, inv, -q.y), 0.f),
-                      fmaxf(fmaf(v.z, inv, -q.z), 0.f), fmaxf(fmaf(v.w, inv, -q.w), 0.f));
-    }
-  } else {
-    const int at = 4 * k - t.shift;
-    for (int j = 0; j < rej; ++j) {
-      const int g = s->gone[j] - at;
-      if (g == 0) v.x = 0.f;
-      if (g == 1) v.y = 0.f;
-      if (g == 2) v.z = 0.f;
-      if (g == 3) v.w = 0.f;
-    }
+// Of `count` sums in the first lanes: the first whose inclusive sum from `cum` on
+// passes the bound (cum becomes what lies before it), else (past) the last one
+// above 0.
+SGL_DEV int find(double x, int count, double* cum, double bound, bool* past) {
+  const int lane = threadIdx.x & 31;
+  double incl = lane < count ? x : 0.0;
+#pragma unroll
+  for (int o = 1; o < kMaxCluster; o <<= 1) {
+    const double y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
   }
-  return v;
+  const uint32_t some = __ballot_sync(0xffffffffu, lane < count && x > 0.0);
+  const uint32_t hits = *past ? 0u : __ballot_sync(0xffffffffu, lane < count && x > 0.0 && *cum + incl > bound);
+  if (hits == 0) *past = true;
+  const int at = hits != 0 ? __ffs(hits) - 1 : 31 - __clz(some);
+  *cum += __shfl_sync(0xffffffffu, incl - x, at & 31);
+  return at;
 }
+static_assert(kWarps <= kMaxCluster, "find() scans that many");
 
 // One CTA of a request's cluster.  kDraft: drafts were drawn from draft_probs.
 template <bool kDraft>
-__global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const DraftArgs a, int cluster) {
+__global__ void __launch_bounds__(kThreads, kDraft ? 2 : 3) verify_drafts_kernel(const DraftArgs a, int cluster) {
   __shared__ Shared s;
   cg::cluster_group cl = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -124,231 +155,293 @@ __global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const DraftArgs
   const int V = a.vocab;
 
   // where the request's nodes start
-  int64_t before = 0;
-  for (int i = tid; i < r; i += kThreads) before += max(0, min(__ldg(a.draft_lens + i), a.max_draft));
+  int64_t off = 0;
+#pragma unroll 4
+  for (int i = lane; i < r; i += 32) off += max(0, min(__ldg(a.draft_lens + i), a.max_draft));
   int n = max(0, min(__ldg(a.draft_lens + r), a.max_draft));
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-  if (lane == 0) s.part[warp] = (int)min(before, (int64_t)a.total_draft);
-  __syncthreads();
-  int64_t off = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) off += s.part[w];
+  for (int o = 16; o > 0; o >>= 1) off += __shfl_xor_sync(0xffffffffu, off, o);
   n = (int)max((int64_t)0, min((int64_t)n, a.total_draft - off));
+  const bool first = rank == 0 && warp == 0;
+  int32_t* path = a.accepted + (int64_t)r * a.max_draft;
   if (n == 0) {  // padding
-    if (rank == 0) {
-      for (int k = tid; k < a.max_draft; k += kThreads) a.accepted[(int64_t)r * a.max_draft + k] = -1;
-      if (tid == 0) a.num_accepted[r] = 0, a.next_tokens[r] = -1;
+    if (first) {
+      for (int k = lane; k < a.max_draft; k += 32) path[k] = -1;
+      if (lane == 0) a.num_accepted[r] = 0, a.next_tokens[r] = -1;
     }
     return;  // (the whole cluster)
   }
   cl.barrier_arrive();  // waited for before the first write into another CTA's memory
-  if (tid < n) {
-    const int64_t t = off + tid;
-    int par = __ldg(a.parents + t);
-    if (tid == 0 || par < 0 || par >= tid) par = -1;
-    const int tok = __ldg(a.draft_tokens + t);
-    float px = 0.f, qx = 1.f;
-    if (par >= 0) {
-      if (tok >= 0 && tok < V) {
-        px = weight(__ldg(a.target_probs + (off + par) * a.target_stride + tok));
-        if (kDraft) qx = weight(__ldg(a.draft_probs + (off + par) * a.draft_stride + tok));
+
+  // the first warp: nodes lane and lane + 32, their parent, token, coin, weights of
+  // the token at the parent
+  int parent[2], token[2];
+  float coin[2], px[2], qx[2], final_coin = 0.f;
+  if (warp == 0) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = lane + 32 * h;
+      parent[h] = -1, token[h] = -1, coin[h] = 0.f, px[h] = 0.f, qx[h] = 1.f;
+      if (i > 0 && i < n) {
+        const int par = __ldg(a.parents + off + i);
+        token[h] = __ldg(a.draft_tokens + off + i);
+        coin[h] = __ldg(a.coins + off + i);
+        if (par >= 0 && par < i) {
+          parent[h] = par;
+          if (token[h] >= 0 && token[h] < V) {
+            px[h] = weight(__ldg(a.target_probs + (off + par) * a.target_stride + token[h]));
+            if (kDraft) qx[h] = weight(__ldg(a.draft_probs + (off + par) * a.draft_stride + token[h]));
+          }
+        }
+      }
+      s.token[i] = token[h];
+    }
+    __syncwarp();
+    final_coin = __ldg(a.final_coins + r);
+  }
+  double mass[2] = {1.0, 1.0};  // lane j % 32's: m after j rejections at the node (j >= 1, with draft rows)
+  double m = 1.0;               // after the latest
+  int at = 0, rej = 0, kept = 1, next = 0;
+  uint64_t gone = 0;  // nodes rejected there
+  if (first && lane == 0) path[0] = 0;
+
+  // The walk, from node `next` on, as far as it goes without a sum: true where it
+  // stands before one (`next` the child that asks), false at its end.  summed: that
+  // sum is m.
+  auto walk = [&](bool summed) {
+    for (;;) {
+      if (!summed) {
+        const uint64_t open = nodes(parent[0] == at, parent[1] == at) & ~((2ull << next) - 1);  // c's children behind
+        if (open == 0) return false;
+        next = __ffsll(open) - 1;
+        if (kDraft && rej > 0) return true;
+      }
+      summed = false;
+      const int i = next, x = pick(token, i);
+      double w = pick(px, i);
+      bool keep;
+      if (kDraft) {
+        const double q = pick(qx, i);
+        for (int j = 0; j < rej; ++j) w = fmax((j == 0 ? w : w / pick(mass, j)) - q, 0.0);
+        keep = w > 0.0 && (double)pick(coin, i) * q * m < w;
+      } else {
+        if ((nodes(token[0] == x, token[1] == x) & gone) != 0) w = 0.0;
+        keep = w > 0.0 && (double)pick(coin, i) * m < w;
+      }
+      if (keep) {
+        if (first && lane == 0) path[kept] = i;
+        at = i, ++kept, rej = 0, gone = 0, m = 1.0;
+      } else {
+        ++rej, gone |= 1ull << i;
+        if (!kDraft) m -= w;
       }
     }
-    s.parent[tid] = par;
-    s.token[tid] = tok;
-    s.coin[tid] = __ldg(a.coins + t);
-    s.px[tid] = px;
-    s.qx[tid] = qx;
-  }
-  if (tid == 0) s.at = 0, s.next = 1, s.rejected = 0, s.accepted = 1, s.path[0] = 0, s.mass[0] = 1.0, s.asks = 0;
-  __syncthreads();
-
-  // a cluster-wide sum of R: pass after pass into alternating slots
-  const int per = ((((V + 3 + 3) / 4 + cluster * kWarps - 1) / (cluster * kWarps)) + 31) / 32 * 32;
-  int pass = 0;
-  auto rows = [&](int node, Row* t, Row* d, const float** drow, bool* same) {
-    *t = row_at(a.target_probs, a.target_stride, off + node);
-    *d = *t;
-    *drow = nullptr;
-    *same = true;
-    if (kDraft) {
-      *drow = a.draft_probs + (off + node) * a.draft_stride;
-      *d = row_at(a.draft_probs, a.draft_stride, off + node);
-      *same = d->shift == t->shift;
-    }
   };
-  auto sum = [&](int node, int rej) {
-    Row t, d;
-    const float* drow;
-    bool same;
-    rows(node, &t, &d, &drow, &same);
-    const int K = (V + t.shift + 3) / 4, k0 = (rank * kWarps + warp) * per, k1 = min(K, k0 + per);
-    const float inv1 = rej > 1 ? (float)(1.0 / s.mass[1]) : 1.f;
-    double total = 0.0;
-    for (int kb = k0; kb < k1; kb += 8 * 32) {
-      float part = 0.f;
+
+  // spans: vectors of a row, `vecs` a lane at a time
+  const int vecs = min(kVecs, max(1, ((V + 6) / 4 + 32 * kWarps * cluster - 1) / (32 * kWarps * cluster)));
+  const int step = 32 * vecs, chunks = ((V + 6) / 4 + step - 1) / step;
+  const int per = (chunks + kWarps * cluster - 1) / (kWarps * cluster) * step;
+  const int k_begin = (rank * kWarps + warp) * per;
+  // R of node `at` after `rej` rejections (every warp's, by now): take(i, e, h, l)
+  // with value e of the lane's vector kb + 32 i + lane, i < count <= kN
+  auto residual = [&](auto most, int kb, int count, auto&& take) {
+    constexpr int kN = decltype(most)::value;
+    const Row t = row_at(a.target_probs, a.target_stride, off + at);
+    const int K = (V + t.shift + 3) / 4;
+    auto load = [&](const Row& row, float4 (&x)[kN]) {  // lies against 16 bytes as t does, or value by value
+      const bool same = row.shift == t.shift;
+      bool full[kN];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < kN; ++i) {
         const int k = kb + 32 * i + lane;
-        if (k < k1) {
-          const float4 v = residual4<kDraft>(t, d, same, drow, k, V, rej, inv1, &s);
-          part += (v.x + v.y) + (v.z + v.w);
+        full[i] = same && i < count && 4 * k >= t.shift && 4 * k - t.shift + 3 < V;
+        x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (full[i]) x[i] = __ldg(reinterpret_cast<const float4*>(row.p) + k);
+      }
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {  // a row's ends
+        const int k = kb + 32 * i + lane;
+        if (i < count && k < K && !full[i]) x[i] = load_each(row.p + row.shift, 4 * k - t.shift, V);
+      }
+    };
+    float4 v[kN];
+    if constexpr (kDraft) {
+      float4 q[kN];
+#pragma unroll
+      for (int i = 0; i < kN; ++i) q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      load(t, v);
+      if (rej > 0) load(row_at(a.draft_probs, a.draft_stride, off + at), q);
+      // the first rejection's difference is exact; each further one multiplies by
+      // 1 / m, two numbers too, and takes q off
+      auto value = [&](int i, int e, float x, float y) {
+        x = weight(x), y = weight(y);
+        Pair r;
+        if (x > y) r.h = __fsub_rn(x, y), r.l = __fsub_rn(__fsub_rn(x, r.h), y);
+#pragma unroll 1
+        for (int j = 1; j < rej; ++j) {
+          const float ih = s.inv_h[j], il = s.inv_l[j];
+          const float ph = __fmul_rn(r.h, ih);
+          const float pl = __fmaf_rn(r.l, ih, __fmaf_rn(r.h, il, __fmaf_rn(r.h, ih, -ph)));
+          r.h = ph, r.l = 0.f;
+          r.add(-y, pl);
+          r.tidy();
+          if (!(r.h > 0.f)) r.h = r.l = 0.f;
+        }
+        take(i, e, r.h, r.l);
+      };
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        value(i, 0, v[i].x, q[i].x);
+        value(i, 1, v[i].y, q[i].y);
+        value(i, 2, v[i].z, q[i].z);
+        value(i, 3, v[i].w, q[i].w);
+      }
+    } else {
+      load(t, v);
+#pragma unroll 1
+      for (uint64_t left = gone; left != 0; left &= left - 1) {
+        const int g = s.token[__ffsll(left) - 1];
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          const int e = g - (4 * (kb + 32 * i + lane) - t.shift);
+          if (e == 0) v[i].x = 0.f;
+          if (e == 1) v[i].y = 0.f;
+          if (e == 2) v[i].z = 0.f;
+          if (e == 3) v[i].w = 0.f;
         }
       }
 #pragma unroll
-      for (int o = 1; o < 8; o <<= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
-      total += (double)part;
+      for (int i = 0; i < kN; ++i) {
+        take(i, 0, weight(v[i].x), 0.f);
+        take(i, 1, weight(v[i].y), 0.f);
+        take(i, 2, weight(v[i].z), 0.f);
+        take(i, 3, weight(v[i].w), 0.f);
+      }
     }
-    total += __shfl_xor_sync(0xffffffffu, total, 8);
-    total += __shfl_xor_sync(0xffffffffu, total, 16);
-    __syncthreads();  // the last pass's warp sums have been read
-    if (lane == 0) s.warp_sum[warp] = total;
+  };
+  const std::integral_constant<int, kVecs> all_vecs;
+  const std::integral_constant<int, 1> one_vec;
+  auto end_of = [&]() { return min(k_begin + per, (V + row_at(a.target_probs, a.target_stride, off + at).shift + 3) / 4); };
+
+  // Passes over the vocabulary: the sum of R, for the walk or for the draw.
+  double total = 0.0;
+  bool drawing = false, again = false;
+  for (int pass = 0;; ++pass) {
+    if (warp == 0) {
+      if (!again) drawing = !walk(pass > 0);
+      if (lane == 0) s.at = at, s.rej = rej, s.gone = gone, s.more = !drawing;
+    }
+    __syncthreads();
+    at = s.at, rej = s.rej, gone = s.gone;
+    const bool more = s.more;
+    Pair part[4];
+    const int k_end = end_of();
+    for (int kb = k_begin; kb < k_end; kb += step)
+      residual(all_vecs, kb, vecs, [&](int, int e, float h, float l) { part[e].add(h, l); });
+#pragma unroll
+    for (int e = 1; e < 4; ++e) part[e].tidy(), part[0].add(part[e].h, part[e].l);
+    const Pair mine = warp_total(part[0]);
+    if (lane == 0) s.warp_sum[warp] = mine.value();
     __syncthreads();
     if (pass == 0) cl.barrier_wait();
-    if (tid < cluster) {
-      double mine = 0.0;
-      for (int w = 0; w < kWarps; ++w) mine += s.warp_sum[w];
-      *cl.map_shared_rank(&s.cta_sum[pass & 1][rank], tid) = mine;
+    if (warp == 0) {
+      double sum = lane < kWarps ? s.warp_sum[lane] : 0.0;
+#pragma unroll
+      for (int o = 1; o < kWarps; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane < cluster) *cl.map_shared_rank(&s.cta_sum[pass & 1][rank], lane) = sum;
     }
     cl.sync();
-    double all = 0.0;
-    for (int c = 0; c < cluster; ++c) all += s.cta_sum[pass & 1][c];
-    ++pass;
-    return all;
-  };
-
-  // the walk; every CTA takes the same steps
-  while (true) {
-    if (tid == 0) {
-      int at = s.at, i = s.next, rej = s.rejected, acc = s.accepted;
-      bool asks = s.asks != 0;
-      s.asks = 0;
-      for (; i < n; ++i) {
-        if (s.parent[i] != at) continue;
-        if (kDraft && rej > 0 && !asks) {  // the sum of R is not known yet
-          s.asks = 1;
-          break;
-        }
-        double m = 1.0, w = s.px[i], q = s.qx[i];
-        if (kDraft) {
-          for (int j = 0; j < rej; ++j) w = fmax(w / s.mass[j] - q, 0.0);
-          m = s.mass[rej];
-        } else {
-          m = s.mass[rej];
-          for (int j = 0; j < rej; ++j)
-            if (s.gone[j] == s.token[i]) w = 0.0;
-        }
-        if (w > 0.0 && (double)s.coin[i] * q * m < w) {
-          at = i, rej = 0;
-          s.path[acc++] = i;
-        } else {
-          if (!kDraft) {
-            s.gone[rej] = s.token[i];
-            s.mass[rej + 1] = s.mass[rej] - w;
+    if (warp == 0) {
+      // (in every CTA the same lanes add the same sums)
+      const double x = lane < cluster ? s.cta_sum[pass & 1][lane] : 0.0;
+      double sum = x;
+#pragma unroll
+      for (int o = 1; o < kMaxCluster; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      total = __shfl_sync(0xffffffffu, sum, 0);
+      again = false;
+      if (more) {
+        m = total;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (lane + 32 * h == rej) {
+            const double inv = m > 0.0 ? 1.0 / m : 0.0;  // (m of 0: nothing is left of R)
+            mass[h] = m, s.inv_h[rej] = (float)inv, s.inv_l[rej] = (float)(inv - (double)(float)inv);
           }
-          ++rej;
-        }
-        asks = false;
+      } else if (!(total > 0.0) && rej > 0) {  // nothing is left: draw from the row itself
+        again = true, rej = 0, gone = 0;
+      } else {
+        // where the sum passes u of the total; a bound that rounding (or a u of 1)
+        // puts past the end is the last weight's
+        int where = -1;
+        double cum = 0.0;
+        const double bound = (double)final_coin * total;
+        bool past = false;
+        if (total > 0.0 && find(x, cluster, &cum, bound, &past) == rank)
+          where = find(lane < kWarps ? s.warp_sum[lane] : 0.0, kWarps, &cum, bound, &past);
+        if (lane == 0) s.found = where, s.cum = cum, s.past = past, s.bound = bound;
       }
-      s.at = at, s.next = i, s.rejected = rej, s.accepted = acc;
+      if (lane == 0) s.more = more || again;
+      __syncwarp();
     }
     __syncthreads();
-    if (!s.asks) break;
-    const double m = sum(s.at, s.rejected);
-    __syncthreads();
-    if (tid == 0) s.mass[s.rejected] = m;
-    __syncthreads();
+    if (!s.more) break;
+    __syncthreads();  // all have read it
   }
-
-  const int at = s.at;
-  int rej = s.rejected;
-  double total = sum(at, rej);
-  if (!(total > 0.0) && rej > 0) {  // nothing is left: draw from the row itself
-    rej = 0;
-    total = sum(at, 0);
-  }
-  if (rank == 0) {
-    for (int k = tid; k < a.max_draft; k += kThreads)
-      a.accepted[(int64_t)r * a.max_draft + k] = k < s.accepted ? s.path[k] : -1;
-    if (tid == 0) {
-      a.num_accepted[r] = s.accepted;
+  if (first) {
+    for (int k = kept + lane; k < a.max_draft; k += 32) path[k] = -1;
+    if (lane == 0) {
+      a.num_accepted[r] = kept;
       if (!(total > 0.0)) a.next_tokens[r] = -1;  // a row without weights
     }
   }
-  if (!(total > 0.0)) return;
+  if (warp != s.found) return;
 
-  // the CTA, the warp and the values among which the sum passes u of the total; a
-  // bound that rounding (or a u of 1) puts past the end is the last weight's
-  const double bound = (double)__ldg(a.final_coins + r) * total;
-  const double* cta = s.cta_sum[(pass - 1) & 1];
-  double cum = 0.0;
-  int found = -1;
-  for (int c = 0; c < cluster; ++c) {
-    if (cum + cta[c] > bound) {
-      found = c;
-      break;
-    }
-    cum += cta[c];
-  }
-  bool past = false;
-  if (found < 0) {
-    past = true;
-    for (int c = 0; c < cluster; ++c)
-      if (cta[c] > 0.0) found = c;
-  }
-  if (found != rank) return;
-  int fw = -1;
-  if (!past) {
-    for (int w = 0; w < kWarps; ++w) {
-      if (cum + s.warp_sum[w] > bound) {
-        fw = w;
-        break;
-      }
-      cum += s.warp_sum[w];
-    }
-  }
-  if (fw < 0) {
-    past = true;
-    for (int w = 0; w < kWarps; ++w)
-      if (s.warp_sum[w] > 0.0) fw = w;
-  }
-  if (fw != warp) return;
-  Row t, d;
-  const float* drow;
-  bool same;
-  rows(at, &t, &d, &drow, &same);
-  const int K = (V + t.shift + 3) / 4, k0 = (rank * kWarps + warp) * per, k1 = min(K, k0 + per);
-  const float inv1 = rej > 1 ? (float)(1.0 / s.mass[1]) : 1.f;
-  int last = -1, token = -1;
-  for (int kb = k0; kb < k1 && token < 0; kb += 32) {
-    const int k = kb + lane;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (k < k1) v = residual4<kDraft>(t, d, same, drow, k, V, rej, inv1, &s);
-    const float x[4] = {v.x, v.y, v.z, v.w};
-    const double mine = ((double)x[0] + (double)x[1]) + ((double)x[2] + (double)x[3]);
-    double incl = mine;
+  // the span's vectors among which the sum passes the bound, or (past, or by a
+  // rounding apart) its last ones above 0; then the value among those
+  bool past = s.past != 0;
+  const double bound = s.bound;
+  double cum = s.cum, before = 0.0;
+  const int shift = row_at(a.target_probs, a.target_stride, off + at).shift, k_end = end_of();
+  int k_hit = -1;
+  bool found = false;
+  for (int kb = k_begin; kb < k_end && !found; kb += step) {
+    Pair part[kVecs];
+    residual(all_vecs, kb, vecs, [&](int i, int, float h, float l) { part[i].add(h, l); });
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    int top = -1, hit = -1;
-    double c = cum + (incl - mine);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      c += (double)x[j];
-      if (x[j] > 0.f) {
-        top = 4 * k - t.shift + j;
-        if (!past && hit < 0 && c > bound) hit = top;
+    for (int i = 0; i < kVecs; ++i) {
+      const double sum = warp_total(part[i]).value();
+      if (!found && sum > 0.0) {
+        k_hit = kb + 32 * i, before = cum;
+        found = !past && cum + sum > bound;
+        cum += sum;
       }
     }
-    const uint32_t hits = __ballot_sync(0xffffffffu, hit >= 0), tops = __ballot_sync(0xffffffffu, top >= 0);
-    if (hits != 0) token = __shfl_sync(0xffffffffu, hit, __ffs(hits) - 1);
-    if (tops != 0) last = __shfl_sync(0xffffffffu, top, 31 - __clz(tops));
-    cum += __shfl_sync(0xffffffffu, incl, 31);
   }
-  if (lane == 0) a.next_tokens[r] = token >= 0 ? token : last;
+  past = !found;
+  double x[4];
+  residual(one_vec, k_hit, 1, [&](int, int e, float h, float l) { x[e] = (double)h + (double)l; });
+  const double mine = (x[0] + x[1]) + (x[2] + x[3]);
+  double incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  int top = -1, hit = -1;
+  double c = before + (incl - mine);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    c += x[e];
+    if (x[e] > 0.0) {
+      top = 4 * (k_hit + lane) - shift + e;
+      if (!past && hit < 0 && c > bound) hit = top;
+    }
+  }
+  const uint32_t hits = __ballot_sync(0xffffffffu, hit >= 0), tops = __ballot_sync(0xffffffffu, top >= 0);
+  const int token_at = hits != 0 ? __shfl_sync(0xffffffffu, hit, __ffs(hits) - 1)
+                                 : __shfl_sync(0xffffffffu, top, 31 - __clz(tops));
+  if (lane == 0) a.next_tokens[r] = token_at;
 }
 
 // A warp a request: the accepted nodes' slots into its row of req_to_token, the
@@ -408,9 +501,10 @@ __global__ void __launch_bounds__(128) commit_drafts_kernel(const CommitArgs a) 
 }  // namespace
 
 sgl_status launch_verify_drafts(const DraftArgs& a, cudaStream_t stream) {
-  // the spans of a cluster's warps hold 128 values at the least
+  // CTAs enough for the part, and no more: a CTA's own latency is some 5 us.  Its
+  // warps take 128 values at the least.
   int cluster = kMaxCluster;
-  while (cluster > 1 && a.vocab < cluster * kWarps * 128) cluster /= 2;
+  while (cluster > 1 && ((int64_t)a.batch * cluster > 1024 || a.vocab < cluster * kWarps * 128)) cluster /= 2;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)cluster;
