@@ -41,9 +41,13 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxCluster = 8;
-// 16-byte vectors of a row that a lane holds at a time (8: the unrolled arithmetic
-// outgrows the instruction cache, 75 us against 27 on 64 chains over 131,072 tokens)
-constexpr int kVecs = 4;
+// 16-byte vectors of a row that a lane holds at a time (8 with draft rows: the
+// unrolled arithmetic outgrows the instruction cache)
+template <bool kDraft>
+constexpr int vecs_held() { return kDraft ? 4 : 8; }
+template <bool kDraft>
+constexpr int ctas_per_sm() { return kDraft ? 2 : 3; }
+constexpr int kParts = 16;  // of a warp's span, whose sums are kept for the draw
 
 // A row as 16-byte vectors: vector k is values 4 k - shift .. + 3.
 struct Row {
@@ -70,7 +74,6 @@ SGL_DEV float weight(float x) {
   x = fmaxf(x, 0.f);  // NaN, too
   return x <= 3.402823466e38f ? x : 0.f;
 }
-SGL_DEV float4 weight4(const float4& v) { return make_float4(weight(v.x), weight(v.y), weight(v.z), weight(v.w)); }
 
 // h + l, l what h has lost.  (No contraction or reordering: the sums are exact.)
 struct Pair {
@@ -119,6 +122,7 @@ struct Shared {
   int token[kMaxDraft];
   float inv_h[kMaxDraft], inv_l[kMaxDraft];  // 1 / m after j rejections, j >= 1
   double warp_sum[kWarps];
+  double part_sum[kWarps][kParts];  // the latest pass's, span by span
   double cta_sum[2][kMaxCluster];  // by pass parity: the cluster's CTAs write here
   // where the drawn token lies: the warp (below 0: not in this CTA), what lies before
   int found, past;
@@ -147,7 +151,8 @@ static_assert(kWarps <= kMaxCluster, "find() scans that many");
 
 // One CTA of a request's cluster.  kDraft: drafts were drawn from draft_probs.
 template <bool kDraft>
-__global__ void __launch_bounds__(kThreads, kDraft ? 2 : 3) verify_drafts_kernel(const DraftArgs a, int cluster) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm<kDraft>()) verify_drafts_kernel(const DraftArgs a, int cluster) {
+  constexpr int kVecs = vecs_held<kDraft>();
   __shared__ Shared s;
   cg::cluster_group cl = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -177,6 +182,7 @@ __global__ void __launch_bounds__(kThreads, kDraft ? 2 : 3) verify_drafts_kernel
   // the token at the parent
   int parent[2], token[2];
   float coin[2], px[2], qx[2], final_coin = 0.f;
+  uint64_t keep_first = 0;
   if (warp == 0) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -196,6 +202,9 @@ __global__ void __launch_bounds__(kThreads, kDraft ? 2 : 3) verify_drafts_kernel
       }
       s.token[i] = token[h];
     }
+    // kept if asked before any sibling (R is the target row, m is 1)
+    keep_first = nodes(px[0] > 0.f && (double)coin[0] * (double)qx[0] < (double)px[0],
+                       px[1] > 0.f && (double)coin[1] * (double)qx[1] < (double)px[1]);
     __syncwarp();
     final_coin = __ldg(a.final_coins + r);
   }
@@ -217,15 +226,19 @@ __global__ void __launch_bounds__(kThreads, kDraft ? 2 : 3) verify_drafts_kernel
         if (kDraft && rej > 0) return true;
       }
       summed = false;
-      const int i = next, x = pick(token, i);
-      double w = pick(px, i);
-      bool keep;
+      const int i = next;
+      bool keep = keep_first >> i & 1;
+      double w = 0.0;
       if (kDraft) {
-        const double q = pick(qx, i);
-        for (int j = 0; j < rej; ++j) w = fmax((j == 0 ? w : w / pick(mass, j)) - q, 0.0);
-        keep = w > 0.0 && (double)pick(coin, i) * q * m < w;
-      } else {
-        if ((nodes(token[0] == x, token[1] == x) & gone) != 0) w = 0.0;
+        if (rej > 0) {
+          const double q = pick(qx, i);
+          w = pick(px, i);
+          for (int j = 0; j < rej; ++j) w = fmax((j == 0 ? w : w / pick(mass, j)) - q, 0.0);
+          keep = w > 0.0 && (double)pick(coin, i) * q * m < w;
+        }
+      } else if (rej > 0 || !keep) {
+        const int x = pick(token, i);
+        if ((nodes(token[0] == x, token[1] == x) & gone) == 0) w = pick(px, i);
         keep = w > 0.0 && (double)pick(coin, i) * m < w;
       }
       if (keep) {
@@ -243,6 +256,7 @@ __global__ void __launch_bounds__(kThreads, kDraft ? 2 : 3) verify_drafts_kernel
   const int step = 32 * vecs, chunks = ((V + 6) / 4 + step - 1) / step;
   const int per = (chunks + kWarps * cluster - 1) / (kWarps * cluster) * step;
   const int k_begin = (rank * kWarps + warp) * per;
+  const int part_vecs = (per / step + kParts - 1) / kParts * step;  // vectors of a part
   // R of node `at` after `rej` rejections (every warp's, by now): take(i, e, h, l)
   // with value e of the lane's vector kb + 32 i + lane, i < count <= kN
   auto residual = [&](auto most, int kb, int count, auto&& take) {
@@ -335,14 +349,26 @@ __global__ void __launch_bounds__(kThreads, kDraft ? 2 : 3) verify_drafts_kernel
     __syncthreads();
     at = s.at, rej = s.rej, gone = s.gone;
     const bool more = s.more;
-    Pair part[4];
     const int k_end = end_of();
-    for (int kb = k_begin; kb < k_end; kb += step)
+    Pair mine;
+    for (int kb = k_begin, j = 0; kb < k_end; kb += step) {
+      Pair part[4];
       residual(all_vecs, kb, vecs, [&](int, int e, float h, float l) { part[e].add(h, l); });
 #pragma unroll
-    for (int e = 1; e < 4; ++e) part[e].tidy(), part[0].add(part[e].h, part[e].l);
-    const Pair mine = warp_total(part[0]);
-    if (lane == 0) s.warp_sum[warp] = mine.value();
+      for (int e = 1; e < 4; ++e) part[e].tidy(), part[0].add(part[e].h, part[e].l);
+      part[0].tidy(), mine.add(part[0].h, part[0].l);
+      if ((kb - k_begin + step) % part_vecs == 0 || kb + step >= k_end) {
+        const double sum = warp_total(mine).value();
+        if (lane == 0) s.part_sum[warp][j] = sum;
+        ++j, mine = Pair();
+      }
+    }
+    __syncwarp();
+    if (lane == 0) {
+      double sum = 0.0;
+      for (int j = 0; k_begin + j * part_vecs < k_end; ++j) sum += s.part_sum[warp][j];
+      s.warp_sum[warp] = sum;
+    }
     __syncthreads();
     if (pass == 0) cl.barrier_wait();
     if (warp == 0) {
@@ -401,11 +427,19 @@ __global__ void __launch_bounds__(kThreads, kDraft ? 2 : 3) verify_drafts_kernel
   // rounding apart) its last ones above 0; then the value among those
   bool past = s.past != 0;
   const double bound = s.bound;
-  double cum = s.cum, before = 0.0;
+  double cum = s.cum, before = cum;
   const int shift = row_at(a.target_probs, a.target_stride, off + at).shift, k_end = end_of();
   int k_hit = -1;
   bool found = false;
-  for (int kb = k_begin; kb < k_end && !found; kb += step) {
+  int k_from = k_begin;
+  for (int j = 0; k_begin + j * part_vecs < k_end; ++j) {  // the part first
+    const double sum = s.part_sum[warp][j];
+    if (sum > 0.0) k_from = k_begin + j * part_vecs, before = cum;
+    if (!past && cum + sum > bound) break;
+    cum += sum;
+  }
+  cum = before;
+  for (int kb = k_from; kb < min(k_end, k_from + part_vecs) && !found; kb += step) {
     Pair part[kVecs];
     residual(all_vecs, kb, vecs, [&](int i, int, float h, float l) { part[i].add(h, l); });
 #pragma unroll
@@ -501,10 +535,11 @@ __global__ void __launch_bounds__(128) commit_drafts_kernel(const CommitArgs a) 
 }  // namespace
 
 sgl_status launch_verify_drafts(const DraftArgs& a, cudaStream_t stream) {
-  // CTAs enough for the part, and no more: a CTA's own latency is some 5 us.  Its
-  // warps take 128 values at the least.
+  // As many CTAs as run at once: half of one's time is a chain of loads, sums and
+  // barriers that its span does not shorten.  Its warps take 128 values at the least.
+  const int at_once = num_sms() * (a.draft_probs != nullptr ? ctas_per_sm<true>() : ctas_per_sm<false>());
   int cluster = kMaxCluster;
-  while (cluster > 1 && ((int64_t)a.batch * cluster > 1024 || a.vocab < cluster * kWarps * 128)) cluster /= 2;
+  while (cluster > 1 && ((int64_t)a.batch * cluster > at_once || a.vocab < cluster * kWarps * 128)) cluster /= 2;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)cluster;
