@@ -31,6 +31,9 @@ What it computes, and where the pages fix it:
   * sliding-window decode and extend with first tokens that stay visible
     (``oracle.window``), and head norms with rotary positions
     (``oracle.rope``): the definitions the header states.
+  * a step over drafted tokens (``oracle.drafts``): attention of a tree, the
+    walk against the target's probabilities, the kept tokens' slots -- the
+    definitions the header states.
   * radix tree (``oracle.radix``): token runs with their KV slots, match
     with node splitting, insert, lock counts on the path to the root,
     leaf-first LRU eviction -- "Inside SGLang", Step 4 and the "SGLang"
@@ -51,6 +54,7 @@ from .attention import (  # noqa: F401
     merge_states,
     cascade_decode_attention,
 )
+from . import drafts  # noqa: F401
 from . import fp8  # noqa: F401
 from . import radix  # noqa: F401
 from . import rope  # noqa: F401

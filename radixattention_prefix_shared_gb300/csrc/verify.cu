@@ -110,6 +110,7 @@ struct Start {
   int32_t kvh, r, tile, off, b, blocks;  // blocks: how many the CTA takes
   int32_t first_req;                     // first request with tokens
   int32_t tokens;                        // of the batch
+  int32_t ctas;                          // that have blocks, each of them at least one
   int64_t pos, total;                    // first block, blocks of the launch
 };
 
@@ -275,8 +276,13 @@ SGL_DEV void find_start(const Params& p, Start* out) {
   if (p.shared_pass) blocks = (int64_t)((tokens * p.g + p.cols - 1) / p.cols) * ((p.shared + BN - 1) / BN);
   const int64_t total = blocks * p.Hkv;
   s.total = total;
-  s.pos = total * blockIdx.x / gridDim.x;
-  s.blocks = (int32_t)(total * (blockIdx.x + 1) / gridDim.x - s.pos);
+  // (a CTA without blocks would leave a state of an earlier call in the middle of a
+  // unit's pieces)
+  s.ctas = (int32_t)min((int64_t)gridDim.x, total);
+  if ((int)blockIdx.x < s.ctas) {
+    s.pos = total * blockIdx.x / s.ctas;
+    s.blocks = (int32_t)(total * (blockIdx.x + 1) / s.ctas - s.pos);
+  }
   if (s.blocks > 0) {
     s.kvh = (int32_t)(s.pos / blocks);
     int64_t rem = s.pos % blocks;
@@ -516,14 +522,18 @@ SGL_DEV void produce(const Params& p, const Start& s, Misc* m, uint32_t sQ, uint
 // and widened to f16 from there, by the threads of the warp that copied them, so
 // every free slot has codes on their way and no staging of its own.  Tiles (K and V
 // in turn) are copied kLag ahead of the one that is widened: as many as leave the
-// MMAs a slot of each ring besides.  (Codes held in registers instead, one block
+// MMAs slots besides.  (Codes held in registers instead, one block
 // ahead: 1,328 us on 48 requests of up to 16,000 tokens, 32 drafts, 32 heads on 8.)
 template <int D, int N>
 SGL_DEV void produce_fp8(const Params& p, const Start& s, Misc* m, uint32_t sQ, uint32_t sKV, int ptid) {
   using C = Cfg<D, N, true>;
   constexpr int kPieces = D / 16;  // 16-byte pieces of a row of codes
   constexpr int kStep = C::kProdThreads / kPieces, kRows = (BN + kStep - 1) / kStep;
-  constexpr int kLag = C::kV == 2 ? 2 : C::kV == 3 ? 3 : 5;  // at most 2 kV - 1 (a wait for a slot ends)
+  // A wait ends as long as what it waits for can be widened before: V's slot the
+  // tile 2 kV before it, and with units of one block the segment (listed once the
+  // scores of the one two before are through) and its Q tile K two blocks before.
+  constexpr int kLag = C::kV == 2 ? 2 : 3;
+  static_assert(kLag <= 2 * C::kV - 1 && kLag <= 3, "a producer waits for what it has not widened");
   const int rc = ptid % kPieces, rb = ptid / kPieces;
   const int raw = (D == 128 ? C::kChunkBytes : 64) + rc * 16;  // the thread's codes in a row's place
   Requests req(p, s);
@@ -943,7 +953,7 @@ SGL_DEV void epilogue(const Params& p, const Start& s, Misc* m, uint32_t tmem, i
         else if (!direct) p.row_ml[row] = ml;
         // (pos + i - b0 + nb - 1: the unit's last block)
         if (b0 == 0)
-          p.info[row] = make_int4(blockIdx.x, whole ? (int)blockIdx.x : owner(s.pos + i + nb - 1, s.total, gridDim.x), et, 0);
+          p.info[row] = make_int4(blockIdx.x, whole ? (int)blockIdx.x : owner(s.pos + i + nb - 1, s.total, s.ctas), et, 0);
       }
     }
     ok = warp_wait(&m->o_full[seg & 1], (seg >> 1) & 1, m, p);
