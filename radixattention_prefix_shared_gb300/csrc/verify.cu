@@ -53,12 +53,14 @@ constexpr int kMaxStages = 12;
 template <int D, int N, bool kFp8>
 struct Cfg {
   static_assert(N <= (kFp8 ? 64 : 128), "columns");
-  static constexpr int kCols = N < 32 ? N : 32;  // columns of a softmax warpgroup: a thread holds them all
+  static constexpr int kCols = N < 32 ? N : 32;  // columns of a softmax warpgroup
+  // of which a thread holds the scores of so many at a time (and the sums of all)
+  static constexpr int kHeld = N == 128 ? 16 : kCols;
   static constexpr int kWgs = N / kCols;
   // warps: softmax, epilogue (4), producers, MMA
   static constexpr int kSoftWarps = 4 * kWgs;
   static constexpr int kProdWarp = kSoftWarps + 4;
-  static constexpr int kProdWarps = kFp8 ? 11 : N == 128 ? 3 : 7;
+  static constexpr int kProdWarps = kFp8 ? 11 : 7;
   static constexpr int kProdThreads = 32 * kProdWarps;
   static constexpr int kMmaWarp = kProdWarp + kProdWarps;
   static constexpr int kThreads = 32 * (kMmaWarp + 1);
@@ -68,10 +70,10 @@ struct Cfg {
   // the copies.
   static constexpr int kWarps = kThreads / 32;
   static constexpr bool kSplitRegs = kWarps > 16;
-  static constexpr int kLaunchRegs = kWarps == 24 ? 80 : 96;
-  static constexpr int kSoftRegs = kFp8 ? (N == 64 ? 104 : 128) : (N == 128 ? 88 : 112);
+  static constexpr int kLaunchRegs = kWarps == 28 ? 72 : kWarps == 24 ? 80 : 96;
+  static constexpr int kSoftRegs = kFp8 ? (N == 64 ? 104 : 128) : (N == 128 ? 80 : 112);
   static constexpr int kEpiRegs = kFp8 && N == 64 ? 56 : 64;
-  static constexpr int kProdRegs = kFp8 ? (N == 64 ? 72 : 96) : (N == 128 ? 64 : 96);
+  static constexpr int kProdRegs = kFp8 ? (N == 64 ? 72 : 96) : (N == 128 ? 56 : 96);
   static_assert(!kSplitRegs || kWarps * kLaunchRegs >= kSoftWarps * kSoftRegs + 4 * kEpiRegs +
                                                            (kProdWarps + 1) * kProdRegs,
                 "register split within the launch's registers");
@@ -755,7 +757,7 @@ SGL_DEV uint32_t p_at(int key, int col) {
 template <int D, int N, bool kFp8>
 SGL_DEV void softmax(const Params& p, const Start& s, Misc* m, uint32_t tmem, uint32_t sP) {
   using C = Cfg<D, N, kFp8>;
-  constexpr int W = C::kCols;
+  constexpr int W = C::kCols, H = C::kHeld, kParts = W / H;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int wg = warp >> 2, q = warp & 3, key = q * 32 + lane, col0 = wg * W, wt = tid & 127;
   const uint32_t bar = 1 + wg;
@@ -782,22 +784,22 @@ SGL_DEV void softmax(const Params& p, const Start& s, Misc* m, uint32_t tmem, ui
       ok = warp_wait(&m->k_done[i % C::kK], (i / C::kK) & 1, m, p) && ok;  // S^T is there
       tc_fence_after();
       const uint32_t tS = tmem + lanes + (i % C::kSBufs) * N + col0;
-      uint32_t x[W];
-      auto load = [&]() {
-        tmem_ld<W>(tS, x);
+      uint32_t x[H];
+      auto load = [&](int part) {
+        tmem_ld<H>(tS + part * H, x);
         if (masked) {
 #pragma unroll
-          for (int e = 0; e < W; ++e)
-            if (!(bits >> e & 1)) x[e] = __float_as_uint(-INFINITY);
+          for (int e = 0; e < H; ++e)
+            if (!(bits >> (part * H + e) & 1)) x[e] = __float_as_uint(-INFINITY);
         }
       };
       // scores against their columns' references, in units of log 2
-      auto relative = [&]() {
+      auto relative = [&](int part) {
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         const float2 s2 = make_float2(sc, sc);
 #pragma unroll
-        for (int e = 0; e < W; e += 4) {
-          const float4 r = *reinterpret_cast<const float4*>(&m->mcol[col0 + e]);
+        for (int e = 0; e < H; e += 4) {
+          const float4 r = *reinterpret_cast<const float4*>(&m->mcol[col0 + part * H + e]);
           const float2 a = ffma2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), s2, make_float2(-r.x, -r.y));
           const float2 c = ffma2(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), s2, make_float2(-r.z, -r.w));
           x[e] = __float_as_uint(a.x), x[e + 1] = __float_as_uint(a.y);
@@ -811,8 +813,13 @@ SGL_DEV void softmax(const Params& p, const Start& s, Misc* m, uint32_t tmem, ui
       // keys (columns may have seen none yet) sets them block by block
       bool redo = opens || (masked && first_masked);
       if (!redo) {
-        load();
-        redo = relative() > C::kAccept;
+        float top = -INFINITY;
+#pragma unroll
+        for (int part = 0; part < kParts; ++part) {
+          load(part);
+          top = fmaxf(top, relative(part));
+        }
+        redo = top > C::kAccept;
       }
       // the warpgroup agrees: lane 0 votes to move the references, lanes 1 to 8
       // that the warp gave up waiting
@@ -822,9 +829,12 @@ SGL_DEV void softmax(const Params& p, const Start& s, Misc* m, uint32_t tmem, ui
       if (votes != 0) {
         if (wt < W) m->mxcol[col0 + wt] = ordered(-INFINITY);
         named_bar_sync(bar, 128);
-        load();
-        const float top = columns<W>(*reinterpret_cast<float(*)[W]>(&x), [](float a, float c) { return fmaxf(a, c); });
-        atomicMax(&m->mxcol[col0 + (lane & (W - 1))], ordered(top));
+#pragma unroll 1
+        for (int part = 0; part < kParts; ++part) {
+          load(part);
+          const float top = columns<H>(*reinterpret_cast<float(*)[H]>(&x), [](float a, float c) { return fmaxf(a, c); });
+          atomicMax(&m->mxcol[col0 + part * H + (lane & (H - 1))], ordered(top));
+        }
         named_bar_sync(bar, 128);
         if (wt < W) {
           const int col = col0 + wt;
@@ -838,38 +848,48 @@ SGL_DEV void softmax(const Params& p, const Start& s, Misc* m, uint32_t tmem, ui
           // O^T of the blocks before comes to the new references
           ok = warp_wait(&m->v_done[(i - 1) % C::kV], ((i - 1) / C::kV) & 1, m, p) && ok;
           tc_fence_after();
-          tmem_ld<W>(tO, x);
 #pragma unroll
-          for (int e = 0; e < W; ++e) {
-            const float a = __int_as_float(m->mxcol[col0 + e]);
-            l[e] *= a;
-            x[e] = __float_as_uint(__uint_as_float(x[e]) * a);
+          for (int part = 0; part < kParts; ++part) {
+            tmem_ld<H>(tO + part * H, x);
+#pragma unroll
+            for (int e = 0; e < H; ++e) {
+              const float a = __int_as_float(m->mxcol[col0 + part * H + e]);
+              l[part * H + e] *= a;
+              x[e] = __float_as_uint(__uint_as_float(x[e]) * a);
+            }
+            tmem_st<H>(tO + part * H, x);
           }
-          tmem_st<W>(tO, x);
           tmem_wait_st();
         }
-        load();
-        relative();
-#pragma unroll
-        for (int e = 0; e < W; ++e)  // a column that has seen no key yet
-          if (m->mcol[col0 + e] == -INFINITY) x[e] = __float_as_uint(-INFINITY);
       }
       // P^T: this key's row, 8 columns a 16-byte piece; its buffer was last read
       // with block i - 2
       if (i >= 2) ok = warp_wait(&m->v_done[(i - 2) % C::kV], ((i - 2) / C::kV) & 1, m, p) && ok;
       const uint32_t pbuf = sP + (i & 1) * C::kPBytes;
 #pragma unroll
-      for (int e = 0; e < W; e += 8) {
-        uint32_t o[4];
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          const int at = e + 2 * d;
-          const float2 w = make_float2(ex2(__uint_as_float(x[at])), ex2(__uint_as_float(x[at + 1])));
-          const float2 sum = fadd2(make_float2(l[at], l[at + 1]), w);
-          l[at] = sum.x, l[at + 1] = sum.y;
-          o[d] = kFp8 ? pack_f16x2(w.x, w.y) : pack_bf16x2(w.x, w.y);
+      for (int part = 0; part < kParts; ++part) {
+        if (kParts > 1 || votes != 0) {
+          load(part);
+          relative(part);
         }
-        st_shared_v4(pbuf + p_at<N>(key, col0 + e), o[0], o[1], o[2], o[3]);
+        if (votes != 0) {
+#pragma unroll
+          for (int e = 0; e < H; ++e)  // a column that has seen no key yet
+            if (m->mcol[col0 + part * H + e] == -INFINITY) x[e] = __float_as_uint(-INFINITY);
+        }
+#pragma unroll
+        for (int e = 0; e < H; e += 8) {
+          uint32_t o[4];
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            const int at = e + 2 * d, c = part * H + at;
+            const float2 w = make_float2(ex2(__uint_as_float(x[at])), ex2(__uint_as_float(x[at + 1])));
+            const float2 sum = fadd2(make_float2(l[c], l[c + 1]), w);
+            l[c] = sum.x, l[c + 1] = sum.y;
+            o[d] = kFp8 ? pack_f16x2(w.x, w.y) : pack_bf16x2(w.x, w.y);
+          }
+          st_shared_v4(pbuf + p_at<N>(key, col0 + part * H + e), o[0], o[1], o[2], o[3]);
+        }
       }
       fence_proxy_async_smem();
       tc_fence_before();
