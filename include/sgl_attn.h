@@ -64,14 +64,14 @@ const char* sgl_status_string(sgl_status status);
 const char* sgl_version(void);
 
 /*
- * sgl_set_device_wait_limit_ns -- limit of the on-chip waits of the extend
- * and cascade-group kernels (failure detection; the pages have no
- * counterpart).
+ * sgl_set_device_wait_limit_ns -- limit of the on-chip waits of the extend,
+ * cascade-group and drafted-token attention kernels (failure detection; the
+ * pages have no counterpart).
  *
  * Each stage barrier wait of sgl_extend_attention(_fp8),
- * sgl_extend_attention_window(_fp8), sgl_mixed_attention and the group pass of
- * sgl_cascade_decode_attention(_fp8) gives up after this much wall
- * time (default 2 s): the kernel then records a nonzero code (0x5701) in the
+ * sgl_extend_attention_window(_fp8), sgl_mixed_attention, the group pass of
+ * sgl_cascade_decode_attention(_fp8) and sgl_verify_attention(_fp8) gives up
+ * after this much wall time (default 2 s): the kernel then records a nonzero code (0x5701) in the
  * status word of its workspace, lets its own copies and tensor-core work
  * finish, frees its tensor memory and returns, leaving that call's output
  * incomplete and the device usable.  A normal call's waits last
@@ -520,8 +520,10 @@ sgl_status sgl_qk_norm_rope_store_kv_fp8(const void* q, int64_t q_stride, const 
  *     prefix_lens  : int32 [batch], >= 0;  draft_lens: int32 [batch]
  *     total_draft  : T (host value); rows of q and out behind the sum of draft_lens
  *                    are not read and stay as they were
- *     max_draft, max_prefix : host values >= the largest length; longer ones are cut.
- *                    prefix + draft_lens <= rtt_stride
+ *     max_draft, max_prefix : host values >= the largest length (a precondition, as
+ *                    prefix + draft_lens <= rtt_stride is: where one fails the
+ *                    outputs are undefined, and nothing is read or written out of
+ *                    bounds)
  *     shared_len   : the batch's rows hold the same slots at positions [0, shared_len)
  *                    (host value, <= every prefix of a request with tokens; 0: nothing
  *                    is shared).  Those keys are read once for all requests.

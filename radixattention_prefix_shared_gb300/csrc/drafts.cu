@@ -18,8 +18,11 @@
 // recomputes it from the target and the draft row.  The warp in whose span the
 // drawn token lies reads that span once more.
 //
-// Bound: HBM (one row, two with draft rows) for large batches, a chain of five
-// dependent loads and a cluster barrier for small ones.
+// Bound: by latency everywhere measured (2 to 3 CTAs an SM).  One chain of 5 over
+// 32,000 tokens 8.9 us: five dependent loads, the scans, two cluster barriers; 64
+// chains of 6 over 131,072 tokens 31 us, 2.2 TB/s of the 67 MB that the rows hold; 200
+// trees of up to 8 picked drafts 51 us, 2.1 TB/s; 24 trees of up to 24 drawn drafts over
+// 50,257 tokens 35 us, some five sums after one another.
 //
 // Sums: most of a vocabulary's weights are some 1e-8 of the sum, so an error of that
 // size moves the drawn token; but this part makes fp64 sums at 1 / 64 of the fp32
@@ -41,10 +44,11 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxCluster = 8;
-// 16-byte vectors of a row that a lane holds at a time (8 with draft rows: the
-// unrolled arithmetic outgrows the instruction cache)
-template <bool kDraft>
-constexpr int vecs_held() { return kDraft ? 4 : 8; }
+// 16-byte vectors of a row that a lane holds at a time.  8: the unrolled arithmetic
+// with draft rows outgrows the instruction cache (64 chains over 131,072 tokens 75 us
+// against 45), without them the registers (one chain over 32,000 11.3 us against 8.9).
+constexpr int kVecs = 4;
+// CTAs an SM that the registers are cut for
 template <bool kDraft>
 constexpr int ctas_per_sm() { return kDraft ? 2 : 3; }
 constexpr int kParts = 16;  // of a warp's span, whose sums are kept for the draw
@@ -152,7 +156,6 @@ static_assert(kWarps <= kMaxCluster, "find() scans that many");
 // One CTA of a request's cluster.  kDraft: drafts were drawn from draft_probs.
 template <bool kDraft>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm<kDraft>()) verify_drafts_kernel(const DraftArgs a, int cluster) {
-  constexpr int kVecs = vecs_held<kDraft>();
   __shared__ Shared s;
   cg::cluster_group cl = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
