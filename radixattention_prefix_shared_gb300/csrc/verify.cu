@@ -46,7 +46,7 @@
 // registers bound it (what spills waits behind the copies).  e4m3: 213, 224, 310 and
 // 591 us, 0.37 and less: shared memory carries each code as a copy, a load, two stores
 // of twice its size and the MMAs' reads, and 64 columns are the most.  One request of
-// 16,384 tokens, 5 drafts: 30 us, six blocks a CTA between 12 us of start and merge.
+// 16,384 tokens, 5 drafts: 25 us, six blocks a CTA between start and merge.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -1126,16 +1126,18 @@ struct Merged {
   float m = -INFINITY, l = 0.f, acc[D / 32];
 };
 
-// A row's pieces in one launch's states, 32 of them at a time.
+// A row's pieces w0, w0 + step, ... in one launch's states, 32 of them at a time.
 template <int D>
-SGL_DEV void merge(const States& st, int64_t row, const int4& at, Merged<D>* r) {
-  constexpr int E = D / 32;
+SGL_DEV void merge(const States& st, int64_t row, const int4& at, int w0, int step, Merged<D>* r) {
+  constexpr int E = D / 32, kBatch = 4;
   const int lane = threadIdx.x & 31;
   const int pieces = at.y - at.x + 1;
+  const float2* whole_ml = pieces == 1 ? st.row_ml + row : nullptr;
   auto entry = [&](int i) -> int64_t { return (int64_t)(i == 0 ? 2 * at.x + 1 : 2 * (at.x + i)) * st.n + at.z; };
-  for (int i0 = 0; i0 < pieces; i0 += 32) {
+  for (int i0 = w0; i0 < pieces; i0 += 32 * step) {
+    const int mine = i0 + lane * step;
     float2 ml = make_float2(-INFINITY, 0.f);
-    if (i0 + lane < pieces) ml = pieces == 1 ? st.row_ml[row] : st.slot_ml[entry(i0 + lane)];
+    if (mine < pieces) ml = whole_ml ? *whole_ml : st.slot_ml[entry(mine)];
     if (!(ml.y > 0.f)) ml.x = -INFINITY;
     float top = ml.x;
 #pragma unroll
@@ -1150,23 +1152,32 @@ SGL_DEV void merge(const States& st, int64_t row, const int4& at, Merged<D>* r) 
     r->l = r->l * keep + sum;
 #pragma unroll
     for (int e = 0; e < E; ++e) r->acc[e] *= keep;
-    const int count = min(32, pieces - i0);
-#pragma unroll 8
-    for (int i = 0; i < count; ++i) {
-      const float f = __shfl_sync(0xffffffffu, w, i);
-      const float* a = (pieces == 1 ? st.row_acc + row * D : st.slot_acc + entry(i0 + i) * D) + lane;
+    const int count = min(32, (pieces - i0 + step - 1) / step);
+    for (int i = 0; i < count; i += kBatch) {
+      float a[kBatch][E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) r->acc[e] = fmaf(f, a[32 * e], r->acc[e]);
+      for (int j = 0; j < kBatch; ++j) {
+        const float* p = (whole_ml ? st.row_acc + row * D : st.slot_acc + entry(i0 + (i + j) * step) * D) + lane;
+#pragma unroll
+        for (int e = 0; e < E; ++e) a[j][e] = i + j < count ? p[32 * e] : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const float f = __shfl_sync(0xffffffffu, w, (i + j) & 31);
+#pragma unroll
+        for (int e = 0; e < E; ++e) r->acc[e] = fmaf(i + j < count ? f : 0.f, a[j][e], r->acc[e]);
+      }
     }
   }
 }
 
-// A warp a (token, query head).
-template <int D>
+// A warp a (token, query head); kSplit: a block, whose warps share its pieces, for
+// calls of few rows (one request of 16,384 tokens, 19 pieces a row: 29.9 -> 24.6 us).
+template <int D, bool kSplit>
 __global__ void __launch_bounds__(128) verify_combine_kernel(const CombineParams p) {
   constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t row = kSplit ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + warp;
   grid_dep_wait();
   if (row >= p.rows || row >= (int64_t)p.status[1] * p.Hq) return;
   const int4 at = p.own.info[row];
@@ -1174,11 +1185,42 @@ __global__ void __launch_bounds__(128) verify_combine_kernel(const CombineParams
   Merged<D> r;
 #pragma unroll
   for (int e = 0; e < E; ++e) r.acc[e] = 0.f;
-  merge<D>(p.own, row, at, &r);
-  if (p.shared.info != nullptr) merge<D>(p.shared, row, p.shared.info[row], &r);
-  const float inv = p.o_scale / r.l;
+  const int w0 = kSplit ? warp : 0, step = kSplit ? 4 : 1;
+  merge<D>(p.own, row, at, w0, step, &r);
+  if (p.shared.info != nullptr) merge<D>(p.shared, row, p.shared.info[row], w0, step, &r);
+  if constexpr (kSplit) {
+    __shared__ float2 ml[4];
+    __shared__ float acc[4][D];
+    if (lane == 0) ml[warp] = make_float2(r.m, r.l);
 #pragma unroll
-  for (int e = 0; e < E; ++e) p.out[row * D + lane + 32 * e] = __float2bfloat16_rn(r.acc[e] * inv);
+    for (int e = 0; e < E; ++e) acc[warp][lane + 32 * e] = r.acc[e];
+    __syncthreads();
+    float top = ml[0].x;
+#pragma unroll
+    for (int w = 1; w < 4; ++w) top = fmaxf(top, ml[w].x);
+    float sum = 0.f, f[4];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) f[w] = ex2(ml[w].x - top), sum += f[w] * ml[w].y;
+    const float inv = p.o_scale / sum;
+    if (threadIdx.x < D) {
+      float o = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) o = fmaf(f[w], acc[w][threadIdx.x], o);
+      p.out[row * D + threadIdx.x] = __float2bfloat16_rn(o * inv);
+    }
+  } else {
+    const float inv = p.o_scale / r.l;
+#pragma unroll
+    for (int e = 0; e < E; ++e) p.out[row * D + lane + 32 * e] = __float2bfloat16_rn(r.acc[e] * inv);
+  }
+}
+
+template <int D>
+cudaError_t launch_combine(const CombineParams& cp, cudaStream_t stream) {
+  // up to 16 blocks an SM a row each
+  if (cp.rows <= (int64_t)num_sms() * 16)
+    return launch_dependent(verify_combine_kernel<D, true>, dim3((unsigned)cp.rows), dim3(128), 0, stream, cp);
+  return launch_dependent(verify_combine_kernel<D, false>, dim3((unsigned)((cp.rows + 3) / 4)), dim3(128), 0, stream, cp);
 }
 
 // ----------------------------------------------------------------- host
@@ -1322,10 +1364,7 @@ sgl_status launch_verify(const VerifyArgs& a, cudaStream_t stream) {
   cp.Hq = prm.Hq;
   cp.rows = rows;
   cp.o_scale = prm.o_scale;
-  const dim3 blocks((unsigned)((rows + 3) / 4));
-  const cudaError_t e = a.head_dim == 128
-                            ? launch_dependent(verify_combine_kernel<128>, blocks, dim3(128), 0, stream, cp)
-                            : launch_dependent(verify_combine_kernel<64>, blocks, dim3(128), 0, stream, cp);
+  const cudaError_t e = a.head_dim == 128 ? launch_combine<128>(cp, stream) : launch_combine<64>(cp, stream);
   return e == cudaSuccess ? SGL_OK : SGL_ERR_CUDA;
 }
 
