@@ -76,14 +76,16 @@ struct Cfg {
   static constexpr int kThreads = 32 * (kMmaWarp + 1);
   // Registers.  16 warps are launched with 128 a thread; with more, the softmax
   // warps take some of the others' (setmaxnreg; the shares add up to the launch's
-  // registers).  A register that does not fit costs much here: its load waits behind
-  // the copies.
+  // registers at most).  A register that does not fit costs much here: its load waits
+  // behind the copies.  The softmax needs 104, the epilogue 80 and the producers 72
+  // without one; 24 warps (e4m3, 64 columns) leave 96, 72 and 72, 28 warps (128 columns)
+  // 80, 64 and 56.
   static constexpr int kWarps = kThreads / 32;
   static constexpr bool kSplitRegs = kWarps > 16;
   static constexpr int kLaunchRegs = kWarps == 28 ? 72 : kWarps == 24 ? 80 : 96;
-  static constexpr int kSoftRegs = kFp8 ? (N == 64 ? 104 : 128) : (N == 128 ? 80 : 112);
-  static constexpr int kEpiRegs = kFp8 && N == 64 ? 56 : 64;
-  static constexpr int kProdRegs = kFp8 ? (N == 64 ? 72 : 96) : (N == 128 ? 56 : 96);
+  static constexpr int kSoftRegs = kWarps == 28 ? 80 : kWarps == 24 ? 96 : 104;
+  static constexpr int kEpiRegs = kWarps == 28 ? 64 : kWarps == 24 ? 72 : 80;
+  static constexpr int kProdRegs = kWarps == 28 ? 56 : kWarps == 24 ? 72 : 96;
   static_assert(!kSplitRegs || kWarps * kLaunchRegs >= kSoftWarps * kSoftRegs + 4 * kEpiRegs +
                                                            (kProdWarps + 1) * kProdRegs,
                 "register split within the launch's registers");
