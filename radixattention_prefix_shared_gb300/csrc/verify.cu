@@ -41,11 +41,11 @@
 //
 // What it measured (of the copy benchmark's 6.78 TB/s, 32 query heads of 128 on 8): 128
 // requests of 1,024 to 32,768 tokens, 8 drafts, 16 query heads on 8: 711 us, 6.8 TB/s,
-// 1.00.  64 requests of 4,000 tokens: 4, 8, 16 and 32 drafts (16 to 128 columns) 179, 182,
-// 218 and 325 us, 0.87 to 0.50: beyond 32 columns the softmax's and the producers'
-// registers bound it (what spills waits behind the copies).  e4m3: 213, 224, 310 and
-// 591 us, 0.37 and less: shared memory carries each code as a copy, a load, two stores
-// of twice its size and the MMAs' reads, and 64 columns are the most.  One request of
+// 1.00.  64 requests of 4,000 tokens: 4, 8, 16 and 32 drafts (16 to 128 columns) 178, 181,
+// 213 and 328 us, 0.87 to 0.49: beyond 32 columns by the softmax's instructions and, at
+// 128, its registers.  e4m3: 210, 217, 307 and 590 us, 0.37 and less: shared memory
+// carries each code as a copy, a load, stores of twice its size and the MMAs' reads, and
+// with 64 columns (the most) the ring has room for two tiles on their way.  One request of
 // 16,384 tokens, 5 drafts: 25 us, six blocks a CTA between start and merge.
 #include <cuda_fp8.h>
 
