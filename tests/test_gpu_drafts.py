@@ -172,6 +172,45 @@ def test_maxima_above_the_lengths():
     assert_attention(W.bf16_bits(case.run(max_draft=10, max_prefix=401, workspace=ws)), c)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_scale_of_the_callers_choice(fp8):
+    c = attention_case(28, Hq=4, Hkv=2, D=128, prefix=[70, 700], drafts=[6, 3], fp8=fp8)
+    case = Case(c)
+    out = W.bf16_bits(case.run(sm_scale=0.031))
+    want, _ = oracle.drafts.verify_attention(
+        c["q"], *(oracle.window.pool_reader(c["pool_" + x], c[x + "_scale"]) for x in "kv"), c["rtt"], c["rpi"],
+        c["prefix"], c["drafts"], c["parents"], 2, sm_scale=0.031)
+    # as in _drafts.py, with sum p |V| <= max |V|; scores here are below 2^4
+    bound = 2.0 ** -8 * np.abs(want) + (2.0 ** -8 + 2.0 ** -12 + 2.0 ** -12) * 6 * (1 if not fp8 else 2)
+    assert (np.abs(oracle.bf16_bits_to_f64(out) - want) <= bound).all()
+    # (another scale is another result)
+    assert np.abs(oracle.bf16_bits_to_f64(out) - oracle.bf16_bits_to_f64(W.bf16_bits(case.run()))).max() > 0.05
+
+
+def test_a_batch_of_padding_and_rows_that_end_with_their_nodes():
+    """No request has nodes: nothing is written.  A prefix and its nodes that fill a
+    row of the table to its end."""
+    c = attention_case(29, Hq=4, Hkv=2, D=64, prefix=[5, 60], drafts=[0, 0])
+    case = Case(c)
+    for shared in (0, 5):
+        out = torch.full_like(case.q, 2.0)
+        case.run(out=out, max_draft=1, shared_len=shared)
+        assert (out == 2.0).all()
+    c = attention_case(30, Hq=4, Hkv=2, D=64, prefix=[130, 60], drafts=[7, 9])
+    c["rtt"] = np.ascontiguousarray(c["rtt"][:, :137])
+    Case(c).check(max_prefix=130)
+
+
+def test_fewer_tokens_than_rows():
+    c = attention_case(31, Hq=4, Hkv=2, D=64, prefix=[30, 200], drafts=[3, 4])
+    c["q"] = np.concatenate([c["q"], c["q"][:2]])
+    c["parents"] = np.concatenate([c["parents"], c["parents"][:2]])
+    case = Case(c)
+    out = torch.full_like(case.q, 2.0)
+    case.check(out=out, total_draft=7)
+    assert (out[7:] == 2.0).all()
+
+
 def test_parents_that_are_none():
     """A parent outside [0, node) is none: the node sees the prefix and itself."""
     c = attention_case(25, Hq=2, Hkv=1, D=64, prefix=[50], drafts=[6])
