@@ -908,15 +908,15 @@ def sgl_verify_drafts(target_probs, draft_tokens, parents, draft_lens, coins, fi
                                        and (draft_probs.stride(1) == 1 or ps[1] == 1)))
           and (accepted is None or (accepted.dtype is i32 and accepted.is_contiguous()
                                     and accepted.get_device() == dev and accepted.shape == (bs[0], md))))
-    if ok:
-        for t in (num_accepted, next_tokens):
-            ok = ok and (t is None or (t.dtype is i32 and t.is_contiguous() and t.get_device() == dev
-                                       and t.shape == bs))
-    if not ok:
+    if not (ok and (num_accepted is None or (num_accepted.dtype is i32 and num_accepted.is_contiguous()
+                                             and num_accepted.get_device() == dev and num_accepted.shape == bs))
+            and (next_tokens is None or (next_tokens.dtype is i32 and next_tokens.is_contiguous()
+                                         and next_tokens.get_device() == dev and next_tokens.shape == bs))):
         _refuse_drafts(name, dict(target_probs=target_probs, draft_probs=draft_probs),
                        dict(draft_tokens=draft_tokens, parents=parents, draft_lens=draft_lens, accepted=accepted,
                             num_accepted=num_accepted, next_tokens=next_tokens))
-    _need(name, 0 < md <= 64, f"max_draft = {md}: trees of 1 to 64 nodes")
+    if not 0 < md <= 64:
+        raise ValueError(f"{name}: max_draft = {md}: trees of 1 to 64 nodes")
     if accepted is None or num_accepted is None or next_tokens is None:
         with _on(stream):
             if accepted is None:
@@ -950,18 +950,31 @@ def sgl_commit_drafts(req_to_token, req_pool_idx, prefix_lens, draft_lens, slots
     T = _torch()
     i32, dev = T.i32, T.current_device()
     ts, bs, ss, xs = req_to_token.shape, req_pool_idx.shape, slots.shape, accepted.shape
-    ok = len(ts) == 2 and len(bs) == 1 and len(ss) == 1 and len(xs) == 2 and xs[0] == bs[0]
-    for t, shape in ((req_to_token, ts), (req_pool_idx, bs), (prefix_lens, bs), (draft_lens, bs), (slots, ss),
-                     (accepted, xs), (num_accepted, bs), (seq_lens, bs), (freed, ss), (num_freed, (1,))):
-        ok = ok and (t is None or (t.dtype is i32 and t.is_contiguous() and t.get_device() == dev
-                                   and t.shape == shape))
-    if not ok:
-        _need_dense(name, i32, req_to_token=req_to_token, req_pool_idx=req_pool_idx, prefix_lens=prefix_lens,
+    if not (len(ts) == 2 and len(bs) == 1 and len(ss) == 1 and len(xs) == 2 and xs[0] == bs[0]
+            and req_to_token.dtype is i32 and req_to_token.is_contiguous() and req_to_token.get_device() == dev
+            and req_pool_idx.dtype is i32 and req_pool_idx.is_contiguous() and req_pool_idx.get_device() == dev
+            and prefix_lens.dtype is i32 and prefix_lens.is_contiguous() and prefix_lens.get_device() == dev
+            and prefix_lens.shape == bs
+            and draft_lens.dtype is i32 and draft_lens.is_contiguous() and draft_lens.get_device() == dev
+            and draft_lens.shape == bs
+            and slots.dtype is i32 and slots.is_contiguous() and slots.get_device() == dev
+            and accepted.dtype is i32 and accepted.is_contiguous() and accepted.get_device() == dev
+            and num_accepted.dtype is i32 and num_accepted.is_contiguous() and num_accepted.get_device() == dev
+            and num_accepted.shape == bs
+            and (seq_lens is None or (seq_lens.dtype is i32 and seq_lens.is_contiguous()
+                                      and seq_lens.get_device() == dev and seq_lens.shape == bs))
+            and (freed is None or (freed.dtype is i32 and freed.is_contiguous() and freed.get_device() == dev
+                                   and freed.shape == ss))
+            and (num_freed is None or (num_freed.dtype is i32 and num_freed.get_device() == dev
+                                       and num_freed.shape == (1,)))):
+        import torch
+        _need_dense(name, torch.int32, req_to_token=req_to_token, req_pool_idx=req_pool_idx, prefix_lens=prefix_lens,
                     draft_lens=draft_lens, slots=slots, accepted=accepted, num_accepted=num_accepted,
                     seq_lens=seq_lens, freed=freed, num_freed=num_freed)
         raise ValueError(f"{name}: req_to_token [rows, stride], one entry a request in req_pool_idx, prefix_lens, "
                          "draft_lens, num_accepted and seq_lens, accepted [batch, max_draft], slots and freed [T]")
-    _need(name, xs[1] <= 64, f"max_draft = {xs[1]}: trees of at most 64 nodes")
+    if xs[1] > 64:
+        raise ValueError(f"{name}: max_draft = {xs[1]}: trees of at most 64 nodes")
     if seq_lens is None or freed is None or num_freed is None:
         with _on(stream):
             if seq_lens is None:
