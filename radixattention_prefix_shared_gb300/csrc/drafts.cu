@@ -51,7 +51,7 @@ constexpr int kVecs = 4;
 // CTAs an SM that the registers are cut for
 template <bool kDraft>
 constexpr int ctas_per_sm() { return kDraft ? 2 : 3; }
-constexpr int kParts = 16;  // of a warp's span, whose sums are kept for the draw
+constexpr int kParts = 8;  // of a warp's span, whose sums are kept for the draw
 
 // A row as 16-byte vectors: vector k is values 4 k - shift .. + 3.
 struct Row {
@@ -126,7 +126,8 @@ struct Shared {
   int token[kMaxDraft];
   float inv_h[kMaxDraft], inv_l[kMaxDraft];  // 1 / m after j rejections, j >= 1
   double warp_sum[kWarps];
-  double part_sum[kWarps][kParts];  // the latest pass's, span by span
+  float2 part_sum[kWarps][kParts];  // the latest pass's, part by part of a span (a Pair each: a
+                                    // conversion to fp64 in the loop costs as much as its loads)
   double cta_sum[2][kMaxCluster];  // by pass parity: the cluster's CTAs write here
   // where the drawn token lies: the warp (below 0: not in this CTA), what lies before
   int found, past;
@@ -151,7 +152,7 @@ SGL_DEV int find(double x, int count, double* cum, double bound, bool* past) {
   *cum += __shfl_sync(0xffffffffu, incl - x, at & 31);
   return at;
 }
-static_assert(kWarps <= kMaxCluster, "find() scans that many");
+static_assert(kWarps <= kMaxCluster && kParts <= kMaxCluster, "find() scans that many");
 
 // One CTA of a request's cluster.  kDraft: drafts were drawn from draft_probs.
 template <bool kDraft>
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kDraft>()) verify_drafts
     at = s.at, rej = s.rej, gone = s.gone;
     const bool more = s.more;
     const int k_end = end_of();
-    Pair mine;
+    Pair mine, span;
     for (int kb = k_begin, j = 0; kb < k_end; kb += step) {
       Pair part[4];
       residual(all_vecs, kb, vecs, [&](int, int e, float h, float l) { part[e].add(h, l); });
@@ -361,17 +362,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kDraft>()) verify_drafts
       for (int e = 1; e < 4; ++e) part[e].tidy(), part[0].add(part[e].h, part[e].l);
       part[0].tidy(), mine.add(part[0].h, part[0].l);
       if ((kb - k_begin + step) % part_vecs == 0 || kb + step >= k_end) {
-        const double sum = warp_total(mine).value();
-        if (lane == 0) s.part_sum[warp][j] = sum;
+        const Pair sum = warp_total(mine);
+        if (lane == 0) s.part_sum[warp][j] = make_float2(sum.h, sum.l);
+        span.tidy(), span.add(sum.h, sum.l);
         ++j, mine = Pair();
       }
     }
-    __syncwarp();
-    if (lane == 0) {
-      double sum = 0.0;
-      for (int j = 0; k_begin + j * part_vecs < k_end; ++j) sum += s.part_sum[warp][j];
-      s.warp_sum[warp] = sum;
-    }
+    if (lane == 0) s.warp_sum[warp] = span.value();
     __syncthreads();
     if (pass == 0) cl.barrier_wait();
     if (warp == 0) {
@@ -434,14 +431,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kDraft>()) verify_drafts
   const int shift = row_at(a.target_probs, a.target_stride, off + at).shift, k_end = end_of();
   int k_hit = -1;
   bool found = false;
-  int k_from = k_begin;
-  for (int j = 0; k_begin + j * part_vecs < k_end; ++j) {  // the part first
-    const double sum = s.part_sum[warp][j];
-    if (sum > 0.0) k_from = k_begin + j * part_vecs, before = cum;
-    if (!past && cum + sum > bound) break;
-    cum += sum;
-  }
-  cum = before;
+  const int parts = (k_end - k_begin + part_vecs - 1) / part_vecs;
+  const float2 mine = lane < parts ? s.part_sum[warp][lane] : make_float2(0.f, 0.f);
+  const int k_from = k_begin + find((double)mine.x + (double)mine.y, parts, &cum, bound, &past) * part_vecs;
   for (int kb = k_from; kb < min(k_end, k_from + part_vecs) && !found; kb += step) {
     Pair part[kVecs];
     residual(all_vecs, kb, vecs, [&](int i, int, float h, float l) { part[i].add(h, l); });
@@ -458,15 +450,15 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kDraft>()) verify_drafts
   past = !found;
   double x[4];
   residual(one_vec, k_hit, 1, [&](int, int e, float h, float l) { x[e] = (double)h + (double)l; });
-  const double mine = (x[0] + x[1]) + (x[2] + x[3]);
-  double incl = mine;
+  const double four = (x[0] + x[1]) + (x[2] + x[3]);
+  double incl = four;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const double y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
   int top = -1, hit = -1;
-  double c = before + (incl - mine);
+  double c = before + (incl - four);
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     c += x[e];
