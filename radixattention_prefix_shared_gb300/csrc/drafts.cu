@@ -19,10 +19,11 @@
 // drawn token lies reads that span once more.
 //
 // Bound: by latency everywhere measured (2 to 3 CTAs an SM).  One chain of 5 over
-// 32,000 tokens 8.9 us: five dependent loads, the scans, two cluster barriers; 64
-// chains of 6 over 131,072 tokens 31 us, 2.2 TB/s of the 67 MB that the rows hold; 200
-// trees of up to 8 picked drafts 51 us, 2.1 TB/s; 24 trees of up to 24 drawn drafts over
-// 50,257 tokens 35 us, some five sums after one another.
+// 32,000 tokens 9.0 us: five dependent loads, the scans, two cluster barriers; 64
+// chains of 6 over 131,072 tokens 29.9 us, 2.2 TB/s of the 67 MB that the rows hold; 200
+// trees of up to 8 picked drafts 47.5 us, 2.2 TB/s (3.3 in the sums: 43 KB on their way
+// an SM); 24 trees of up to 24 drawn drafts over 50,257 tokens 34 us, some five sums
+// after one another.
 //
 // Sums: most of a vocabulary's weights are some 1e-8 of the sum, so an error of that
 // size moves the drawn token; but this part makes fp64 sums at 1 / 64 of the fp32
@@ -92,6 +93,16 @@ struct Pair {
     l = __fsub_rn(l, __fsub_rn(s, h)), h = s;
   }
   SGL_DEV double value() const { return (double)h + (double)l; }
+};
+// Two such sums side by side, in packed arithmetic (a - b as a + (-1) b: exact).
+struct Pair2 {
+  float2 h = make_float2(0.f, 0.f), l = make_float2(0.f, 0.f);
+  SGL_DEV void add(float2 x, float2 y) {
+    const float2 minus = make_float2(-1.f, -1.f);
+    const float2 s = fadd2(h, x), b = ffma2(h, minus, s);
+    const float2 e = fadd2(ffma2(ffma2(b, minus, s), minus, h), ffma2(b, minus, x));
+    h = s, l = fadd2(l, fadd2(e, y));
+  }
 };
 SGL_DEV Pair warp_total(Pair p) {
 #pragma unroll
@@ -261,8 +272,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kDraft>()) verify_drafts
   const int per = (chunks + kWarps * cluster - 1) / (kWarps * cluster) * step;
   const int k_begin = (rank * kWarps + warp) * per;
   const int part_vecs = (per / step + kParts - 1) / kParts * step;  // vectors of a part
-  // R of node `at` after `rej` rejections (every warp's, by now): take(i, e, h, l)
-  // with value e of the lane's vector kb + 32 i + lane, i < count <= kN
+  // R of node `at` after `rej` rejections (every warp's, by now): take(i, h, l) with
+  // the values of the lane's vector kb + 32 i + lane, i < count <= kN
   auto residual = [&](auto most, int kb, int count, auto&& take) {
     constexpr int kN = decltype(most)::value;
     const Row t = row_at(a.target_probs, a.target_stride, off + at);
@@ -292,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kDraft>()) verify_drafts
       if (rej > 0) load(row_at(a.draft_probs, a.draft_stride, off + at), q);
       // the first rejection's difference is exact; each further one multiplies by
       // 1 / m, two numbers too, and takes q off
-      auto value = [&](int i, int e, float x, float y) {
+      auto value = [&](float x, float y) {
         x = weight(x), y = weight(y);
         Pair r;
         if (x > y) r.h = __fsub_rn(x, y), r.l = __fsub_rn(__fsub_rn(x, r.h), y);
@@ -306,14 +317,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kDraft>()) verify_drafts
           r.tidy();
           if (!(r.h > 0.f)) r.h = r.l = 0.f;
         }
-        take(i, e, r.h, r.l);
+        return r;
       };
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
-        value(i, 0, v[i].x, q[i].x);
-        value(i, 1, v[i].y, q[i].y);
-        value(i, 2, v[i].z, q[i].z);
-        value(i, 3, v[i].w, q[i].w);
+        const Pair a0 = value(v[i].x, q[i].x), a1 = value(v[i].y, q[i].y), a2 = value(v[i].z, q[i].z),
+                   a3 = value(v[i].w, q[i].w);
+        take(i, make_float4(a0.h, a1.h, a2.h, a3.h), make_float4(a0.l, a1.l, a2.l, a3.l));
       }
     } else {
       load(t, v);
@@ -331,10 +341,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kDraft>()) verify_drafts
       }
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
-        take(i, 0, weight(v[i].x), 0.f);
-        take(i, 1, weight(v[i].y), 0.f);
-        take(i, 2, weight(v[i].z), 0.f);
-        take(i, 3, weight(v[i].w), 0.f);
+        take(i, make_float4(weight(v[i].x), weight(v[i].y), weight(v[i].z), weight(v[i].w)),
+             make_float4(0.f, 0.f, 0.f, 0.f));
       }
     }
   };
@@ -356,11 +364,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kDraft>()) verify_drafts
     const int k_end = end_of();
     Pair mine, span;
     for (int kb = k_begin, j = 0; kb < k_end; kb += step) {
-      Pair part[4];
-      residual(all_vecs, kb, vecs, [&](int, int e, float h, float l) { part[e].add(h, l); });
-#pragma unroll
-      for (int e = 1; e < 4; ++e) part[e].tidy(), part[0].add(part[e].h, part[e].l);
-      part[0].tidy(), mine.add(part[0].h, part[0].l);
+      Pair2 part[2];
+      residual(all_vecs, kb, vecs, [&](int, const float4& h, const float4& l) {
+        part[0].add(make_float2(h.x, h.y), make_float2(l.x, l.y));
+        part[1].add(make_float2(h.z, h.w), make_float2(l.z, l.w));
+      });
+      part[0].add(part[1].h, part[1].l);
+      mine.add(part[0].h.x, part[0].l.x);
+      mine.add(part[0].h.y, part[0].l.y);
       if ((kb - k_begin + step) % part_vecs == 0 || kb + step >= k_end) {
         const Pair sum = warp_total(mine);
         if (lane == 0) s.part_sum[warp][j] = make_float2(sum.h, sum.l);
@@ -436,7 +447,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kDraft>()) verify_drafts
   const int k_from = k_begin + find((double)mine.x + (double)mine.y, parts, &cum, bound, &past) * part_vecs;
   for (int kb = k_from; kb < min(k_end, k_from + part_vecs) && !found; kb += step) {
     Pair part[kVecs];
-    residual(all_vecs, kb, vecs, [&](int i, int, float h, float l) { part[i].add(h, l); });
+    residual(all_vecs, kb, vecs, [&](int i, const float4& h, const float4& l) {
+      part[i].add(h.x, l.x), part[i].add(h.y, l.y), part[i].add(h.z, l.z), part[i].add(h.w, l.w);
+    });
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       const double sum = warp_total(part[i]).value();
@@ -449,7 +462,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<kDraft>()) verify_drafts
   }
   past = !found;
   double x[4];
-  residual(one_vec, k_hit, 1, [&](int, int e, float h, float l) { x[e] = (double)h + (double)l; });
+  residual(one_vec, k_hit, 1, [&](int, const float4& h, const float4& l) {
+    x[0] = (double)h.x + (double)l.x, x[1] = (double)h.y + (double)l.y;
+    x[2] = (double)h.z + (double)l.z, x[3] = (double)h.w + (double)l.w;
+  });
   const double four = (x[0] + x[1]) + (x[2] + x[3]);
   double incl = four;
 #pragma unroll
