@@ -100,7 +100,7 @@ struct Cfg {
   static constexpr int kPChunkBytes = 128 * kPRow;
   static constexpr int kPBytes = (N + 63) / 64 * kPChunkBytes;
   static constexpr uint64_t kPLayout = N >= 64 ? 2 : N == 32 ? 4 : 6;  // 128-, 64-, 32-byte swizzle
-  static constexpr int kMiscBytes = 3072;
+  static constexpr int kMiscBytes = 3 * 1024;
   static constexpr int kFit = (227 * 1024 - kMiscBytes - kQBufs * kQBytes - 2 * kPBytes) / kTileBytes;
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
   static constexpr int kK = (kStages + 1) / 2, kV = kStages / 2;  // the K and the V ring
@@ -153,7 +153,7 @@ struct Misc {
   int32_t mxcol[128];  // its block maximum, as an ordered integer; then (as a float) its rescaling
   float lcol[2][128];  // at a segment's end: sums over the keys, references (then output factors)
 };
-static_assert(sizeof(Misc) <= 3072, "barriers and column states");
+static_assert(sizeof(Misc) <= 3 * 1024, "barriers and column states");
 
 struct Params {
   const __nv_bfloat16* q;
