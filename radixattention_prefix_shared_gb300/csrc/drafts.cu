@@ -22,7 +22,7 @@
 // 32,000 tokens 9.0 us: five dependent loads, the scans, two cluster barriers; 64
 // chains of 6 over 131,072 tokens 29.9 us, 2.2 TB/s of the 67 MB that the rows hold; 200
 // trees of up to 8 picked drafts 47.5 us, 2.2 TB/s; 24 trees of up to 24 drawn drafts over
-// 50,257 tokens 34 us, some five sums after one another.
+// 50,257 tokens 35 us, some five sums after one another.
 //
 // Sums: most of a vocabulary's weights are some 1e-8 of the sum, so an error of that
 // size moves the drawn token; but this part makes fp64 sums at 1 / 64 of the fp32
