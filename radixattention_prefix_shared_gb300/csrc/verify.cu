@@ -872,6 +872,7 @@ SGL_DEV void softmax(const Params& p, const Start& s, Misc* m, uint32_t tmem, ui
             tmem_st<H>(tO + part * H, x);
           }
           tmem_wait_st();
+          named_bar_sync(bar, 128);  // all have read the factors: the segment's end writes sums there
         }
       }
       // P^T: this key's row, 8 columns a 16-byte piece; its buffer was last read
