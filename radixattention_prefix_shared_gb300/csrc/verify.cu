@@ -1174,6 +1174,12 @@ SGL_DEV void merge(const States& st, int64_t row, const int4& at, int w0, int st
   }
 }
 
+// Whether an entry of info names slots of its launch.  Where a wait gave up, rows' entries
+// are what the workspace held before.
+SGL_DEV bool named(const int4& at, int n) {
+  return at.x >= 0 && at.x <= at.y && at.y < kMaxCtas && at.z >= 0 && at.z < n;
+}
+
 // A warp a (token, query head); kSplit: a block, whose warps share its pieces, for
 // calls of few rows (one request of 16,384 tokens, 19 pieces a row: 29.9 -> 24.6 us).
 template <int D, bool kSplit>
@@ -1184,13 +1190,15 @@ __global__ void __launch_bounds__(128) verify_combine_kernel(const CombineParams
   grid_dep_wait();
   if (row >= p.rows || row >= (int64_t)p.status[1] * p.Hq) return;
   const int4 at = p.own.info[row];
+  const int4 at_shared = p.shared.info != nullptr ? p.shared.info[row] : make_int4(0, 0, 0, 0);
+  if (!named(at, p.own.n) || (p.shared.info != nullptr && !named(at_shared, p.shared.n))) return;
   if (at.x == at.y && p.own.row_ml == nullptr) return;  // written by the CTA that had its unit whole
   Merged<D> r;
 #pragma unroll
   for (int e = 0; e < E; ++e) r.acc[e] = 0.f;
   const int w0 = kSplit ? warp : 0, step = kSplit ? 4 : 1;
   merge<D>(p.own, row, at, w0, step, &r);
-  if (p.shared.info != nullptr) merge<D>(p.shared, row, p.shared.info[row], w0, step, &r);
+  if (p.shared.info != nullptr) merge<D>(p.shared, row, at_shared, w0, step, &r);
   if constexpr (kSplit) {
     __shared__ float2 ml[4];
     __shared__ float acc[4][D];
