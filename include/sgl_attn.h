@@ -559,9 +559,10 @@ sgl_status sgl_qk_norm_rope_store_kv_fp8(const void* q, int64_t q_stride, const 
  *     accepted     : int32 [batch, max_draft]: the kept nodes, root first, then -1
  *     num_accepted : int32 [batch]: how many (>= 1)
  *     next_tokens  : int32 [batch]: -1 where the row has no positive weight
- *   A padding row gets 0 kept nodes and next token -1.  Weights that are negative,
- *   infinite or NaN count as 0.  Sums are held to some 45 bits (pairs of fp32 numbers,
- *   then fp64).
+ *   Outputs lie apart from the inputs and from one another (an overlap is
+ *   SGL_ERR_INVALID_ARG).  A padding row gets 0 kept nodes and next token -1.
+ *   Weights that are negative, infinite or NaN count as 0.  Sums are held to some 45
+ *   bits (pairs of fp32 numbers, then fp64).
  *
  * sgl_commit_drafts -- the kept nodes' slots enter the request's row, the others are
  *   given back:

@@ -910,6 +910,23 @@ bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
   return x < y + nb && y < x + na;
 }
 
+struct Span {
+  const void* p;
+  size_t n;  // bytes
+};
+// Whether what a call writes lies apart from what it reads and from one another (its
+// CTAs read and write at the same time).
+bool apart(const Span* out, int n_out, const Span* in, int n_in) {
+  const auto meet = [](const Span& a, const Span& b) { return a.n > 0 && b.n > 0 && overlaps(a.p, a.n, b.p, b.n); };
+  for (int i = 0; i < n_out; ++i) {
+    for (int j = 0; j < n_in; ++j)
+      if (meet(out[i], in[j])) return false;
+    for (int j = 0; j < i; ++j)
+      if (meet(out[i], out[j])) return false;
+  }
+  return true;
+}
+
 sgl_status qk_rope_entry(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                          int64_t v_stride, const void* q_weight, const void* k_weight, float eps,
                          const int32_t* positions, int32_t n_axes, const float* inv_freq,
@@ -1126,6 +1143,13 @@ sgl_status sgl_verify_drafts(const float* target_probs, int64_t target_stride, c
   if (max_draft < 1 || !draft_lens || !accepted || !num_accepted || !next_tokens) return SGL_ERR_INVALID_ARG;
   if (total_draft > 0 && (!target_probs || !draft_tokens || !parents || !coins || !final_coins))
     return SGL_ERR_INVALID_ARG;
+  const size_t T = (size_t)total_draft, rows = T > 0 ? T - 1 : 0, B = (size_t)batch;
+  const auto probs = [&](int64_t stride) { return T > 0 ? (rows * (size_t)stride + (size_t)vocab) * 4 : 0; };
+  const Span out[3] = {{accepted, 4 * B * (size_t)max_draft}, {num_accepted, 4 * B}, {next_tokens, 4 * B}};
+  const Span in[7] = {{target_probs, probs(target_stride)}, {draft_probs, draft_probs ? probs(draft_stride) : 0},
+                      {draft_tokens, 4 * T}, {parents, 4 * T}, {draft_lens, 4 * B}, {coins, 4 * T},
+                      {final_coins, 4 * B}};
+  if (!apart(out, 3, in, 7)) return SGL_ERR_INVALID_ARG;
   DraftArgs a;
   a.target_probs = target_probs;
   a.target_stride = target_stride;
