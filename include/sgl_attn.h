@@ -572,8 +572,11 @@ sgl_status sgl_qk_norm_rope_store_kv_fp8(const void* q, int64_t q_stride, const 
  *     *num_freed their number (entries of freed behind it stay as they were).
  *     slots        : int32 [T], the drafted tokens' slots
  *     accepted, num_accepted : as sgl_verify_drafts writes them (ascending nodes)
- *     seq_lens     : int32 [batch];  freed: int32 [T];  num_freed: int32 [1]
- *   The rows of a batch's requests differ.  Positions outside the row and nodes
+ *     seq_lens     : int32 [batch], may be prefix_lens itself;  freed: int32 [T];
+ *                    num_freed: int32 [1]
+ *   What is written (req_to_token, seq_lens, freed, num_freed) lies apart from what is
+ *   read and from one another otherwise: slots that are a part of the table, or freed
+ *   over slots, are SGL_ERR_INVALID_ARG.  The rows of a batch's requests differ.  Positions outside the row and nodes
  *   outside the request are skipped.
  */
 size_t sgl_verify_workspace_bytes(int32_t batch, int32_t total_draft, int32_t max_draft,

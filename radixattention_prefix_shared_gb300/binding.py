@@ -886,7 +886,7 @@ def sgl_verify_drafts(target_probs, draft_tokens, parents, draft_lens, coins, fi
 
     ``target_probs`` [T, vocab] (and ``draft_probs``, where drafts were drawn from
     it): the distribution after each node; rows may lie apart.  ``coins`` [T] and
-    ``final_coins`` [batch] are uniform in [0, 1)."""
+    ``final_coins`` [batch] are uniform in [0, 1).  No output may lie over an input."""
     name = "sgl_verify_drafts"
     T = _torch()
     i32, f32, dev = T.i32, T.f32, T.current_device()
@@ -945,7 +945,8 @@ def sgl_commit_drafts(req_to_token, req_pool_idx, prefix_lens, draft_lens, slots
     """The kept nodes' slots (``slots`` [T]: the drafted tokens') into the requests'
     rows of ``req_to_token``, behind their prefixes; returns the new ``seq_lens``
     [batch], the other nodes' slots (``freed`` [T], listed from the front) and their
-    number (``num_freed`` [1])."""
+    number (``num_freed`` [1]).  ``seq_lens`` may be ``prefix_lens``; no other output may
+    lie over an input, nor ``slots`` within the table."""
     name = "sgl_commit_drafts"
     T = _torch()
     i32, dev = T.i32, T.current_device()

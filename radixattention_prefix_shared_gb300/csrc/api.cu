@@ -1185,6 +1185,13 @@ sgl_status sgl_commit_drafts(int32_t* req_to_token, int32_t rtt_rows, int32_t rt
   if (max_draft < 1 || !req_to_token || !req_pool_idx || !prefix_lens || !draft_lens || !accepted ||
       !num_accepted || !seq_lens || (total_draft > 0 && (!slots || !freed)))
     return SGL_ERR_INVALID_ARG;
+  const size_t T = 4 * (size_t)total_draft, B = 4 * (size_t)batch;
+  const Span out[4] = {{req_to_token, 4 * (size_t)rtt_rows * (size_t)rtt_stride}, {seq_lens, B}, {freed, T},
+                       {num_freed, 4}};
+  // (a request's warp alone reads its prefix, before it writes the new length)
+  const Span in[6] = {{req_pool_idx, B}, {prefix_lens, seq_lens == prefix_lens ? 0 : B}, {draft_lens, B}, {slots, T},
+                      {accepted, B * (size_t)max_draft}, {num_accepted, B}};
+  if (!apart(out, 4, in, 6)) return SGL_ERR_INVALID_ARG;
   CommitArgs a;
   a.req_to_token = req_to_token;
   a.rtt_rows = rtt_rows;

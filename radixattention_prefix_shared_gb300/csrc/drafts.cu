@@ -510,11 +510,13 @@ __global__ void __launch_bounds__(128) commit_drafts_kernel(const CommitArgs a) 
   }
   const int n = max(0, min(__ldg(a.draft_lens + r), a.max_draft));
   const int count = max(0, min(__ldg(a.num_accepted + r), n));
-  const int prefix = __ldg(a.prefix_lens + r);
+  int prefix = 0;
   if (lane == 0) {
+    prefix = a.prefix_lens[r];  // (seq_lens may be the same array)
     a.seq_lens[r] = prefix + count;
     if (r == a.batch - 1) *a.num_freed = (int32_t)(free_at + n - count);
   }
+  prefix = __shfl_sync(0xffffffffu, prefix, 0);
   if (n == 0) return;  // padding: its row of the table is not looked at
   const int row = __ldg(a.req_pool_idx + r);
   uint32_t kept[2] = {0u, 0u};

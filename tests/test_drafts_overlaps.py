@@ -37,3 +37,26 @@ def test_walk(cuda_lib, out, other):
     at = _apart(sizes)
     for where in (at[other], at[other] + sizes[other] - 4, at[other] - sizes[out] + 4):
         assert walk(cuda_lib, at | {out: where}) == INVALID
+
+
+SLOTS_IN = dict(rpi=4 * BATCH, pre=4 * BATCH, dl=4 * BATCH, slots=4 * T, acc=4 * BATCH * MOST, num=4 * BATCH)
+SLOTS_OUT = dict(rtt=4 * ROWS * STRIDE, seq=4 * BATCH, freed=4 * T, nf=4)
+
+
+def commit(lib, at):
+    return lib.sgl_commit_drafts(_ptr(at["rtt"]), ROWS, STRIDE, _ptr(at["rpi"]), _ptr(at["pre"]), _ptr(at["dl"]),
+                                 _ptr(at["slots"]), _ptr(at["acc"]), _ptr(at["num"]), BATCH, T, MOST, _ptr(at["seq"]),
+                                 _ptr(at["freed"]), _ptr(at["nf"]), None)
+
+
+@pytest.mark.parametrize("out", SLOTS_OUT)
+@pytest.mark.parametrize("other", [*SLOTS_IN, *SLOTS_OUT])
+def test_commit(cuda_lib, out, other):
+    if out == other:
+        return
+    sizes = SLOTS_IN | SLOTS_OUT
+    at = _apart(sizes)
+    for where in (at[other], at[other] + sizes[other] - 4, at[other] - sizes[out] + 4):
+        if (out, other, where) == ("seq", "pre", at["pre"]):
+            continue    # the new lengths in the old ones' place
+        assert commit(cuda_lib, at | {out: where}) == INVALID

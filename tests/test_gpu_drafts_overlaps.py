@@ -5,9 +5,11 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+import oracle  # noqa: E402
 from radixattention_prefix_shared_gb300 import binding as B  # noqa: E402
 
 from _drafts import accept_case, want_accept  # noqa: E402
+from test_gpu_drafts import commit_case  # noqa: E402
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
@@ -41,3 +43,25 @@ def test_walk():
                               accepted=rest[4:-4].view(4, most), num_accepted=rest[:4], next_tokens=rest[-4:])
     for x, w in zip(got, want_accept(c)):
         assert np.array_equal(x.cpu().numpy(), w)
+
+
+def test_commit():
+    c = commit_case(302, [3, 0, 7, 20, 1])
+    new = lambda: [torch.from_numpy(c[k]).to(DEV) for k in ("rtt", "rpi", "pre", "drafts", "slots", "acc", "cnt")]  # noqa: E731
+    t = new()
+    rtt, rpi, pre, lens, slots, acc, cnt = t
+    for kw in (dict(freed=slots), dict(seq_lens=cnt), dict(seq_lens=lens), dict(seq_lens=rpi), dict(seq_lens=slots[2:7]),
+               dict(num_freed=pre[:1]), dict(num_freed=rtt.view(-1)[5:6]), dict(freed=acc.view(-1)[: len(slots)])):
+        _refused(B.sgl_commit_drafts, *t, **kw)
+    # the one request's slots as they stand in its row
+    view = rtt.view(-1)[5: 5 + len(slots)]
+    _refused(B.sgl_commit_drafts, *t[:4], view, acc, cnt)
+    assert all(torch.equal(a, b) for a, b in zip(t, new()))
+    # the new lengths in place of the old ones, over many requests
+    c = commit_case(303, [7] * 200)
+    rtt, rpi, pre, lens, slots, acc, cnt = t = new()
+    seq, freed, count = B.sgl_commit_drafts(*t, seq_lens=pre)
+    want = oracle.drafts.commit_drafts(c["rtt"], c["rpi"], c["pre"], c["drafts"], c["slots"], c["acc"], c["cnt"])
+    assert seq.data_ptr() == pre.data_ptr() and np.array_equal(seq.cpu().numpy(), want[1])
+    assert np.array_equal(rtt.cpu().numpy(), want[0]) and np.array_equal(freed.cpu().numpy()[: len(want[2])], want[2])
+    assert count.tolist() == [len(want[2])]
