@@ -523,7 +523,8 @@ sgl_status sgl_qk_norm_rope_store_kv_fp8(const void* q, int64_t q_stride, const 
  *     max_draft, max_prefix : host values >= the largest length (a precondition, as
  *                    prefix + draft_lens <= rtt_stride is: where one fails the
  *                    outputs are undefined, and nothing is read or written out of
- *                    bounds)
+ *                    bounds); max_draft <= total_draft, as max_extend of an extend,
+ *                    and max_prefix < rtt_stride (SGL_ERR_INVALID_ARG otherwise)
  *     shared_len   : the batch's rows hold the same slots at positions [0, shared_len)
  *                    (host value, <= every prefix of a request with tokens; 0: nothing
  *                    is shared).  Those keys are read once for all requests.

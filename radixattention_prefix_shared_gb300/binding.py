@@ -814,6 +814,8 @@ def _verify(name, q, pool_k, pool_v, scales, req_to_token, req_pool_idx, prefix_
     if not (-_I32 <= max_draft <= _I32 and -_I32 <= max_prefix <= _I32 and -_I32 <= shared_len <= _I32
             and -_I32 <= total):
         _need_i32(name, max_draft=max_draft, max_prefix=max_prefix, shared_len=shared_len, total_draft=total)
+    if total < max_draft <= 64:  # a tree has no more nodes than the step
+        max_draft = max(total, 0)
     dims = _dims_ref(qs[1], ks[1], ks[2], ks[0], float(sm_scale))
     if out is None or workspace is None:
         with _on(stream):
@@ -840,7 +842,8 @@ def sgl_verify_attention(q, pool_k, pool_v, req_to_token, req_pool_idx, prefix_l
     and the nodes above them (``parents``: indices among the request's nodes, -1
     for none).  The drafted tokens' K and V are stored first, at positions prefix,
     prefix + 1, ... of the request's row.  ``shared_len``: positions whose slots all
-    rows of the batch share, read once."""
+    rows of the batch share, read once.  ``max_draft`` (at most 64) and ``max_prefix``
+    are bounds: a loop may pass the same ones every step."""
     return _verify("sgl_verify_attention", q, pool_k, pool_v, (), req_to_token, req_pool_idx, prefix_lens, draft_lens,
                    parents, out, max_draft, max_prefix, shared_len, total_draft, workspace, sm_scale, stream)
 
