@@ -111,51 +111,55 @@ class Batch:
         sms = torch.cuda.get_device_properties(0).multi_processor_count
         return segments(self.prefix, self.drafts, self.Hq, self.Hkv, self.fp8, sms)
 
-    def _values(self, pool, r, h, i):
-        x = pool[self.slots[r], h]
-        return x.view(torch.float8_e4m3fn).double() * self.scales[i] if self.fp8 else x.double()
+    def _values(self, pool, r, i):
+        """[KV heads, keys, D] of request r."""
+        x = pool[self.slots[r]]
+        x = x.view(torch.float8_e4m3fn).double() * self.scales[i] if self.fp8 else x.double()
+        return x.transpose(0, 1)
 
     def visible(self, r):
         """[nodes, keys] of request r."""
         p, par = self.prefix[r], self.par[r]
-        see = torch.zeros(len(par), p + len(par), dtype=torch.bool)
-        see[:, :p] = True
+        tree = np.zeros((len(par), len(par)), bool)
         for i, up in enumerate(par):
             if up >= 0:
-                see[i] = see[up]
-            see[i, p + i] = True
-        return see.to(self.q.device)
+                tree[i] = tree[up]
+            tree[i, i] = True
+        return torch.from_numpy(np.concatenate([np.ones((len(par), p), bool), tree], 1)).to(self.q.device)
+
+    def _scores(self, r, see):
+        g, t0, x = self.Hq // self.Hkv, sum(self.drafts[:r]), self.drafts[r]
+        q = self.q[t0: t0 + x].double().view(x, self.Hkv, g, self.D).transpose(0, 1)
+        k = self._values(self.pool_k, r, 0)[:, None].transpose(-1, -2)
+        hidden = ~see[None, :, None]
+        s, reach = (q @ k) * self.D ** -0.5, (q.abs() @ k.abs()) * self.D ** -0.5
+        return s.masked_fill(hidden, -math.inf), reach.masked_fill(hidden, 0.0)
 
     def scores(self, r, h):
         """[nodes, heads of KV head h, keys] in float64, hidden ones -inf, and the
         products' absolute sums."""
-        g, t0, x = self.Hq // self.Hkv, sum(self.drafts[:r]), self.drafts[r]
-        q = self.q[t0: t0 + x, h * g: (h + 1) * g].double()
-        k = self._values(self.pool_k, r, h, 0)
-        s, reach = (q @ k.T) * self.D ** -0.5, (q.abs() @ k.abs().T) * self.D ** -0.5
-        hidden = ~self.visible(r)[:, None]
-        return s.masked_fill(hidden, -math.inf), reach.masked_fill(hidden, 0.0)
+        return tuple(x[h] for x in self._scores(r, self.visible(r)))
 
     def want(self):
         """(out, terms) as ``oracle.drafts.verify_attention``."""
         shape = self.q.shape
         out, spread = (torch.zeros(shape, dtype=torch.float64, device=self.q.device) for _ in range(2))
         reach, floor = (torch.zeros(*shape[:2], 1, dtype=torch.float64, device=self.q.device) for _ in range(2))
-        g, t0 = self.Hq // self.Hkv, 0
+        t0 = 0
         for r, x in enumerate(self.drafts):
             if x == 0:
                 continue
             see = self.visible(r)
-            for h in range(self.Hkv):
-                s, a = self.scores(r, h)
-                v = self._values(self.pool_v, r, h, 1)
-                w = torch.exp(s - s.amax(-1, keepdim=True))
-                total = w.sum(-1, keepdim=True)
-                at = slice(t0, t0 + x), slice(h * g, (h + 1) * g)
-                out[at], spread[at] = (w @ v) / total, (w @ v.abs()) / total
-                reach[at] = a.amax(-1, keepdim=True)
-                most = torch.where(see[:, :, None], v.abs(), 0.0).amax((1, 2))
-                floor[at] = see.sum(-1)[:, None, None] * most[:, None, None] / total
+            s, a = self._scores(r, see)
+            v = self._values(self.pool_v, r, 1)[:, None]
+            w = torch.exp(s - s.amax(-1, keepdim=True))
+            total = w.sum(-1, keepdim=True)
+            rows = lambda y: y.transpose(0, 1).flatten(1, 2)  # noqa: E731
+            at = slice(t0, t0 + x)
+            out[at], spread[at] = rows((w @ v) / total), rows((w @ v.abs()) / total)
+            reach[at] = rows(a.amax(-1, keepdim=True))
+            most = torch.where(see, v.abs().amax(-1), 0.0).amax(-1)[:, :, None, None]  # [KV heads, nodes, 1, 1]
+            floor[at] = rows(see.sum(-1)[:, None, None] * most / total)
             t0 += x
         return out, dict(spread=spread, reach=reach, floor=floor)
 
