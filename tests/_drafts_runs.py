@@ -52,13 +52,15 @@ class Batch:
     req_to_token behind a request's nodes name pool rows that are NaN.
 
     step: None, or by how much (in units of the softmax's exponent) the scores of a
-    block of keys lie above those of the block before."""
+    block of keys lie above those of the block before.  shared: positions whose slots
+    are the same in every row."""
 
-    def __init__(self, seed, *, Hq, Hkv, D, prefix, drafts, fp8=False, kind="tree", std=1.0, step=None, dev="cuda:0"):
+    def __init__(self, seed, *, Hq, Hkv, D, prefix, drafts, fp8=False, kind="tree", std=1.0, step=None, shared=0,
+                 dev="cuda:0"):
         g = np.random.default_rng(seed)
         gen = torch.Generator(device=dev).manual_seed(seed)
         randn = lambda *s: torch.randn(*s, generator=gen, device=dev)  # noqa: E731
-        self.Hq, self.Hkv, self.D, self.fp8 = Hq, Hkv, D, fp8
+        self.Hq, self.Hkv, self.D, self.fp8, self.shared = Hq, Hkv, D, fp8, shared
         self.prefix, self.drafts = [int(x) for x in prefix], [int(x) for x in drafts]
         self.par = [tree(g, x, kind) for x in self.drafts]
         live = sum(p + x for p, x in zip(prefix, drafts))
@@ -69,7 +71,8 @@ class Batch:
         depth = np.zeros(S, np.int64)  # a slot's block in its request
         at, self.slots = 0, []
         for r, (p, x) in enumerate(zip(prefix, drafts)):
-            mine = perm[at: at + p + x]
+            mine = perm[at: at + p + x].copy()
+            mine[:shared] = perm[:shared]
             rtt[rpi[r], : p + x] = mine
             depth[mine] = np.arange(p + x) // BLOCK
             self.slots.append(torch.from_numpy(mine.astype(np.int64)).to(dev))
@@ -98,14 +101,15 @@ class Batch:
 
     def new_workspace(self):
         return B.new_workspace(B.verify_workspace_bytes(len(self.drafts), sum(self.drafts), max(self.drafts),
-                                                        max(self.prefix), 0,
+                                                        max(self.prefix), self.shared,
                                                         B.make_dims(self.Hq, self.Hkv, self.D, len(self.pool_k))),
                                self.q.device)
 
     def run(self, **kw):
         f = B.sgl_verify_attention_fp8 if self.fp8 else B.sgl_verify_attention
         return f(self.q, self.pool_k, self.pool_v, *self.scales, self.rtt, self.rpi, self.prefix_lens,
-                 self.draft_lens, self.parents, max_draft=max(self.drafts), max_prefix=max(self.prefix), **kw)
+                 self.draft_lens, self.parents, max_draft=max(self.drafts), max_prefix=max(self.prefix),
+                 shared_len=self.shared, **kw)
 
     def segments(self):
         sms = torch.cuda.get_device_properties(0).multi_processor_count
