@@ -657,8 +657,8 @@ size_t sgl_cascade_decode_workspace_bytes(int32_t batch, int32_t max_seq_len, in
  * 3).  The slots of sgl_qk_norm_rope_store_kv are checked with
  * sgl_check_store_kv_indices, which reports a padding token's as kind 1: give it
  * the other tokens' alone.
- * sgl_check_verify_indices checks what sgl_verify_attention reads: rows, lengths (an
- * entry of draft_lens of 0 is a padding row), slots, parents and the shared prefix.
+ * sgl_check_verify_indices checks what sgl_verify_attention reads: rows, lengths,
+ * slots, parents and the shared prefix; of a padding row (draft_lens 0 or less) nothing.
  * sgl_check_store_kv_indices needs a scratch bitmap of (pool_size+7)/8 bytes
  * (rounded up to 16) in `bitmap`; it is cleared by the call.
  * sgl_check_cascade_groups needs sgl_check_cascade_scratch_bytes(batch,

@@ -69,6 +69,7 @@ __global__ void check_store_kernel(const int32_t* __restrict__ slots, int32_t n,
 // mode 0: extend (lens_a = prefix, lens_b = extend; the prefix slots are read);
 // mode 2: the same over an e4m3 pool (prefix and suffix slots are read);
 // mode 1: decode (lens_a = seq).
+// mode 3: drafted tokens over either pool (as mode 2; a row without tokens is padding).
 // With a window (window > 0, modes 1 and 2) only the positions some query sees
 // are checked: [0, sinks) and those past the first query's position less the
 // window; decode and extend lengths may then be 0 (a padding row).
@@ -78,6 +79,7 @@ __global__ void check_rows_kernel(const int32_t* __restrict__ rtt, int32_t rtt_r
                                   int32_t max_a, int32_t max_b, int32_t window, int32_t sinks,
                                   int32_t* err) {
   const int r = blockIdx.x;
+  if (mode == 3 && lens_b[r] <= 0) return;
   if (window > 0 && (mode == 1 ? lens_a[r] : lens_b[r]) == 0) {
     // a padding row: nothing of it is read, its row of the table either
     if (mode != 1 && lens_a[r] < 0 && threadIdx.x == 0) report(err, 3, r, 0, lens_a[r]);
@@ -103,7 +105,7 @@ __global__ void check_rows_kernel(const int32_t* __restrict__ rtt, int32_t rtt_r
       if (threadIdx.x == 0) report(err, 5, r, 0, pl > max_a ? pl : el);
       return;
     }
-    n = mode == 2 ? pl + el : pl;
+    n = mode >= 2 ? pl + el : pl;
     if (window > 0) lo = max(0, pl - window + 1);
   } else {
     const int32_t sl = lens_a[r];
@@ -130,11 +132,12 @@ __global__ void check_rows_kernel(const int32_t* __restrict__ rtt, int32_t rtt_r
   }
 }
 
-__global__ void check_sum_kernel(const int32_t* __restrict__ lens, int32_t batch, int32_t total,
+// (least: what an entry counts for at the least)
+__global__ void check_sum_kernel(const int32_t* __restrict__ lens, int32_t batch, int32_t total, int32_t least,
                                  int32_t* err) {
   __shared__ long long part[32];
   long long s = 0;
-  for (int i = threadIdx.x; i < batch; i += blockDim.x) s += lens[i];
+  for (int i = threadIdx.x; i < batch; i += blockDim.x) s += max(lens[i], least);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
@@ -704,7 +707,7 @@ sgl_status check_extend(const int32_t* req_to_token, int32_t rtt_rows, int32_t r
   check_rows_kernel<<<(unsigned)batch, 256, 0, s>>>(req_to_token, rtt_rows, rtt_stride, req_pool_idx,
                                                     prefix_lens, extend_lens, mode, pool_size,
                                                     max_prefix, max_extend, window, sinks, d_error);
-  check_sum_kernel<<<1, 1024, 0, s>>>(extend_lens, batch, total_extend, d_error);
+  check_sum_kernel<<<1, 1024, 0, s>>>(extend_lens, batch, total_extend, mode == 3 ? 0 : INT32_MIN, d_error);
   return last_launch();
 }
 }  // namespace
@@ -1122,7 +1125,7 @@ sgl_status sgl_check_verify_indices(const int32_t* req_to_token, int32_t rtt_row
   if (shared_len < 0 || shared_len > max_prefix || (batch > 0 && !parents)) return SGL_ERR_INVALID_ARG;
   const sgl_status st =
       check_extend(req_to_token, rtt_rows, rtt_stride, req_pool_idx, prefix_lens, draft_lens, batch, total_draft,
-                   max_draft, max_prefix, pool_size, d_error, stream, 2, INT32_MAX, 0);
+                   max_draft, max_prefix, pool_size, d_error, stream, 3);
   if (st != SGL_OK || batch == 0) return st;
   check_trees_kernel<<<(unsigned)batch, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
       req_to_token, rtt_rows, rtt_stride, req_pool_idx, prefix_lens, draft_lens, parents, total_draft, shared_len,
