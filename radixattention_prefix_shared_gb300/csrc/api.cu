@@ -1122,11 +1122,12 @@ sgl_status sgl_check_verify_indices(const int32_t* req_to_token, int32_t rtt_row
                                     const int32_t* draft_lens, const int32_t* parents, int32_t batch,
                                     int32_t total_draft, int32_t max_draft, int32_t max_prefix, int32_t shared_len,
                                     int64_t pool_size, int32_t* d_error, sgl_stream_t stream) {
-  if (shared_len < 0 || shared_len > max_prefix || (batch > 0 && !parents)) return SGL_ERR_INVALID_ARG;
+  if (shared_len < 0 || shared_len > max_prefix || (batch > 0 && total_draft != 0 && !parents))
+    return SGL_ERR_INVALID_ARG;
   const sgl_status st =
       check_extend(req_to_token, rtt_rows, rtt_stride, req_pool_idx, prefix_lens, draft_lens, batch, total_draft,
                    max_draft, max_prefix, pool_size, d_error, stream, 3);
-  if (st != SGL_OK || batch == 0) return st;
+  if (st != SGL_OK || batch == 0 || total_draft == 0) return st;
   check_trees_kernel<<<(unsigned)batch, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
       req_to_token, rtt_rows, rtt_stride, req_pool_idx, prefix_lens, draft_lens, parents, total_draft, shared_len,
       d_error);
