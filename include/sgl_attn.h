@@ -515,7 +515,9 @@ sgl_status sgl_qk_norm_rope_store_kv_fp8(const void* q, int64_t q_stride, const 
  *   over j < prefix_lens[r] and j = prefix_lens[r] + k, k = i or above i, K_j and V_j
  *   the pool rows at req_to_token[row, j]: the drafted tokens' K and V are stored
  *   first, node k's slot at position prefix_lens[r] + k.  A chain (parents i - 1) is
- *   sgl_extend_attention over the pool.
+ *   sgl_extend_attention over the pool, which is the faster call from some 64 query rows
+ *   a KV head (nodes x query heads a KV head) on, unless requests are few.  Keys and
+ *   values that some node of a request sees are finite (a hidden one has weight 0).
  *     parents      : int32 [T]
  *     prefix_lens  : int32 [batch], >= 0;  draft_lens: int32 [batch]
  *     total_draft  : T (host value); rows of q and out behind the sum of draft_lens

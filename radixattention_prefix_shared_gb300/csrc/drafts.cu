@@ -79,7 +79,8 @@ SGL_DEV float weight(float x) {
   return x <= 3.402823466e38f ? x : 0.f;
 }
 
-// h + l, l what h has lost.  (No contraction or reordering: the sums are exact.)
+// h + l, l what h has lost: Knuth's two-sum, whose error term is exact.  (No contraction or
+// reordering.)
 struct Pair {
   float h = 0.f, l = 0.f;
   SGL_DEV void add(float h2, float l2) {

@@ -40,13 +40,16 @@
 // a block's end nor at a unit's.  Waits are bounded as in the extend kernels.
 //
 // What it measured (of the copy benchmark's 6.78 TB/s, 32 query heads of 128 on 8): 128
-// requests of 1,024 to 32,768 tokens, 8 drafts, 16 query heads on 8: 711 us, 6.8 TB/s,
-// 1.00.  64 requests of 4,000 tokens: 4, 8, 16 and 32 drafts (16 to 128 columns) 178, 181,
-// 213 and 328 us, 0.87 to 0.49: beyond 32 columns by the softmax's instructions and, at
-// 128, its registers.  e4m3: 210, 217, 307 and 590 us, 0.37 and less: shared memory
+// requests of 1,024 to 32,768 tokens, 8 drafts, 16 query heads on 8: 711 to 741 us, 6.5 to
+// 6.8 TB/s, 0.96 to 1.00.  64 requests of 4,000 tokens: 4, 8, 16 and 32 drafts (16 to 128
+// columns) 174, 177, 209 and 326 us, 0.89 to 0.49: beyond 32 columns by what the warps
+// issue and wait for (128 columns: 10,400 warp instructions a block, issue slots busy 52%,
+// DRAM 46%, tensor pipe 20%).  e4m3: 207, 213, 306 and 592 us, 0.38 and less: shared memory
 // carries each code as a copy, a load, stores of twice its size and the MMAs' reads, and
 // with 64 columns (the most) the ring has room for two tiles on their way.  One request of
-// 16,384 tokens, 5 drafts: 25 us, six blocks a CTA between start and merge.
+// 16,384 tokens, 5 drafts: 25 us, six blocks a CTA between start and merge.  A chain of
+// more than 64 query rows a KV head is faster as an extend where requests are many (64
+// x 32 drafts: 266 us).
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -150,7 +153,8 @@ struct Misc {
   Start start;
   Segment seg[2];
   alignas(16) float mcol[128];  // a column's reference (read four at a time)
-  int32_t mxcol[128];  // its block maximum, as an ordered integer; then (as a float) its rescaling
+  int32_t mxcol[128];  // its block maximum, as an ordered integer; then (as a float) its rescaling;
+                       // at a segment's end a warp's sums
   float lcol[2][128];  // at a segment's end: sums over the keys, references (then output factors)
 };
 static_assert(sizeof(Misc) <= 3 * 1024, "barriers and column states");
